@@ -1,9 +1,10 @@
-// abi.cpp -- the extern "C" entry points declared in include/nvfp4.h:
-// argument validation (before anything is enqueued) and dispatch to the
+// abi.cpp -- the extern "C" entry points declared in include/nvfp4.h and
+// include/nvfp4_serving.h: argument validation (before anything is enqueued) and dispatch to the
 // kernel launchers.  The library allocates no memory and keeps no state.
 #include <hip/hip_runtime.h>
 
 #include "../../include/nvfp4.h"
+#include "../../include/nvfp4_serving.h"
 #include "internal.h"
 
 namespace {
@@ -234,10 +235,11 @@ int silu_mul_nvfp4_quantize_ws(const void* x, int64_t b, int64_t m, int64_t k2, 
 
 static_assert(NVFP4_GEMM_WS_BYTES == nvfp4::kGemmWsBytes, "GEMM workspace size");
 
-static int gemm_common(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf,
-                       const float* alpha, const int32_t* mask, const void* bias, const void* d,
-                       const void* l1, void* out, int64_t E, int64_t m, int64_t n, int64_t k,
-                       int64_t r, void* ws, int64_t ws_bytes, void* stream) {
+// Every check of a GEMM call; fills g when they pass.
+static int gemm_check(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf,
+                      const float* alpha, const int32_t* mask, const void* bias, const void* d,
+                      const void* l1, void* out, int64_t E, int64_t m, int64_t n, int64_t k,
+                      int64_t r, void* ws, int64_t ws_bytes, nvfp4::GemmArgs& g) {
     if (!a || !b || !a_sf || !b_sf || !alpha || !out) return NVFP4_NULL_POINTER;
     if (!dim_ok(E) || !dim_ok(m) || !dim_ok(n) || k < 16 || k % 16 != 0 || k > kMaxDim)
         return NVFP4_BAD_SHAPE;
@@ -251,11 +253,20 @@ static int gemm_common(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, 
         return NVFP4_MISALIGNED;
     if (ws && ws_bytes < NVFP4_GEMM_WS_BYTES) return NVFP4_BAD_SHAPE;
     if (ws && !aligned16(ws)) return NVFP4_MISALIGNED;
-    nvfp4::GemmArgs g{};
     g.a = a; g.b = b; g.a_sf = a_sf; g.b_sf = b_sf; g.alpha = alpha; g.mask = mask;
     g.bias = (const uint16_t*)bias; g.d = (const uint16_t*)d; g.l1 = (const uint16_t*)l1;
     g.out = (uint16_t*)out; g.E = E; g.m = m; g.n = n; g.k = k; g.r = r;
     g.ws = (float*)ws;
+    return NVFP4_OK;
+}
+
+static int gemm_common(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf,
+                       const float* alpha, const int32_t* mask, const void* bias, const void* d,
+                       const void* l1, void* out, int64_t E, int64_t m, int64_t n, int64_t k,
+                       int64_t r, void* ws, int64_t ws_bytes, void* stream) {
+    nvfp4::GemmArgs g{};
+    const int st = gemm_check(a, b, a_sf, b_sf, alpha, mask, bias, d, l1, out, E, m, n, k, r, ws, ws_bytes, g);
+    if (st != NVFP4_OK) return st;
     return launch_status(nvfp4::launch_gemm(g, (hipStream_t)stream));
 }
 
@@ -392,6 +403,103 @@ int nvfp4_alpha(const float* gs_a, const float* gs_b, float* alpha, int64_t coun
     if (((uintptr_t)gs_a & 3u) || ((uintptr_t)gs_b & 3u) || ((uintptr_t)alpha & 3u))
         return NVFP4_MISALIGNED;
     return launch_status(nvfp4::launch_alpha(gs_a, gs_b, alpha, count, (hipStream_t)stream));
+}
+
+int nvfp4_moe_small(const void* x, int64_t t, int64_t h, const void* logits, int logits_dtype, int64_t E,
+                    int64_t top_k, int score, int renormalize, const uint8_t* w13, const uint8_t* w13_sf,
+                    const float* alpha13, const uint8_t* w2, const uint8_t* w2_sf, const float* alpha2,
+                    int64_t inter, void* out, int32_t* topk_ids, float* topk_weights, void* workspace,
+                    int64_t workspace_bytes, void* stream) {
+    if (!x || !logits || !w13 || !w13_sf || !alpha13 || !w2 || !w2_sf || !alpha2 || !out || !topk_ids ||
+        !topk_weights || !workspace)
+        return NVFP4_NULL_POINTER;
+    if (logits_dtype != NVFP4_BF16 && logits_dtype != NVFP4_F32) return NVFP4_BAD_DTYPE;
+    if (!dim_ok(t) || !dim_ok(E) || !dim_ok(top_k) || top_k > E) return NVFP4_BAD_SHAPE;
+    if (!dim_ok(h) || h % 16 != 0 || !dim_ok(inter) || inter % 16 != 0) return NVFP4_BAD_SHAPE;
+    if (t > NVFP4_MOE_SMALL_MAX_TOKENS || E > NVFP4_MOE_SMALL_MAX_EXPERTS || top_k > NVFP4_MOE_SMALL_MAX_TOP_K)
+        return NVFP4_UNSUPPORTED;
+    if (score != NVFP4_ROUTE_SOFTMAX && score != NVFP4_ROUTE_SIGMOID) return NVFP4_UNSUPPORTED;
+    // one expert's weights (2 inter x h codes) and its scale buffers
+    if (inter > ((int64_t)1 << 31) / h || !gemm_sf_ok(2 * inter, h / 16) || !gemm_sf_ok(h, inter / 16))
+        return NVFP4_UNSUPPORTED;
+    if (workspace_bytes < NVFP4_MOE_SMALL_WS_BYTES(t, top_k, inter)) return NVFP4_BAD_SHAPE;
+    if (!aligned16(x) || !aligned16(logits) || !aligned16(w13) || !aligned16(w13_sf) || !aligned16(w2) ||
+        !aligned16(w2_sf) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)alpha13 & 3u) ||
+        ((uintptr_t)alpha2 & 3u) || ((uintptr_t)topk_ids & 3u) || ((uintptr_t)topk_weights & 3u))
+        return NVFP4_MISALIGNED;
+    nvfp4::MoeSmallArgs a{};
+    a.x = (const uint16_t*)x; a.logits = logits; a.logits_bf16 = logits_dtype == NVFP4_BF16;
+    a.sigmoid = score == NVFP4_ROUTE_SIGMOID; a.renorm = renormalize != 0;
+    a.w13 = w13; a.w13_sf = w13_sf; a.alpha13 = alpha13;
+    a.w2 = w2; a.w2_sf = w2_sf; a.alpha2 = alpha2;
+    a.out = (uint16_t*)out; a.ids = topk_ids; a.weights = topk_weights; a.ws = workspace;
+    a.t = (int)t; a.h = (int)h; a.inter = (int)inter; a.E = (int)E; a.top_k = (int)top_k;
+    return launch_status(nvfp4::launch_moe_small(a, (hipStream_t)stream));
+}
+
+// The adapters' own arguments, and the workspace that holds d.
+static int adapters_check(const void* x, const void* lora_a, const void* lora_b, const int32_t* adapter,
+                          const float* scaling, int64_t m, int64_t n, int64_t k, int64_t r, int64_t n_adapters,
+                          const void* workspace, int64_t workspace_bytes) {
+    if (!x || !lora_a || !lora_b || !adapter || !workspace) return NVFP4_NULL_POINTER;
+    if (r < 8 || r % 8 != 0 || r > NVFP4_ADAPTERS_MAX_RANK) return NVFP4_BAD_RANK;
+    if (!dim_ok(m) || !dim_ok(n) || !dim_ok(n_adapters) || k < 16 || k % 16 != 0 || k > kMaxDim)
+        return NVFP4_BAD_SHAPE;
+    if ((m + 15) / 16 > 65535) return NVFP4_BAD_SHAPE;
+    if (workspace_bytes < NVFP4_ADAPTERS_WS_BYTES(m, r)) return NVFP4_BAD_SHAPE;
+    if (!aligned16(x) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(workspace) ||
+        ((uintptr_t)adapter & 3u) || ((uintptr_t)scaling & 3u))
+        return NVFP4_MISALIGNED;
+    return NVFP4_OK;
+}
+
+static nvfp4::AdapterArgs adapter_args(const void* x, const void* lora_a, const void* lora_b,
+                                       const int32_t* adapter, const float* scaling, int64_t m, int64_t n,
+                                       int64_t k, int64_t r, int64_t n_adapters, void* workspace) {
+    nvfp4::AdapterArgs a{};
+    a.x = (const uint16_t*)x; a.lora_a = (const uint16_t*)lora_a; a.lora_b = (const uint16_t*)lora_b;
+    a.adapter = adapter; a.scaling = scaling; a.d = (float*)workspace;
+    a.m = m; a.n = n; a.k = k; a.r = r; a.n_adapters = n_adapters;
+    return a;
+}
+
+int nvfp4_linear_adapters(const void* x, const uint8_t* b, const uint8_t* b_sf, const float* alpha,
+                          const void* lora_a, const void* lora_b, const int32_t* adapter, const float* scaling,
+                          const void* bias, void* out, int64_t m, int64_t n, int64_t k, int64_t r,
+                          int64_t n_adapters, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!b || !b_sf || !alpha || !out) return NVFP4_NULL_POINTER;
+    const int st = adapters_check(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace,
+                                  workspace_bytes);
+    if (st != NVFP4_OK) return st;
+    if (!gemm_sf_ok(n, k / 16)) return NVFP4_UNSUPPORTED;
+    if (!aligned16(b) || !aligned16(b_sf) || !aligned16(out) || ((uintptr_t)alpha & 3u) || (bias && !aligned16(bias)))
+        return NVFP4_MISALIGNED;
+    const nvfp4::AdapterArgs a = adapter_args(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace);
+    const hipError_t e = nvfp4::launch_adapter_down(a, (hipStream_t)stream);
+    if (e != hipSuccess) return launch_status(e);
+    return launch_status(nvfp4::launch_w4a16_adapters(a, b, b_sf, alpha, (const uint16_t*)bias, (uint16_t*)out,
+                                                      (hipStream_t)stream));
+}
+
+int nvfp4_gemm_adapters(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf, const uint8_t* b_sf,
+                        const float* alpha, const void* x, const void* lora_a, const void* lora_b,
+                        const int32_t* adapter, const float* scaling, const void* bias, void* out, int64_t m,
+                        int64_t n, int64_t k, int64_t r, int64_t n_adapters, void* workspace,
+                        int64_t workspace_bytes, void* stream) {
+    int st = adapters_check(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace, workspace_bytes);
+    if (st != NVFP4_OK) return st;
+    // the split-tail schedule's partial tiles behind d, where they fit
+    const int64_t dbytes = NVFP4_ADAPTERS_WS_BYTES(m, r);
+    void* const part = workspace_bytes >= dbytes + NVFP4_GEMM_WS_BYTES ? (char*)workspace + dbytes : nullptr;
+    nvfp4::GemmArgs g{};
+    st = gemm_check(a, b, a_sf, b_sf, alpha, nullptr, bias, nullptr, nullptr, out, 1, m, n, k, 0, part,
+                    NVFP4_GEMM_WS_BYTES, g);
+    if (st != NVFP4_OK) return st;
+    const nvfp4::AdapterArgs ad = adapter_args(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace);
+    const hipError_t e = nvfp4::launch_adapter_down(ad, (hipStream_t)stream);
+    if (e != hipSuccess) return launch_status(e);
+    g.r = r; g.ad_d = ad.d; g.ad_b = ad.lora_b; g.adapter = adapter; g.n_adapters = n_adapters;
+    return launch_status(nvfp4::launch_gemm(g, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -45,14 +45,36 @@
 #include "gemm_common.h"
 #include "internal.h"
 #include "quant_block.h"
+#include "skinny_w4.h"
 
 namespace nvfp4 {
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 // Epilogues of k_gemm: bf16 output; bf16 output after the rank-r LoRA-up
-// term; or silu_and_mul of the gate | up output quantized to NVFP4.
-enum Epilogue { EPI_PLAIN = 0, EPI_LORA = 1, EPI_SILUQ = 2 };
+// term; silu_and_mul of the gate | up output quantized to NVFP4; or bf16 output
+// after the rank-r term of each row's own adapter.
+enum Epilogue { EPI_PLAIN = 0, EPI_LORA = 1, EPI_SILUQ = 2, EPI_ADAPT = 3 };
+
+// Adapter of output row m (-1: none, past M, or an id outside [0, L)).
+__device__ __forceinline__ int row_adapter(const GParams& p, int64_t m) {
+    if (m >= p.M) return -1;
+    const int a = p.ad_ids[m];
+    return a >= 0 && a < p.ad_n ? a : -1;
+}
+
+// Eight fp32 values (32-byte aligned to 16) as two bf16 fragments hi + lo, the
+// sum within 2^-16 of the value.
+__device__ __forceinline__ void load_split8(const float* src, bf16x8& hi, bf16x8& lo) {
+    const f32x4 a = *(const f32x4*)src, b = *(const f32x4*)(src + 4);
+    uint32_t h[4], l[4];
+    split_bf16x2(a[0], a[1], h[0], l[0]);
+    split_bf16x2(a[2], a[3], h[1], l[1]);
+    split_bf16x2(b[0], b[1], h[2], l[2]);
+    split_bf16x2(b[2], b[3], h[3], l[3]);
+    hi = __builtin_bit_cast(bf16x8, u32x4{h[0], h[1], h[2], h[3]});
+    lo = __builtin_bit_cast(bf16x8, u32x4{l[0], l[1], l[2], l[3]});
+}
 
 // Waves per SIMD each configuration is compiled for: a 128x128 wave tile
 // takes the whole register file (256 accumulators per lane); smaller wave
@@ -540,6 +562,60 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
         }
     }
 
+    if constexpr (EPI == EPI_ADAPT) {
+        // the rank-r term of each row's own adapter, unscaled by alpha: a row's
+        // accumulators (one lane pair's) take alpha first, and the epilogue and
+        // the fixup launch give it none.  Rows without an adapter stay as they
+        // are, so they come out as the plain GEMM's, bit for bit.  The wave's
+        // rows are served adapter by adapter: the first row not yet served names
+        // one, the rows that share it take part together and the others enter
+        // as zeros.
+        const float al = p.alpha[e];
+        int id[FM];
+        uint32_t rem[FM];
+#pragma unroll
+        for (int i = 0; i < FM; i++) {
+            id[i] = KS == 1 || i == grp ? row_adapter(p, m0 + wm * WM + i * 32 + l32) : -1;
+            rem[i] = lora ? (uint32_t)__ballot(id[i] >= 0) : 0u;
+            const float s = id[i] >= 0 ? al : 1.0f;
+#pragma unroll
+            for (int in = 0; in < FN; in++) acc[in][i] *= s;
+        }
+        while (true) {
+            int a = -1;
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+                if (a < 0 && rem[i]) a = __builtin_amdgcn_readlane(id[i], __builtin_ctz(rem[i]));
+            if (a < 0) break;
+#pragma unroll
+            for (int i = 0; i < FM; i++) rem[i] &= ~(uint32_t)__ballot(id[i] == a);
+            for (int kr = 0; kr < p.r; kr += 16) {
+                const bool in_r = kr + h * 8 < p.r;  // r is a multiple of 8
+                bf16x8 hi[FM], lo[FM];
+#pragma unroll
+                for (int i = 0; i < FM; i++) {
+                    hi[i] = lo[i] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
+                    if (in_r && id[i] == a)
+                        load_split8(p.ad_d + (m0 + wm * WM + i * 32 + l32) * p.r + kr + h * 8, hi[i], lo[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < FN; i++) {
+                    int64_t row = n0 + wn * WN + i * 32 + l32;
+                    row = row < p.N ? row : p.N - 1;
+                    u32x4 v = {0u, 0u, 0u, 0u};
+                    if (in_r) v = *(const u32x4*)(p.ad_b + ((int64_t)a * p.N + row) * p.r + kr + h * 8);
+                    const bf16x8 ol = __builtin_bit_cast(bf16x8, v);
+#pragma unroll
+                    for (int im = 0; im < FM; im++)
+                        if (KS == 1 || im == grp) {
+                            acc[i][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[im], acc[i][im], 0, 0, 0);
+                            acc[i][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[im], acc[i][im], 0, 0, 0);
+                        }
+                }
+            }
+        }
+    }
+
     if (SK && slot >= 0) {
         // fp32 partial tile, fragment-major: the v-th 4 floats of every lane
         // of fragment f (32-row block f / (BN/32), 32-column block f % (BN/32))
@@ -569,7 +645,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
     static_assert(NW * 32 * PITCH <= NST * STAGE, "epilogue staging fits in the pipeline's LDS");
     barrier();
     lds_u8* const ep = sm + wave * 32 * PITCH;
-    const float alpha = p.alpha[e];
+    const float alpha_e = p.alpha[e];
     uint16_t* O = p.out + (int64_t)e * p.M * p.N;
     constexpr int CPR = WN / 8;        // 16-byte pieces per staged row
     // the bias of this lane's columns (4 consecutive per fragment column and
@@ -594,6 +670,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
 #pragma unroll
     for (int im = 0; im < FM; im++) {
         if (KS == 2 && im != grp) continue;  // the other K group stores this fragment row
+        const float alpha = EPI == EPI_ADAPT && row_adapter(p, m0 + wm * WM + im * 32 + l32) >= 0 ? 1.0f : alpha_e;
         // lane (l32, h) of fragment in: row l32, columns in*32 + 8g + 4h .. +3
 #pragma unroll
         for (int in = 0; in < FN; in++) {
@@ -725,7 +802,8 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
 // together.  Exits at once when nothing was split.
 constexpr int kFixupThreads = 1024;
 
-template <int BM, int BN, int KS>
+// ADAPT: the partial sums of rows with an adapter carry alpha already.
+template <int BM, int BN, int KS, bool ADAPT = false>
 __global__ __launch_bounds__(kFixupThreads) void k_gemm_fixup(GParams p) {
     constexpr int ITEMS = BM * BN / 4;  // float4 items of one partial tile
     static_assert(ITEMS % kFixupThreads == 0, "a workgroup's items lie in one tile");
@@ -754,7 +832,7 @@ __global__ __launch_bounds__(kFixupThreads) void k_gemm_fixup(GParams p) {
             for (int u = 0; u < 8; u++)
                 if (j0 + u < pl.S) s += t[u];
         }
-        const float alpha = p.alpha[e];
+        const float alpha = ADAPT && row_adapter(p, m) >= 0 ? 1.0f : p.alpha[e];
         uint16_t* const O = p.out + (int64_t)e * p.M * p.N;
         float y[4];
 #pragma unroll
@@ -773,7 +851,7 @@ __global__ __launch_bounds__(kFixupThreads) void k_gemm_fixup(GParams p) {
 }
 
 template <int BM, int BN, int WGM, int WGN, int NST, int KS = 1>
-static hipError_t launch_tile(GParams p, bool lora, hipStream_t st) {
+static hipError_t launch_tile(GParams p, Epilogue epi, hipStream_t st) {
     p.tiles_m = (int)((p.M + BM - 1) / BM);
     p.tiles_n = (int)((p.N + BN - 1) / BN);
     const int tiles = p.tiles_m * p.tiles_n;
@@ -781,7 +859,10 @@ static hipError_t launch_tile(GParams p, bool lora, hipStream_t st) {
     dim3 grid(tiles, 1, (unsigned)p.E ? (unsigned)p.E : 1u);
     constexpr int threads = 64 * WGM * WGN * KS;
     const bool aligned = (p.K % 128) == 0;
-    if (lora) {
+    if (epi == EPI_ADAPT) {
+        if (aligned) k_gemm<BM, BN, WGM, WGN, NST, KS, true, EPI_ADAPT><<<grid, threads, 0, st>>>(p);
+        else k_gemm<BM, BN, WGM, WGN, NST, KS, false, EPI_ADAPT><<<grid, threads, 0, st>>>(p);
+    } else if (epi == EPI_LORA) {
         if (aligned) k_gemm<BM, BN, WGM, WGN, NST, KS, true, EPI_LORA><<<grid, threads, 0, st>>>(p);
         else k_gemm<BM, BN, WGM, WGN, NST, KS, false, EPI_LORA><<<grid, threads, 0, st>>>(p);
     } else {
@@ -794,7 +875,7 @@ static hipError_t launch_tile(GParams p, bool lora, hipStream_t st) {
 // Split-tail launch (see sk_plan) and, with a workspace, the launch that
 // adds the split tiles' partial sums.
 template <int BM, int BN, int WGM, int WGN, int NST, int KS>
-static hipError_t launch_tile_sk(GParams p, bool lora, float* ws, int G, hipStream_t st) {
+static hipError_t launch_tile_sk(GParams p, Epilogue epi, float* ws, int G, hipStream_t st) {
     p.tiles_m = (int)((p.M + BM - 1) / BM);
     p.tiles_n = (int)((p.N + BN - 1) / BN);
     p.xcd_chunk = 0;
@@ -805,14 +886,18 @@ static hipError_t launch_tile_sk(GParams p, bool lora, float* ws, int G, hipStre
     // rounds for every tile of every expert, plus the tail round
     const int64_t tmax = p.E * p.tiles_m * p.tiles_n;
     const dim3 grid((unsigned)(G * (tmax / G + 1)), 1, 1);
-    if (lora) {
+    if (epi == EPI_ADAPT) {
+        if (aligned) k_gemm<BM, BN, WGM, WGN, NST, KS, true, EPI_ADAPT, true><<<grid, threads, 0, st>>>(p);
+        else k_gemm<BM, BN, WGM, WGN, NST, KS, false, EPI_ADAPT, true><<<grid, threads, 0, st>>>(p);
+    } else if (epi == EPI_LORA) {
         if (aligned) k_gemm<BM, BN, WGM, WGN, NST, KS, true, EPI_LORA, true><<<grid, threads, 0, st>>>(p);
         else k_gemm<BM, BN, WGM, WGN, NST, KS, false, EPI_LORA, true><<<grid, threads, 0, st>>>(p);
     } else {
         if (aligned) k_gemm<BM, BN, WGM, WGN, NST, KS, true, EPI_PLAIN, true><<<grid, threads, 0, st>>>(p);
         else k_gemm<BM, BN, WGM, WGN, NST, KS, false, EPI_PLAIN, true><<<grid, threads, 0, st>>>(p);
     }
-    if (ws) k_gemm_fixup<BM, BN, KS><<<dim3((unsigned)G), kFixupThreads, 0, st>>>(p);
+    if (ws && epi == EPI_ADAPT) k_gemm_fixup<BM, BN, KS, true><<<dim3((unsigned)G), kFixupThreads, 0, st>>>(p);
+    else if (ws) k_gemm_fixup<BM, BN, KS><<<dim3((unsigned)G), kFixupThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -845,7 +930,7 @@ static hipError_t launch_tile_siluq(GParams p, hipStream_t st) {
 // ---------------------------------------------------------------------------
 constexpr int kSkinnyWaves = 8;  // K ranges of a workgroup (two waves per SIMD)
 
-template <bool ALIGNED, bool LORA>
+template <bool ALIGNED, int EPI>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
     const int t = threadIdx.x, lane = t & 63;
@@ -913,7 +998,28 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
             }
         }
     }
-    if constexpr (LORA) {
+    if constexpr (EPI == EPI_ADAPT) {
+        // the rank-r term of each row's own adapter (as in k_gemm), the tile's
+        // distinct adapters dealt to the waves
+        const int id = row_adapter(p, m0 + r);
+        acc *= id >= 0 ? p.alpha[0] : 1.0f;
+        uint32_t rem = (uint32_t)(__ballot(id >= 0) & 0xFFFF);
+        for (int turn = 0; rem; turn++) {
+            const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(rem));
+            rem &= ~(uint32_t)__ballot(id == a);
+            if (turn % kSkinnyWaves != wave) continue;
+            for (int kr = 0; kr < p.r; kr += 32) {
+                bf16x8 hi = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u}), lo = hi, ol = hi;
+                if (kr + g * 8 < p.r) {
+                    ol = __builtin_bit_cast(bf16x8, *(const u32x4*)(p.ad_b + ((int64_t)a * p.N + brow) * p.r + kr + g * 8));
+                    if (id == a) load_split8(p.ad_d + (m0 + r) * p.r + kr + g * 8, hi, lo);
+                }
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, acc, 0, 0, 0);
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, acc, 0, 0, 0);
+            }
+        }
+    }
+    if constexpr (EPI == EPI_LORA) {
         if (wave == 0) {  // rank-r bf16 correction, once, into wave 0's partial
             const int64_t drow = arow, lrow = brow;
             for (int kr = 0; kr < p.r; kr += 32) {
@@ -933,7 +1039,7 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
     // lane: output row m0 + r, columns n0 + 4g .. n0 + 4g + 3
     const int64_t m = m0 + r;
     if (m >= valid) return;
-    const float alpha = p.alpha[e];
+    const float alpha = EPI == EPI_ADAPT && row_adapter(p, m) >= 0 ? 1.0f : p.alpha[e];
     uint16_t* O = p.out + (int64_t)e * p.M * p.N + m * p.N;
     const int64_t n = n0 + 4 * g;
     float y[4];
@@ -968,21 +1074,6 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
 // conversion.  Any M works (grid y = M / 16); large M is better served by
 // quantizing the activation and using the NVFP4 x NVFP4 kernels.
 // ---------------------------------------------------------------------------
-
-// 8 FP4 codes of one dword times one block scale -> 8 bf16 (exact).
-__device__ __forceinline__ bf16x8 dequant8_bf16(uint32_t w, float s) {
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
-    const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
-    const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
-    const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
-    const bf16x2 h0 = __builtin_convertvector(f32x2{v0[0] * s, v0[1] * s}, bf16x2);
-    const bf16x2 h1 = __builtin_convertvector(f32x2{v1[0] * s, v1[1] * s}, bf16x2);
-    const bf16x2 h2 = __builtin_convertvector(f32x2{v2[0] * s, v2[1] * s}, bf16x2);
-    const bf16x2 h3 = __builtin_convertvector(f32x2{v3[0] * s, v3[1] * s}, bf16x2);
-    return bf16x8{h0[0], h0[1], h1[0], h1[1], h2[0], h2[1], h3[0], h3[1]};
-}
 
 template <bool ALIGNED>
 __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_w4a16(GParams p) {
@@ -1087,15 +1178,18 @@ hipError_t launch_gemm_w4a16(const GemmArgs& g, hipStream_t st) {
     return hipGetLastError();
 }
 
-static hipError_t launch_skinny(GParams p, bool lora, hipStream_t st) {
+static hipError_t launch_skinny(GParams p, Epilogue epi, hipStream_t st) {
     dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)((p.M + 15) / 16), (unsigned)p.E);
     const bool aligned = (p.K % 128) == 0;
-    if (lora) {
-        if (aligned) k_gemm_skinny<true, true><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
-        else k_gemm_skinny<false, true><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
+    if (epi == EPI_ADAPT) {
+        if (aligned) k_gemm_skinny<true, EPI_ADAPT><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
+        else k_gemm_skinny<false, EPI_ADAPT><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
+    } else if (epi == EPI_LORA) {
+        if (aligned) k_gemm_skinny<true, EPI_LORA><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
+        else k_gemm_skinny<false, EPI_LORA><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
     } else {
-        if (aligned) k_gemm_skinny<true, false><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
-        else k_gemm_skinny<false, false><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
+        if (aligned) k_gemm_skinny<true, EPI_PLAIN><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
+        else k_gemm_skinny<false, EPI_PLAIN><<<grid, 64 * kSkinnyWaves, 0, st>>>(p);
     }
     return hipGetLastError();
 }
@@ -1160,20 +1254,21 @@ hipError_t launch_gemm(const GemmArgs& g, hipStream_t st) {
     p.rpb = (int)((g.n + 127) / 128 * 128);
     p.sfa = (int64_t)p.rpa * cp;
     p.sfb = (int64_t)p.rpb * cp;
-    const bool lora = g.d != nullptr;
+    p.ad_d = g.ad_d; p.ad_b = g.ad_b; p.ad_ids = g.adapter; p.ad_n = (int)g.n_adapters;
+    const Epilogue epi = g.ad_d ? EPI_ADAPT : g.d ? EPI_LORA : EPI_PLAIN;
     const Tile t = pick_tile(g.m, g.n, g.k, g.E);
     if (use_split_schedule(g, t)) {
         const int G = sk_grid_size();
         if (G <= 0) return hipErrorInvalidDevice;
-        return launch_tile_sk<128, 256, 2, 2, 2, 2>(p, lora, g.ws, G, st);
+        return launch_tile_sk<128, 256, 2, 2, 2, 2>(p, epi, g.ws, G, st);
     }
     switch (t) {
-    case Tile::T256x256: return launch_tile<256, 256, 4, 2, 2>(p, lora, st);
-    case Tile::T256x192: return launch_tile<256, 192, 4, 2, 2>(p, lora, st);
-    case Tile::T128x256: return launch_tile<128, 256, 2, 2, 2>(p, lora, st);
-    case Tile::T128x256K2: return launch_tile<128, 256, 2, 2, 2, 2>(p, lora, st);
-    case Tile::Skinny: return launch_skinny(p, lora, st);
-    default: return launch_tile<128, 128, 2, 2, 2>(p, lora, st);
+    case Tile::T256x256: return launch_tile<256, 256, 4, 2, 2>(p, epi, st);
+    case Tile::T256x192: return launch_tile<256, 192, 4, 2, 2>(p, epi, st);
+    case Tile::T128x256: return launch_tile<128, 256, 2, 2, 2>(p, epi, st);
+    case Tile::T128x256K2: return launch_tile<128, 256, 2, 2, 2, 2>(p, epi, st);
+    case Tile::Skinny: return launch_skinny(p, epi, st);
+    default: return launch_tile<128, 128, 2, 2, 2>(p, epi, st);
     }
 }
 

@@ -42,6 +42,11 @@ struct GParams {
     // split-tail schedule (persistent K-split launch)
     float* part;         // fp32 partial tiles of the split tail tiles, or null (no split)
     int sk_grid;         // workgroups of the persistent launch
+    // adapter epilogue (EPI_ADAPT): d [M, r] fp32, adapters' B [L, N, r], ids [M]
+    const float* ad_d;
+    const uint16_t* ad_b;
+    const int32_t* ad_ids;
+    int ad_n;            // L
 };
 
 // 8 FP4 codes of one dword times one block scale -> 8 fp16 (exact): the
@@ -53,6 +58,21 @@ __device__ __forceinline__ f16x8 dequant8(uint32_t w, _Float16 s) {
     const f16x2 p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * ss;
     const f16x2 p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * ss;
     return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// 8 FP4 codes of one dword times one block scale -> 8 bf16 (exact).
+__device__ __forceinline__ bf16x8 dequant8_bf16(uint32_t w, float s) {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    const f32x2 v0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0);
+    const f32x2 v1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+    const f32x2 v2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2);
+    const f32x2 v3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+    const bf16x2 h0 = __builtin_convertvector(f32x2{v0[0] * s, v0[1] * s}, bf16x2);
+    const bf16x2 h1 = __builtin_convertvector(f32x2{v1[0] * s, v1[1] * s}, bf16x2);
+    const bf16x2 h2 = __builtin_convertvector(f32x2{v2[0] * s, v2[1] * s}, bf16x2);
+    const bf16x2 h3 = __builtin_convertvector(f32x2{v3[0] * s, v3[1] * s}, bf16x2);
+    return bf16x8{h0[0], h0[1], h1[0], h1[1], h2[0], h2[1], h3[0], h3[1]};
 }
 
 __device__ __forceinline__ uint32_t word(const u32x4& v, int j) {

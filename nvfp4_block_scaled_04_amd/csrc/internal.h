@@ -60,6 +60,11 @@ struct GemmArgs {
     uint16_t* out;         // [E, m, n]
     int64_t E, m, n, k, r;
     float* ws = nullptr;   // kGemmWsSlots partial 128x256 fp32 tiles for the split-tail schedule, or null
+    // adapter epilogue (E = 1): row i gets ad_d[i] @ ad_b[adapter[i]]^T, unscaled by alpha
+    const float* ad_d = nullptr;         // [m, r], or null: no adapters
+    const uint16_t* ad_b = nullptr;      // [n_adapters, n, r]
+    const int32_t* adapter = nullptr;    // [m]
+    int64_t n_adapters = 0;
 };
 
 // Workspace of the split-tail GEMM schedule: one fp32 128x256 partial tile
@@ -99,6 +104,42 @@ struct LinearSmallArgs {
     int64_t m, n, k;        // m <= kLinearSmallMaxRows; k % 128 == 0, k <= kLinearSmallMaxK
 };
 hipError_t launch_linear_small(const LinearSmallArgs& a, hipStream_t st);
+
+// A whole mixture-of-experts layer for a few tokens (t <= 64).
+struct MoeSmallArgs {
+    const uint16_t* x;       // [t, h]
+    const void* logits;      // [t, E] bf16 or fp32
+    bool logits_bf16, sigmoid, renorm;
+    const uint8_t* w13;      // [E, 2 inter, h/2]
+    const uint8_t* w13_sf;
+    const float* alpha13;    // [E]
+    const uint8_t* w2;       // [E, h, inter/2]
+    const uint8_t* w2_sf;
+    const float* alpha2;     // [E]
+    uint16_t* out;           // [t, h]
+    int32_t* ids;            // [t, top_k]
+    float* weights;          // [t, top_k]
+    void* ws;                // NVFP4_MOE_SMALL_WS_BYTES
+    int t, h, inter, E, top_k;
+};
+hipError_t launch_moe_small(const MoeSmallArgs& a, hipStream_t st);
+
+// Low-rank adapters of rows: lora_a [n_adapters, r, k], lora_b [n_adapters, n, r],
+// adapter [m] (outside [0, n_adapters): none).
+struct AdapterArgs {
+    const uint16_t* x;       // [m, k]
+    const uint16_t* lora_a;
+    const uint16_t* lora_b;
+    const int32_t* adapter;
+    const float* scaling;    // [n_adapters] or null
+    float* d;                // [m, r]: scaling * x @ lora_a[adapter]^T (0 without one)
+    int64_t m, n, k, r, n_adapters;
+};
+// Writes d.
+hipError_t launch_adapter_down(const AdapterArgs& a, hipStream_t st);
+// out = alpha * x @ dequant(b)^T + d @ lora_b[adapter]^T (+ bias).
+hipError_t launch_w4a16_adapters(const AdapterArgs& a, const uint8_t* b, const uint8_t* b_sf, const float* alpha,
+                                 const uint16_t* bias, uint16_t* out, hipStream_t st);
 
 // MX setting (32-element blocks, ue8m0 scales, no global scale).
 struct MxQuantizeArgs {

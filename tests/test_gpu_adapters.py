@@ -1,0 +1,255 @@
+"""nvfp4_linear_adapters and nvfp4_gemm_adapters against a plain 64-bit form:
+every output within the error the arithmetic allows, at sizes on both sides of
+every tile, rank and slice boundary, through every tile the prefill GEMM picks,
+and over adapter lists in any order."""
+import pytest
+import torch
+
+import serving_ref as R
+from gpu_util import OUT_CANARY, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mods():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    from nvfp4_block_scaled_04_amd import ops, serving
+    return serving, ops
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def pool(g, m, n, k, r, L, ids="mixed"):
+    p = dict(lora_a=(torch.randn(L, r, k, device="cuda", generator=g) / k ** 0.5).bfloat16(),
+             lora_b=(torch.randn(L, n, r, device="cuda", generator=g)).bfloat16(),
+             scaling=torch.rand(L, device="cuda", generator=g) * 2 + 0.25)
+    a = torch.randint(-1, L, (m,), device="cuda", generator=g, dtype=torch.int32)
+    if ids == "none":
+        a[:] = -1
+    elif ids == "one":
+        a[:] = L - 1
+    elif ids == "each":
+        a = (torch.arange(m, device="cuda") % L).int()
+    elif ids == "runs":
+        a = (torch.arange(m, device="cuda") * 7 // m % L).int()
+    elif ids == "wild":   # ids no pool holds: as if there were none
+        a = torch.tensor([L, -1, 0, -2 ** 31, 2 ** 31 - 1, L - 1], device="cuda", dtype=torch.int32).repeat(m)[:m].contiguous()
+    p["adapter"] = a
+    return p
+
+
+def fresh(m, n):
+    return torch.full((m, n), OUT_CANARY, dtype=torch.int16, device="cuda").view(torch.bfloat16)
+
+
+def workspace(nbytes):
+    return torch.full((nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+DECODE = [  # m, n, k, r, L, ids, scaling, bias
+    (1, 16, 16, 8, 1, "one", True, False),
+    (1, 40, 128, 16, 3, "one", False, True),
+    (2, 1, 48, 8, 2, "each", True, True),
+    (15, 33, 144, 24, 5, "mixed", True, False),
+    (16, 1000, 1040, 40, 20, "each", True, True),
+    (17, 64, 512, 256, 4, "mixed", True, False),
+    (23, 130, 2608, 24, 12, "wild", True, True),
+    (32, 48, 272, 64, 40, "each", False, False),
+    (33, 96, 640, 128, 7, "mixed", True, False),
+    (64, 272, 1024, 32, 48, "each", True, False),
+    (64, 272, 1024, 136, 2, "none", True, True),
+    (65, 80, 256, 16, 9, "mixed", True, True),
+    (200, 144, 384, 72, 33, "runs", True, False),
+]
+
+
+@pytest.mark.parametrize("m,n,k,r,L,ids,scaled,biased", DECODE)
+def test_decode(mods, m, n, k, r, L, ids, scaled, biased):
+    serving, _ = mods
+    say("linear_adapters", m, n, k, r, L, ids)
+    g = gen(m + n + k)
+    p = pool(g, m, n, k, r, L, ids)
+    s = p["scaling"] if scaled else None
+    b, sf = R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    alpha = torch.full((1,), 0.02, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    bias = torch.randn(n, device="cuda", generator=g).bfloat16() if biased else None
+    out = fresh(m, n)
+    serving.nvfp4_linear_adapters(x, b, sf, alpha, p["lora_a"], p["lora_b"], p["adapter"], scaling=s, bias=bias, out=out,
+                                  workspace=workspace(serving.adapters_ws_bytes(m, r)))
+    w = R.dequant(b, sf)
+    ref, bound = R.adapters(x.double() @ w.t() * alpha.double(), x.double().abs() @ w.abs().t() * alpha.double(), k, x,
+                            p["lora_a"], p["lora_b"], p["adapter"], s, bias)
+    assert R.worst(out, ref, bound) <= 1.0
+
+
+PREFILL = [  # m, n, k, r, L, ids, bias, workspace of the split-tail schedule
+    (1, 32, 16, 8, 1, "one", False, False),            # skinny kernel
+    (64, 100, 272, 40, 20, "each", True, False),
+    (65, 33, 128, 8, 3, "mixed", True, False),          # 128 x 128 tile
+    (300, 520, 1040, 24, 40, "each", False, False),
+    (1003, 2056, 2000, 40, 9, "runs", True, False),
+    (2000, 1928, 256, 16, 5, "wild", True, False),      # 128 x 256, two K groups
+    (1928, 4096, 144, 16, 5, "runs", False, False),
+    (2048, 4104, 896, 16, 6, "mixed", False, False),    # 128 x 256, odd number of steps
+    (4000, 3480, 272, 32, 6, "runs", True, False),      # one round of 256 x 192
+    (4096, 8200, 144, 32, 6, "runs", False, False),     # 256 x 256
+    (3968, 2560, 1008, 32, 6, "runs", True, True),      # split tail
+    (3968, 2560, 1008, 32, 200, "mixed", True, True),
+]
+
+
+@pytest.mark.parametrize("m,n,k,r,L,ids,biased,split", PREFILL)
+def test_prefill(mods, m, n, k, r, L, ids, biased, split):
+    serving, ops = mods
+    say("gemm_adapters", m, n, k, r, L, ids, split)
+    g = gen(m + n + k)
+    p = pool(g, m, n, k, r, L, ids)
+    a, a_sf, b, b_sf = R.rand_fp4(g, m, k=k), R.rand_sf(g, m, k), R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    alpha = torch.full((1,), 3e-4, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    bias = torch.randn(n, device="cuda", generator=g).bfloat16() if biased else None
+    out = fresh(m, n)
+    serving.nvfp4_gemm_adapters(a, b, a_sf, b_sf, alpha, x, p["lora_a"], p["lora_b"], p["adapter"], scaling=p["scaling"],
+                                bias=bias, out=out, workspace=workspace(serving.adapters_ws_bytes(m, r, split)))
+    left, w = R.dequant(a, a_sf), R.dequant(b, b_sf)
+    ref, bound = R.adapters(left @ w.t() * alpha.double(), left.abs() @ w.abs().t() * alpha.double(), k, x, p["lora_a"],
+                            p["lora_b"], p["adapter"], p["scaling"], bias)
+    assert R.worst(out, ref, bound) <= 1.0
+    if not split:  # rows without an adapter are the plain GEMM's, bit for bit
+        plain = ops.nvfp4_gemm(a, b, a_sf, b_sf, alpha, bias=bias)
+        rows = (p["adapter"] < 0) | (p["adapter"] >= L)
+        assert torch.equal(out[rows], plain[rows])
+
+
+def test_non_finite_row_stays_in_its_row(mods):
+    """A row with NaN or inf, and an adapter with NaN that one row uses, reach
+    those rows only."""
+    serving, _ = mods
+    say("adapters: non-finite rows")
+    g = gen(2)
+    m, n, k, r, L = 20, 48, 256, 16, 5
+    p = pool(g, m, n, k, r, L, "each")
+    b, sf = R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    alpha = torch.full((1,), 0.02, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    p["adapter"][p["adapter"] == 4] = 3
+    p["adapter"][11] = 4
+    run = lambda x: serving.nvfp4_linear_adapters(x, b, sf, alpha, p["lora_a"], p["lora_b"], p["adapter"])
+    good = run(x)
+    x[3, 5], x[18, 200] = float("nan"), float("inf")
+    p["lora_a"][4, 2, 9] = float("nan")
+    out = run(x)
+    keep = [i for i in range(m) if i not in (3, 11, 18)]
+    assert torch.equal(out[keep], good[keep])
+    assert out[3].isnan().all() and out[11].isnan().all() and not out[18].isfinite().any()
+
+
+def test_adapter_pool_past_32_bits(mods):
+    """A pool whose last adapter lies beyond 2^32 bytes."""
+    serving, _ = mods
+    say("adapters: 4.4 GB pools")
+    g = gen(4)
+    m, n, k, r, L = 18, 4096, 4096, 128, 4200
+    la = torch.zeros(L, r, k, dtype=torch.bfloat16, device="cuda")
+    lb = torch.zeros(L, n, r, dtype=torch.bfloat16, device="cuda")
+    assert la.numel() * 2 > 2 ** 32
+    for a in (0, L - 1):
+        la[a] = (torch.randn(r, k, device="cuda", generator=g) / 64).bfloat16()
+        lb[a] = torch.randn(n, r, device="cuda", generator=g).bfloat16()
+    ids = torch.tensor([0, L - 1, -1] * 6, dtype=torch.int32, device="cuda")
+    b, sf = R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    alpha = torch.full((1,), 0.02, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    out = serving.nvfp4_linear_adapters(x, b, sf, alpha, la, lb, ids)
+    w = R.dequant(b, sf)
+    ref, bound = R.adapters(x.double() @ w.t() * alpha.double(), x.double().abs() @ w.abs().t() * alpha.double(), k, x, la,
+                            lb, ids, None, None)
+    assert R.worst(out, ref, bound) <= 1.0
+
+
+@pytest.mark.parametrize("m", [16, 300, 3968])
+def test_repeats_streams_and_graph(mods, m):
+    """The same bits on a second call, on another stream, and on three replays of
+    a captured graph with the workspace and the output overwritten in between."""
+    serving, _ = mods
+    say("adapters: repeats, stream, graph", m)
+    g = gen(6)
+    n, k, r, L = 2560, 256, 24, 7
+    p = pool(g, m, n, k, r, L, "mixed")
+    b, b_sf = R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    a, a_sf = R.rand_fp4(g, m, k=k), R.rand_sf(g, m, k)
+    alpha = torch.full((1,), 3e-4, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    ws, out = workspace(serving.adapters_ws_bytes(m, r, True)), fresh(m, n)
+    lora = (p["lora_a"], p["lora_b"], p["adapter"])
+    calls = [lambda: serving.nvfp4_gemm_adapters(a, b, a_sf, b_sf, alpha, x, *lora, scaling=p["scaling"], out=out,
+                                                 workspace=ws)]
+    if m <= 300:
+        calls.append(lambda: serving.nvfp4_linear_adapters(x, b, b_sf, alpha, *lora, scaling=p["scaling"], out=out,
+                                                           workspace=ws))
+    for go in calls:
+        go()
+        want = out.clone()
+
+        def same():
+            torch.cuda.synchronize()
+            return torch.equal(out, want)
+
+        def scribble():
+            out.fill_(3)
+            ws.fill_(0xFF)
+
+        scribble()
+        go()
+        assert same()
+        scribble()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            go()
+        torch.cuda.current_stream().wait_stream(side)
+        assert same()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            go()
+        for _ in range(3):
+            scribble()
+            graph.replay()
+            assert same()
+
+
+def test_refusals(mods):
+    serving, _ = mods
+    say("adapters: refusals")
+    g = gen(7)
+    m, n, k, r, L = 8, 32, 64, 16, 3
+    p = pool(g, m, n, k, r, L)
+    b, sf = R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    alpha = torch.ones(1, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    la, lb, ad = p["lora_a"], p["lora_b"], p["adapter"]
+    f = serving.nvfp4_linear_adapters
+    for bad in (lambda: f(x.float(), b, sf, alpha, la, lb, ad), lambda: f(x, b, sf, alpha, la.float(), lb, ad),
+                lambda: f(x, b, sf, alpha, la, lb[:, :, :8].contiguous(), ad), lambda: f(x, b, sf, alpha, la, lb, ad.long()),
+                lambda: f(x, b, sf, alpha, la, lb, ad[:-1]), lambda: f(x, b, sf, alpha, la[:2], lb, ad),
+                lambda: f(x, b[:, :16].contiguous(), sf, alpha, la, lb, ad), lambda: f(x, b, sf[:-1], alpha, la, lb, ad),
+                lambda: f(x, b, sf, alpha, la, lb, ad, scaling=torch.ones(2, device="cuda")),
+                lambda: f(x, b, sf, alpha, la, lb, ad, bias=torch.ones(n, device="cuda")),
+                lambda: f(x, b, sf, alpha, la, lb, ad, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
+                lambda: f(x, b, sf, alpha, la, lb, ad.cpu()),
+                lambda: serving.nvfp4_gemm_adapters(b[:7], b, sf, sf, alpha, x, la, lb, ad)):
+        with pytest.raises(ValueError):
+            bad()
+    la12, lb12 = la[:, :12].contiguous(), lb[:, :, :12].contiguous()
+    out = torch.full((m, n), 5.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(RuntimeError, match="rank"):
+        f(x, b, sf, alpha, la12, lb12, ad, out=out)
+    torch.cuda.synchronize()
+    assert bool((out == 5).all())
