@@ -29,12 +29,12 @@ enum nvfp4_route_score {
 #define NVFP4_MOE_SMALL_MAX_TOP_K 16
 
 /*
- * Bytes of workspace of nvfp4_moe_small: the raw routing weight (fp32) of each
- * of the t * top_k (token, expert) pairs, and the pairs' activations, `inter`
- * columns each, as two bf16 halves.
+ * Bytes of workspace of nvfp4_moe_small: the activations of the t * top_k
+ * (token, expert) pairs, `inter` columns each, as two bf16 halves; 1024 rows of
+ * partial fp32 outputs; the routing tables; a counter per 16 output columns.
  */
-#define NVFP4_MOE_SMALL_WS_BYTES(t, top_k, inter) \
-    (4096 + 4 * (int64_t)(t) * (int64_t)(top_k) * (int64_t)(inter))
+#define NVFP4_MOE_SMALL_WS_BYTES(t, top_k, h, inter) \
+    (4 * (int64_t)(t) * (int64_t)(top_k) * (int64_t)(inter) + 4096 * (int64_t)(h) + 4096 + (int64_t)(h) / 4)
 
 /*
  * A whole mixture-of-experts layer for a few tokens, in two launches.
@@ -58,13 +58,13 @@ enum nvfp4_route_score {
  *   w2: [E, h, inter/2]; w2_sf: [E, pad_up(h,128)*pad_up(inter/16,4)];
  *   alpha13, alpha2: [E] fp32 (1 / the weights' global scales).
  *   out: [t, h] bf16; topk_ids: [t, top_k] int32; topk_weights: [t, top_k] fp32.
- *   workspace: workspace_bytes >= NVFP4_MOE_SMALL_WS_BYTES(t, top_k, inter),
+ *   workspace: workspace_bytes >= NVFP4_MOE_SMALL_WS_BYTES(t, top_k, h, inter),
  *   16-byte aligned; contents ignored on entry, undefined on exit; calls that
  *   share one must not overlap.
  * Requires 1 <= t <= 64, 1 <= E <= 256, 1 <= top_k <= min(E, 16), h and inter
  * >= 16 and multiples of 16.  Returns NVFP4_NULL_POINTER, NVFP4_BAD_SHAPE (also
  * for a workspace that is too small), NVFP4_BAD_DTYPE, NVFP4_UNSUPPORTED (the
- * limits above; an unknown score; a weight matrix of one expert over 2^31 bytes)
+ * limits above; an unknown score; one expert's w13 of 2^31 bytes or more)
  * or NVFP4_MISALIGNED before launching anything.
  */
 int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int logits_dtype, int64_t E,

@@ -405,6 +405,9 @@ int nvfp4_alpha(const float* gs_a, const float* gs_b, float* alpha, int64_t coun
     return launch_status(nvfp4::launch_alpha(gs_a, gs_b, alpha, count, (hipStream_t)stream));
 }
 
+static_assert(4096 == nvfp4::kMoePartRows * 4 && nvfp4::kMoePartRows >= NVFP4_MOE_SMALL_MAX_TOKENS,
+              "the workspace holds the partial sums");
+
 int nvfp4_moe_small(const void* x, int64_t t, int64_t h, const void* logits, int logits_dtype, int64_t E,
                     int64_t top_k, int score, int renormalize, const uint8_t* w13, const uint8_t* w13_sf,
                     const float* alpha13, const uint8_t* w2, const uint8_t* w2_sf, const float* alpha2,
@@ -419,10 +422,12 @@ int nvfp4_moe_small(const void* x, int64_t t, int64_t h, const void* logits, int
     if (t > NVFP4_MOE_SMALL_MAX_TOKENS || E > NVFP4_MOE_SMALL_MAX_EXPERTS || top_k > NVFP4_MOE_SMALL_MAX_TOP_K)
         return NVFP4_UNSUPPORTED;
     if (score != NVFP4_ROUTE_SOFTMAX && score != NVFP4_ROUTE_SIGMOID) return NVFP4_UNSUPPORTED;
-    // one expert's weights (2 inter x h codes) and its scale buffers
-    if (inter > ((int64_t)1 << 31) / h || !gemm_sf_ok(2 * inter, h / 16) || !gemm_sf_ok(h, inter / 16))
+    // 32-bit offsets: one expert's weights (2 inter x h codes) and scales, the
+    // tokens, the activations' two halves
+    if (inter > (((int64_t)1 << 31) - 1) / h || t * h * 2 >= ((int64_t)1 << 31) ||
+        t * top_k * inter * 4 >= ((int64_t)1 << 31) || !gemm_sf_ok(2 * inter, h / 16) || !gemm_sf_ok(h, inter / 16))
         return NVFP4_UNSUPPORTED;
-    if (workspace_bytes < NVFP4_MOE_SMALL_WS_BYTES(t, top_k, inter)) return NVFP4_BAD_SHAPE;
+    if (workspace_bytes < NVFP4_MOE_SMALL_WS_BYTES(t, top_k, h, inter)) return NVFP4_BAD_SHAPE;
     if (!aligned16(x) || !aligned16(logits) || !aligned16(w13) || !aligned16(w13_sf) || !aligned16(w2) ||
         !aligned16(w2_sf) || !aligned16(out) || !aligned16(workspace) || ((uintptr_t)alpha13 & 3u) ||
         ((uintptr_t)alpha2 & 3u) || ((uintptr_t)topk_ids & 3u) || ((uintptr_t)topk_weights & 3u))
@@ -471,7 +476,8 @@ int nvfp4_linear_adapters(const void* x, const uint8_t* b, const uint8_t* b_sf, 
     const int st = adapters_check(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace,
                                   workspace_bytes);
     if (st != NVFP4_OK) return st;
-    if (!gemm_sf_ok(n, k / 16)) return NVFP4_UNSUPPORTED;
+    // 32-bit offsets into 64 weight rows and 64 activation rows
+    if (k > ((int64_t)1 << 23) || !gemm_sf_ok(n, k / 16)) return NVFP4_UNSUPPORTED;
     if (!aligned16(b) || !aligned16(b_sf) || !aligned16(out) || ((uintptr_t)alpha & 3u) || (bias && !aligned16(bias)))
         return NVFP4_MISALIGNED;
     const nvfp4::AdapterArgs a = adapter_args(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace);

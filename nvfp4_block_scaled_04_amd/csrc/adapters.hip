@@ -132,18 +132,17 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
     const int64_t brow = n0 + r < p.N ? n0 + r : p.N - 1;
     const int rowb = (int)(p.K / 2);
     const uint8_t* const B = p.b + brow * rowb;
-    const uint8_t* const F = p.b_sf + scale_row_off(brow, p.cpa4);
+    const uint8_t* const F = p.b_sf + scale_byte_off(brow, 2 * g, p.cpa4);
     const uint16_t* X[TT];
     int id[TT];
 #pragma unroll
     for (int i = 0; i < TT; i++) {
         const int64_t m = m0 + 16 * i + r;
-        X[i] = m < p.M ? p.x + m * p.K : nullptr;
+        X[i] = m < p.M ? p.x + m * p.K + 32 * g : nullptr;
         id[i] = adapter_of(p, m);
     }
     const int nch = (int)((p.K + kChunk - 1) / kChunk);
-    const int per = (nch + kAdWaves - 1) / kAdWaves;
-    const int c0 = wave * per, c1 = c0 + per < nch ? c0 + per : nch;
+    const int c0 = nch * wave / kAdWaves, c1 = nch * (wave + 1) / kAdWaves;
     f32x4 acc[TT];
 #pragma unroll
     for (int i = 0; i < TT; i++) acc[i] = f32x4{0, 0, 0, 0};
@@ -154,10 +153,22 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const int c = cb + u < c1 ? cb + u : c1 - 1;  // past the range: reload, never used
-            w[u] = load_w4<WHOLE>(B, c, g, rowb);
-            s[u] = load_s4<WHOLE>(F, c, g, p.nblk);
+            const int left = (int)p.K - c * kChunk - 32 * g;
+            w[u] = u32x4{0, 0, 0, 0};
+            s[u] = 0;
+            if (WHOLE || left >= 32) w[u] = *(const u32x4*)(B + c * 64 + g * 16);
+            else if (left >= 16) {
+                const u32x2 h = *(const u32x2*)(B + c * 64 + g * 16);
+                w[u] = u32x4{h.x, h.y, 0, 0};
+            }
+            if (WHOLE || left > 0) s[u] = *(const uint16_t*)(F + (int64_t)c * 1024) & (WHOLE || left >= 32 ? 0xFFFFu : 0xFFu);
 #pragma unroll
-            for (int i = 0; i < TT; i++) load_x16<WHOLE>(xv[u][i], X[i], c, g, (int)p.K);
+            for (int i = 0; i < TT; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    xv[u][i][j] = u32x4{0, 0, 0, 0};
+                    if (X[i] && (WHOLE || left > 8 * j)) xv[u][i][j] = *(const u32x4*)(X[i] + c * kChunk + 8 * j);
+                }
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {

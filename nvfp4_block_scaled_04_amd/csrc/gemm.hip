@@ -1218,13 +1218,17 @@ static Tile pick_tile(int64_t m, int64_t n, int64_t k, int64_t E) {
     return Tile::T128x128;
 }
 
+int device_cus() {
+    int dev = 0, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+        return 0;
+    return cus;
+}
+
 // Workgroups of a persistent launch: one per CU, at most the workspace's
 // slot count.
 static int sk_grid_size() {
-    int dev = 0, cus = 0;
-    if (hipGetDevice(&dev) != hipSuccess || hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-        cus <= 0)
-        return 0;
+    const int cus = device_cus();
     return cus < kGemmWsSlots ? cus : kGemmWsSlots;
 }
 

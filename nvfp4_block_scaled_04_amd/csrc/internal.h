@@ -105,6 +105,12 @@ struct LinearSmallArgs {
 };
 hipError_t launch_linear_small(const LinearSmallArgs& a, hipStream_t st);
 
+// CUs of the current device, or 0.
+int device_cus();
+
+// Rows of partial sums the layer's second product may leave in the workspace.
+constexpr int kMoePartRows = 1024;
+
 // A whole mixture-of-experts layer for a few tokens (t <= 64).
 struct MoeSmallArgs {
     const uint16_t* x;       // [t, h]

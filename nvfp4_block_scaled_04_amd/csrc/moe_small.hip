@@ -1,23 +1,25 @@
 // moe_small.hip -- a whole mixture-of-experts layer for a few tokens in two
 // launches, on NVFP4 expert weights and bf16 tokens.
 //
-// What is computed (n tokens x, router logits, E experts of H -> I -> H):
+// What is computed (tokens x, router logits, E experts of H -> I -> H):
 //   chosen(i) = the top_k experts by (logit descending, index ascending) among
 //               logits that are neither NaN nor -inf
 //   w(i, e)   = softmax or sigmoid of the logit (/ the chosen ones' sum)
 //   [g, u]    = alpha13[e] * x[i] @ W13[e]^T,   a = g / (1 + e^-g) * u
 //   out[i]    = sum_e w(i, e) * alpha2[e] * a @ W2[e]^T
 //
-// First launch (k_moe_up): one workgroup per 16 gate and 16 up rows of an
-// expert.  It routes for itself (a token's logits are one load per lane), finds
-// the tokens that chose its expert, and streams the 32 weight rows once against
-// up to 16 of them.  The activation leaves multiplied by the unnormalised
-// routing weight and alpha2, so the second launch is one long product.
-// Second launch (k_moe_down): one workgroup per 16 output columns; its K axis is
-// the chosen experts' I axes laid end to end, dealt to the waves in contiguous
-// ranges.  Each wave adds an expert's product into its own fp32 accumulators of
-// all tokens in LDS, and the waves' accumulators are summed in wave order: no
-// atomics, the same result on every call.
+// First launch (k_moe_up): every workgroup routes for itself, once -- 16 lanes a
+// token, top_k rounds of a maximum over DPP -- and then walks its share of the
+// (chosen expert, 16 gate and 16 up rows) items.  A wave streams an item's 32
+// weight rows once against up to 16 of the tokens that chose the expert; with
+// few items, the K axis of one is split over S waves.  The activation leaves
+// multiplied by w(i, e) and alpha2, so the second launch is one long product.
+// Second launch (k_moe_down): a workgroup has 128 output columns, 16 a wave, and
+// a share of the K axis, which is the chosen experts' I axes laid end to end.  Its
+// waves walk the same chunks and share the activations in LDS; each adds an
+// expert's product into the fp32 sums of its own columns, and of the several
+// workgroups of a column tile the last to finish adds their sums in the order of
+// the shares: no atomic sums, the same result on every call.
 //
 // Bound: the chosen experts' weights are read once (9/16 byte an element), the
 // rest is small; the kernels are built to keep weight loads in flight.
@@ -26,12 +28,16 @@
 #include "internal.h"
 #include "skinny_w4.h"
 
+#include <type_traits>
+
 namespace nvfp4 {
 namespace {
 
-constexpr int kNone = 255;       // rank of a token that did not choose the expert
-constexpr int kUpWaves = 8;
-constexpr int kDownWaves = 16;
+constexpr int kWaves = 8;    // of either kernel's workgroups; two of them share a CU
+constexpr int kThreads = 64 * kWaves;
+constexpr int kXBytes = 16 << 10;  // LDS for activations: 4 chunks of 16 rows, 64 of one
+constexpr int kSumPitch = 132;     // floats of a token's row of sums (128 columns, padded)
+typedef W4Ring<2, 3> UpRing;       // with x and the tables, LDS for two workgroups a CU
 
 struct EParams {
     const uint16_t* x;         // [T, H]
@@ -45,365 +51,498 @@ struct EParams {
     uint16_t* out;             // [T, H]
     int32_t* ids;              // [T, k]
     float* weights;            // [T, k]
-    float* raw;                // [T, k] unnormalised weights
+    void* routes;              // Routes, from the first launch for the second
+    int32_t* arrived;          // [H/16] shares of a column tile that are done (k_moe_down)
     uint16_t* act_hi;          // [T * k, I], row t * k + slot
     uint16_t* act_lo;
+    float* part;               // [H/16, shares, T, 16] partial sums (k_moe_down with shares > 1)
     int64_t w13_sfsz, w2_sfsz; // scale bytes of one expert
     int T, H, I, E, k;
     int lg_bf16, sigmoid, renorm;
-    int by_slot;               // workgroup row y is the y-th chosen expert (else expert y)
-    int tiles, xcd_chunk;
+    int shares;                // most workgroups that share a column tile (k_moe_down)
 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// Logit of expert j of token t; NaN and j >= E read as -inf (never chosen).
-__device__ __forceinline__ float load_logit(const EParams& p, int t, int j) {
-    if (j >= p.E) return neg_inf();
-    const int64_t at = (int64_t)t * p.E + j;
-    const float v = p.lg_bf16 ? bf16_lo((uint32_t)((const uint16_t*)p.logits)[at]) : ((const float*)p.logits)[at];
-    return v == v ? v : neg_inf();
-}
-
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v = __builtin_fmaxf(v, __shfl_xor(v, o));
+// All-reduce over the 16 lanes of a DPP row: the neighbour in a pair, the other
+// pair of a quad, the mirrored quad of 8, the mirrored half of 16.
+template <typename T, typename F>
+__device__ __forceinline__ T row16(T v, F f) {
+    auto step = [&](auto ctl) {
+        const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctl)::value, 0xF, 0xF, true);
+        v = f(v, __builtin_bit_cast(T, o));
+    };
+    step(std::integral_constant<int, 0xB1>{});
+    step(std::integral_constant<int, 0x4E>{});
+    step(std::integral_constant<int, 0x141>{});
+    step(std::integral_constant<int, 0x140>{});
     return v;
 }
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o);
-    return v;
+__device__ __forceinline__ float row16_max(float v) {
+    return row16(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
+__device__ __forceinline__ float row16_sum(float v) {
+    return row16(v, [](float a, float b) { return a + b; });
+}
+__device__ __forceinline__ int row16_min(int v) {
+    return row16(v, [](int a, int b) { return a < b ? a : b; });
 }
 
-// Unnormalised weight of a chosen expert with logit l of a token whose largest
-// logit is top; lg: the lane's logits of that token.  Softmax: exp(l - top),
-// divided by the sum over all experts unless the chosen ones' sum divides it
-// later.  Sigmoid, to be divided by the chosen ones' sum: every value scaled by
-// exp(-min(top, 0)), so that very negative logits keep their ratios.
-template <int NR>
-__device__ __forceinline__ float route_weight(const EParams& p, float l, float top, const float lg[NR]) {
-    if (!p.sigmoid) {
-        const float u = expf(l - top);
-        if (p.renorm) return u;
-        float s = 0.0f;
+// The value of lane l ^ 8 within a row of 16 (DPP row_ror:8).
+__device__ __forceinline__ float row_half(float v) {
+    return bits_f((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f_bits(v), 0x128, 0xF, 0xF, true));
+}
+
+// What the launches know of the routing: the chosen experts, ascending, each
+// packed with its number of tokens and the start of their list, and the lists of
+// (token, slot), tokens ascending.  The first launch makes it in LDS and leaves a
+// copy in the workspace for the second.
+struct alignas(16) Routes {
+    uint32_t act[256];    // expert | tokens << 8 | first of the list << 16
+    uint16_t list[1024];  // token << 4 | slot
+    int32_t nact;
+    int32_t most;         // most tokens on one expert
+};
+static_assert(sizeof(Routes) <= 4096, "room in the workspace");
+__device__ __forceinline__ int act_expert(uint32_t a) { return a & 255; }
+__device__ __forceinline__ int act_tokens(uint32_t a) { return a >> 8 & 255; }
+__device__ __forceinline__ int act_first(uint32_t a) { return a >> 16; }
+
+// Exclusive prefix sum over a wave; total: the whole sum.
+__device__ __forceinline__ int wave_prefix(int v, int& total) {
+    int s = v;
 #pragma unroll
-        for (int i = 0; i < NR; i++) s += expf(lg[i] - top);
-        return u / wave_sum(s);
+    for (int o = 1; o < 64; o *= 2) {
+        const int u = __shfl_up(s, o);
+        if ((int)(threadIdx.x & 63) >= o) s += u;
     }
-    if (l >= 0.0f) return 1.0f / (1.0f + expf(-l));
-    const float base = p.renorm ? __builtin_fminf(top, 0.0f) : 0.0f;
-    return expf(l - base) / (1.0f + expf(l));
+    total = __shfl(s, 63);
+    return s - v;
 }
 
-// Tile index of blockIdx.x: XCD x (workgroups are dealt round-robin) takes the
-// x-th contiguous eighth, so tiles that share scale lines share an L2.
-__device__ __forceinline__ int tile_of(const EParams& p) {
-    const int b = blockIdx.x;
-    return p.xcd_chunk ? (b & 7) * p.xcd_chunk + (b >> 3) : b;
-}
-
-// NR: logits a lane holds of one token (ceil(E / 64)).
+// NR: logits a lane holds of a token (E <= 16 NR).
 template <int NR, bool WHOLE>
-__global__ __launch_bounds__(64 * kUpWaves) void k_moe_up(EParams p) {
+__global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
-    __shared__ uint8_t rank_of[64];          // slot in which a token chose this expert, or kNone
-    __shared__ float weight_of[64];          // its unnormalised weight
-    __shared__ uint64_t active[NR];          // experts that any token chose (by_slot)
-    __shared__ int members[64];
-    __shared__ f32x4 part[kUpWaves][2][64];
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* const rings = smem;                             // the waves' weight rings; then the parts' sums
+    uint8_t* const xs = smem + kWaves * UpRing::BYTES;       // x of a block of chunks
+    Routes& R = *(Routes*)(xs + kXBytes);
+    float* const weight_of = (float*)(&R + 1);               // [T * k]
+    int16_t* const choice = (int16_t*)(weight_of + p.T * p.k);  // [T][k]
+    int* const count = (int*)rings;                          // [256] tokens of an expert (before the rings are used)
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int tile = tile_of(p);
-    const bool teller = blockIdx.x == 0;     // writes its expert's routing results
 
-    // 1. the expert of this workgroup
-    int e = blockIdx.y;
-    if (p.by_slot) {
-        if (t < NR) active[t] = 0;
-        __syncthreads();
-        for (int tok = wave; tok < p.T; tok += kUpWaves) {
-            float lg[NR];
-#pragma unroll
-            for (int i = 0; i < NR; i++) lg[i] = load_logit(p, tok, lane + 64 * i);
-            uint64_t got[NR] = {};
-            for (int j = 0; j < p.k; j++) {
-                float m = lg[0];
-#pragma unroll
-                for (int i = 1; i < NR; i++) m = __builtin_fmaxf(m, lg[i]);
-                m = wave_max(m);
-                if (m == neg_inf()) break;
-                bool done = false;
-#pragma unroll
-                for (int i = 0; i < NR; i++) {  // the lowest index that holds the maximum
-                    const uint64_t at = __ballot(lg[i] == m);
-                    if (!done && at) {
-                        done = true;
-                        const int l = __builtin_ctzll(at);
-                        got[i] |= (uint64_t)1 << l;
-                        if (lane == l) lg[i] = neg_inf();
-                    }
-                }
-            }
-            if (lane == 0) {
-#pragma unroll
-                for (int i = 0; i < NR; i++)
-                    if (got[i]) atomicOr((unsigned long long*)&active[i], (unsigned long long)got[i]);
-            }
-        }
-        __syncthreads();
-        int left = blockIdx.y;  // the e-th set bit
-        e = -1;
-#pragma unroll
-        for (int i = 0; i < NR; i++) {
-            uint64_t bits = active[i];
-            const int n = __builtin_popcountll(bits);
-            if (e < 0 && left < n) {
-                for (int q = 0; q < left; q++) bits &= bits - 1;
-                e = 64 * i + __builtin_ctzll(bits);
-            }
-            left -= n;
-        }
-        e = __builtin_amdgcn_readfirstlane(e);
-    }
-
-    // 2. the tokens that chose it: e is in slot `better` of a token if `better`
-    //    of its logits come before e's
-    for (int tok = wave; tok < p.T; tok += kUpWaves) {
+    // 1. routing: 16 lanes a token, its logits in registers
+    if (t < 256) count[t] = 0;
+    if (blockIdx.x == 0)
+        for (int i = t; i < p.H / 16; i += kThreads) p.arrived[i] = 0;
+    __syncthreads();
+    const int l16 = lane & 15;
+    for (int t0 = wave * 4; t0 < p.T; t0 += kWaves * 4) {
+        const int tok = t0 + (lane >> 4);
         float lg[NR];
-        float mx = neg_inf();
-        int able = 0;
 #pragma unroll
         for (int i = 0; i < NR; i++) {
-            lg[i] = load_logit(p, tok, lane + 64 * i);
-            mx = __builtin_fmaxf(mx, lg[i]);
-            able += __builtin_popcountll(__ballot(lg[i] > neg_inf()));
-        }
-        if (teller && blockIdx.y == 0 && lane < p.k && lane >= able) {  // slots left over
-            p.ids[tok * p.k + lane] = -1;
-            p.raw[tok * p.k + lane] = 0.0f;
-        }
-        if (e < 0) continue;
-        float le = neg_inf();
-        int better = 0;
-#pragma unroll
-        for (int i = 0; i < NR; i++)
-            if (e >> 6 == i) le = __shfl(lg[i], e & 63);
-#pragma unroll
-        for (int i = 0; i < NR; i++)
-            better += __builtin_popcountll(__ballot(lg[i] > le || (lg[i] == le && lane + 64 * i < e)));
-        const bool in = le > neg_inf() && better < p.k;
-        float u = 0.0f;
-        if (in) {
-            u = route_weight<NR>(p, le, wave_max(mx), lg);
-            if (teller && lane == 0) {
-                p.ids[tok * p.k + better] = e;
-                p.raw[tok * p.k + better] = u;
+            const int j = l16 + 16 * i;
+            lg[i] = neg_inf();
+            if (tok < p.T && j < p.E) {
+                const int64_t at = (int64_t)tok * p.E + j;
+                const float v = p.lg_bf16 ? bf16_lo((uint32_t)((const uint16_t*)p.logits)[at]) : ((const float*)p.logits)[at];
+                lg[i] = v == v ? v : neg_inf();  // NaN is never chosen
             }
+        }
+        float top = lg[0];
+#pragma unroll
+        for (int i = 1; i < NR; i++) top = __builtin_fmaxf(top, lg[i]);
+        top = row16_max(top);
+        float den = 1.0f;
+        if (!p.sigmoid && !p.renorm) {
+            den = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NR; i++) den += lg[i] == neg_inf() ? 0.0f : expf(lg[i] - top);
+            den = row16_sum(den);
+        }
+        int mine = -1;            // lane j of the token keeps the expert of slot j
+        float ml = neg_inf();
+        for (int j = 0; j < p.k; j++) {
+            float m = lg[0];
+#pragma unroll
+            for (int i = 1; i < NR; i++) m = __builtin_fmaxf(m, lg[i]);
+            m = row16_max(m);
+            int at = p.E;  // the lowest index that holds the maximum
+#pragma unroll
+            for (int i = NR - 1; i >= 0; i--)
+                if (lg[i] == m) at = l16 + 16 * i;
+            at = row16_min(at);
+            if (m > neg_inf() && l16 == j) {
+                mine = at;
+                ml = m;
+            }
+#pragma unroll
+            for (int i = 0; i < NR; i++)
+                if (l16 + 16 * i == at) lg[i] = neg_inf();
+        }
+        // its weight.  Softmax: exp(l - top) over the sum of all, or of the chosen
+        // ones.  Sigmoid over the chosen ones' sum: every value is scaled by
+        // exp(-min(top, 0)), so that very negative logits keep their ratios.
+        float u = 0.0f;
+        if (mine >= 0) {
+            if (!p.sigmoid) u = expf(ml - top) / den;
+            else if (ml >= 0.0f) u = 1.0f / (1.0f + expf(-ml));
+            else u = expf(ml - (p.renorm ? __builtin_fminf(top, 0.0f) : 0.0f)) / (1.0f + expf(ml));
+        }
+        if (p.renorm) {
+            const float s = row16_sum(u);
+            if (mine >= 0) u /= s;
+        }
+        if (tok < p.T && l16 < p.k) {
+            weight_of[tok * p.k + l16] = u;
+            choice[tok * p.k + l16] = (int16_t)mine;
+            if (mine >= 0) atomicAdd(&count[mine], 1);
+            if (blockIdx.x == 0) {
+                p.ids[tok * p.k + l16] = mine;
+                p.weights[tok * p.k + l16] = u;
+            }
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {
+        int na = 0, pairs = 0, most = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 64) {
+            const int n = e0 + lane < p.E ? count[e0 + lane] : 0;
+            int sum;
+            const int first = pairs + wave_prefix(n, sum);
+            const uint64_t some = __ballot(n > 0);
+            if (n > 0)
+                R.act[na + __builtin_popcountll(some & (((uint64_t)1 << lane) - 1))] =
+                    (uint32_t)(e0 + lane) | (uint32_t)n << 8 | (uint32_t)first << 16;
+            na += __builtin_popcountll(some);
+            pairs += sum;
+            most = most > n ? most : n;
+        }
+#pragma unroll
+        for (int o = 32; o >= 1; o >>= 1) {
+            const int u = __shfl_xor(most, o);
+            most = most > u ? most : u;
         }
         if (lane == 0) {
-            rank_of[tok] = (uint8_t)(in ? better : kNone);
-            weight_of[tok] = u;
+            R.nact = na;
+            R.most = most;
         }
     }
-    if (e < 0) return;
     __syncthreads();
-    const bool mem = lane < p.T && rank_of[lane < p.T ? lane : 0] != kNone;
-    const uint64_t mask = __ballot(mem);
-    const int n = __builtin_popcountll(mask);
-    if (n == 0) return;
-    if (wave == 0 && mem) members[__builtin_popcountll(mask & (((uint64_t)1 << lane) - 1))] = lane;
+    const int nact = __builtin_amdgcn_readfirstlane(R.nact);
+    for (int i = wave; i < nact; i += kWaves) {  // an expert's tokens, lane by lane
+        const uint32_t a = R.act[i];
+        int slot = -1;
+        if (lane < p.T)
+            for (int j = 0; j < p.k; j++)
+                if (choice[lane * p.k + j] == act_expert(a)) slot = j;
+        const uint64_t in = __ballot(slot >= 0);
+        if (slot >= 0) R.list[act_first(a) + __builtin_popcountll(in & (((uint64_t)1 << lane) - 1))] = (uint16_t)(lane << 4 | slot);
+    }
     __syncthreads();
+    if (blockIdx.x == 0)
+        for (int i = t; i < (int)sizeof(Routes) / 4; i += kThreads) ((uint32_t*)p.routes)[i] = ((const uint32_t*)&R)[i];
 
-    // 3. 16 gate and 16 up rows against the members, 16 at a time
+    // 2. items: (chosen expert, up to 8 / S tiles of 16 gate and 16 up rows), the K
+    //    axis of a tile split over S waves: as many as give every wave something,
+    //    as long as LDS holds a chunk of x for each part
     const int r = lane & 15, g = lane >> 4;
-    const int rowb = p.H / 2, nblk = p.H / 16, cpa4 = (nblk + 3) / 4;
+    const int rowb = p.H / 2, cpa4 = (p.H / 16 + 3) / 4;
     const int nch = (p.H + kChunk - 1) / kChunk;
-    const int per = (nch + kUpWaves - 1) / kUpWaves;
-    const int c0 = wave * per, c1 = c0 + per < nch ? c0 + per : nch;
-    const int row = tile * 16 + r;  // I is a multiple of 16: always a row
-    const uint8_t* const W = p.w13 + (int64_t)e * 2 * p.I * rowb;
-    const uint8_t* const S = p.w13_sf + (int64_t)e * p.w13_sfsz;
-    const uint8_t* const B[2] = {W + (int64_t)row * rowb, W + (int64_t)(p.I + row) * rowb};
-    const uint8_t* const F[2] = {S + scale_row_off(row, cpa4), S + scale_row_off(p.I + row, cpa4)};
-    const float a13 = p.alpha13[e], a2 = p.alpha2[e];
-    for (int m0 = 0; m0 < n; m0 += 16) {
-        const uint16_t* const X = m0 + r < n ? p.x + (int64_t)members[m0 + r] * p.H : nullptr;
-        f32x4 acc[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
-        constexpr int U = 4;  // chunks whose loads are in flight together
-        for (int cb = c0; cb < c1; cb += U) {
-            u32x4 w[U][2], xv[U][4];
-            uint32_t s[U][2];
+    const int tiles = p.I / 16;
+    const int most = __builtin_amdgcn_readfirstlane(R.most), rows_most = most < 32 ? most : 32;
+    int S = 1;
+    while (S < kWaves && nact * tiles * S * 2 <= (int)gridDim.x * kWaves && 2 * S * rows_most * 256 <= kXBytes) S *= 2;
+    const int ipw = kWaves / S, sub = wave / S, part_of = wave % S;
+    const int gpe = (tiles + ipw - 1) / ipw, items = nact * gpe;  // groups of an expert, of all
+    const int cps = (nch + S - 1) / S;                            // chunks of a part
+    const int c0 = cps * part_of < nch ? cps * part_of : nch, c1 = c0 + cps < nch ? c0 + cps : nch;
+    const int G = gridDim.x, b = blockIdx.x;
+    // S workgroups cover the 8 tiles of a band of 128 rows, whose scales share
+    // lines: they are neighbours on one XCD (workgroups are dealt round-robin)
+    const int w0 = G % (8 * S) == 0 ? (b / 8 / S * 8 + b % 8) * S + b / 8 % S : b;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.x, (uint32_t)(p.T * p.H * 2));
+    UpRing ring;
+    ring.init(rings + wave * UpRing::BYTES, lane);
+    for (int idx = w0; idx < items; idx += G) {
+        const int ai = idx / gpe, tile = (idx - ai * gpe) * ipw + sub;
+        const uint32_t a = (uint32_t)__builtin_amdgcn_readfirstlane((int)R.act[ai]);
+        const int e = act_expert(a), n = act_tokens(a);
+        const uint16_t* const list = R.list + act_first(a);
+        const bool live = tile < tiles;
+        const float a13 = p.alpha13[e], a2 = p.alpha2[e];
+        ring.aim(make_rsrc(p.w13 + (int64_t)e * 2 * p.I * rowb, (uint32_t)(2 * p.I * rowb)),
+                 make_rsrc(p.w13_sf + (int64_t)e * p.w13_sfsz, (uint32_t)p.w13_sfsz),
+                 {live ? tile * 16 : 0, p.I + (live ? tile * 16 : 0)}, rowb, cpa4, lane);
+        // XT tiles of 16 tokens at a time, the first of them the m0-th
+        auto pass = [&](auto xt, int m0) {
+            constexpr int XT = decltype(xt)::value;
+            const int nr = n - m0 < 16 * XT ? n - m0 : 16 * XT;  // rows of x
+            const int cb = kXBytes / (nr * 256) / S;             // chunks of every part in a block
+            if (idx != w0 || m0) __syncthreads();  // nobody is at the previous pass's LDS any more
+            int ca = c0;
+            auto next = [&]() {
+                if (ca < c1) ring.issue(ca++);
+            };
+            if (live)
+                for (int u = 0; u < UpRing::DEPTH; u++) next();
+            XBlock<kXBytes / 16 / kThreads> xb;
+            auto load_block = [&](int k0) {
+                xb.load(rx, [&](int i) { return (uint32_t)((list[m0 + i] >> 4) * p.H * 2); }, nr, S * cb, p.H, t, kThreads, [&](int lc) {
+                    const int q = lc / cb, c = cps * q + k0 + lc - q * cb;
+                    return k0 + lc - q * cb < cps && c < nch ? c : -1;
+                });
+            };
+            load_block(0);
+            XLane xl[XT];
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int c = cb + u < c1 ? cb + u : c1 - 1;  // past the range: reload, never used
+            for (int i = 0; i < XT; i++) xl[i].set(xs, 16 * i + r < nr ? 16 * i + r : nr - 1, g);  // absent: any row
+            f32x4 acc[2][XT];
 #pragma unroll
-                for (int f = 0; f < 2; f++) {
-                    w[u][f] = load_w4<WHOLE>(B[f], c, g, rowb);
-                    s[u][f] = load_s4<WHOLE>(F[f], c, g, nblk);
+            for (int f = 0; f < 2; f++)
+#pragma unroll
+                for (int i = 0; i < XT; i++) acc[f][i] = f32x4{0, 0, 0, 0};
+            for (int k0 = 0; k0 < cps; k0 += cb) {
+                if (k0) __syncthreads();  // the previous block is consumed
+                xb.store(xs, nr, S * cb, t, kThreads);
+                __syncthreads();
+                if (k0 + cb < cps) load_block(k0 + cb);  // the next block is on its way while this one is used
+                const int b0 = c0 + k0, b1 = b0 + cb < c1 ? b0 + cb : c1;
+                if (live) consume<XT, WHOLE>(ring, acc, xl, part_of * cb * nr * 256, nr * 256, b0, b1, g, p.H, next);
+            }
+            if (S > 1) {  // the parts' sums, in part order
+                __syncthreads();
+                f32x4* const part = (f32x4*)rings;
+#pragma unroll
+                for (int f = 0; f < 2; f++)
+#pragma unroll
+                    for (int i = 0; i < XT; i++) part[((f * XT + i) * kWaves + wave) * 64 + lane] = acc[f][i];
+                __syncthreads();
+                if (part_of != 0) return;
+                for (int v = 1; v < S; v++)
+#pragma unroll
+                    for (int f = 0; f < 2; f++)
+#pragma unroll
+                        for (int i = 0; i < XT; i++) acc[f][i] += part[((f * XT + i) * kWaves + wave + v) * 64 + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < XT; i++) {
+                if (!live || 16 * i + r >= nr) continue;  // lane: its token, columns 4 g .. 4 g + 3 of the tile
+                const int it = list[m0 + 16 * i + r], pair = (it >> 4) * p.k + (it & 15);
+                const float wt = weight_of[pair] * a2;
+                float v4[4];
+#pragma unroll
+                for (int v = 0; v < 4; v++) {
+                    const float gt = a13 * acc[0][i][v];
+                    v4[v] = gt / (1.0f + expf(-gt)) * (a13 * acc[1][i][v]) * wt;
                 }
-                load_x16<WHOLE>(xv[u], X, c, g, p.H);
+                uint32_t h0, l0, h1, l1;
+                split_bf16x2(v4[0], v4[1], h0, l0);
+                split_bf16x2(v4[2], v4[3], h1, l1);
+                const int64_t at = (int64_t)pair * p.I + tile * 16 + 4 * g;
+                *(u32x2*)(p.act_hi + at) = u32x2{h0, h1};
+                *(u32x2*)(p.act_lo + at) = u32x2{l0, l1};
             }
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                if (cb + u >= c1) break;
-#pragma unroll
-                for (int f = 0; f < 2; f++) {
-                    const float s0 = __builtin_amdgcn_cvt_f32_fp8(s[u][f], 0), s1 = __builtin_amdgcn_cvt_f32_fp8(s[u][f], 1);
-#pragma unroll
-                    for (int j = 0; j < 4; j++)
-                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dequant8_bf16(word(w[u][f], j), j < 2 ? s0 : s1),
-                                                                         __builtin_bit_cast(bf16x8, xv[u][j]), acc[f], 0, 0, 0);
-                }
-            }
+        };
+        if (n <= 16) {
+            pass(std::integral_constant<int, 1>{}, 0);
+        } else {
+            for (int m0 = 0; m0 < n; m0 += 32) pass(std::integral_constant<int, 2>{}, m0);
         }
-        part[wave][0][lane] = acc[0];
-        part[wave][1][lane] = acc[1];
-        __syncthreads();
-        if (wave == 0 && m0 + r < n) {  // the waves' sums in wave order; lane: token r, columns 4 g ..
-            f32x4 sg = part[0][0][lane], su = part[0][1][lane];
-#pragma unroll
-            for (int v = 1; v < kUpWaves; v++) {
-                sg += part[v][0][lane];
-                su += part[v][1][lane];
-            }
-            const int tok = members[m0 + r];
-            const float wt = weight_of[tok] * a2;
-            float a[4];
-#pragma unroll
-            for (int v = 0; v < 4; v++) {
-                const float gt = a13 * sg[v];
-                a[v] = gt / (1.0f + expf(-gt)) * (a13 * su[v]) * wt;
-            }
-            uint32_t h0, l0, h1, l1;
-            split_bf16x2(a[0], a[1], h0, l0);
-            split_bf16x2(a[2], a[3], h1, l1);
-            const int64_t at = (int64_t)(tok * p.k + rank_of[tok]) * p.I + tile * 16 + 4 * g;
-            *(u32x2*)(p.act_hi + at) = u32x2{h0, h1};
-            *(u32x2*)(p.act_lo + at) = u32x2{l0, l1};
-        }
-        __syncthreads();
     }
 #endif
 }
 
-template <bool WHOLE>
-__global__ __launch_bounds__(64 * kDownWaves) void k_moe_down(EParams p) {
+// Workgroup (128 output columns, share of the K axis): wave w has columns 16 w ..
+// + 15 to itself, and all walk the same (expert, chunk) range.
+template <int D, bool WHOLE>
+__global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ __align__(4) uint8_t rank_of[256 * 64];  // [E][T] slot, or kNone
-    __shared__ int active[256];                    // the chosen experts, ascending
-    __shared__ uint32_t chosen[8];                 // bit e % 32 of word e / 32
-    __shared__ float sums[kDownWaves][64][17];     // each wave's [token][column] sums (padded rows)
-    __shared__ float inv[64];
+    typedef W4Ring<1, D> Ring;
+    extern __shared__ __align__(16) uint8_t smem[];
+    uint8_t* const rings = smem;                             // the waves' weight rings
+    uint8_t* const xs = smem + kWaves * Ring::BYTES;         // activations of a block of chunks
+    Routes& R = *(Routes*)(xs + kXBytes);
+    float* const sums = (float*)(&R + 1);                    // [T][kSumPitch]: sums of every token and column
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int tile = tile_of(p);
-    const int np = p.T * p.k;
 
-    for (int i = t; i < (p.E * p.T + 3) / 4; i += 64 * kDownWaves) ((uint32_t*)rank_of)[i] = 0xFFFFFFFFu;
-    for (int i = lane; i < 64 * 17; i += 64) (&sums[wave][0][0])[i] = 0.0f;
-    if (t < 8) chosen[t] = 0;
+    for (int i = t; i < (int)sizeof(Routes) / 4; i += kThreads) ((uint32_t*)&R)[i] = ((const uint32_t*)p.routes)[i];
+    for (int i = t; i < p.T * kSumPitch; i += kThreads) sums[i] = 0.0f;
     __syncthreads();
-    for (int i = t; i < np; i += 64 * kDownWaves) {
-        const int e = p.ids[i];
-        if (e >= 0) {
-            rank_of[e * p.T + i / p.k] = (uint8_t)(i % p.k);
-            atomicOr(&chosen[e >> 5], 1u << (e & 31));
-        }
-    }
-    if (t < p.T) {
-        float s = 0.0f;
-        for (int j = 0; j < p.k; j++) s += p.raw[t * p.k + j];
-        const float v = p.renorm && p.ids[t * p.k] >= 0 ? 1.0f / s : 1.0f;
-        inv[t] = v;
-        if (blockIdx.x == 0)
-            for (int j = 0; j < p.k; j++) p.weights[t * p.k + j] = p.raw[t * p.k + j] * v;
-    }
-    __syncthreads();
-    int nact = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const uint32_t w = chosen[i];
-        if (t < 32 && (w >> t & 1)) active[nact + __builtin_popcount(w & ((1u << t) - 1))] = 32 * i + t;
-        nact += __builtin_popcount(w);
-    }
-    __syncthreads();
+    const int nact = __builtin_amdgcn_readfirstlane(R.nact);
 
     const int r = lane & 15, g = lane >> 4;
-    const int rowb = p.I / 2, nblk = p.I / 16, cpa4 = (nblk + 3) / 4;
+    const int rowb = p.I / 2, cpa4 = (p.I / 16 + 3) / 4;
     const int nch = (p.I + kChunk - 1) / kChunk;
-    const int row = tile * 16 + r;  // H is a multiple of 16
     const int total = nact * nch;
-    const int q0 = (int)((int64_t)total * wave / kDownWaves), q1 = (int)((int64_t)total * (wave + 1) / kDownWaves);
-    for (int q = q0; q < q1;) {
-        const int at = q / nch, e = __builtin_amdgcn_readfirstlane(active[at]);
-        const int c0 = q - at * nch, c1 = q1 - at * nch < nch ? q1 - at * nch : nch;  // this expert's chunks
-        q += c1 - c0;
-        const uint8_t* const B = p.w2 + ((int64_t)e * p.H + row) * rowb;
-        const uint8_t* const F = p.w2_sf + (int64_t)e * p.w2_sfsz + scale_row_off(row, cpa4);
-        const int rk = lane < p.T ? rank_of[e * p.T + lane] : kNone;
-        uint64_t left = __ballot(rk != kNone);
-        while (left) {  // up to 16 of its tokens at a time: lane r takes the r-th
-            uint64_t rest = left;
-            for (int i = 0; i < r; i++) rest &= rest - 1;
-            const int tok = rest ? __builtin_ctzll(rest) : -1;
-            for (int i = 0; i < 16; i++) left &= left - 1;
-            const int slot = __shfl(rk, tok < 0 ? 0 : tok);
-            const int64_t pair = tok < 0 ? 0 : (int64_t)(tok * p.k + slot) * p.I;
-            const uint16_t* const XH = tok < 0 ? nullptr : p.act_hi + pair;
-            const uint16_t* const XL = tok < 0 ? nullptr : p.act_lo + pair;
-            f32x4 acc = {0, 0, 0, 0};
-            constexpr int U = 2;
-            for (int cb = c0; cb < c1; cb += U) {
-                u32x4 w[U], xh[U][4], xl[U][4];
-                uint32_t s[U];
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    const int c = cb + u < c1 ? cb + u : c1 - 1;
-                    w[u] = load_w4<WHOLE>(B, c, g, rowb);
-                    s[u] = load_s4<WHOLE>(F, c, g, nblk);
-                    load_x16<WHOLE>(xh[u], XH, c, g, p.I);
-                    load_x16<WHOLE>(xl[u], XL, c, g, p.I);
-                }
-#pragma unroll
-                for (int u = 0; u < U; u++) {
-                    if (cb + u >= c1) break;
-                    const float s0 = __builtin_amdgcn_cvt_f32_fp8(s[u], 0), s1 = __builtin_amdgcn_cvt_f32_fp8(s[u], 1);
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const bf16x8 wv = dequant8_bf16(word(w[u], j), j < 2 ? s0 : s1);
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, xh[u][j]), acc, 0, 0, 0);
-                        acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, xl[u][j]), acc, 0, 0, 0);
-                    }
-                }
-            }
-            if (tok >= 0) {
-#pragma unroll
-                for (int v = 0; v < 4; v++) sums[wave][tok][4 * g + v] += acc[v];
-            }
+    // shares of at least 4 chunks; the rest of the workgroups has nothing to do
+    const int shares = total < 4 * p.shares ? (total < 4 ? 1 : total / 4) : p.shares;
+    const int share = blockIdx.y;
+    if (share >= shares) return;
+    const int tile = blockIdx.x * kWaves + wave, tiles = p.H / 16;
+    const bool live = tile < tiles;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.act_hi, (uint32_t)(p.T * p.k * p.I * 4));  // both halves
+    const int q0 = (int)((int64_t)total * share / shares), q1 = (int)((int64_t)total * (share + 1) / shares);
+    // A pass: the chunks of [q0, q1) that lie in one expert, with up to 16 of its
+    // tokens (8 where it has no more).
+    struct Pass {
+        int at, m0;
+    };
+    const int last = (q1 - 1) / nch;  // place of the range's last expert
+    auto act_of = [&](int at) { return (uint32_t)__builtin_amdgcn_readfirstlane((int)R.act[at]); };
+    auto after = [&](Pass q) {
+        q.m0 += 16;
+        if (q.m0 >= act_tokens(act_of(q.at))) q = Pass{q.at + 1, 0};
+        return q;
+    };
+    auto begin_of = [&](int at) { return q0 > at * nch ? q0 - at * nch : 0; };
+    auto end_of = [&](int at) { return q1 - at * nch < nch ? q1 - at * nch : nch; };
+    auto tokens_of = [&](Pass q) {
+        const int n = act_tokens(act_of(q.at)) - q.m0;
+        return n < 16 ? n : 16;
+    };
+    Ring ring;
+    ring.init(rings + wave * Ring::BYTES, lane);
+    Pass aimed = {q0 / nch, 0};
+    int ca = 0, ce = 0;
+    auto aim = [&]() {
+        ca = ce = 0;
+        if (!live || aimed.at > last) return;
+        const int e = act_expert(act_of(aimed.at));
+        ring.aim(make_rsrc(p.w2 + (int64_t)e * p.H * rowb, (uint32_t)(p.H * rowb)),
+                 make_rsrc(p.w2_sf + (int64_t)e * p.w2_sfsz, (uint32_t)p.w2_sfsz), {tile * 16}, rowb, cpa4, lane);
+        ca = begin_of(aimed.at);
+        ce = end_of(aimed.at);
+    };
+    auto next = [&]() {
+        while (ca == ce && aimed.at <= last) {
+            aimed = after(aimed);
+            aim();
         }
+        if (ca < ce) ring.issue(ca++);
+    };
+    XBlock<kXBytes / 16 / kThreads> xb;
+    auto load_block = [&](Pass q, int b0) {  // rows: the tokens' high halves, then their low ones
+        const int nt = tokens_of(q), cb = kXBytes / (nt * 512), end = end_of(q.at);
+        const uint16_t* const list = R.list + act_first(act_of(q.at)) + q.m0;
+        xb.load(
+            rx,
+            [&](int i) {
+                const int lo = i >= nt, it = list[i - lo * nt];
+                return (uint32_t)(((it >> 4) * p.k + (it & 15) + lo * p.T * p.k) * p.I * 2);
+            },
+            2 * nt, cb, p.I, t, kThreads, [&](int lc) { return b0 + lc < end ? b0 + lc : -1; });
+    };
+    Pass cur = {q0 / nch, 0};
+    if (total > 0) {
+        aim();
+        for (int u = 0; u < D; u++) next();
+        load_block(cur, begin_of(cur.at));
     }
-    __syncthreads();
-    for (int i = t; i < p.T * 16; i += 64 * kDownWaves) {
-        const int tok = i >> 4, col = i & 15;
-        float s = sums[0][tok][col];
+    while (total > 0 && cur.at <= last) {
+        const Pass nxt = after(cur);
+        const int c0 = begin_of(cur.at), c1 = end_of(cur.at);
+        const int nt = tokens_of(cur), nr = 2 * nt, cb = kXBytes / (nr * 256);
+        // XT = 1: up to 8 tokens, lanes r < 8 with their activations' high halves and
+        // the others with the low ones; XT = 2: up to 16, a tile of each
+        auto pass = [&](auto xt) {
+            constexpr int XT = decltype(xt)::value, NT = 8 * XT;
+            XLane xl[XT];
+            const int tl = (r & (NT - 1)) < nt ? r & (NT - 1) : nt - 1;  // absent: any row
+            if constexpr (XT == 1) {
+                xl[0].set(xs, (r >> 3) * nt + tl, g);
+            } else {
+                xl[0].set(xs, tl, g);
+                xl[1].set(xs, nt + tl, g);
+            }
+            f32x4 acc[1][XT];
 #pragma unroll
-        for (int v = 1; v < kDownWaves; v++) s += sums[v][tok][col];
-        p.out[(int64_t)tok * p.H + tile * 16 + col] = (uint16_t)pack_bf16x2(s * inv[tok], 0.0f);
+            for (int i = 0; i < XT; i++) acc[0][i] = f32x4{0, 0, 0, 0};
+            for (int b0 = c0; b0 < c1; b0 += cb) {
+                const int b1 = b0 + cb < c1 ? b0 + cb : c1;
+                __syncthreads();  // the previous block is consumed
+                xb.store(xs, nr, cb, t, kThreads);
+                __syncthreads();
+                // the next block is on its way while this one is used
+                if (b1 < c1) load_block(cur, b1);
+                else if (nxt.at <= last) load_block(nxt, begin_of(nxt.at));
+                if (live) consume<XT, WHOLE>(ring, acc, xl, 0, nr * 256, b0, b1, g, p.I, next);
+            }
+            const int it = R.list[act_first(act_of(cur.at)) + cur.m0 + tl];
+#pragma unroll
+            for (int v = 0; v < 4; v++) {
+                const float s = acc[0][0][v] + (XT == 1 ? row_half(acc[0][0][v]) : acc[0][XT - 1][v]);
+                if (r < nt) sums[(it >> 4) * kSumPitch + wave * 16 + 4 * g + v] += s;
+            }
+        };
+        if (nt <= 8) pass(std::integral_constant<int, 1>{});
+        else pass(std::integral_constant<int, 2>{});
+        cur = nxt;
+    }
+    // the wave's own columns (no other wave of the workgroup has touched them)
+    if (!live) return;
+    uint16_t* const O = p.out + tile * 16;
+    const int col = lane & 15;
+    if (shares == 1) {
+        for (int tok = lane >> 4; tok < p.T; tok += 4)
+            O[(int64_t)tok * p.H + col] = (uint16_t)pack_bf16x2(sums[tok * kSumPitch + wave * 16 + col], 0.0f);
+        return;
+    }
+    // several workgroups have these columns: each leaves its sums in memory, and
+    // the wave that finds the others done adds them, in the order of the shares.
+    // Device-scope stores and loads (sc1) pass by the XCDs' own L2s, so no cache
+    // is written back or dropped; the stores are waited for before the count.
+    constexpr int kDevice = 16;
+    const int n16 = p.T * 64;  // bytes of a share's sums of this tile
+    const __amdgpu_buffer_rsrc_t part = make_rsrc(p.part + (int64_t)tile * p.shares * p.T * 16, (uint32_t)(shares * n16));
+    for (int i = lane; i < p.T * 4; i += 64) {
+        const f32x4 v = *(const f32x4*)&sums[(i >> 2) * kSumPitch + wave * 16 + (i & 3) * 4];
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), part, i * 16, share * n16, kDevice);
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    int before = 0;
+    if (lane == 0) before = __hip_atomic_fetch_add(&p.arrived[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (__builtin_amdgcn_readfirstlane(before) != shares - 1) return;
+    asm volatile("" ::: "memory");
+    for (int i = lane; i < p.T * 4; i += 64) {
+        f32x4 s = {0, 0, 0, 0};
+        constexpr int U = 8;  // loads in flight together
+        for (int v0 = 0; v0 < shares; v0 += U) {
+            u32x4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; u++)  // past the last share: past the resource, zeros
+                v[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(part, i * 16 + (v0 + u) * n16, 0, kDevice));
+#pragma unroll
+            for (int u = 0; u < U; u++) s += __builtin_bit_cast(f32x4, v[u]);
+        }
+        *(u32x2*)(O + (int64_t)(i >> 2) * p.H + (i & 3) * 4) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
     }
 #endif
 }
 
 template <int NR>
-void launch_up(const EParams& p, dim3 grid, hipStream_t st) {
-    if (p.H % kChunk == 0) k_moe_up<NR, true><<<grid, 64 * kUpWaves, 0, st>>>(p);
-    else k_moe_up<NR, false><<<grid, 64 * kUpWaves, 0, st>>>(p);
+void launch_up(const EParams& p, int grid, size_t lds, hipStream_t st) {
+    if (p.H % kChunk == 0) k_moe_up<NR, true><<<grid, kThreads, lds, st>>>(p);
+    else k_moe_up<NR, false><<<grid, kThreads, lds, st>>>(p);
+}
+
+template <int D>
+void launch_down(const EParams& p, dim3 grid, size_t tables, hipStream_t st) {
+    const size_t lds = kWaves * W4Ring<1, D>::BYTES + kXBytes + (size_t)p.T * kSumPitch * 4 + tables;
+    if (p.I % kChunk == 0) k_moe_down<D, true><<<grid, kThreads, lds, st>>>(p);
+    else k_moe_down<D, false><<<grid, kThreads, lds, st>>>(p);
 }
 
 }  // namespace
 
 hipError_t launch_moe_small(const MoeSmallArgs& a, hipStream_t st) {
+    const int cus = device_cus();
+    if (cus <= 0) return hipErrorInvalidDevice;
     EParams p{};
     p.x = a.x; p.logits = a.logits; p.lg_bf16 = a.logits_bf16;
     p.w13 = a.w13; p.w13_sf = a.w13_sf; p.alpha13 = a.alpha13;
@@ -411,25 +550,36 @@ hipError_t launch_moe_small(const MoeSmallArgs& a, hipStream_t st) {
     p.out = a.out; p.ids = a.ids; p.weights = a.weights;
     p.T = a.t; p.H = a.h; p.I = a.inter; p.E = a.E; p.k = a.top_k;
     p.sigmoid = a.sigmoid; p.renorm = a.renorm;
-    p.raw = (float*)a.ws;  // T * k <= 1024 floats in the first 4 KiB
-    p.act_hi = (uint16_t*)((char*)a.ws + 4096);
-    p.act_lo = p.act_hi + (int64_t)a.t * a.top_k * a.inter;
     p.w13_sfsz = (int64_t)((2 * a.inter + 127) / 128 * 128) * ((a.h / 16 + 3) / 4 * 4);
     p.w2_sfsz = (int64_t)((a.h + 127) / 128 * 128) * ((a.inter / 16 + 3) / 4 * 4);
-    // fewer pairs than experts: a workgroup row per chosen expert, else one per expert
-    p.by_slot = a.t * a.top_k < a.E;
-    const int rows = p.by_slot ? a.t * a.top_k : a.E;
-    p.tiles = a.inter / 16;
-    p.xcd_chunk = p.tiles % 8 == 0 ? p.tiles / 8 : 0;
-    const dim3 grid((unsigned)p.tiles, (unsigned)rows);
-    const int nr = (a.E + 63) / 64;
-    if (nr == 1) launch_up<1>(p, grid, st);
-    else if (nr == 2) launch_up<2>(p, grid, st);
-    else launch_up<4>(p, grid, st);
-    p.tiles = a.h / 16;
-    p.xcd_chunk = p.tiles % 8 == 0 ? p.tiles / 8 : 0;
-    if (a.inter % kChunk == 0) k_moe_down<true><<<dim3((unsigned)p.tiles), 64 * kDownWaves, 0, st>>>(p);
-    else k_moe_down<false><<<dim3((unsigned)p.tiles), 64 * kDownWaves, 0, st>>>(p);
+    // workspace: the activations' two halves, the partial sums of the second
+    // launch (kMoePartRows rows of h), the tiles' counters
+    const int64_t acts = (int64_t)a.t * a.top_k * a.inter;
+    p.act_hi = (uint16_t*)a.ws;
+    p.act_lo = p.act_hi + acts;
+    p.part = (float*)(p.act_lo + acts);
+    p.routes = p.part + (int64_t)kMoePartRows * a.h;
+    p.arrived = (int32_t*)((char*)p.routes + 4096);
+    const int most = a.t * a.top_k < a.E ? a.t * a.top_k : a.E;  // experts that can be chosen
+    const size_t tables = sizeof(Routes);
+    // first launch: two workgroups a CU, or one per tile if there are fewer
+    const int64_t items = (int64_t)most * (a.inter / 16);
+    const int grid = (int)(items < 2 * cus ? items : 2 * cus);
+    const size_t lds = kWaves * UpRing::BYTES + kXBytes + tables + (size_t)a.t * a.top_k * 6;
+    if (a.E <= 16) launch_up<1>(p, grid, lds, st);
+    else if (a.E <= 64) launch_up<4>(p, grid, lds, st);
+    else if (a.E <= 128) launch_up<8>(p, grid, lds, st);
+    else launch_up<16>(p, grid, lds, st);
+    // second launch: two workgroups a CU as far as the partial sums have room
+    const int cols = (a.h + 127) / 128;
+    p.shares = 2 * cus / cols;
+    if (p.shares > 32) p.shares = 32;
+    if (p.shares > kMoePartRows / a.t) p.shares = kMoePartRows / a.t;
+    if (p.shares < 1) p.shares = 1;
+    // the ring's depth by what LDS has left beside the sums: two workgroups a CU up
+    // to 32 tokens, one with a deeper ring beyond
+    if (a.t <= 32) launch_down<4>(p, dim3((unsigned)cols, (unsigned)p.shares), tables, st);
+    else launch_down<8>(p, dim3((unsigned)cols, (unsigned)p.shares), tables, st);
     return hipGetLastError();
 }
 

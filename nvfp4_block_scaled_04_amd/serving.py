@@ -39,9 +39,9 @@ def _load():
 _lib = _load()
 
 
-def moe_small_ws_bytes(t, top_k, inter):
+def moe_small_ws_bytes(t, top_k, h, inter):
     """NVFP4_MOE_SMALL_WS_BYTES: workspace bytes of nvfp4_moe_small."""
-    return 4096 + 4 * t * top_k * inter
+    return 4 * t * top_k * inter + 4096 * h + 4096 + h // 4
 
 
 def adapters_ws_bytes(m, r, split_tail=False):
@@ -88,7 +88,7 @@ def nvfp4_moe_small(x, logits, w13, w13_sf, alpha13, w2, w2_sf, alpha2, top_k, s
         topk_ids = torch.empty(t, max(k, 0), dtype=torch.int32, device=dev)
     if topk_weights is None:
         topk_weights = torch.empty(t, max(k, 0), dtype=torch.float32, device=dev)
-    workspace = _workspace(workspace, moe_small_ws_bytes(t, k, inter), dev)
+    workspace = _workspace(workspace, moe_small_ws_bytes(t, k, h, inter), dev)
     _dev(x, "x", BF16, t * h, dev)
     _dev(logits, "logits", _LOGITS, t * E, dev)
     _dev(w13, "w13", BYTES, E * inter * h, dev)

@@ -38,7 +38,7 @@ def check(serving, x, logits, w, k, score, renorm):
     out = torch.full((t, h), OUT_CANARY, dtype=torch.int16, device="cuda").view(torch.bfloat16)
     ids = torch.full((t, k), 77, dtype=torch.int32, device="cuda")
     wts = torch.full((t, k), NAN, device="cuda")
-    ws = torch.full((serving.moe_small_ws_bytes(t, k, inter),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((serving.moe_small_ws_bytes(t, k, h, inter),), 0xFF, dtype=torch.uint8, device="cuda")
     serving.nvfp4_moe_small(x, logits, *w.values(), k, score=score, renormalize=renorm, out=out, topk_ids=ids,
                             topk_weights=wts, workspace=ws)
     ref, bound, rid, rw = R.moe(x, logits, *w.values(), k, score, renorm)
@@ -156,7 +156,7 @@ def test_repeats_streams_and_graph(serving):
     a captured graph with the workspace and the outputs overwritten in between."""
     say("moe: repeats, stream, graph")
     x, lg, w = layer(8, 33, 272, 144, 20)
-    ws = torch.full((serving.moe_small_ws_bytes(33, 3, 144),), 0xFF, dtype=torch.uint8, device="cuda")
+    ws = torch.full((serving.moe_small_ws_bytes(33, 3, 272, 144),), 0xFF, dtype=torch.uint8, device="cuda")
     out = torch.empty(33, 272, dtype=torch.bfloat16, device="cuda")
     ids = torch.empty(33, 3, dtype=torch.int32, device="cuda")
     wts = torch.empty(33, 3, device="cuda")

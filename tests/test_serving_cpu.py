@@ -43,7 +43,7 @@ MOE = dict(x=P, t=4, h=64, logits=P, dt=1, E=8, k=2, score=0, renorm=1, w13=P, s
     ({"dt": 2}, DTYPE), ({"t": 0}, SHAPE), ({"t": -1}, SHAPE), ({"t": 65}, UNSUP), ({"E": 0}, SHAPE), ({"E": 257}, UNSUP),
     ({"k": 0}, SHAPE), ({"k": 9}, SHAPE), ({"E": 64, "k": 17}, UNSUP), ({"h": 0}, SHAPE), ({"h": 40}, SHAPE),
     ({"inter": 8}, SHAPE), ({"inter": 0}, SHAPE), ({"score": 2}, UNSUP), ({"h": 1 << 24, "inter": 256}, UNSUP),
-    ({"wsb": 4096 + 4 * 4 * 2 * 32 - 1}, SHAPE), ({"x": P + 8}, MISAL), ({"w13": P + 4}, MISAL), ({"w2": P + 8}, MISAL),
+    ({"wsb": 4 * 4 * 2 * 32 + 4096 * 64 + 4096 + 16 - 1}, SHAPE), ({"x": P + 8}, MISAL), ({"w13": P + 4}, MISAL), ({"w2": P + 8}, MISAL),
     ({"sf13": P + 8}, MISAL), ({"sf2": P + 8}, MISAL), ({"logits": P + 4}, MISAL), ({"out": P + 2}, MISAL),
     ({"ws": P + 8}, MISAL), ({"ids": P + 2}, MISAL), ({"wts": P + 1}, MISAL), ({"al13": P + 2}, MISAL), ({"al2": P + 3}, MISAL),
 ])
@@ -77,18 +77,18 @@ def test_gemm_adapters_validation(serving, change, status):
 
 
 def test_workspace_sizes(serving, tmp_path):
-    shapes = [(1, 1, 16), (64, 16, 8192), (7, 3, 48)]
+    shapes = [(1, 1, 16), (64, 16, 8192), (7, 3, 48)]   # (t, top_k, h), inter = 2 h; (m, ., r)
     src = tmp_path / "ws.c"
     lines = ["#include <stdio.h>", '#include "nvfp4_serving.h"', "int main(void) {"]
     for a, b, c in shapes:
-        lines.append(f'  printf("%lld %lld\\n", (long long)NVFP4_MOE_SMALL_WS_BYTES({a}, {b}, {c}), '
+        lines.append(f'  printf("%lld %lld\\n", (long long)NVFP4_MOE_SMALL_WS_BYTES({a}, {b}, {c}, {2 * c}), '
                      f"(long long)NVFP4_ADAPTERS_WS_BYTES({a}, {c}));")
     src.write_text("\n".join(lines + ["  return 0;", "}"]) + "\n")
     exe = tmp_path / "ws"
     subprocess.run(["gcc", "-Wall", "-Werror", "-I", os.path.dirname(HEADER), str(src), "-o", str(exe)], check=True)
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.split("\n")
     for (a, b, c), line in zip(shapes, out):
-        assert [int(v) for v in line.split()] == [serving.moe_small_ws_bytes(a, b, c), serving.adapters_ws_bytes(a, c)]
+        assert [int(v) for v in line.split()] == [serving.moe_small_ws_bytes(a, b, c, 2 * c), serving.adapters_ws_bytes(a, c)]
     assert serving.adapters_ws_bytes(5, 24, split_tail=True) == serving.adapters_ws_bytes(5, 24) + 33554432
 
 
