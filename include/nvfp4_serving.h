@@ -30,11 +30,12 @@ enum nvfp4_route_score {
 
 /*
  * Bytes of workspace of nvfp4_moe_small: the activations of the t * top_k
- * (token, expert) pairs, `inter` columns each, as two bf16 halves; 1024 rows of
- * partial fp32 outputs; the routing tables; a counter per 16 output columns.
+ * (token, expert) pairs, `inter` fp32 columns each; 1024 rows of partial fp32
+ * outputs; the routing tables; a counter per 16 output columns (h rounded up to
+ * 128).
  */
 #define NVFP4_MOE_SMALL_WS_BYTES(t, top_k, h, inter) \
-    (4 * (int64_t)(t) * (int64_t)(top_k) * (int64_t)(inter) + 4096 * (int64_t)(h) + 4096 + (int64_t)(h) / 4)
+    (4 * (int64_t)(t) * (int64_t)(top_k) * (int64_t)(inter) + 4096 + (4096 * 4 + 1) * (((int64_t)(h) + 127) / 128 * 32))
 
 /*
  * A whole mixture-of-experts layer for a few tokens, in two launches.
@@ -49,9 +50,9 @@ enum nvfp4_route_score {
  *   [g, u]    = alpha13[e] * x[i] @ W13[e]^T
  *   a         = g / (1 + exp(-g)) * u
  *   out[i, :] = bf16(sum over the chosen e of topk_weights * alpha2[e] * a @ W2[e]^T).
- * A token that chose no expert gets zeros.  Sums are formed in fp32; a enters
- * the second product as the sum of two bf16 values (2^-16 of a), the dequantized
- * weights are exact.  Results are the same on every call (no atomic sums).
+ * A token that chose no expert gets zeros.  Sums and a are formed in fp32, a enters
+ * the second product as two fp16 values (2^-20 of a), the dequantized weights are
+ * exact.  Results are the same on every call (no atomic sums).
  *   x: [t, h] bf16; logits: [t, E], bf16 (logits_dtype 0) or fp32 (1).
  *   w13: [E, 2*inter, h/2] packed e2m1, gate rows [0, inter) then up rows;
  *   w13_sf: [E, pad_up(2*inter,128)*pad_up(h/16,4)] ue4m3, swizzled;

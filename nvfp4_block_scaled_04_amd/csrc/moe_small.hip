@@ -28,16 +28,27 @@
 #include "internal.h"
 #include "skinny_w4.h"
 
-#include <type_traits>
-
 namespace nvfp4 {
 namespace {
 
 constexpr int kWaves = 8;    // of either kernel's workgroups; two of them share a CU
 constexpr int kThreads = 64 * kWaves;
 constexpr int kXBytes = 16 << 10;  // LDS for activations: 4 chunks of 16 rows, 64 of one
-constexpr int kSumPitch = 132;     // floats of a token's row of sums (128 columns, padded)
+constexpr int kInvBytes = kXBytes / 64;  // a float per row and chunk
 typedef W4Ring<2, 3> UpRing;       // with x and the tables, LDS for two workgroups a CU
+
+// Second launch: up to 32 tokens, two workgroups of 8 waves share a CU; beyond, the
+// sums take the LDS, and one workgroup of 16 waves has a CU where there are enough
+// columns for that (64 tokens over 32 experts of 4096 x 2048: 67 us, 77 with 8
+// waves; 61 tokens over 60 of 2064 x 1104, too few: 66 us, 50 with 8 waves).
+template <int NW>
+struct DownShape {
+    typedef W4Ring<1, NW == 8 ? 4 : 3> Ring;
+    static constexpr int kX = NW == 8 ? 16 << 10 : 24 << 10;  // LDS for activations
+    static constexpr int kInv = kX / 64;                      // a float per row and chunk
+    static constexpr int kPitch = 16 * NW + 4;                // floats of a token's row of sums
+    static constexpr int kFixed = NW * Ring::BYTES + kX + kInv;
+};
 
 struct EParams {
     const uint16_t* x;         // [T, H]
@@ -52,10 +63,9 @@ struct EParams {
     int32_t* ids;              // [T, k]
     float* weights;            // [T, k]
     void* routes;              // Routes, from the first launch for the second
-    int32_t* arrived;          // [H/16] shares of a column tile that are done (k_moe_down)
-    uint16_t* act_hi;          // [T * k, I], row t * k + slot
-    uint16_t* act_lo;
-    float* part;               // [H/16, shares, T, 16] partial sums (k_moe_down with shares > 1)
+    int32_t* arrived;          // [8 * ceil(H/128)] shares of a column tile that are done (k_moe_down)
+    float* act;                // [T * k, I], row t * k + slot: w(i, e) * alpha2 * a
+    float* part;               // [8 * ceil(H/128), shares, T, 16] partial sums (k_moe_down with shares > 1)
     int64_t w13_sfsz, w2_sfsz; // scale bytes of one expert
     int T, H, I, E, k;
     int lg_bf16, sigmoid, renorm;
@@ -64,23 +74,6 @@ struct EParams {
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// All-reduce over the 16 lanes of a DPP row: the neighbour in a pair, the other
-// pair of a quad, the mirrored quad of 8, the mirrored half of 16.
-template <typename T, typename F>
-__device__ __forceinline__ T row16(T v, F f) {
-    auto step = [&](auto ctl) {
-        const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctl)::value, 0xF, 0xF, true);
-        v = f(v, __builtin_bit_cast(T, o));
-    };
-    step(std::integral_constant<int, 0xB1>{});
-    step(std::integral_constant<int, 0x4E>{});
-    step(std::integral_constant<int, 0x141>{});
-    step(std::integral_constant<int, 0x140>{});
-    return v;
-}
-__device__ __forceinline__ float row16_max(float v) {
-    return row16(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
-}
 __device__ __forceinline__ float row16_sum(float v) {
     return row16(v, [](float a, float b) { return a + b; });
 }
@@ -101,7 +94,6 @@ struct alignas(16) Routes {
     uint32_t act[256];    // expert | tokens << 8 | first of the list << 16
     uint16_t list[1024];  // token << 4 | slot
     int32_t nact;
-    int32_t most;         // most tokens on one expert
 };
 static_assert(sizeof(Routes) <= 4096, "room in the workspace");
 __device__ __forceinline__ int act_expert(uint32_t a) { return a & 255; }
@@ -127,32 +119,39 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const rings = smem;                             // the waves' weight rings; then the parts' sums
     uint8_t* const xs = smem + kWaves * UpRing::BYTES;       // x of a block of chunks
-    Routes& R = *(Routes*)(xs + kXBytes);
+    float* const inv = (float*)(xs + kXBytes);               // their inverse scales
+    Routes& R = *(Routes*)(xs + kXBytes + kInvBytes);
     float* const weight_of = (float*)(&R + 1);               // [T * k]
     int16_t* const choice = (int16_t*)(weight_of + p.T * p.k);  // [T][k]
     int* const count = (int*)rings;                          // [256] tokens of an expert (before the rings are used)
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
 
-    // 1. routing: 16 lanes a token, its logits in registers
-    if (t < 256) count[t] = 0;
-    if (blockIdx.x == 0)
-        for (int i = t; i < p.H / 16; i += kThreads) p.arrived[i] = 0;
-    __syncthreads();
+    // 1. routing: 16 lanes a token, its logits in registers (the first tokens' are on
+    //    their way while the counts are cleared)
     const int l16 = lane & 15;
-    for (int t0 = wave * 4; t0 < p.T; t0 += kWaves * 4) {
-        const int tok = t0 + (lane >> 4);
-        float lg[NR];
+    auto load_logits = [&](int tok, float (&lg)[NR]) {
 #pragma unroll
         for (int i = 0; i < NR; i++) {
             const int j = l16 + 16 * i;
             lg[i] = neg_inf();
             if (tok < p.T && j < p.E) {
                 const int64_t at = (int64_t)tok * p.E + j;
-                const float v = p.lg_bf16 ? bf16_lo((uint32_t)((const uint16_t*)p.logits)[at]) : ((const float*)p.logits)[at];
-                lg[i] = v == v ? v : neg_inf();  // NaN is never chosen
+                lg[i] = p.lg_bf16 ? bf16_lo((uint32_t)((const uint16_t*)p.logits)[at]) : ((const float*)p.logits)[at];
             }
         }
+    };
+    float lg[NR];
+    load_logits(wave * 4 + (lane >> 4), lg);
+    if (t < 256) count[t] = 0;
+    if (blockIdx.x == 0)
+        for (int i = t; i < (p.H + 127) / 128 * 8; i += kThreads) p.arrived[i] = 0;
+    __syncthreads();
+    for (int t0 = wave * 4; t0 < p.T; t0 += kWaves * 4) {
+        const int tok = t0 + (lane >> 4);
+        if (t0 >= kWaves * 4) load_logits(tok, lg);
+#pragma unroll
+        for (int i = 0; i < NR; i++) lg[i] = lg[i] == lg[i] ? lg[i] : neg_inf();  // NaN is never chosen
         float top = lg[0];
 #pragma unroll
         for (int i = 1; i < NR; i++) top = __builtin_fmaxf(top, lg[i]);
@@ -208,44 +207,45 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
         }
     }
     __syncthreads();
-    if (wave == 0) {
-        int na = 0, pairs = 0, most = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 64) {
-            const int n = e0 + lane < p.E ? count[e0 + lane] : 0;
-            int sum;
-            const int first = pairs + wave_prefix(n, sum);
-            const uint64_t some = __ballot(n > 0);
-            if (n > 0)
-                R.act[na + __builtin_popcountll(some & (((uint64_t)1 << lane) - 1))] =
-                    (uint32_t)(e0 + lane) | (uint32_t)n << 8 | (uint32_t)first << 16;
-            na += __builtin_popcountll(some);
-            pairs += sum;
-            most = most > n ? most : n;
-        }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) {
-            const int u = __shfl_xor(most, o);
-            most = most > u ? most : u;
-        }
-        if (lane == 0) {
-            R.nact = na;
-            R.most = most;
-        }
+    // the chosen experts: every wave writes the same list and reads back its own
+    int nact = 0, pairs = 0, most = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 64) {
+        const int n = e0 + lane < p.E ? count[e0 + lane] : 0;
+        const uint64_t some = __ballot(n > 0);
+        int sum;
+        const int first = pairs + wave_prefix(n, sum);
+        if (n > 0)
+            R.act[nact + __builtin_popcountll(some & (((uint64_t)1 << lane) - 1))] =
+                (uint32_t)(e0 + lane) | (uint32_t)n << 8 | (uint32_t)first << 16;
+        nact += __builtin_popcountll(some);
+        pairs += sum;
+        most = most > n ? most : n;
     }
-    __syncthreads();
-    const int nact = __builtin_amdgcn_readfirstlane(R.nact);
-    for (int i = wave; i < nact; i += kWaves) {  // an expert's tokens, lane by lane
-        const uint32_t a = R.act[i];
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) {
+        const int u = __shfl_xor(most, o);
+        most = most > u ? most : u;
+    }
+    nact = __builtin_amdgcn_readfirstlane(nact);
+    most = __builtin_amdgcn_readfirstlane(most);
+    __builtin_amdgcn_wave_barrier();
+    // an expert's tokens, lane by lane, into its place of the list
+    auto list_tokens = [&](uint32_t a) {
         int slot = -1;
         if (lane < p.T)
             for (int j = 0; j < p.k; j++)
                 if (choice[lane * p.k + j] == act_expert(a)) slot = j;
         const uint64_t in = __ballot(slot >= 0);
         if (slot >= 0) R.list[act_first(a) + __builtin_popcountll(in & (((uint64_t)1 << lane) - 1))] = (uint16_t)(lane << 4 | slot);
-    }
-    __syncthreads();
-    if (blockIdx.x == 0)
+        __builtin_amdgcn_wave_barrier();
+    };
+    if (blockIdx.x == gridDim.x - 1) {  // the copy for the second launch
+        if (t == 0) R.nact = nact;
+        for (int i = wave; i < nact; i += kWaves) list_tokens(R.act[i]);
+        __syncthreads();
         for (int i = t; i < (int)sizeof(Routes) / 4; i += kThreads) ((uint32_t*)p.routes)[i] = ((const uint32_t*)&R)[i];
+    }
+    __syncthreads();  // count shares the rings' LDS
 
     // 2. items: (chosen expert, up to 8 / S tiles of 16 gate and 16 up rows), the K
     //    axis of a tile split over S waves: as many as give every wave something,
@@ -253,8 +253,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
     const int r = lane & 15, g = lane >> 4;
     const int rowb = p.H / 2, cpa4 = (p.H / 16 + 3) / 4;
     const int nch = (p.H + kChunk - 1) / kChunk;
-    const int tiles = p.I / 16;
-    const int most = __builtin_amdgcn_readfirstlane(R.most), rows_most = most < 32 ? most : 32;
+    const int tiles = (p.I + 127) / 128 * 8;
+    const int rows_most = most < 32 ? most : 32;
     int S = 1;
     while (S < kWaves && nact * tiles * S * 2 <= (int)gridDim.x * kWaves && 2 * S * rows_most * 256 <= kXBytes) S *= 2;
     const int ipw = kWaves / S, sub = wave / S, part_of = wave % S;
@@ -273,11 +273,12 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
         const uint32_t a = (uint32_t)__builtin_amdgcn_readfirstlane((int)R.act[ai]);
         const int e = act_expert(a), n = act_tokens(a);
         const uint16_t* const list = R.list + act_first(a);
+        list_tokens(a);  // every wave the same
         const bool live = tile < tiles;
         const float a13 = p.alpha13[e], a2 = p.alpha2[e];
         ring.aim(make_rsrc(p.w13 + (int64_t)e * 2 * p.I * rowb, (uint32_t)(2 * p.I * rowb)),
                  make_rsrc(p.w13_sf + (int64_t)e * p.w13_sfsz, (uint32_t)p.w13_sfsz),
-                 {live ? tile * 16 : 0, p.I + (live ? tile * 16 : 0)}, rowb, cpa4, lane);
+                 {0, p.I}, live ? tile : 0, p.I, rowb, cpa4, lane);
         // XT tiles of 16 tokens at a time, the first of them the m0-th
         auto pass = [&](auto xt, int m0) {
             constexpr int XT = decltype(xt)::value;
@@ -290,17 +291,18 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
             };
             if (live)
                 for (int u = 0; u < UpRing::DEPTH; u++) next();
-            XBlock<kXBytes / 16 / kThreads> xb;
-            auto load_block = [&](int k0) {
-                xb.load(rx, [&](int i) { return (uint32_t)((list[m0 + i] >> 4) * p.H * 2); }, nr, S * cb, p.H, t, kThreads, [&](int lc) {
-                    const int q = lc / cb, c = cps * q + k0 + lc - q * cb;
-                    return k0 + lc - q * cb < cps && c < nch ? c : -1;
-                });
-            };
-            load_block(0);
+            XBlock<kXBytes / 16 / kThreads, false> xb;
+            xb.prepare(
+                nr, nr, S * cb, t, kThreads, [&](int R_) { return (uint32_t)((list[m0 + R_] >> 4) * p.H * 2); },
+                [&](int lc) { return cps * (lc / cb) + lc % cb; },
+                [&](int lc) { return cps * (lc / cb + 1) < nch ? cps * (lc / cb + 1) : nch; });
+            xb.load(rx, 0, p.H, t);
             XLane xl[XT];
 #pragma unroll
-            for (int i = 0; i < XT; i++) xl[i].set(xs, 16 * i + r < nr ? 16 * i + r : nr - 1, g);  // absent: any row
+            for (int i = 0; i < XT; i++) {
+                const int row = 16 * i + r < nr ? 16 * i + r : nr - 1;  // absent: any row
+                xl[i].set(xs, inv, row, row, g);
+            }
             f32x4 acc[2][XT];
 #pragma unroll
             for (int f = 0; f < 2; f++)
@@ -308,11 +310,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
                 for (int i = 0; i < XT; i++) acc[f][i] = f32x4{0, 0, 0, 0};
             for (int k0 = 0; k0 < cps; k0 += cb) {
                 if (k0) __syncthreads();  // the previous block is consumed
-                xb.store(xs, nr, S * cb, t, kThreads);
+                xb.store(xs, inv, 0, k0, t);
                 __syncthreads();
-                if (k0 + cb < cps) load_block(k0 + cb);  // the next block is on its way while this one is used
+                if (k0 + cb < cps) xb.load(rx, k0 + cb, p.H, t);  // the next block is on its way while this one is used
                 const int b0 = c0 + k0, b1 = b0 + cb < c1 ? b0 + cb : c1;
-                if (live) consume<XT, WHOLE>(ring, acc, xl, part_of * cb * nr * 256, nr * 256, b0, b1, g, p.H, next);
+                if (live) consume<XT, WHOLE>(ring, acc, xl, part_of * cb * nr, nr, b0, b1, g, p.H, next);
             }
             if (S > 1) {  // the parts' sums, in part order
                 __syncthreads();
@@ -331,7 +333,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
             }
 #pragma unroll
             for (int i = 0; i < XT; i++) {
-                if (!live || 16 * i + r >= nr) continue;  // lane: its token, columns 4 g .. 4 g + 3 of the tile
+                const int col = band_row(tile, 4 * g);  // lane: its token, columns col .. col + 3 (I is a multiple of 16)
+                if (!live || 16 * i + r >= nr || col >= p.I) continue;
                 const int it = list[m0 + 16 * i + r], pair = (it >> 4) * p.k + (it & 15);
                 const float wt = weight_of[pair] * a2;
                 float v4[4];
@@ -340,12 +343,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
                     const float gt = a13 * acc[0][i][v];
                     v4[v] = gt / (1.0f + expf(-gt)) * (a13 * acc[1][i][v]) * wt;
                 }
-                uint32_t h0, l0, h1, l1;
-                split_bf16x2(v4[0], v4[1], h0, l0);
-                split_bf16x2(v4[2], v4[3], h1, l1);
-                const int64_t at = (int64_t)pair * p.I + tile * 16 + 4 * g;
-                *(u32x2*)(p.act_hi + at) = u32x2{h0, h1};
-                *(u32x2*)(p.act_lo + at) = u32x2{l0, l1};
+                *(f32x4*)(p.act + (int64_t)pair * p.I + col) = f32x4{v4[0], v4[1], v4[2], v4[3]};
             }
         };
         if (n <= 16) {
@@ -357,16 +355,19 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
 #endif
 }
 
-// Workgroup (128 output columns, share of the K axis): wave w has columns 16 w ..
-// + 15 to itself, and all walk the same (expert, chunk) range.
-template <int D, bool WHOLE>
-__global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
+// Workgroup (16 NW output columns, share of the K axis): a wave has 16 columns to
+// itself, and all walk the same (expert, chunk) range.
+template <int NW, bool WHOLE>
+__global__ __launch_bounds__(64 * NW, 4) void k_moe_down(EParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    typedef W4Ring<1, D> Ring;
+    typedef DownShape<NW> Shape;
+    typedef typename Shape::Ring Ring;
+    constexpr int kThreads = 64 * NW, kXBytes = Shape::kX, D = Ring::DEPTH, kSumPitch = Shape::kPitch;
     extern __shared__ __align__(16) uint8_t smem[];
     uint8_t* const rings = smem;                             // the waves' weight rings
-    uint8_t* const xs = smem + kWaves * Ring::BYTES;         // activations of a block of chunks
-    Routes& R = *(Routes*)(xs + kXBytes);
+    uint8_t* const xs = smem + NW * Ring::BYTES;             // activations of a block of chunks
+    float* const inv = (float*)(xs + kXBytes);               // their inverse scales
+    Routes& R = *(Routes*)(xs + kXBytes + Shape::kInv);
     float* const sums = (float*)(&R + 1);                    // [T][kSumPitch]: sums of every token and column
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -384,9 +385,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
     const int shares = total < 4 * p.shares ? (total < 4 ? 1 : total / 4) : p.shares;
     const int share = blockIdx.y;
     if (share >= shares) return;
-    const int tile = blockIdx.x * kWaves + wave, tiles = p.H / 16;
-    const bool live = tile < tiles;
-    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.act_hi, (uint32_t)(p.T * p.k * p.I * 4));  // both halves
+    const int tile = blockIdx.x * NW + wave;  // the wave's 16 columns: band_row(tile, 0 .. 15)
+    const int mine0 = (wave >> 3) * 128 + (wave & 7) * 4;  // the first of them in sums; 32 apart from 4 to 4
+    const bool live = band_row(tile, 0) < p.H;
+    const __amdgpu_buffer_rsrc_t rx = make_rsrc(p.act, (uint32_t)(p.T * p.k * p.I * 4));
     const int q0 = (int)((int64_t)total * share / shares), q1 = (int)((int64_t)total * (share + 1) / shares);
     // A pass: the chunks of [q0, q1) that lie in one expert, with up to 16 of its
     // tokens (8 where it has no more).
@@ -415,7 +417,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
         if (!live || aimed.at > last) return;
         const int e = act_expert(act_of(aimed.at));
         ring.aim(make_rsrc(p.w2 + (int64_t)e * p.H * rowb, (uint32_t)(p.H * rowb)),
-                 make_rsrc(p.w2_sf + (int64_t)e * p.w2_sfsz, (uint32_t)p.w2_sfsz), {tile * 16}, rowb, cpa4, lane);
+                 make_rsrc(p.w2_sf + (int64_t)e * p.w2_sfsz, (uint32_t)p.w2_sfsz), {0}, tile, p.H, rowb, cpa4, lane);
         ca = begin_of(aimed.at);
         ce = end_of(aimed.at);
     };
@@ -426,28 +428,28 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
         }
         if (ca < ce) ring.issue(ca++);
     };
-    XBlock<kXBytes / 16 / kThreads> xb;
-    auto load_block = [&](Pass q, int b0) {  // rows: the tokens' high halves, then their low ones
-        const int nt = tokens_of(q), cb = kXBytes / (nt * 512), end = end_of(q.at);
+    // chunks of a block: what LDS holds and one piece a thread fills
+    auto block_of = [&](int nt) { return kXBytes / (nt * 512) < kThreads / (nt * 16) ? kXBytes / (nt * 512) : kThreads / (nt * 16); };
+    XBlock<1, true> xb;
+    auto prepare = [&](Pass q) {  // rows in LDS: the tokens' high halves, then their low ones
+        const int nt = tokens_of(q), end = end_of(q.at), begin = begin_of(q.at);
         const uint16_t* const list = R.list + act_first(act_of(q.at)) + q.m0;
-        xb.load(
-            rx,
-            [&](int i) {
-                const int lo = i >= nt, it = list[i - lo * nt];
-                return (uint32_t)(((it >> 4) * p.k + (it & 15) + lo * p.T * p.k) * p.I * 2);
-            },
-            2 * nt, cb, p.I, t, kThreads, [&](int lc) { return b0 + lc < end ? b0 + lc : -1; });
+        xb.prepare(
+            nt, 2 * nt, block_of(nt), t, kThreads,
+            [&](int i) { return (uint32_t)(((list[i] >> 4) * p.k + (list[i] & 15)) * p.I * 4); },
+            [&](int lc) { return begin + lc; }, [&](int) { return end; });
     };
     Pass cur = {q0 / nch, 0};
     if (total > 0) {
         aim();
         for (int u = 0; u < D; u++) next();
-        load_block(cur, begin_of(cur.at));
+        prepare(cur);
+        xb.load(rx, 0, p.I, t);
     }
     while (total > 0 && cur.at <= last) {
         const Pass nxt = after(cur);
         const int c0 = begin_of(cur.at), c1 = end_of(cur.at);
-        const int nt = tokens_of(cur), nr = 2 * nt, cb = kXBytes / (nr * 256);
+        const int nt = tokens_of(cur), nr = 2 * nt, cb = block_of(nt);
         // XT = 1: up to 8 tokens, lanes r < 8 with their activations' high halves and
         // the others with the low ones; XT = 2: up to 16, a tile of each
         auto pass = [&](auto xt) {
@@ -455,10 +457,10 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
             XLane xl[XT];
             const int tl = (r & (NT - 1)) < nt ? r & (NT - 1) : nt - 1;  // absent: any row
             if constexpr (XT == 1) {
-                xl[0].set(xs, (r >> 3) * nt + tl, g);
+                xl[0].set(xs, inv, (r >> 3) * nt + tl, tl, g);
             } else {
-                xl[0].set(xs, tl, g);
-                xl[1].set(xs, nt + tl, g);
+                xl[0].set(xs, inv, tl, tl, g);
+                xl[1].set(xs, inv, nt + tl, tl, g);
             }
             f32x4 acc[1][XT];
 #pragma unroll
@@ -466,31 +468,39 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
             for (int b0 = c0; b0 < c1; b0 += cb) {
                 const int b1 = b0 + cb < c1 ? b0 + cb : c1;
                 __syncthreads();  // the previous block is consumed
-                xb.store(xs, nr, cb, t, kThreads);
+                xb.store(xs, inv, nt, b0 - c0, t);
                 __syncthreads();
                 // the next block is on its way while this one is used
-                if (b1 < c1) load_block(cur, b1);
-                else if (nxt.at <= last) load_block(nxt, begin_of(nxt.at));
-                if (live) consume<XT, WHOLE>(ring, acc, xl, 0, nr * 256, b0, b1, g, p.I, next);
+                if (b1 < c1) {
+                    xb.load(rx, b1 - c0, p.I, t);
+                } else if (nxt.at <= last) {
+                    prepare(nxt);
+                    xb.load(rx, 0, p.I, t);
+                }
+                if (live) consume<XT, WHOLE>(ring, acc, xl, 0, nr, b0, b1, g, p.I, next);
             }
             const int it = R.list[act_first(act_of(cur.at)) + cur.m0 + tl];
 #pragma unroll
             for (int v = 0; v < 4; v++) {
                 const float s = acc[0][0][v] + (XT == 1 ? row_half(acc[0][0][v]) : acc[0][XT - 1][v]);
-                if (r < nt) sums[(it >> 4) * kSumPitch + wave * 16 + 4 * g + v] += s;
+                if (r < nt) sums[(it >> 4) * kSumPitch + mine0 + 32 * g + v] += s;
             }
         };
         if (nt <= 8) pass(std::integral_constant<int, 1>{});
         else pass(std::integral_constant<int, 2>{});
         cur = nxt;
     }
-    // the wave's own columns (no other wave of the workgroup has touched them)
+    // the wave's own columns (no other wave of the workgroup has touched them), four
+    // of a token at a time: item i is token i / 4, quarter i % 4
     if (!live) return;
-    uint16_t* const O = p.out + tile * 16;
-    const int col = lane & 15;
+    auto mine = [&](int i) { return *(const f32x4*)&sums[(i >> 2) * kSumPitch + mine0 + (i & 3) * 32]; };
+    auto put = [&](int i, f32x4 v) {
+        const int col = band_row(tile, 4 * (i & 3));
+        if (col < p.H)  // H is a multiple of 16
+            *(u32x2*)(p.out + (int64_t)(i >> 2) * p.H + col) = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    };
     if (shares == 1) {
-        for (int tok = lane >> 4; tok < p.T; tok += 4)
-            O[(int64_t)tok * p.H + col] = (uint16_t)pack_bf16x2(sums[tok * kSumPitch + wave * 16 + col], 0.0f);
+        for (int i = lane; i < p.T * 4; i += 64) put(i, mine(i));
         return;
     }
     // several workgroups have these columns: each leaves its sums in memory, and
@@ -501,8 +511,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
     const int n16 = p.T * 64;  // bytes of a share's sums of this tile
     const __amdgpu_buffer_rsrc_t part = make_rsrc(p.part + (int64_t)tile * p.shares * p.T * 16, (uint32_t)(shares * n16));
     for (int i = lane; i < p.T * 4; i += 64) {
-        const f32x4 v = *(const f32x4*)&sums[(i >> 2) * kSumPitch + wave * 16 + (i & 3) * 4];
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), part, i * 16, share * n16, kDevice);
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, mine(i)), part, i * 16, share * n16, kDevice);
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     int before = 0;
@@ -511,7 +520,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
     asm volatile("" ::: "memory");
     for (int i = lane; i < p.T * 4; i += 64) {
         f32x4 s = {0, 0, 0, 0};
-        constexpr int U = 8;  // loads in flight together
+        constexpr int U = 16;  // loads in flight together
         for (int v0 = 0; v0 < shares; v0 += U) {
             u32x4 v[U];
 #pragma unroll
@@ -520,7 +529,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_down(EParams p) {
 #pragma unroll
             for (int u = 0; u < U; u++) s += __builtin_bit_cast(f32x4, v[u]);
         }
-        *(u32x2*)(O + (int64_t)(i >> 2) * p.H + (i & 3) * 4) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+        put(i, s);
     }
 #endif
 }
@@ -531,11 +540,18 @@ void launch_up(const EParams& p, int grid, size_t lds, hipStream_t st) {
     else k_moe_up<NR, false><<<grid, kThreads, lds, st>>>(p);
 }
 
-template <int D>
-void launch_down(const EParams& p, dim3 grid, size_t tables, hipStream_t st) {
-    const size_t lds = kWaves * W4Ring<1, D>::BYTES + kXBytes + (size_t)p.T * kSumPitch * 4 + tables;
-    if (p.I % kChunk == 0) k_moe_down<D, true><<<grid, kThreads, lds, st>>>(p);
-    else k_moe_down<D, false><<<grid, kThreads, lds, st>>>(p);
+template <int NW>
+void launch_down(EParams p, int cus, int most_shares, hipStream_t st) {
+    typedef DownShape<NW> Shape;
+    // enough workgroups for every CU, as far as the partial sums have room
+    const int cols = (p.H + 16 * NW - 1) / (16 * NW);
+    p.shares = (p.T <= 32 ? 2 : 1) * cus / cols;
+    if (p.shares > most_shares) p.shares = most_shares;
+    if (p.shares < 1) p.shares = 1;
+    const size_t lds = Shape::kFixed + sizeof(Routes) + (size_t)p.T * Shape::kPitch * 4;
+    const dim3 grid((unsigned)cols, (unsigned)p.shares);
+    if (p.I % kChunk == 0) k_moe_down<NW, true><<<grid, 64 * NW, lds, st>>>(p);
+    else k_moe_down<NW, false><<<grid, 64 * NW, lds, st>>>(p);
 }
 
 }  // namespace
@@ -552,34 +568,29 @@ hipError_t launch_moe_small(const MoeSmallArgs& a, hipStream_t st) {
     p.sigmoid = a.sigmoid; p.renorm = a.renorm;
     p.w13_sfsz = (int64_t)((2 * a.inter + 127) / 128 * 128) * ((a.h / 16 + 3) / 4 * 4);
     p.w2_sfsz = (int64_t)((a.h + 127) / 128 * 128) * ((a.inter / 16 + 3) / 4 * 4);
-    // workspace: the activations' two halves, the partial sums of the second
+    // workspace: the activations, the partial sums of the second
     // launch (kMoePartRows rows of h), the tiles' counters
     const int64_t acts = (int64_t)a.t * a.top_k * a.inter;
-    p.act_hi = (uint16_t*)a.ws;
-    p.act_lo = p.act_hi + acts;
-    p.part = (float*)(p.act_lo + acts);
-    p.routes = p.part + (int64_t)kMoePartRows * a.h;
+    p.act = (float*)a.ws;
+    p.part = p.act + acts;
+    p.routes = p.part + (int64_t)kMoePartRows * ((a.h + 127) / 128 * 128);
     p.arrived = (int32_t*)((char*)p.routes + 4096);
     const int most = a.t * a.top_k < a.E ? a.t * a.top_k : a.E;  // experts that can be chosen
-    const size_t tables = sizeof(Routes);
-    // first launch: two workgroups a CU, or one per tile if there are fewer
-    const int64_t items = (int64_t)most * (a.inter / 16);
-    const int grid = (int)(items < 2 * cus ? items : 2 * cus);
-    const size_t lds = kWaves * UpRing::BYTES + kXBytes + tables + (size_t)a.t * a.top_k * 6;
+    // first launch: two workgroups a CU, one where that leaves a wave fewer than 8
+    // chunks (one token over 8 experts of 5120 x 8192: 16.8 us against 19.0; at 40
+    // chunks a wave, 92 against 90), or one per tile if there are fewer
+    const int64_t items = (int64_t)most * ((a.inter + 127) / 128 * 8);
+    const bool few = items * ((a.h + kChunk - 1) / kChunk) < 8 * (int64_t)(2 * cus * kWaves);
+    const int wgs = few ? cus : 2 * cus;
+    const int grid = (int)(items < wgs ? items : wgs);
+    const size_t lds = kWaves * UpRing::BYTES + kXBytes + kInvBytes + sizeof(Routes) + (size_t)a.t * a.top_k * 6;
     if (a.E <= 16) launch_up<1>(p, grid, lds, st);
     else if (a.E <= 64) launch_up<4>(p, grid, lds, st);
     else if (a.E <= 128) launch_up<8>(p, grid, lds, st);
     else launch_up<16>(p, grid, lds, st);
-    // second launch: two workgroups a CU as far as the partial sums have room
-    const int cols = (a.h + 127) / 128;
-    p.shares = 2 * cus / cols;
-    if (p.shares > 32) p.shares = 32;
-    if (p.shares > kMoePartRows / a.t) p.shares = kMoePartRows / a.t;
-    if (p.shares < 1) p.shares = 1;
-    // the ring's depth by what LDS has left beside the sums: two workgroups a CU up
-    // to 32 tokens, one with a deeper ring beyond
-    if (a.t <= 32) launch_down<4>(p, dim3((unsigned)cols, (unsigned)p.shares), tables, st);
-    else launch_down<8>(p, dim3((unsigned)cols, (unsigned)p.shares), tables, st);
+    const int shares = kMoePartRows / a.t < 32 ? kMoePartRows / a.t : 32;
+    if (a.t > 32 && (a.h + 255) / 256 * shares >= cus) launch_down<16>(p, cus, shares, st);
+    else launch_down<8>(p, cus, shares, st);
     return hipGetLastError();
 }
 

@@ -5,9 +5,18 @@
 // A wave works on fragments of 16 weight rows and 16 activation rows.  Lane l
 // (row r = l % 16, group g = l / 16) holds, per chunk of 128 columns, columns
 // 32 g .. 32 g + 31 of its weight row (16 bytes) and of its activation row,
-// and feeds four v_mfma_f32_16x16x32_bf16 slices from them: the same order of
+// and feeds four v_mfma_f32_16x16x32_f16 slices from them: the same order of
 // K on both operands.  The product lands with activation row l % 16 and weight
 // rows 4 (l / 16) .. + 3 in lane l.
+//
+// Why fp16: e2m1 times a ue4m3 scale is exact in it and takes half the
+// instructions that exact bf16 weights take (one conversion and one packed
+// multiplication for two codes).  The activations, bf16 or fp32, become fp16
+// when they are put into LDS, scaled by a power of two per row and chunk that
+// brings the largest of the 128 columns to [2^14, 2^15): a bf16 value keeps all
+// its bits down to 2^-29 of that largest one, and what lies below is off by less
+// than 2^-39 of it, far under the fp32 sums' own rounding.  The chunk's product
+// is scaled back as it is added to the fp32 accumulators.
 //
 // The weights come through LDS: every wave has a ring of K chunks of its own, into
 // which buffer loads write directly (no registers, no address arithmetic: the
@@ -15,6 +24,8 @@
 // load instruction takes 64 contiguous bytes of 16 rows, lane by lane; the
 // fragment is read from LDS in the matrix instruction's order.
 #pragma once
+
+#include <type_traits>
 
 #include "device_common.h"
 #include "gemm_common.h"
@@ -42,56 +53,132 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) { return (uint32_t)(
 
 // ---- activations in LDS ----------------------------------------------------
 // A workgroup's waves share the activation rows: `nr` rows of a block of chunks
-// sit in LDS, [chunk][nr][256 bytes], a row of a chunk in 16 pieces of 16 bytes (8
-// columns), piece q of row R in slot q ^ R, so that the 16 lanes of a read (one
-// piece of 16 rows) touch every bank once.  Loading the rows into each wave's
-// registers from memory instead makes them four of every five bytes in flight
-// in a CU and halves the rate at which weights arrive.
+// sit in LDS as fp16, [chunk][nr][256 bytes], a row of a chunk in 16 pieces of 16
+// bytes (8 columns), piece q of row R in slot q ^ R, so that the 16 lanes of a read
+// (one piece of 16 rows) touch every bank once; and their inverse scales,
+// [chunk][nr] floats.  Loading the rows into each wave's registers from memory
+// instead makes them four of every five bytes in flight in a CU and halves the
+// rate at which weights arrive.
 __device__ __forceinline__ int piece_off(int R, int q) { return R * 256 + ((q ^ R) & 15) * 16; }
 
-// One thread's part of a block, NV pieces of 16 bytes, on its way from memory to
-// LDS.  Local chunk lc of the block is chunk lo(lc) of K, or none where that is
-// negative; off(R) is the byte offset of row R in x.  Columns past K are zeros.
-template <int NV>
-struct XBlock {
-    u32x4 v[NV];
+// All-reduce over the 16 lanes of a DPP row: the neighbour in a pair, the other
+// pair of a quad, the mirrored quad of 8, the mirrored half of 16.
+template <typename T, typename F>
+__device__ __forceinline__ T row16(T v, F f) {
+    auto step = [&](auto ctl) {
+        const int o = __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctl)::value, 0xF, 0xF, true);
+        v = f(v, __builtin_bit_cast(T, o));
+    };
+    step(std::integral_constant<int, 0xB1>{});
+    step(std::integral_constant<int, 0x4E>{});
+    step(std::integral_constant<int, 0x141>{});
+    step(std::integral_constant<int, 0x140>{});
+    return v;
+}
+__device__ __forceinline__ float row16_max(float v) {
+    return row16(v, [](float a, float b) { return __builtin_fmaxf(a, b); });
+}
 
-    template <typename O, typename F>
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, O off, int nr, int nlc, int K, int t, int nt, F lo) {
+// One thread's part of a block on its way from memory to LDS: NV times 8 columns
+// of a row of a chunk, the 16 lanes of a DPP row having the chunk between them.
+// WIDE: x is fp32 and gives two rows, its high and its low fp16 half (the low one
+// `split` rows after the high one); otherwise x is bf16.
+template <int NV, bool WIDE>
+struct XBlock {
+    u32x4 v[NV][WIDE ? 2 : 1];
+    uint32_t vo[NV];   // byte offset of the columns in chunk 0 of x
+    int c0[NV], ce[NV];  // chunk of x at k0 = 0, end of its range (0: no part in the block)
+    int at[NV];        // local chunk and row: lc * nr + R
+    int row[NV];
+
+    // Local chunk lc of the block at k0 is chunk first(lc) + k0 of x, up to end(lc);
+    // off(R): byte offset of row R in x (rows loaded: nl); nr: rows in LDS.
+    template <typename O, typename F, typename E>
+    __device__ __forceinline__ void prepare(int nl, int nr, int nlc, int t, int nt, O off, F first, E end) {
 #pragma unroll
         for (int u = 0; u < NV; u++) {
-            const int i = t + u * nt, lc = i / (nr * 16), R = i % (nr * 16) >> 4;
-            const int c = lc < nlc ? lo(lc) : -1, col = c * kChunk + (i & 15) * 8;
-            v[u] = buf_load16(x, c >= 0 && col < K ? off(R) + 2 * col : kNoRow, 0);
+            const int i = t + u * nt, lc = i / (nl * 16), R = i % (nl * 16) >> 4;
+            c0[u] = first(lc);
+            ce[u] = lc < nlc ? end(lc) : 0;
+            vo[u] = off(R) + (i & 15) * (WIDE ? 32 : 16);
+            at[u] = lc * nr + R;
+            row[u] = R;
         }
     }
-    __device__ __forceinline__ void store(uint8_t* dst, int nr, int nlc, int t, int nt) const {
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t x, int k0, int K, int t) {
 #pragma unroll
         for (int u = 0; u < NV; u++) {
-            const int i = t + u * nt, lc = i / (nr * 16), R = i % (nr * 16) >> 4;
-            if (lc < nlc) *(u32x4*)(dst + lc * nr * 256 + piece_off(R, i & 15)) = v[u];
+            const int c = c0[u] + k0;
+            const bool in = c < ce[u] && c * kChunk + (t & 15) * 8 < K;  // columns past K are zeros
+#pragma unroll
+            for (int h = 0; h < (WIDE ? 2 : 1); h++)
+                v[u][h] = buf_load16(x, in ? vo[u] + (uint32_t)c * (WIDE ? 512 : 256) + 16 * h : kNoRow, 0);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* xs, float* inv, int split, int k0, int t) const {
+#pragma unroll
+        for (int u = 0; u < NV; u++) {
+            float f[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                f[i] = WIDE ? bits_f(v[u][(WIDE ? 1 : 0) * (i >> 2)][i & 3]) : i & 1 ? bf16_hi(v[u][0][i >> 1]) : bf16_lo(v[u][0][i >> 1]);
+            float m = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 8; i++) m = __builtin_fmaxf(m, __builtin_fabsf(f[i]));
+            m = row16_max(m);
+            // biased exponent of the largest value (255 for an infinity, whose row
+            // keeps its finite values finite), not below that of 2^-112
+            int e = (int)(f_bits(m) >> 23);
+            e = e < 15 ? 15 : e;
+            const float sc = bits_f((uint32_t)(127 + 14 + 127 - e) << 23);  // 2^(14 - exponent)
+#pragma unroll
+            for (int i = 0; i < 8; i++) f[i] *= sc;
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const auto hv = __builtin_amdgcn_cvt_pkrtz(f[2 * i], f[2 * i + 1]);
+                h[i] = __builtin_bit_cast(uint32_t, hv);
+                if (WIDE) {  // an infinity's low half is 0
+                    const float r0 = f[2 * i] - (float)hv[0], r1 = f[2 * i + 1] - (float)hv[1];
+                    l[i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(r0 == r0 ? r0 : 0.0f, r1 == r1 ? r1 : 0.0f));
+                }
+            }
+            if (c0[u] + k0 >= ce[u]) continue;
+            uint8_t* const d = xs + (at[u] - row[u]) * 256;
+            *(u32x4*)(d + piece_off(row[u], t & 15)) = u32x4{h[0], h[1], h[2], h[3]};
+            if (WIDE) *(u32x4*)(d + piece_off(row[u] + split, t & 15)) = u32x4{l[0], l[1], l[2], l[3]};
+            if ((t & 15) == 0) inv[at[u]] = bits_f((uint32_t)(e - 14) << 23);  // 2^(exponent - 14)
         }
     }
 };
 
-// The lane's addresses of its four pieces of a row in LDS (chunk 0 of a block).
+// The lane's addresses of its four pieces of row R in LDS (chunk 0 of a block), and
+// of the inverse scale of row Rs.
 struct XLane {
-    uint32_t a[4];
-    __device__ __forceinline__ void set(const uint8_t* xs, int R, int g) {
+    uint32_t a[4], s;
+    __device__ __forceinline__ void set(const uint8_t* xs, const float* inv, int R, int Rs, int g) {
 #pragma unroll
         for (int j = 0; j < 4; j++) a[j] = lds_addr(xs) + piece_off(R, 4 * g + j);
+        s = lds_addr(inv) + Rs * 4;
     }
-    // the lane's 32 columns of the chunk at byte `at` of the block
-    __device__ __forceinline__ void read(bf16x8 (&x)[4], int at) const {
+    // the lane's 32 columns of the chunk whose rows start at row `at` of the block
+    __device__ __forceinline__ void read(f16x8 (&x)[4], float& inv, int at) const {
         asm volatile(
-            "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\ts_waitcnt lgkmcnt(0)"
-            : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
-            : "v"(a[0] + at), "v"(a[1] + at), "v"(a[2] + at), "v"(a[3] + at)
+            "ds_read_b128 %0, %5\n\tds_read_b128 %1, %6\n\tds_read_b128 %2, %7\n\tds_read_b128 %3, %8\n\tds_read_b32 %4, %9\n\ts_waitcnt lgkmcnt(0)"
+            : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3]), "=&v"(inv)
+            : "v"(a[0] + at * 256), "v"(a[1] + at * 256), "v"(a[2] + at * 256), "v"(a[3] + at * 256), "v"(s + at * 4)
             : "memory");
     }
 };
 
 // ---- the weight ring of a wave ----------------------------------------------
+// Rows of a fragment: tile t takes rows 4 (t % 8) .. + 3 of each of the four 32-row
+// quarters of band t / 8 (128 rows).  The scale layout keeps those 16 rows' scales
+// of a column group in 64 contiguous bytes; of 16 consecutive rows they would be a
+// quarter of 256 bytes (read alone, codes and scales of 8 experts of 16384 x 5120:
+// 78.5 us with consecutive rows, 72.8 us with whole lines of scales).
+__device__ __forceinline__ int band_row(int tile, int r) { return (tile >> 3) * 128 + (r >> 2) * 32 + (tile & 7) * 4 + (r & 3); }
+
 // NF fragments of 16 weight rows, D chunks in LDS.  `aim` points the loads at a
 // matrix and rows, `issue` starts the load of a chunk into the next free slot,
 // `take` waits for the oldest one, and run through `consume` multiplies it.  The
@@ -113,24 +200,25 @@ struct W4Ring {
         const int r = lane & 15, g = lane >> 4;
         base = ring;
         rw = lds_addr(ring) + r * 64 + ((g ^ swz(r)) << 4);
-        rs = lds_addr(ring) + NF * 1024 + r * 8 + 2 * g;
+        rs = lds_addr(ring) + NF * 1024 + (g >> 1) * 64 + ((r & 3) * 4 + (r >> 2)) * 4 + (g & 1) * 2;
         head = tail = ahead = 0;
     }
-    // row0[f]: first row of fragment f
-    __device__ __forceinline__ void aim(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, const int (&row0)[NF], int rowb,
-                                        int cpa4, int lane) {
+    // Fragment f: rows first[f] + band_row(tile, 0 .. 15) of the matrix, those past
+    // the `rows` of its part read as the last one.
+    __device__ __forceinline__ void aim(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, const int (&first)[NF], int tile,
+                                        int rows, int rowb, int cpa4, int lane) {
         w = codes;
         s = scales;
         // codes: lane l loads row l / 4's slot l % 4, which holds piece (l % 4) ^ swz(row)
-        const int lr = lane >> 2;
+        const int lr = lane >> 2, x = band_row(tile, lr) < rows ? band_row(tile, lr) : rows - 1;
 #pragma unroll
-        for (int f = 0; f < NF; f++)
-            vw[f] = (uint32_t)(row0[f] + lr) * (uint32_t)rowb + (((lane & 3) ^ swz(lr)) << 4);
-        // scales: a dword (4 blocks) per fragment, row and column group of the chunk
-        // (NF = 1: the upper half of the wave loads the same again)
-        const int sr = (lane & 31) >> 1;
-        const int row = (NF == 2 && lane >= 32 ? row0[NF - 1] : row0[0]) + sr;
-        vs = (uint32_t)((row >> 7) * cpa4 * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (lane & 1) * 512);
+        for (int f = 0; f < NF; f++) vw[f] = (uint32_t)(first[f] + x) * (uint32_t)rowb + (((lane & 3) ^ swz(lr)) << 4);
+        // scales: a dword (4 blocks) per fragment, column group of the chunk and row,
+        // in the order of memory (NF = 1: the upper half of the wave loads the same
+        // again)
+        const int sr = (lane & 3) * 4 + (lane >> 2 & 3), y = band_row(tile, sr) < rows ? band_row(tile, sr) : rows - 1;
+        const int row = (NF == 2 && lane >= 32 ? first[NF - 1] : first[0]) + y;
+        vs = (uint32_t)((row >> 7) * cpa4 * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (lane >> 4 & 1) * 512);
     }
     __device__ __forceinline__ void issue(int c) {
         lds_byte* const dst = (lds_byte*)base + head * SLOT;
@@ -164,38 +252,44 @@ struct W4Ring {
 
 // acc[f][i] += fragment f times activation tile i over the chunks [b0, b1) of a
 // ring; next() starts the load of the chunk that comes after those under way, if
-// there is one.  x: the lane's rows, chunk b0 at byte x_at, a chunk every x_step
-// bytes.  WHOLE: K is a multiple of 128; otherwise the scales of blocks past K
-// count as zero (their codes may be the next row's).
+// there is one.  x: the lane's rows, chunk b0 at row `at` of the block, a chunk
+// every `step` rows.  WHOLE: K is a multiple of 128; otherwise the scales of blocks
+// past K count as zero (their codes may be the next row's).
 template <int XT, bool WHOLE, int NF, int D, typename F>
-__device__ __forceinline__ void consume(W4Ring<NF, D>& ring, f32x4 (&acc)[NF][XT], const XLane (&x)[XT], int x_at, int x_step, int b0,
+__device__ __forceinline__ void consume(W4Ring<NF, D>& ring, f32x4 (&acc)[NF][XT], const XLane (&x)[XT], int at, int step, int b0,
                                         int b1, int g, int K, F next) {
     for (int c = b0; c < b1; c++) {
         u32x4 cw[NF];
         uint32_t cs[NF];
         ring.take(cw, cs);
         next();
-        bf16x8 xv[XT][4];
+        f16x8 xv[XT][4];
+        float inv[XT];
 #pragma unroll
-        for (int i = 0; i < XT; i++) x[i].read(xv[i], x_at);
-        x_at += x_step;
+        for (int i = 0; i < XT; i++) x[i].read(xv[i], inv[i], at);
+        at += step;
         if (!WHOLE) {
             const int left = K - c * kChunk - 32 * g;
             const uint32_t keep = left >= 32 ? 0xFFFFu : left >= 16 ? 0xFFu : 0u;
 #pragma unroll
             for (int f = 0; f < NF; f++) cs[f] &= keep;
         }
+        f32x4 t[NF][XT];
 #pragma unroll
         for (int f = 0; f < NF; f++) {
-            const float s0 = __builtin_amdgcn_cvt_f32_fp8(cs[f], 0), s1 = __builtin_amdgcn_cvt_f32_fp8(cs[f], 1);
+            const f16x2 s2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(cs[f], 1.0f, false);
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const bf16x8 wv = dequant8_bf16(word(cw[f], j), j < 2 ? s0 : s1);
+                const f16x8 wv = dequant8(word(cw[f], j), s2[j >> 1]);
 #pragma unroll
                 for (int i = 0; i < XT; i++)
-                    acc[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, xv[i][j], acc[f][i], 0, 0, 0);
+                    t[f][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wv, xv[i][j], j ? t[f][i] : f32x4{0, 0, 0, 0}, 0, 0, 0);
             }
         }
+#pragma unroll
+        for (int f = 0; f < NF; f++)
+#pragma unroll
+            for (int i = 0; i < XT; i++) acc[f][i] += t[f][i] * inv[i];
     }
 }
 

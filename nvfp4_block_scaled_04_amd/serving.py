@@ -41,7 +41,7 @@ _lib = _load()
 
 def moe_small_ws_bytes(t, top_k, h, inter):
     """NVFP4_MOE_SMALL_WS_BYTES: workspace bytes of nvfp4_moe_small."""
-    return 4 * t * top_k * inter + 4096 * h + 4096 + h // 4
+    return 4 * t * top_k * inter + 4096 + (4096 * 4 + 1) * ((h + 127) // 128 * 32)
 
 
 def adapters_ws_bytes(m, r, split_tail=False):

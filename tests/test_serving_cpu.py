@@ -43,7 +43,7 @@ MOE = dict(x=P, t=4, h=64, logits=P, dt=1, E=8, k=2, score=0, renorm=1, w13=P, s
     ({"dt": 2}, DTYPE), ({"t": 0}, SHAPE), ({"t": -1}, SHAPE), ({"t": 65}, UNSUP), ({"E": 0}, SHAPE), ({"E": 257}, UNSUP),
     ({"k": 0}, SHAPE), ({"k": 9}, SHAPE), ({"E": 64, "k": 17}, UNSUP), ({"h": 0}, SHAPE), ({"h": 40}, SHAPE),
     ({"inter": 8}, SHAPE), ({"inter": 0}, SHAPE), ({"score": 2}, UNSUP), ({"h": 1 << 24, "inter": 256}, UNSUP),
-    ({"wsb": 4 * 4 * 2 * 32 + 4096 * 64 + 4096 + 16 - 1}, SHAPE), ({"x": P + 8}, MISAL), ({"w13": P + 4}, MISAL), ({"w2": P + 8}, MISAL),
+    ({"wsb": 4 * 4 * 2 * 32 + 4096 + 4096 * 128 + 32 - 1}, SHAPE), ({"x": P + 8}, MISAL), ({"w13": P + 4}, MISAL), ({"w2": P + 8}, MISAL),
     ({"sf13": P + 8}, MISAL), ({"sf2": P + 8}, MISAL), ({"logits": P + 4}, MISAL), ({"out": P + 2}, MISAL),
     ({"ws": P + 8}, MISAL), ({"ids": P + 2}, MISAL), ({"wts": P + 1}, MISAL), ({"al13": P + 2}, MISAL), ({"al2": P + 3}, MISAL),
 ])
