@@ -75,8 +75,9 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
                     int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace the adapter calls need: the rows' projections onto their
- * adapters' r ranks, fp32. */
-#define NVFP4_ADAPTERS_WS_BYTES(m, r) (((int64_t)(m) * (int64_t)(r) * 4 + 255) / 256 * 256)
+ * adapters' r ranks, fp32, and counters.  With NVFP4_GEMM_WS_BYTES (nvfp4.h) more
+ * they spread a product over more workgroups, whose partial sums go there. */
+#define NVFP4_ADAPTERS_WS_BYTES(m, r) (((int64_t)(m) * (int64_t)(r) * 4 + 255) / 256 * 256 + 8192)
 
 /* Largest adapter rank (NVFP4_BAD_RANK beyond it). */
 #define NVFP4_ADAPTERS_MAX_RANK 256
@@ -88,16 +89,21 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
  *                    + scaling[a] * (x[i] @ lora_a[a]^T) @ lora_b[a]^T (+ bias)),
  * the adapter's term left out where adapter[i] is outside [0, n_adapters) (-1
  * by custom).  Rows may use any adapters in any order; each distinct adapter of
- * 16 consecutive rows is read once for them.  The projection onto the ranks is
- * summed and kept in fp32 and enters the second product as two bf16 halves.
+ * 16 consecutive rows (64 beyond 32 rows) is read once for them.  The projection
+ * onto the ranks is summed and kept in fp32 and enters the second product as two
+ * bf16 halves (2^-16 of it).  Results are the same on every call (no atomic sums).
+ * Non-finite values of a row or an adapter reach the rows that hold or use them.
  *   x: [m, k] bf16; b: [n, k/2]; b_sf: swizzled scales; alpha: [1] fp32.
  *   lora_a: [n_adapters, r, k] bf16; lora_b: [n_adapters, n, r] bf16 (adapters of
  *   lower rank padded with zeros); adapter: [m] int32; scaling: NULL (1.0) or
  *   [n_adapters] fp32; bias: NULL or [n] bf16; out: [m, n] bf16.
  *   workspace: workspace_bytes >= NVFP4_ADAPTERS_WS_BYTES(m, r), 16-byte aligned,
- *   contents ignored on entry; calls that share one must not overlap.
+ *   contents ignored on entry; calls that share one must not overlap.  With
+ *   NVFP4_GEMM_WS_BYTES more the K axis of more than 16 rows is split over
+ *   workgroups (the same results but for the order of the fp32 sums).
  * Requires m, n >= 1, n_adapters >= 1, k >= 16, k % 16 == 0, r in 8 .. 256 and a
- * multiple of 8 (NVFP4_BAD_RANK).  Any m works; for many rows quantize the
+ * multiple of 8 (NVFP4_BAD_RANK), n * r below 2^32 and k at most 2^23
+ * (NVFP4_UNSUPPORTED).  Any m up to 2^20 works; for many rows quantize the
  * activation and use nvfp4_gemm_adapters.
  */
 int nvfp4_linear_adapters(const void *x, const uint8_t *b, const uint8_t *b_sf, const float *alpha,

@@ -63,17 +63,17 @@ __device__ __forceinline__ int row_adapter(const GParams& p, int64_t m) {
     return a >= 0 && a < p.ad_n ? a : -1;
 }
 
-// Eight fp32 values (32-byte aligned to 16) as two bf16 fragments hi + lo, the
-// sum within 2^-16 of the value.
-__device__ __forceinline__ void load_split8(const float* src, bf16x8& hi, bf16x8& lo) {
-    const f32x4 a = *(const f32x4*)src, b = *(const f32x4*)(src + 4);
+// Eight fp32 values as two bf16 fragments hi + lo, the sum within 2^-16 of the value
+// (zeros where not `on`).
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, bool on, bf16x8& hi, bf16x8& lo) {
     uint32_t h[4], l[4];
     split_bf16x2(a[0], a[1], h[0], l[0]);
     split_bf16x2(a[2], a[3], h[1], l[1]);
     split_bf16x2(b[0], b[1], h[2], l[2]);
     split_bf16x2(b[2], b[3], h[3], l[3]);
-    hi = __builtin_bit_cast(bf16x8, u32x4{h[0], h[1], h[2], h[3]});
-    lo = __builtin_bit_cast(bf16x8, u32x4{l[0], l[1], l[2], l[3]});
+    const u32x4 z = {0u, 0u, 0u, 0u};
+    hi = __builtin_bit_cast(bf16x8, on ? u32x4{h[0], h[1], h[2], h[3]} : z);
+    lo = __builtin_bit_cast(bf16x8, on ? u32x4{l[0], l[1], l[2], l[3]} : z);
 }
 
 // Waves per SIMD each configuration is compiled for: a 128x128 wave tile
@@ -589,28 +589,61 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
             if (a < 0) break;
 #pragma unroll
             for (int i = 0; i < FM; i++) rem[i] &= ~(uint32_t)__ballot(id[i] == a);
+            // rows that do not share it keep their sums by selection, not by a product
+            // with zeros: its values may be infinite or NaN.  (Not needed where all do.)
+            bool all = true;
+#pragma unroll
+            for (int i = 0; i < FM; i++)
+                if (KS == 1 || i == grp) all = all && (uint32_t)__ballot(id[i] == a) == 0xFFFFFFFFu;
+            const uint16_t* const lb = p.ad_b + (int64_t)a * p.N * p.r;
+            uint32_t ob[FN], od[FM];  // element offsets of the lane's rows (r <= 256: 32 bits hold a matrix's 2^24 rows)
+#pragma unroll
+            for (int i = 0; i < FN; i++) {
+                const int64_t row = n0 + wn * WN + i * 32 + l32;
+                ob[i] = (uint32_t)((row < p.N ? row : p.N - 1) * p.r);
+            }
+#pragma unroll
+            for (int i = 0; i < FM; i++) {
+                const int64_t row = m0 + wm * WM + i * 32 + l32;
+                od[i] = (uint32_t)((row < p.M ? row : p.M - 1) * p.r);
+            }
+            // 16 ranks at a time, every load of a step under way together
             for (int kr = 0; kr < p.r; kr += 16) {
                 const bool in_r = kr + h * 8 < p.r;  // r is a multiple of 8
+                const int k = in_r ? kr + h * 8 : p.r - 8;
+                u32x4 bv[FN];
+                f32x4 dv[FM][2];
+#pragma unroll
+                for (int i = 0; i < FN; i++) bv[i] = *(const u32x4*)(lb + ob[i] + k);
+#pragma unroll
+                for (int i = 0; i < FM; i++)
+                    if (KS == 1 || i == grp) {
+                        dv[i][0] = *(const f32x4*)(p.ad_d + od[i] + k);
+                        dv[i][1] = *(const f32x4*)(p.ad_d + od[i] + k + 4);
+                    }
                 bf16x8 hi[FM], lo[FM];
 #pragma unroll
-                for (int i = 0; i < FM; i++) {
-                    hi[i] = lo[i] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
-                    if (in_r && id[i] == a)
-                        load_split8(p.ad_d + (m0 + wm * WM + i * 32 + l32) * p.r + kr + h * 8, hi[i], lo[i]);
-                }
+                for (int i = 0; i < FM; i++)
+                    if (KS == 1 || i == grp) split8(dv[i][0], dv[i][1], in_r && id[i] == a, hi[i], lo[i]);
 #pragma unroll
                 for (int i = 0; i < FN; i++) {
-                    int64_t row = n0 + wn * WN + i * 32 + l32;
-                    row = row < p.N ? row : p.N - 1;
-                    u32x4 v = {0u, 0u, 0u, 0u};
-                    if (in_r) v = *(const u32x4*)(p.ad_b + ((int64_t)a * p.N + row) * p.r + kr + h * 8);
-                    const bf16x8 ol = __builtin_bit_cast(bf16x8, v);
+                    const bf16x8 ol = __builtin_bit_cast(bf16x8, in_r ? bv[i] : u32x4{0u, 0u, 0u, 0u});
 #pragma unroll
-                    for (int im = 0; im < FM; im++)
-                        if (KS == 1 || im == grp) {
+                    for (int im = 0; im < FM; im++) {
+                        if (KS == 2 && im != grp) continue;
+                        if (all) {
                             acc[i][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[im], acc[i][im], 0, 0, 0);
                             acc[i][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[im], acc[i][im], 0, 0, 0);
+                        } else {
+                            f32x16 z;
+#pragma unroll
+                            for (int v = 0; v < 16; v++) z[v] = 0.0f;
+                            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[im], z, 0, 0, 0);
+                            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[im], z, 0, 0, 0);
+#pragma unroll
+                            for (int v = 0; v < 16; v++) acc[i][im][v] += id[im] == a ? z[v] : 0.0f;
                         }
+                    }
                 }
             }
         }
@@ -1012,10 +1045,13 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
                 bf16x8 hi = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u}), lo = hi, ol = hi;
                 if (kr + g * 8 < p.r) {
                     ol = __builtin_bit_cast(bf16x8, *(const u32x4*)(p.ad_b + ((int64_t)a * p.N + brow) * p.r + kr + g * 8));
-                    if (id == a) load_split8(p.ad_d + (m0 + r) * p.r + kr + g * 8, hi, lo);
+                    const float* const d = p.ad_d + (id == a ? m0 + r : 0) * p.r + kr + g * 8;
+                    split8(*(const f32x4*)d, *(const f32x4*)(d + 4), id == a, hi, lo);
                 }
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, acc, 0, 0, 0);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, acc, 0, 0, 0);
+                f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, acc, 0, 0, 0);
+                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, t, 0, 0, 0);
+#pragma unroll
+                for (int v = 0; v < 4; v++) acc[v] = id == a ? t[v] : acc[v];  // the others' by selection
             }
         }
     }

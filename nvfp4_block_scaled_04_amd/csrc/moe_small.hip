@@ -278,7 +278,7 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
         const float a13 = p.alpha13[e], a2 = p.alpha2[e];
         ring.aim(make_rsrc(p.w13 + (int64_t)e * 2 * p.I * rowb, (uint32_t)(2 * p.I * rowb)),
                  make_rsrc(p.w13_sf + (int64_t)e * p.w13_sfsz, (uint32_t)p.w13_sfsz),
-                 {0, p.I}, live ? tile : 0, p.I, rowb, cpa4, lane);
+                 {0, p.I}, {p.I, 2 * p.I}, live ? tile : 0, 0, rowb, cpa4, lane);
         // XT tiles of 16 tokens at a time, the first of them the m0-th
         auto pass = [&](auto xt, int m0) {
             constexpr int XT = decltype(xt)::value;
@@ -417,7 +417,7 @@ __global__ __launch_bounds__(64 * NW, 4) void k_moe_down(EParams p) {
         if (!live || aimed.at > last) return;
         const int e = act_expert(act_of(aimed.at));
         ring.aim(make_rsrc(p.w2 + (int64_t)e * p.H * rowb, (uint32_t)(p.H * rowb)),
-                 make_rsrc(p.w2_sf + (int64_t)e * p.w2_sfsz, (uint32_t)p.w2_sfsz), {0}, tile, p.H, rowb, cpa4, lane);
+                 make_rsrc(p.w2_sf + (int64_t)e * p.w2_sfsz, (uint32_t)p.w2_sfsz), {0}, {p.H}, tile, 0, rowb, cpa4, lane);
         ca = begin_of(aimed.at);
         ce = end_of(aimed.at);
     };

@@ -203,21 +203,25 @@ struct W4Ring {
         rs = lds_addr(ring) + NF * 1024 + (g >> 1) * 64 + ((r & 3) * 4 + (r >> 2)) * 4 + (g & 1) * 2;
         head = tail = ahead = 0;
     }
-    // Fragment f: rows first[f] + band_row(tile, 0 .. 15) of the matrix, those past
-    // the `rows` of its part read as the last one.
-    __device__ __forceinline__ void aim(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, const int (&first)[NF], int tile,
-                                        int rows, int rowb, int cpa4, int lane) {
+    // Fragment f: rows first[f] + band_row(tile, 0 .. 15) of the matrix, those from
+    // end[f] on read as the last one before it; the codes' offsets count from row0.
+    __device__ __forceinline__ void aim(__amdgpu_buffer_rsrc_t codes, __amdgpu_buffer_rsrc_t scales, const int (&first)[NF],
+                                        const int (&end)[NF], int tile, int row0, int rowb, int cpa4, int lane) {
         w = codes;
         s = scales;
         // codes: lane l loads row l / 4's slot l % 4, which holds piece (l % 4) ^ swz(row)
-        const int lr = lane >> 2, x = band_row(tile, lr) < rows ? band_row(tile, lr) : rows - 1;
+        const int lr = lane >> 2;
 #pragma unroll
-        for (int f = 0; f < NF; f++) vw[f] = (uint32_t)(first[f] + x) * (uint32_t)rowb + (((lane & 3) ^ swz(lr)) << 4);
+        for (int f = 0; f < NF; f++) {
+            const int x = first[f] + band_row(tile, lr);
+            vw[f] = (uint32_t)((x < end[f] ? x : end[f] - 1) - row0) * (uint32_t)rowb + (((lane & 3) ^ swz(lr)) << 4);
+        }
         // scales: a dword (4 blocks) per fragment, column group of the chunk and row,
         // in the order of memory (NF = 1: the upper half of the wave loads the same
         // again)
-        const int sr = (lane & 3) * 4 + (lane >> 2 & 3), y = band_row(tile, sr) < rows ? band_row(tile, sr) : rows - 1;
-        const int row = (NF == 2 && lane >= 32 ? first[NF - 1] : first[0]) + y;
+        const int f = NF == 2 && lane >= 32 ? NF - 1 : 0;
+        int row = first[f] + band_row(tile, (lane & 3) * 4 + (lane >> 2 & 3));
+        row = row < end[f] ? row : end[f] - 1;
         vs = (uint32_t)((row >> 7) * cpa4 * 512 + (row & 31) * 16 + ((row & 127) >> 5) * 4 + (lane >> 4 & 1) * 512);
     }
     __device__ __forceinline__ void issue(int c) {

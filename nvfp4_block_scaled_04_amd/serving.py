@@ -44,10 +44,10 @@ def moe_small_ws_bytes(t, top_k, h, inter):
     return 4 * t * top_k * inter + 4096 + (4096 * 4 + 1) * ((h + 127) // 128 * 32)
 
 
-def adapters_ws_bytes(m, r, split_tail=False):
-    """NVFP4_ADAPTERS_WS_BYTES: workspace bytes of the adapter calls; with
-    split_tail, what nvfp4_gemm_adapters needs for the split-tail schedule."""
-    return (m * r * 4 + 255) // 256 * 256 + (_ops.GEMM_WS_BYTES if split_tail else 0)
+def adapters_ws_bytes(m, r, split=False):
+    """NVFP4_ADAPTERS_WS_BYTES: workspace bytes of the adapter calls; with split,
+    also room for the partial sums of products spread over more workgroups."""
+    return (m * r * 4 + 255) // 256 * 256 + 8192 + (_ops.GEMM_WS_BYTES if split else 0)
 
 
 def _workspace(workspace, need, dev):
@@ -135,7 +135,9 @@ def nvfp4_linear_adapters(x, b, b_sf, alpha, lora_a, lora_b, adapter, scaling=No
     scale), lora_a: [L, r, k] and lora_b: [L, n, r] bf16, adapter: [m] int32 (a
     row's adapter; outside [0, L): none), scaling: [L] fp32 or None -> out [m, n]
     bf16 = alpha * x @ dequant(b)^T + scaling * (x @ lora_a^T) @ lora_b^T (+bias).
-    For decode (few rows); each row has its own adapter, in any order."""
+    For decode (few rows); each row has its own adapter, in any order.  workspace:
+    adapters_ws_bytes(m, r, split=True) bytes (allocated when None), or without
+    split, where few workgroups then walk the whole K axis."""
     _dims(b, "b", 2)
     n = b.shape[0]
     m, k, r, L = _adapters(x, lora_a, lora_b, adapter, scaling, bias, n)
@@ -144,7 +146,7 @@ def nvfp4_linear_adapters(x, b, b_sf, alpha, lora_a, lora_b, adapter, scaling=No
         raise ValueError(f"b must be [n, {k // 2}] packed FP4, got {tuple(b.shape)}")
     if out is None:
         out = torch.empty(m, n, dtype=torch.bfloat16, device=dev)
-    workspace = _workspace(workspace, adapters_ws_bytes(m, r), dev)
+    workspace = _workspace(workspace, adapters_ws_bytes(m, r, workspace is None), dev)
     _dev(b, "b", BYTES, n * (k // 2), dev)
     _dev(b_sf, "b_sf", BYTES, sf_size(n, k), dev)
     _dev(alpha, "alpha", F32, 1, dev)
@@ -160,8 +162,8 @@ def nvfp4_gemm_adapters(a, b, a_sf, b_sf, alpha, x, lora_a, lora_b, adapter, sca
                         workspace=None):
     """The same beside the block-scaled NVFP4 product, for prefill: a: [m, k/2]
     and a_sf, the quantized x, with alpha = 1 / (gs_a * gs_b); x: [m, k] bf16 for
-    the adapters.  With a workspace of adapters_ws_bytes(m, r, split_tail=True)
-    bytes the GEMM takes the split-tail schedule."""
+    the adapters.  With a workspace of adapters_ws_bytes(m, r, split=True) bytes
+    (as by default) the GEMM takes the split-tail schedule."""
     _dims(a, "a", 2)
     _dims(b, "b", 2)
     n = b.shape[0]
@@ -172,7 +174,7 @@ def nvfp4_gemm_adapters(a, b, a_sf, b_sf, alpha, x, lora_a, lora_b, adapter, sca
                          f"{tuple(b.shape)}")
     if out is None:
         out = torch.empty(m, n, dtype=torch.bfloat16, device=dev)
-    workspace = _workspace(workspace, adapters_ws_bytes(m, r), dev)
+    workspace = _workspace(workspace, adapters_ws_bytes(m, r, workspace is None), dev)
     _ops._operands(a, b, a_sf, b_sf, 1, m, n, k, dev, sf_size)
     _dev(alpha, "alpha", F32, 1, dev)
     _dev(out, "out", BF16, m * n, dev)

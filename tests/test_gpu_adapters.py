@@ -66,13 +66,17 @@ DECODE = [  # m, n, k, r, L, ids, scaling, bias
     (64, 272, 1024, 136, 2, "none", True, True),
     (65, 80, 256, 16, 9, "mixed", True, True),
     (200, 144, 384, 72, 33, "runs", True, False),
+    (48, 1048, 2576, 200, 30, "each", True, True),
+    (64, 520, 4096, 64, 64, "each", True, False),
+    (31, 256, 128, 8, 3, "wild", False, True),
 ]
 
 
+@pytest.mark.parametrize("split", [False, True])
 @pytest.mark.parametrize("m,n,k,r,L,ids,scaled,biased", DECODE)
-def test_decode(mods, m, n, k, r, L, ids, scaled, biased):
+def test_decode(mods, m, n, k, r, L, ids, scaled, biased, split):
     serving, _ = mods
-    say("linear_adapters", m, n, k, r, L, ids)
+    say("linear_adapters", m, n, k, r, L, ids, split)
     g = gen(m + n + k)
     p = pool(g, m, n, k, r, L, ids)
     s = p["scaling"] if scaled else None
@@ -82,7 +86,7 @@ def test_decode(mods, m, n, k, r, L, ids, scaled, biased):
     bias = torch.randn(n, device="cuda", generator=g).bfloat16() if biased else None
     out = fresh(m, n)
     serving.nvfp4_linear_adapters(x, b, sf, alpha, p["lora_a"], p["lora_b"], p["adapter"], scaling=s, bias=bias, out=out,
-                                  workspace=workspace(serving.adapters_ws_bytes(m, r)))
+                                  workspace=workspace(serving.adapters_ws_bytes(m, r, split)))
     w = R.dequant(b, sf)
     ref, bound = R.adapters(x.double() @ w.t() * alpha.double(), x.double().abs() @ w.abs().t() * alpha.double(), k, x,
                             p["lora_a"], p["lora_b"], p["adapter"], s, bias)
@@ -253,3 +257,28 @@ def test_refusals(mods):
         f(x, b, sf, alpha, la12, lb12, ad, out=out)
     torch.cuda.synchronize()
     assert bool((out == 5).all())
+
+
+@pytest.mark.parametrize("m", [20, 64, 300, 2048])
+def test_non_finite_adapter_stays_with_its_rows(mods, m):
+    """An adapter whose second matrix holds NaN or inf reaches the rows that use it
+    only, though other rows of the same tile are multiplied beside them."""
+    serving, _ = mods
+    say("adapters: non-finite lora_b", m)
+    g = gen(12)
+    n, k, r, L = 272, 256, 24, 6
+    p = pool(g, m, n, k, r, L, "mixed")
+    b, b_sf, a, a_sf = R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k), R.rand_fp4(g, m, k=k), R.rand_sf(g, m, k)
+    alpha = torch.full((1,), 3e-4, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    calls = [lambda: serving.nvfp4_gemm_adapters(a, b, a_sf, b_sf, alpha, x, p["lora_a"], p["lora_b"], p["adapter"])]
+    if m <= 300:
+        calls.append(lambda: serving.nvfp4_linear_adapters(x, b, b_sf, alpha, p["lora_a"], p["lora_b"], p["adapter"]))
+    good = [f() for f in calls]
+    p["lora_b"][2, 5, 3] = float("nan")
+    p["lora_b"][4, :, 20] = float("inf")
+    rows = (p["adapter"] != 2) & (p["adapter"] != 4)
+    for f, want in zip(calls, good):
+        out = f()
+        assert torch.equal(out[rows], want[rows])
+        assert out[p["adapter"] == 2][:, 5].isnan().all() and not out[p["adapter"] == 4].isfinite().any()
