@@ -75,9 +75,9 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
                     int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace the adapter calls need: the rows' projections onto their
- * adapters' r ranks, fp32, and counters.  With NVFP4_GEMM_WS_BYTES (nvfp4.h) more
- * they spread a product over more workgroups, whose partial sums go there. */
-#define NVFP4_ADAPTERS_WS_BYTES(m, r) (((int64_t)(m) * (int64_t)(r) * 4 + 255) / 256 * 256 + 8192)
+ * adapters' r ranks, fp32.  With NVFP4_GEMM_WS_BYTES (nvfp4.h) more they spread
+ * a product over more workgroups, whose partial sums go there. */
+#define NVFP4_ADAPTERS_WS_BYTES(m, r) (((int64_t)(m) * (int64_t)(r) * 4 + 255) / 256 * 256)
 
 /* Largest adapter rank (NVFP4_BAD_RANK beyond it). */
 #define NVFP4_ADAPTERS_MAX_RANK 256
@@ -99,8 +99,8 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
  *   [n_adapters] fp32; bias: NULL or [n] bf16; out: [m, n] bf16.
  *   workspace: workspace_bytes >= NVFP4_ADAPTERS_WS_BYTES(m, r), 16-byte aligned,
  *   contents ignored on entry; calls that share one must not overlap.  With
- *   NVFP4_GEMM_WS_BYTES more the K axis of more than 16 rows is split over
- *   workgroups (the same results but for the order of the fp32 sums).
+ *   NVFP4_GEMM_WS_BYTES more the K axis may be split over workgroups (the same
+ *   results but for the order of the fp32 sums).
  * Requires m, n >= 1, n_adapters >= 1, k >= 16, k % 16 == 0, r in 8 .. 256 and a
  * multiple of 8 (NVFP4_BAD_RANK), n * r below 2^32 and k at most 2^23
  * (NVFP4_UNSUPPORTED).  Any m up to 2^20 works; for many rows quantize the
@@ -119,8 +119,8 @@ int nvfp4_linear_adapters(const void *x, const uint8_t *b, const uint8_t *b_sf, 
  * t = adapter[i].  The adapters' term is added to the GEMM's fp32 accumulators
  * before the output is written; a row without an adapter comes out as
  * nvfp4_gemm's (nvfp4_gemm_ws's), bit for bit.
- *   a: [m, k/2], a_sf: its scales; alpha: [1] fp32 = 1 / (gs_a * gs_b); the rest
- *   as nvfp4_linear_adapters.
+ *   a: [m, k/2], a_sf: its scales; alpha: [1] fp32 = 1 / (gs_a * gs_b); the rest,
+ *   and the limits, as nvfp4_linear_adapters.
  *   workspace: as there; with NVFP4_ADAPTERS_WS_BYTES(m, r) + NVFP4_GEMM_WS_BYTES
  *   bytes or more the GEMM takes the split-tail schedule of nvfp4_gemm_ws.
  */

@@ -442,8 +442,7 @@ int nvfp4_moe_small(const void* x, int64_t t, int64_t h, const void* logits, int
     return launch_status(nvfp4::launch_moe_small(a, (hipStream_t)stream));
 }
 
-static_assert(NVFP4_ADAPTERS_WS_BYTES(1, 64) == 256 + nvfp4::kAdCounters * 4 && nvfp4::kAdPartBytes == NVFP4_GEMM_WS_BYTES,
-              "the workspace holds d, the counters and the partial sums");
+static_assert(nvfp4::kAdPartBytes == NVFP4_GEMM_WS_BYTES, "the workspace holds the partial sums");
 
 // The adapters' own arguments, and the workspace that holds d.
 static int adapters_check(const void* x, const void* lora_a, const void* lora_b, const int32_t* adapter,
@@ -454,7 +453,8 @@ static int adapters_check(const void* x, const void* lora_a, const void* lora_b,
     if (!dim_ok(m) || !dim_ok(n) || !dim_ok(n_adapters) || k < 16 || k % 16 != 0 || k > kMaxDim)
         return NVFP4_BAD_SHAPE;
     if ((m + 15) / 16 > 65535) return NVFP4_BAD_SHAPE;
-    if (n * r >= (int64_t)1 << 32) return NVFP4_UNSUPPORTED;  // 32-bit offsets into one adapter's matrix
+    // 32-bit offsets into one adapter's B, and into 64 rows of x, A or the weight
+    if (n * r >= (int64_t)1 << 32 || k > ((int64_t)1 << 23)) return NVFP4_UNSUPPORTED;
     if (workspace_bytes < NVFP4_ADAPTERS_WS_BYTES(m, r)) return NVFP4_BAD_SHAPE;
     if (!aligned16(x) || !aligned16(lora_a) || !aligned16(lora_b) || !aligned16(workspace) ||
         ((uintptr_t)adapter & 3u) || ((uintptr_t)scaling & 3u))
@@ -472,8 +472,7 @@ static nvfp4::AdapterArgs adapter_args(const void* x, const void* lora_a, const 
     return a;
 }
 
-// The workspace: d; the counters; and, where it is large enough, the partial sums.
-static int64_t adapter_d_bytes(int64_t m, int64_t r) { return (m * r * 4 + 255) / 256 * 256; }
+// The workspace: d, and, where it is large enough, the partial sums.
 static void* adapter_parts(void* workspace, int64_t workspace_bytes, int64_t m, int64_t r) {
     const int64_t own = NVFP4_ADAPTERS_WS_BYTES(m, r);
     return workspace_bytes >= own + NVFP4_GEMM_WS_BYTES ? (char*)workspace + own : nullptr;
@@ -487,12 +486,10 @@ int nvfp4_linear_adapters(const void* x, const uint8_t* b, const uint8_t* b_sf, 
     const int st = adapters_check(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace,
                                   workspace_bytes);
     if (st != NVFP4_OK) return st;
-    // 32-bit offsets into 64 weight rows and 64 activation rows
-    if (k > ((int64_t)1 << 23) || !gemm_sf_ok(n, k / 16)) return NVFP4_UNSUPPORTED;
+    if (!gemm_sf_ok(n, k / 16)) return NVFP4_UNSUPPORTED;
     if (!aligned16(b) || !aligned16(b_sf) || !aligned16(out) || ((uintptr_t)alpha & 3u) || (bias && !aligned16(bias)))
         return NVFP4_MISALIGNED;
-    nvfp4::AdapterArgs a = adapter_args(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace);
-    a.counters = (int32_t*)((char*)workspace + adapter_d_bytes(m, r));
+    const nvfp4::AdapterArgs a = adapter_args(x, lora_a, lora_b, adapter, scaling, m, n, k, r, n_adapters, workspace);
     const hipError_t e = nvfp4::launch_adapter_down(a, (hipStream_t)stream);
     if (e != hipSuccess) return launch_status(e);
     return launch_status(nvfp4::launch_w4a16_adapters(a, b, b_sf, alpha, (const uint16_t*)bias, (uint16_t*)out,

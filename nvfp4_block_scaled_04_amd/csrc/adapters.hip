@@ -44,9 +44,8 @@ struct AParams {
     int64_t M, N, K;
     int R, L;
     int cpa4, nblk;
-    // k_w4_wide: partial sums and counters of the workgroups that share a tile
+    // k_w4_wide: partial sums of the workgroups that share a tile
     float* part;
-    int32_t* arrived;
     int shares;
 };
 
@@ -84,19 +83,84 @@ __device__ __forceinline__ void split8(f32x4 a, f32x4 b, bool on, bf16x8& hi, bf
     lo = __builtin_bit_cast(bf16x8, on ? u32x4{l[0], l[1], l[2], l[3]} : z);
 }
 
+// A wave's ring of slices in LDS: NT tiles of 16 bf16 rows, 32 columns (64 bytes)
+// a slice, D slices.  A load instruction takes 64 contiguous bytes of a row in four
+// neighbouring lanes; taken straight into the matrix instruction's lanes (one row
+// each) the same bytes come from L2 at a third of the rate (35 against 106 KB/us
+// and CU).
+template <int NT, int D>
+struct RowRing {
+    static_assert(NT <= 6, "operands of take");
+    static constexpr int SLOT = NT * 1024, BYTES = D * SLOT;
+    __amdgpu_buffer_rsrc_t src[NT];
+    uint32_t vo[NT];  // the lane's source offset
+    uint32_t rd;      // the lane's LDS address in slot 0
+    uint8_t* base;
+    int head, tail, ahead;
+
+    __device__ __forceinline__ void init(uint8_t* ring, int lane) {
+        base = ring;
+        rd = lds_addr(ring) + (lane & 15) * 64 + (((lane >> 4) ^ swz(lane & 15)) << 4);
+        head = tail = ahead = 0;
+    }
+    // rows of tile i: `rows` rows of K columns at `p` (past them: the last one); a
+    // lane that is not `on` gets zeros and reads nothing, by an offset past the
+    // source's end (16 rows of 2^24 bytes at most, and no sum with a slice's
+    // offset wraps)
+    __device__ __forceinline__ void aim(int i, const uint16_t* p, int rows, int64_t K, int lane, bool on = true) {
+        const int lr = lane >> 2, row = lr < rows ? lr : rows - 1;
+        src[i] = make_rsrc(p, (uint32_t)(rows * K * 2));
+        vo[i] = on ? (uint32_t)(row * K * 2) + (((lane & 3) ^ swz(lr)) << 4) : 0x80000000u;
+    }
+    __device__ __forceinline__ void issue(int s) {
+        lds_byte* const dst = (lds_byte*)base + head * SLOT;
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(src[i], (__attribute__((address_space(3))) void*)(dst + i * 1024), 16, vo[i], s * 64, 0, 0);
+        head = head + 1 == D ? 0 : head + 1;
+        ahead++;
+    }
+    __device__ __forceinline__ void take(bf16x8 (&v)[NT]) {
+        if (ahead == D) wait_vmcnt<(D - 1) * NT>();
+        else wait_vmcnt<0>();
+        const uint32_t a = rd + tail * SLOT;
+        if constexpr (NT == 2)
+            asm volatile("ds_read_b128 %0, %2\n\tds_read_b128 %1, %2 offset:1024\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0]), "=&v"(v[1]) : "v"(a) : "memory");
+        else if constexpr (NT == 3)
+            asm volatile("ds_read_b128 %0, %3\n\tds_read_b128 %1, %3 offset:1024\n\tds_read_b128 %2, %3 offset:2048\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]) : "v"(a) : "memory");
+        else if constexpr (NT == 4)
+            asm volatile("ds_read_b128 %0, %4\n\tds_read_b128 %1, %4 offset:1024\n\tds_read_b128 %2, %4 offset:2048\n\t"
+                         "ds_read_b128 %3, %4 offset:3072\n\ts_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]) : "v"(a) : "memory");
+        else {
+            static_assert(NT == 6, "operands");
+            asm volatile("ds_read_b128 %0, %6\n\tds_read_b128 %1, %6 offset:1024\n\tds_read_b128 %2, %6 offset:2048\n\t"
+                         "ds_read_b128 %3, %6 offset:3072\n\tds_read_b128 %4, %6 offset:4096\n\tds_read_b128 %5, %6 offset:5120\n\t"
+                         "s_waitcnt lgkmcnt(0)"
+                         : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]) : "v"(a) : "memory");
+        }
+        tail = tail + 1 == D ? 0 : tail + 1;
+        ahead--;
+    }
+};
+
 // Workgroup (group of 16 RT ranks x, tile of 16 TT rows y, share z of the tile's
 // distinct adapters): K split over NW waves, slices of 32 columns.  Many rows
 // take TT = 2: an adapter's A is then read once per 32 rows.
-template <int RT, int TT, int NW>
+template <int RT, int TT, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
-    __shared__ f32x4 part[NW][RT * TT][64];
+    constexpr int NT = RT + TT;
+    typedef RowRing<NT, D> Ring;
+    static_assert(Ring::BYTES >= RT * TT * 1024, "the partial sums take the rings' place");
+    __shared__ __align__(16) uint8_t rings[NW * Ring::BYTES];
+    f32x4* const part = (f32x4*)rings;  // [NW][RT * TT][64]
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int r = lane & 15, g = lane >> 4;
     const int64_t m0 = (int64_t)blockIdx.y * (16 * TT);
-    if (p.arrived && blockIdx.x + blockIdx.y + blockIdx.z == 0)  // for the product that follows
-        for (int i = t; i < kAdCounters; i += 64 * NW) p.arrived[i] = 0;
     int id[TT];         // adapter of the lane's row of each 16
     uint32_t rem = 0;   // rows of the tile not yet served
 #pragma unroll
@@ -113,6 +177,8 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
             if (m0 + 16 * i + r < p.M && id[i] < 0)
                 for (int c = p0 + g; c < p0 + 16 * RT && c < p.R; c += 4) p.d[(m0 + 16 * i + r) * p.R + c] = 0.0f;
     }
+    Ring ring;
+    ring.init(rings + wave * Ring::BYTES, lane);
     for (int j = 0; rem; j++) {
         const int lead = __builtin_ctz(rem);
         int a = __builtin_amdgcn_readlane(id[0], lead & 15);
@@ -120,58 +186,50 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 #pragma unroll
         for (int i = 0; i < TT; i++) rem &= ~((uint32_t)(__ballot(id[i] == a) & 0xFFFF) << (16 * i));
         if (j % (int)gridDim.z != (int)blockIdx.z) continue;
-        f32x4 acc[RT][TT];
-        const uint16_t* A[RT];
-        const uint16_t* X[TT];
 #pragma unroll
         for (int i = 0; i < RT; i++) {
-            const int c = p0 + 16 * i + r < p.R ? p0 + 16 * i + r : p.R - 1;  // past R: never stored
-            A[i] = p.la + ((int64_t)a * p.R + c) * p.K + 8 * g;
-#pragma unroll
-            for (int q = 0; q < TT; q++) acc[i][q] = f32x4{0, 0, 0, 0};
+            const int c = p0 + 16 * i < p.R ? p0 + 16 * i : p.R - 1;  // past R: never stored
+            ring.aim(i, p.la + ((int64_t)a * p.R + c) * p.K, p.R - c < 16 ? p.R - c : 16, p.K, lane);
         }
 #pragma unroll
-        for (int i = 0; i < TT; i++) X[i] = p.x + (id[i] == a ? m0 + 16 * i + r : 0) * p.K + 8 * g;
-        constexpr int U = RT + TT <= 2 ? 8 : RT + TT <= 4 ? 5 : 3;  // slices whose loads are in flight together
-        for (int sb = s0; sb < s1; sb += U) {
-            u32x4 xv[U][TT], av[U][RT];
+        for (int i = 0; i < TT; i++) {
+            const int64_t first = m0 + 16 * i < p.M ? m0 + 16 * i : p.M - 1;
+            // other adapters' rows, and those past M, are zeros
+            ring.aim(RT + i, p.x + first * p.K, (int)(p.M - first < 16 ? p.M - first : 16), p.K, lane, __shfl(id[i], lane >> 2) == a);
+        }
+        f32x4 acc[RT][TT];
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                const int s = sb + u < s1 ? sb + u : s1 - 1;  // past the range: reload, never used
-                const bool in = 32 * s + 8 * g < p.K;
+        for (int i = 0; i < RT; i++)
 #pragma unroll
-                for (int i = 0; i < TT; i++) {
-                    xv[u][i] = u32x4{0, 0, 0, 0};
-                    if (in && id[i] == a) xv[u][i] = *(const u32x4*)(X[i] + 32 * s);
-                }
+            for (int q = 0; q < TT; q++) acc[i][q] = f32x4{0, 0, 0, 0};
+        __syncthreads();  // the previous adapter's sums are read
 #pragma unroll
-                for (int i = 0; i < RT; i++) {
-                    av[u][i] = u32x4{0, 0, 0, 0};
-                    if (in) av[u][i] = *(const u32x4*)(A[i] + 32 * s);
-                }
+        for (int u = 0; u < D; u++)
+            if (s0 + u < s1) ring.issue(s0 + u);
+        for (int s = s0; s < s1; s++) {
+            bf16x8 v[NT];
+            ring.take(v);
+            if (s + D < s1) ring.issue(s + D);
+            if (32 * s + 8 * g >= p.K) {  // past K (K % 32 == 16): the next row's, or nothing
+#pragma unroll
+                for (int i = 0; i < NT; i++) v[i] = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u});
             }
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                if (sb + u >= s1) break;
+            for (int i = 0; i < RT; i++)
 #pragma unroll
-                for (int i = 0; i < RT; i++)
-#pragma unroll
-                    for (int q = 0; q < TT; q++)
-                        acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                            __builtin_bit_cast(bf16x8, av[u][i]), __builtin_bit_cast(bf16x8, xv[u][q]), acc[i][q], 0, 0, 0);
-            }
+                for (int q = 0; q < TT; q++) acc[i][q] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v[i], v[RT + q], acc[i][q], 0, 0, 0);
         }
         // the waves' partial sums, in wave order; lane: row r, ranks 4 g .. 4 g + 3
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < RT; i++)
 #pragma unroll
-            for (int q = 0; q < TT; q++) part[wave][i * TT + q][lane] = acc[i][q];
+            for (int q = 0; q < TT; q++) part[(wave * RT * TT + i * TT + q) * 64 + lane] = acc[i][q];
         __syncthreads();
         if (wave < RT * TT) {
-            f32x4 s = part[0][wave][lane];
+            f32x4 s = part[wave * 64 + lane];
 #pragma unroll
-            for (int v = 1; v < NW; v++) s += part[v][wave][lane];
+            for (int v = 1; v < NW; v++) s += part[(v * RT * TT + wave) * 64 + lane];
             const int c = p0 + 16 * (wave / TT) + 4 * g, q = wave % TT;
             const bool mine = (TT == 2 && q ? id[TT - 1] : id[0]) == a;
             if (mine && c < p.R) *(f32x4*)(p.d + (m0 + 16 * q + r) * p.R + c) = s * (p.scaling ? p.scaling[a] : 1.0f);  // R % 8 == 0
@@ -180,13 +238,13 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 #endif
 }
 
-// Weight-only product of up to 16 rows and 16 weight rows, the K chunks split over
-// the waves, and so are the rows' distinct adapters, whose loads come first (the
-// first weight loads are under way meanwhile).
-template <bool WHOLE>
+// Weight-only product of up to 16 TT rows and 16 weight rows, the K chunks split
+// over the waves, and so are the rows' distinct adapters, whose loads come first
+// (the first weight loads are under way meanwhile).
+template <int TT, bool WHOLE>
 __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
-    __shared__ f32x4 part[kAdWaves][64];
+    __shared__ f32x4 part[kAdWaves][TT][64];
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int r = lane & 15, g = lane >> 4;
@@ -195,12 +253,17 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
     const int rowb = (int)(p.K / 2);
     const uint8_t* const B = p.b + brow * rowb + g * 16;
     const uint8_t* const F = p.b_sf + scale_byte_off(brow, 2 * g, p.cpa4);
-    const uint16_t* const X = r < p.M ? p.x + r * p.K + 32 * g : nullptr;
-    const int id = adapter_of(p, r);
+    const uint16_t* X[TT];
+    int id[TT];
+#pragma unroll
+    for (int i = 0; i < TT; i++) {
+        X[i] = 16 * i + r < p.M ? p.x + (16 * i + r) * p.K + 32 * g : nullptr;
+        id[i] = adapter_of(p, 16 * i + r);
+    }
     const int nch = (int)((p.K + kChunk - 1) / kChunk);
     const int c0 = nch * wave / kAdWaves, c1 = nch * (wave + 1) / kAdWaves;
-    constexpr int U = 4;  // chunks whose loads are in flight together
-    u32x4 w[U], xv[U][4];
+    constexpr int U = TT == 1 ? 4 : 2;  // chunks whose loads are in flight together
+    u32x4 w[U], xv[U][TT][4];
     uint32_t s[U];
     auto load_w = [&](int cb) {
 #pragma unroll
@@ -219,66 +282,79 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
         }
     };
     load_w(c0);
-    f32x4 ad = {0, 0, 0, 0};
-    uint32_t rem = (uint32_t)(__ballot(id >= 0) & 0xFFFF);
-    for (int turn = 0; rem; turn++) {
-        const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(rem));
-        rem &= ~(uint32_t)__ballot(id == a);
-        if (turn % kAdWaves != wave) continue;
-        const uint16_t* const LB = p.lb + ((int64_t)a * p.N + brow) * p.R + 8 * g;
-        const float* const D = p.d + (id == a ? r : 0) * p.R + 8 * g;
-        for (int k0 = 0; k0 < p.R; k0 += 32) {
-            const bool in = k0 + 8 * g < p.R;
-            const int k = in ? k0 : 0;
-            const u32x4 bv = *(const u32x4*)(LB + k - (in ? 0 : 8 * g));
-            const f32x4 d0 = *(const f32x4*)(D + k - (in ? 0 : 8 * g)), d1 = *(const f32x4*)(D + k - (in ? 0 : 8 * g) + 4);
-            bf16x8 hi, lo;
-            split8(d0, d1, in && id == a, hi, lo);
-            const bf16x8 ol = __builtin_bit_cast(bf16x8, in ? bv : u32x4{0, 0, 0, 0});
-            f32x4 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, f32x4{0, 0, 0, 0}, 0, 0, 0);
-            z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, z, 0, 0, 0);
+    f32x4 ad[TT];
+    int turn = 0;  // distinct adapters seen, over all 16-row tiles
 #pragma unroll
-            for (int v = 0; v < 4; v++) ad[v] += id == a ? z[v] : 0.0f;
+    for (int i = 0; i < TT; i++) {
+        ad[i] = f32x4{0, 0, 0, 0};
+        uint32_t rem = (uint32_t)(__ballot(id[i] >= 0) & 0xFFFF);
+        for (; rem; turn++) {
+            const int a = __builtin_amdgcn_readlane(id[i], __builtin_ctz(rem));
+            const bool mine = id[i] == a;
+            rem &= ~(uint32_t)__ballot(mine);
+            if (turn % kAdWaves != wave) continue;
+            const uint16_t* const LB = p.lb + ((int64_t)a * p.N + brow) * p.R;
+            const float* const D = p.d + (mine ? 16 * i + r : 0) * p.R;
+            for (int k0 = 0; k0 < p.R; k0 += 32) {
+                const bool in = k0 + 8 * g < p.R;
+                const int k = in ? k0 + 8 * g : 0;
+                const u32x4 bv = *(const u32x4*)(LB + k);
+                bf16x8 hi, lo;
+                split8(*(const f32x4*)(D + k), *(const f32x4*)(D + k + 4), in && mine, hi, lo);
+                const bf16x8 ol = __builtin_bit_cast(bf16x8, in ? bv : u32x4{0, 0, 0, 0});
+                f32x4 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, f32x4{0, 0, 0, 0}, 0, 0, 0);
+                z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, z, 0, 0, 0);
+#pragma unroll
+                for (int v = 0; v < 4; v++) ad[i][v] += mine ? z[v] : 0.0f;
+            }
         }
     }
-    f32x4 acc = {0, 0, 0, 0};
+    f32x4 acc[TT];
+#pragma unroll
+    for (int i = 0; i < TT; i++) acc[i] = f32x4{0, 0, 0, 0};
     for (int cb = c0; cb < c1; cb += U) {
         if (cb != c0) load_w(cb);
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const int c = cb + u < c1 ? cb + u : c1 - 1, left = (int)p.K - c * kChunk - 32 * g;
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                xv[u][j] = u32x4{0, 0, 0, 0};
-                if (X && (WHOLE || left > 8 * j)) xv[u][j] = *(const u32x4*)(X + c * kChunk + 8 * j);
-            }
+            for (int i = 0; i < TT; i++)
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    xv[u][i][j] = u32x4{0, 0, 0, 0};
+                    if (X[i] && (WHOLE || left > 8 * j)) xv[u][i][j] = *(const u32x4*)(X[i] + c * kChunk + 8 * j);
+                }
         }
 #pragma unroll
         for (int u = 0; u < U; u++) {
             if (cb + u >= c1) break;
             const float f0 = __builtin_amdgcn_cvt_f32_fp8(s[u], 0), f1 = __builtin_amdgcn_cvt_f32_fp8(s[u], 1);
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(dequant8_bf16(word(w[u], j), j < 2 ? f0 : f1),
-                                                              __builtin_bit_cast(bf16x8, xv[u][j]), acc, 0, 0, 0);
+            for (int j = 0; j < 4; j++) {
+                const bf16x8 wv = dequant8_bf16(word(w[u], j), j < 2 ? f0 : f1);
+#pragma unroll
+                for (int i = 0; i < TT; i++)
+                    acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv, __builtin_bit_cast(bf16x8, xv[u][i][j]), acc[i], 0, 0, 0);
+            }
         }
     }
-    // the waves' partial sums, in wave order
-    part[wave][lane] = acc * p.alpha[0] + ad;
-    __syncthreads();
-    if (wave != 0 || r >= p.M) return;
-    f32x4 y = part[0][lane];
+    // the waves' partial sums, in wave order; wave i takes row tile i
 #pragma unroll
-    for (int v = 1; v < kAdWaves; v++) y += part[v][lane];
-    store4(p, r, n0 + 4 * g, y);
+    for (int i = 0; i < TT; i++) part[wave][i][lane] = acc[i] * p.alpha[0] + ad[i];
+    __syncthreads();
+    if (wave >= TT || 16 * wave + r >= p.M) return;
+    f32x4 y = part[0][wave][lane];
+#pragma unroll
+    for (int v = 1; v < kAdWaves; v++) y += part[v][wave][lane];
+    store4(p, 16 * wave + r, n0 + 4 * g, y);
 #endif
 }
 
 // Weight-only product of 16 XT rows and 256 columns, a share of the K axis and of
 // the rows' distinct adapters: a wave has 32 columns to itself (two fragments, 128
-// columns apart), the waves share x in LDS.  Of several workgroups of one tile
-// each leaves its sums in memory and the last to finish adds them, wave by wave, in
-// the order of the shares.
+// columns apart), the waves share x in LDS.  Where several workgroups share a tile,
+// each leaves its sums in memory for k_wide_sum (a launch more; the last of them
+// adding all took 12 us for 64 rows of 12 shares).
 constexpr int kWideX = 32 << 10;  // LDS for x: 2 chunks of 64 rows; and 64 ranks of d
 constexpr int kWideD = 68;        // floats of a row of d there (64 ranks, padded)
 typedef W4Ring<2, 3> WideRing;
@@ -438,39 +514,35 @@ __global__ __launch_bounds__(64 * kAdWaves, 2) void k_w4_wide(AParams p) {
             if (shares == 1) put(f, i, acc[f][i]);
         }
     if (shares == 1) return;
-    // device-scope stores and loads (sc1) pass by the XCDs' own L2s; the stores are
-    // waited for before the count
-    constexpr int kDevice = 16, kWave = 2 * XT * 1024;  // bytes of a wave's sums
-    const int64_t place = ((int64_t)blockIdx.z * gridDim.x + blockIdx.x) * kAdWaves + wave;
-    const __amdgpu_buffer_rsrc_t part = make_rsrc((uint8_t*)p.part + place * shares * kWave, (uint32_t)(shares * kWave));
-#pragma unroll
-    for (int f = 0; f < 2; f++)
-#pragma unroll
-        for (int i = 0; i < XT; i++)
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[f][i]), part,
-                                                   share * kWave + (f * XT + i) * 1024 + lane * 16, 0, kDevice);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    int before = 0;
-    if (lane == 0) before = __hip_atomic_fetch_add(&p.arrived[place], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (__builtin_amdgcn_readfirstlane(before) != shares - 1) return;
-    asm volatile("" ::: "memory");
+    // its sums of the rows, [share][row][N rounded up to 4]
+    const int64_t np = (p.N + 3) / 4 * 4;
 #pragma unroll
     for (int f = 0; f < 2; f++)
 #pragma unroll
         for (int i = 0; i < XT; i++) {
-            f32x4 y = {0, 0, 0, 0};
-            constexpr int U = 16;  // loads in flight together
-            for (int v0 = 0; v0 < shares; v0 += U) {
-                u32x4 v[U];
-#pragma unroll
-                for (int u = 0; u < U; u++)  // past the last share: past the resource, zeros
-                    v[u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                         part, (v0 + u) * kWave + (f * XT + i) * 1024 + lane * 16, 0, kDevice));
-#pragma unroll
-                for (int u = 0; u < U; u++) y += __builtin_bit_cast(f32x4, v[u]);
-            }
-            put(f, i, y);
+            const int n = n0 + 128 * f + band_row(wave, 4 * g);
+            if (16 * i + r < nr && n < N) *(f32x4*)(p.part + ((int64_t)share * p.M + m0 + 16 * i + r) * np + n) = acc[f][i];
         }
+#endif
+}
+
+// The shares' sums, in their order, four columns a thread.
+__global__ __launch_bounds__(256) void k_wide_sum(AParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int64_t np4 = (p.N + 3) / 4, all = p.M * np4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= all) return;
+    const f32x4* const P = (const f32x4*)p.part + i;
+    f32x4 y = {0, 0, 0, 0};
+    constexpr int U = 16;  // loads in flight together
+    for (int v0 = 0; v0 < p.shares; v0 += U) {
+        f32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) v[u] = v0 + u < p.shares ? P[(v0 + u) * all] : f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < U; u++) y += v[u];
+    }
+    store4(p, i / np4, i % np4 * 4, y);
 #endif
 }
 
@@ -486,53 +558,78 @@ AParams params(const AdapterArgs& a) {
 }  // namespace
 
 hipError_t launch_adapter_down(const AdapterArgs& a, hipStream_t st) {
-    AParams p = params(a);
-    p.arrived = a.counters;
+    const AParams p = params(a);
     const unsigned ranks = (unsigned)((a.r + 15) / 16);
     if (a.m <= 64) {
         // few rows: a workgroup per 16 ranks and distinct adapter, since the
         // adapters' reads are the work
-        k_adapter_down<1, 1, 16><<<dim3(ranks, (unsigned)((a.m + 15) / 16), a.m < 16 ? (unsigned)a.m : 16u), 1024, 0, st>>>(p);
+        k_adapter_down<1, 1, 16, 4><<<dim3(ranks, (unsigned)((a.m + 15) / 16), a.m < 16 ? (unsigned)a.m : 16u), 1024, 0, st>>>(p);
         return hipGetLastError();
     }
     // many rows: up to four tiles of ranks on one read of x, an adapter's A once per
-    // 32 rows, and two workgroups share a row tile's adapters (a prompt's end falls
-    // inside a tile)
-    const unsigned rows = (unsigned)((a.m + 31) / 32);
-    if (ranks == 1) k_adapter_down<1, 2, 16><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
-    else if (ranks == 2) k_adapter_down<2, 2, 16><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
-    else k_adapter_down<4, 2, 8><<<dim3((ranks + 3) / 4, rows, 2), 512, 0, st>>>(p);
+    // 32 rows where those still give every CU a tile, and two workgroups share a row
+    // tile's adapters (a prompt's end falls inside a tile)
+    const bool wide = (a.m + 31) / 32 >= 256;
+    const unsigned rows = (unsigned)((a.m + (wide ? 31 : 15)) / (wide ? 32 : 16));
+    if (wide) {
+        if (ranks == 1) k_adapter_down<1, 2, 16, 3><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
+        else if (ranks == 2) k_adapter_down<2, 2, 16, 2><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
+        else k_adapter_down<4, 2, 8, 3><<<dim3((ranks + 3) / 4, rows, 2), 512, 0, st>>>(p);
+    } else {
+        if (ranks == 1) k_adapter_down<1, 1, 16, 4><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
+        else if (ranks <= 3) k_adapter_down<2, 1, 16, 3><<<dim3((ranks + 1) / 2, rows, 2), 1024, 0, st>>>(p);
+        else k_adapter_down<3, 1, 16, 2><<<dim3((ranks + 2) / 3, rows, 2), 1024, 0, st>>>(p);
+    }
     return hipGetLastError();
 }
 
 template <int XT>
-static void launch_wide(AParams p, int cus, bool split, hipStream_t st) {
-    const int cols = (int)((p.N + 255) / 256), rows = (int)((p.M + 16 * XT - 1) / (16 * XT)), nch = (int)((p.K + kChunk - 1) / kChunk);
-    // one workgroup a CU; a share has 2 chunks at least
-    p.shares = split && cols * rows * kAdWaves <= kAdCounters ? cus / (cols * rows) : 1;
-    if (p.shares > nch / 2) p.shares = nch / 2;
-    if (p.shares < 1) p.shares = 1;
+static void launch_wide(AParams p, int cus, hipStream_t st) {
+    const int64_t cols = (p.N + 255) / 256, rows = (p.M + 16 * XT - 1) / (16 * XT), nch = (p.K + kChunk - 1) / kChunk;
+    // one workgroup a CU, as far as the partial sums have room; a share has 2
+    // chunks at least
+    int64_t shares = p.part ? cus / (cols * rows) : 1;
+    const int64_t room = kAdPartBytes / (p.M * ((p.N + 3) / 4 * 16));
+    if (shares > room) shares = room;
+    if (shares > nch / 2) shares = nch / 2;
+    p.shares = (int)(shares < 1 ? 1 : shares);
     const dim3 grid((unsigned)cols, (unsigned)p.shares, (unsigned)rows);
     if (p.K % kChunk == 0) k_w4_wide<XT, true><<<grid, 64 * kAdWaves, 0, st>>>(p);
     else k_w4_wide<XT, false><<<grid, 64 * kAdWaves, 0, st>>>(p);
+    if (p.shares > 1) k_wide_sum<<<dim3((unsigned)((p.M * ((p.N + 3) / 4) + 255) / 256)), 256, 0, st>>>(p);
+}
+
+template <int TT>
+static void launch_narrow(const AParams& p, hipStream_t st) {
+    const dim3 grid((unsigned)((p.N + 15) / 16));
+    if (p.K % kChunk == 0) k_w4a16_adapters<TT, true><<<grid, 64 * kAdWaves, 0, st>>>(p);
+    else k_w4a16_adapters<TT, false><<<grid, 64 * kAdWaves, 0, st>>>(p);
 }
 
 hipError_t launch_w4a16_adapters(const AdapterArgs& a, const uint8_t* b, const uint8_t* b_sf, const float* alpha,
                                  const uint16_t* bias, uint16_t* out, float* part, hipStream_t st) {
     AParams p = params(a);
     p.b = b; p.b_sf = b_sf; p.alpha = alpha; p.bias = bias; p.out = out;
-    p.part = part; p.arrived = a.counters;
+    p.part = part;
     const int cus = device_cus();
     if (cus <= 0) return hipErrorInvalidDevice;
-    if (a.m <= 16) {
-        const dim3 grid((unsigned)((p.N + 15) / 16));
-        if (p.K % kChunk == 0) k_w4a16_adapters<true><<<grid, 64 * kAdWaves, 0, st>>>(p);
-        else k_w4a16_adapters<false><<<grid, 64 * kAdWaves, 0, st>>>(p);
-    } else if (a.m <= 32) {
-        launch_wide<2>(p, cus, part != nullptr, st);
-    } else {
-        launch_wide<4>(p, cus, part != nullptr, st);
+    // Small weights: 16 columns a workgroup, whose waves read the rows themselves
+    // (one launch, no sums between workgroups).  It is ahead while every workgroup is
+    // resident at once and a wave's K range is one step of loads; larger weights
+    // take the shared tiles.  us, this form against the tiles: 16 rows, 1024 x 1024
+    // 6.8 : 10.2, 4096 x 4096 9.0 : 14.0, 8192 x 4096 14.2 : 16.2, 5120 x 8192 24.2 :
+    // 16.2, 16384 x 1024 23.4 : 13.4; 32 rows, 2048 x 2048 6.9 : 12.6, 4096 x 4096
+    // 13.0 : 17.9, 8192 x 4096 21.8 : 20.4; 64 rows, 4096 x 4096 21.5 : 26.0,
+    // 8192 x 4096 40.8 : 27.9.  (The rule gives away up to 2.6 us for 1 to 16 rows
+    // of a weight of few columns and 8192 in K: 2048 x 8192, 1 row, 8.4 : 11.0.)
+    if (a.m <= 64 && a.k <= 4 * kAdWaves * kChunk && a.n <= (a.m <= 16 ? 8192 : 4096)) {
+        if (a.m <= 16) launch_narrow<1>(p, st);
+        else if (a.m <= 32) launch_narrow<2>(p, st);
+        else launch_narrow<4>(p, st);
     }
+    else if (a.m <= 16) launch_wide<1>(p, cus, st);
+    else if (a.m <= 32) launch_wide<2>(p, cus, st);
+    else launch_wide<4>(p, cus, st);
     return hipGetLastError();
 }
 

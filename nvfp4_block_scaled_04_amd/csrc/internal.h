@@ -140,13 +140,10 @@ struct AdapterArgs {
     const float* scaling;    // [n_adapters] or null
     float* d;                // [m, r]: scaling * x @ lora_a[adapter]^T (0 without one)
     int64_t m, n, k, r, n_adapters;
-    int32_t* counters = nullptr;  // kAdCounters of them, or null
 };
-// Counters of the decode product's shared tiles (one per wave of a tile), and the
-// bytes of their partial sums: at most 512 tiles of 64 rows x 256 columns.
-constexpr int kAdCounters = 2048;
+// Bytes of the decode product's partial sums.
 constexpr int64_t kAdPartBytes = kGemmWsBytes;
-// Writes d and clears the counters.
+// Writes d.
 hipError_t launch_adapter_down(const AdapterArgs& a, hipStream_t st);
 // out = alpha * x @ dequant(b)^T + d @ lora_b[adapter]^T (+ bias).  part:
 // kAdPartBytes, or null (a workgroup then walks the whole K axis).

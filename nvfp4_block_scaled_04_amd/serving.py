@@ -47,7 +47,7 @@ def moe_small_ws_bytes(t, top_k, h, inter):
 def adapters_ws_bytes(m, r, split=False):
     """NVFP4_ADAPTERS_WS_BYTES: workspace bytes of the adapter calls; with split,
     also room for the partial sums of products spread over more workgroups."""
-    return (m * r * 4 + 255) // 256 * 256 + 8192 + (_ops.GEMM_WS_BYTES if split else 0)
+    return (m * r * 4 + 255) // 256 * 256 + (_ops.GEMM_WS_BYTES if split else 0)
 
 
 def _workspace(workspace, need, dev):

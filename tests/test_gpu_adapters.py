@@ -69,6 +69,16 @@ DECODE = [  # m, n, k, r, L, ids, scaling, bias
     (48, 1048, 2576, 200, 30, "each", True, True),
     (64, 520, 4096, 64, 64, "each", True, False),
     (31, 256, 128, 8, 3, "wild", False, True),
+    (3, 24, 4240, 16, 3, "each", True, False),          # shared tiles: K beyond one step
+    (16, 8210, 400, 40, 9, "mixed", True, True),        # and more columns than workgroups
+    (31, 300, 4128, 24, 9, "mixed", False, True),
+    (24, 4100, 256, 72, 5, "each", True, False),
+    (64, 260, 5136, 136, 70, "each", True, True),
+    (47, 4104, 640, 16, 4, "wild", True, False),
+    (8200, 24, 48, 16, 5, "runs", True, False),         # projections of many rows: 32-row tiles
+    (8193, 40, 272, 32, 40, "mixed", True, True),
+    (8225, 16, 144, 200, 6, "runs", False, False),
+    (300, 40, 336, 56, 9, "each", True, False),         # 16-row tiles, 4 tiles of ranks
 ]
 
 

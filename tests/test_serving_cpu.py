@@ -51,15 +51,16 @@ def test_moe_small_validation(serving, change, status):
     assert serving._lib.nvfp4_moe_small(*{**MOE, **change}.values()) == status
 
 
-LIN = dict(x=P, b=P, sf=P, alpha=P, la=P, lb=P, ad=P, sc=None, bias=None, out=P, m=4, n=32, k=64, r=16, L=3, ws=P, wsb=256 + 8192,
+LIN = dict(x=P, b=P, sf=P, alpha=P, la=P, lb=P, ad=P, sc=None, bias=None, out=P, m=4, n=32, k=64, r=16, L=3, ws=P, wsb=256,
            stream=None)
 GEMM = dict(a=P, b=P, asf=P, sf=P, alpha=P, x=P, la=P, lb=P, ad=P, sc=None, bias=None, out=P, m=4, n=32, k=64, r=16, L=3,
-            ws=P, wsb=256 + 8192, stream=None)
+            ws=P, wsb=256, stream=None)
 COMMON = [
     *[({n: None}, NULLP) for n in ("x", "b", "sf", "alpha", "la", "lb", "ad", "out", "ws")],
     ({"r": 0}, RANK), ({"r": -8}, RANK), ({"r": 12}, RANK), ({"r": 264}, RANK), ({"m": 0}, SHAPE), ({"n": 0}, SHAPE),
-    ({"k": 8}, SHAPE), ({"k": 72}, SHAPE), ({"L": 0}, SHAPE), ({"wsb": 255 + 8192}, SHAPE), ({"m": 1 << 21, "wsb": 1 << 40}, SHAPE),
-    ({"n": 1 << 24, "k": 1 << 12}, UNSUP), ({"n": 1 << 29, "k": 16}, UNSUP), ({"x": P + 8}, MISAL), ({"la": P + 8}, MISAL), ({"lb": P + 2}, MISAL),
+    ({"k": 8}, SHAPE), ({"k": 72}, SHAPE), ({"L": 0}, SHAPE), ({"wsb": 255}, SHAPE), ({"m": 1 << 21, "wsb": 1 << 40}, SHAPE),
+    ({"n": 1 << 24, "k": 1 << 12}, UNSUP), ({"n": 1 << 29, "k": 16}, UNSUP), ({"k": (1 << 23) + 16}, UNSUP),
+    ({"x": P + 8}, MISAL), ({"la": P + 8}, MISAL), ({"lb": P + 2}, MISAL),
     ({"ad": P + 2}, MISAL), ({"sc": P + 2}, MISAL), ({"bias": P + 2}, MISAL), ({"ws": P + 4}, MISAL), ({"b": P + 8}, MISAL),
     ({"sf": P + 8}, MISAL), ({"alpha": P + 2}, MISAL), ({"out": P + 8}, MISAL),
 ]
