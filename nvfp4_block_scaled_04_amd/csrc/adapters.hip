@@ -4,17 +4,17 @@
 // (The prefill product is the block-scaled GEMM's adapter epilogue, gemm.hip.)
 //
 // What is computed, a = adapter[i] (none outside [0, L)):
-//   d[i, :]   = scaling[a] * x[i] @ A[a]^T                      (k_adapter_down)
+//   d[i, :]   = scaling[a] * x[i] @ A[a]^T                     (k_adapter_down)
 //   out[i, :] = alpha * x[i] @ dequant(W)^T + d[i] @ B[a]^T (+ bias)
 //
 // Rows may use any adapters in any order.  A wave finds the distinct adapters of
 // its rows by ballots over their ids: the first row not yet served names one, all
 // rows that share it are served together.  So an adapter is read once per tile of
 // rows, whatever the order, and rows without one cost nothing.  The other rows of
-// the tile are multiplied beside them (as zeros, an adapter's values may be
-// infinite), and their products are left out by selection.  d stays in fp32 and
-// enters the second product as two bf16 halves (2^-16 of d); the adapters' own
-// bf16 values are exact.
+// the tile are multiplied beside them and their products left out by selection (an
+// adapter's values may be infinite).  d is summed in fp32 and kept as two bf16
+// halves (2^-16 of d, no more bytes than fp32, and the second product takes them as
+// they are); the adapters' own bf16 values are exact.
 //
 // Bound: for decode the weight and the adapters that the batch uses, each read
 // once; the projections are short, so their parts are spread over as many waves
@@ -40,7 +40,7 @@ struct AParams {
     const float* scaling;      // [L] or null
     const uint16_t* bias;      // [N] or null
     uint16_t* out;             // [M, N]
-    float* d;                  // [M, R]
+    uint16_t* d;               // [M, 2, R]
     int64_t M, N, K;
     int R, L;
     int cpa4, nblk;
@@ -71,16 +71,10 @@ __device__ __forceinline__ void store4(const AParams& p, int64_t m, int64_t n, f
     }
 }
 
-// Eight fp32 values as two bf16 fragments hi + lo (zeros where not `on`).
-__device__ __forceinline__ void split8(f32x4 a, f32x4 b, bool on, bf16x8& hi, bf16x8& lo) {
-    uint32_t h[4], l[4];
-    split_bf16x2(a[0], a[1], h[0], l[0]);
-    split_bf16x2(a[2], a[3], h[1], l[1]);
-    split_bf16x2(b[0], b[1], h[2], l[2]);
-    split_bf16x2(b[2], b[3], h[3], l[3]);
-    const u32x4 z = {0u, 0u, 0u, 0u};
-    hi = __builtin_bit_cast(bf16x8, on ? u32x4{h[0], h[1], h[2], h[3]} : z);
-    lo = __builtin_bit_cast(bf16x8, on ? u32x4{l[0], l[1], l[2], l[3]} : z);
+// Eight bf16 of d, or zeros.
+__device__ __forceinline__ bf16x8 d8(const uint16_t* d, bool on) {
+    const u32x4 v = *(const u32x4*)d;
+    return __builtin_bit_cast(bf16x8, on ? v : u32x4{0u, 0u, 0u, 0u});
 }
 
 // A wave's ring of slices in LDS: NT tiles of 16 bf16 rows, 32 columns (64 bytes)
@@ -175,7 +169,8 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 #pragma unroll
         for (int i = 0; i < TT; i++)
             if (m0 + 16 * i + r < p.M && id[i] < 0)
-                for (int c = p0 + g; c < p0 + 16 * RT && c < p.R; c += 4) p.d[(m0 + 16 * i + r) * p.R + c] = 0.0f;
+                for (int c = p0 + 8 * (g >> 1); c < p0 + 16 * RT && c < p.R; c += 16)
+                    *(u32x4*)(p.d + ((m0 + 16 * i + r) * 2 + (g & 1)) * p.R + c) = u32x4{0u, 0u, 0u, 0u};
     }
     Ring ring;
     ring.init(rings + wave * Ring::BYTES, lane);
@@ -232,7 +227,15 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
             for (int v = 1; v < NW; v++) s += part[(v * RT * TT + wave) * 64 + lane];
             const int c = p0 + 16 * (wave / TT) + 4 * g, q = wave % TT;
             const bool mine = (TT == 2 && q ? id[TT - 1] : id[0]) == a;
-            if (mine && c < p.R) *(f32x4*)(p.d + (m0 + 16 * q + r) * p.R + c) = s * (p.scaling ? p.scaling[a] : 1.0f);  // R % 8 == 0
+            if (mine && c < p.R) {  // R % 8 == 0
+                s *= p.scaling ? p.scaling[a] : 1.0f;
+                uint32_t hi[2], lo[2];
+                split_bf16x2(s[0], s[1], hi[0], lo[0]);
+                split_bf16x2(s[2], s[3], hi[1], lo[1]);
+                uint16_t* const dst = p.d + (m0 + 16 * q + r) * 2 * p.R + c;
+                *(u32x2*)dst = u32x2{hi[0], hi[1]};
+                *(u32x2*)(dst + p.R) = u32x2{lo[0], lo[1]};
+            }
         }
     }
 #endif
@@ -294,13 +297,12 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
             rem &= ~(uint32_t)__ballot(mine);
             if (turn % kAdWaves != wave) continue;
             const uint16_t* const LB = p.lb + ((int64_t)a * p.N + brow) * p.R;
-            const float* const D = p.d + (mine ? 16 * i + r : 0) * p.R;
+            const uint16_t* const D = p.d + (mine ? 16 * i + r : 0) * 2 * p.R;
             for (int k0 = 0; k0 < p.R; k0 += 32) {
                 const bool in = k0 + 8 * g < p.R;
                 const int k = in ? k0 + 8 * g : 0;
                 const u32x4 bv = *(const u32x4*)(LB + k);
-                bf16x8 hi, lo;
-                split8(*(const f32x4*)(D + k), *(const f32x4*)(D + k + 4), in && mine, hi, lo);
+                const bf16x8 hi = d8(D + k, in && mine), lo = d8(D + p.R + k, in && mine);
                 const bf16x8 ol = __builtin_bit_cast(bf16x8, in ? bv : u32x4{0, 0, 0, 0});
                 f32x4 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, f32x4{0, 0, 0, 0}, 0, 0, 0);
                 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, z, 0, 0, 0);
@@ -356,7 +358,7 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 // each leaves its sums in memory for k_wide_sum (a launch more; the last of them
 // adding all took 12 us for 64 rows of 12 shares).
 constexpr int kWideX = 32 << 10;  // LDS for x: 2 chunks of 64 rows; and 64 ranks of d
-constexpr int kWideD = 68;        // floats of a row of d there (64 ranks, padded)
+constexpr int kWideD = 136;       // bf16 of a row of d there (64 ranks' halves, padded)
 typedef W4Ring<2, 3> WideRing;
 
 template <int XT, bool WHOLE>
@@ -365,7 +367,7 @@ __global__ __launch_bounds__(64 * kAdWaves, 2) void k_w4_wide(AParams p) {
     __shared__ __align__(16) uint8_t rings[kAdWaves * WideRing::BYTES];
     __shared__ __align__(16) uint8_t xs[kWideX];
     __shared__ float inv[kWideX / 256];
-    static_assert(64 * kWideD * 4 <= kWideX, "64 ranks of 64 rows fit");
+    static_assert(64 * kWideD * 2 <= kWideX, "64 ranks of 64 rows fit");
     constexpr int kThreads = 64 * kAdWaves;
     const int t = threadIdx.x, lane = t & 63;
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -405,12 +407,12 @@ __global__ __launch_bounds__(64 * kAdWaves, 2) void k_w4_wide(AParams p) {
         for (int i = 0; i < XT; i++) ad[f][i] = f32x4{0, 0, 0, 0};
     const uint64_t some = __ballot(id >= 0);
     for (int k0 = 0; some && k0 < p.R; k0 += 64) {
-        float* const ds = (float*)xs;
+        uint16_t* const ds = (uint16_t*)xs;
         __syncthreads();
         for (int i = t; i < nr * 16; i += kThreads) {
-            const int k = k0 + (i & 15) * 4;
-            *(f32x4*)(ds + (i >> 4) * kWideD + (i & 15) * 4) =
-                k < p.R ? *(const f32x4*)(p.d + (m0 + (i >> 4)) * p.R + k) : f32x4{0, 0, 0, 0};
+            const int q = i & 15, k = k0 + (q & 7) * 8;  // a row's 8 pieces of the first halves, 8 of the second
+            *(u32x4*)(ds + (i >> 4) * kWideD + q * 8) =
+                k < p.R ? *(const u32x4*)(p.d + ((m0 + (i >> 4)) * 2 + (q >> 3)) * p.R + k) : u32x4{0u, 0u, 0u, 0u};
         }
         __syncthreads();
         // this share's adapters in turn, the next one's B under way
@@ -445,9 +447,8 @@ __global__ __launch_bounds__(64 * kAdWaves, 2) void k_w4_wide(AParams p) {
 #pragma unroll
                 for (int s = 0; s < 2; s++) {
                     const bool in = k0 + 32 * s + 8 * g < p.R;
-                    const float* const d = ds + (16 * i + r) * kWideD + 32 * s + 8 * g;
-                    bf16x8 hi, lo;
-                    split8(*(const f32x4*)d, *(const f32x4*)(d + 4), on && in, hi, lo);
+                    const uint16_t* const d = ds + (16 * i + r) * kWideD + 32 * s + 8 * g;
+                    const bf16x8 hi = d8(d, on && in), lo = d8(d + 64, on && in);
 #pragma unroll
                     for (int f = 0; f < 2; f++) {
                         const bf16x8 ol = __builtin_bit_cast(bf16x8, in ? bv[buf][f][s] : u32x4{0u, 0u, 0u, 0u});

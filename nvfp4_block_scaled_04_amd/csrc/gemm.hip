@@ -63,19 +63,6 @@ __device__ __forceinline__ int row_adapter(const GParams& p, int64_t m) {
     return a >= 0 && a < p.ad_n ? a : -1;
 }
 
-// Eight fp32 values as two bf16 fragments hi + lo, the sum within 2^-16 of the value
-// (zeros where not `on`).
-__device__ __forceinline__ void split8(f32x4 a, f32x4 b, bool on, bf16x8& hi, bf16x8& lo) {
-    uint32_t h[4], l[4];
-    split_bf16x2(a[0], a[1], h[0], l[0]);
-    split_bf16x2(a[2], a[3], h[1], l[1]);
-    split_bf16x2(b[0], b[1], h[2], l[2]);
-    split_bf16x2(b[2], b[3], h[3], l[3]);
-    const u32x4 z = {0u, 0u, 0u, 0u};
-    hi = __builtin_bit_cast(bf16x8, on ? u32x4{h[0], h[1], h[2], h[3]} : z);
-    lo = __builtin_bit_cast(bf16x8, on ? u32x4{l[0], l[1], l[2], l[3]} : z);
-}
-
 // Waves per SIMD each configuration is compiled for: a 128x128 wave tile
 // takes the whole register file (256 accumulators per lane); smaller wave
 // tiles are held to 256 registers so two waves share a SIMD.
@@ -199,6 +186,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
     static_assert(BM % 32 == 0 && BN % 32 == 0 && (EVEN || NST == 2), "whole fragments; uneven loads need two stages");
     static_assert(NST == 2 || NST == 3, "two or three LDS stages");
     __shared__ __align__(16) uint8_t smem[KS * NST * STAGE];
+    __shared__ int32_t ids[EPI == EPI_ADAPT ? BM : 1];  // the tile rows' adapters
 
     const int t = threadIdx.x;
     const int lane = t & 63;
@@ -441,7 +429,13 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
     // Step kt lives in stage (kt - kb) % NST; its loads are issued NST-1 steps
     // ahead.  Both K groups run the same number of steps, so the workgroup
     // barriers pair up.
+    static_assert(EPI != EPI_ADAPT || 64 * NW * KS >= BM, "a thread per tile row");
+    int my_id = -1;
+    if constexpr (EPI == EPI_ADAPT) my_id = t < BM ? row_adapter(p, m0 + t) : -1;
     issue(kb, sm);
+    if constexpr (EPI == EPI_ADAPT) {  // seen by all at the next barrier
+        if (t < BM) ids[t] = my_id;
+    }
     if constexpr (NST == 3) issue(kb + 1 < ke ? kb + 1 : kb, sm + STAGE);
     wait_vmcnt<ND * (NST - 2)>();  // step kb has landed (this wave's part)
     barrier();
@@ -566,86 +560,129 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
         // the rank-r term of each row's own adapter, unscaled by alpha: a row's
         // accumulators (one lane pair's) take alpha first, and the epilogue and
         // the fixup launch give it none.  Rows without an adapter stay as they
-        // are, so they come out as the plain GEMM's, bit for bit.  The wave's
+        // are, so they come out as the plain GEMM's, bit for bit.  The tile's
         // rows are served adapter by adapter: the first row not yet served names
-        // one, the rows that share it take part together and the others enter
-        // as zeros.
+        // one, and the rows that share it take part together.  32 ranks at a time
+        // come through LDS (the pipeline's, free now): d's halves once, the adapters' B in
+        // two buffers, the next one's on its way while one is used.
+        constexpr int OFF_Z = BM * 128, ZB = BN * 64;  // d: 128 bytes a row; a buffer of B
+        static_assert(OFF_Z + 2 * ZB <= KS * NST * STAGE && BM % 64 == 0, "d and B fit in the pipeline's LDS");
+        constexpr int NWT = NW * KS;
+        constexpr uint32_t kNothing = 0x80000000u;  // an offset past any source: zeros (both are below 2^20 bytes)
+        lds_u8* const zs = (lds_u8*)smem;
+        const int rows = (int)(p.M - m0 < BM ? p.M - m0 : BM), cols = (int)(p.N - n0 < BN ? p.N - n0 : BN);
         const float al = p.alpha[e];
-        int id[FM];
-        uint32_t rem[FM];
+        // the wave's fragment rows (a K group holds one, kept as the first here)
+        constexpr int NM = KS == 2 ? 1 : FM;
+        if constexpr (KS == 2) {
 #pragma unroll
-        for (int i = 0; i < FM; i++) {
-            id[i] = KS == 1 || i == grp ? row_adapter(p, m0 + wm * WM + i * 32 + l32) : -1;
-            rem[i] = lora ? (uint32_t)__ballot(id[i] >= 0) : 0u;
+            for (int in = 0; in < FN; in++) acc[in][0] = grp ? acc[in][1] : acc[in][0];
+        }
+        auto row0 = [&](int im) { return wm * WM + (KS == 2 ? grp : im) * 32; };
+        int idw[BM / 64], id[NM];  // the tile's rows, 64 a register; the wave's
+        uint64_t some[BM / 64];
+#pragma unroll
+        for (int i = 0; i < BM / 64; i++) {
+            idw[i] = ids[64 * i + lane];
+            some[i] = lora ? __ballot(idw[i] >= 0) : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < NM; i++) {
+            id[i] = ids[row0(i) + l32];
             const float s = id[i] >= 0 ? al : 1.0f;
 #pragma unroll
             for (int in = 0; in < FN; in++) acc[in][i] *= s;
         }
-        while (true) {
-            int a = -1;
+        for (int k0 = 0; k0 < p.r; k0 += 32) {
+            uint64_t rem[BM / 64];
 #pragma unroll
-            for (int i = 0; i < FM; i++)
-                if (a < 0 && rem[i]) a = __builtin_amdgcn_readlane(id[i], __builtin_ctz(rem[i]));
+            for (int i = 0; i < BM / 64; i++) rem[i] = some[i];
+            auto find = [&]() {  // the next adapter, or -1
+                int a = -1;
+#pragma unroll
+                for (int i = 0; i < BM / 64; i++)
+                    if (a < 0 && rem[i]) a = __builtin_amdgcn_readlane(idw[i], __builtin_ctzll(rem[i]));
+#pragma unroll
+                for (int i = 0; i < BM / 64; i++) rem[i] &= ~__ballot(idw[i] == a);
+                return a;
+            };
+            auto load_b = [&](int a, int buf) {
+                const __amdgpu_buffer_rsrc_t rb = make_rsrc(p.ad_b + ((int64_t)a * p.N + n0) * p.r, (uint32_t)(cols * p.r * 2));
+#pragma unroll
+                for (int i = 0; i < (BN / 16 + NWT - 1) / NWT; i++) {
+                    const int j = i * NWT + wave_wg, row = j * 16 + (lane >> 2), c = k0 + 8 * ((lane & 3) ^ swz(row));
+                    if ((BN / 16) % NWT == 0 || j < BN / 16)
+                        __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, (__attribute__((address_space(3))) void*)(zs + OFF_Z + buf * ZB + j * 1024),
+                                                                 16, row < cols && c < p.r ? (uint32_t)(row * p.r + c) * 2 : kNothing, 0, 0, 0);
+                }
+            };
+            int a = find();
             if (a < 0) break;
+            barrier();  // the pipeline, or the previous ranks, are consumed
+            const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.ad_d + m0 * 2 * p.r, (uint32_t)(rows * p.r * 4));
 #pragma unroll
-            for (int i = 0; i < FM; i++) rem[i] &= ~(uint32_t)__ballot(id[i] == a);
-            // rows that do not share it keep their sums by selection, not by a product
-            // with zeros: its values may be infinite or NaN.  (Not needed where all do.)
-            bool all = true;
-#pragma unroll
-            for (int i = 0; i < FM; i++)
-                if (KS == 1 || i == grp) all = all && (uint32_t)__ballot(id[i] == a) == 0xFFFFFFFFu;
-            const uint16_t* const lb = p.ad_b + (int64_t)a * p.N * p.r;
-            uint32_t ob[FN], od[FM];  // element offsets of the lane's rows (r <= 256: 32 bits hold a matrix's 2^24 rows)
-#pragma unroll
-            for (int i = 0; i < FN; i++) {
-                const int64_t row = n0 + wn * WN + i * 32 + l32;
-                ob[i] = (uint32_t)((row < p.N ? row : p.N - 1) * p.r);
+            for (int i = 0; i < BM / 8 / NWT; i++) {
+                const int j = i * NWT + wave_wg, row = j * 8 + (lane >> 3), q = (lane & 7) ^ (row & 7), c = k0 + 8 * (q & 3);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (__attribute__((address_space(3))) void*)(zs + j * 1024), 16,
+                                                         row < rows && c < p.r ? (uint32_t)((2 * row + (q >> 2)) * p.r + c) * 2 : kNothing, 0, 0, 0);
             }
+            static_assert((BM / 8) % NWT == 0, "whole rounds of d");
+            load_b(a, 0);
+            for (int buf = 0; a >= 0; buf ^= 1) {
+                wait_vmcnt<0>();
+                barrier();  // this one's B is there, and the other buffer is free
+                const int next = find();
+                if (next >= 0) load_b(next, buf ^ 1);
+                const lds_u8* const zb = zs + OFF_Z + buf * ZB + (wn * WN + l32) * 64;
+                auto b_at = [&](int in, int sl) {
+                    return __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(zb + in * 2048 + (((2 * sl + h) ^ xr) << 4)));
+                };
 #pragma unroll
-            for (int i = 0; i < FM; i++) {
-                const int64_t row = m0 + wm * WM + i * 32 + l32;
-                od[i] = (uint32_t)((row < p.M ? row : p.M - 1) * p.r);
-            }
-            // 16 ranks at a time, every load of a step under way together
-            for (int kr = 0; kr < p.r; kr += 16) {
-                const bool in_r = kr + h * 8 < p.r;  // r is a multiple of 8
-                const int k = in_r ? kr + h * 8 : p.r - 8;
-                u32x4 bv[FN];
-                f32x4 dv[FM][2];
+                for (int im = 0; im < NM; im++) {
+                    const uint64_t mine = __ballot(id[im] == a);
+                    if (!mine) continue;
+                    const lds_u8* const zd = zs + (row0(im) + l32) * 128;
+                    bf16x8 hi[2], lo[2];
 #pragma unroll
-                for (int i = 0; i < FN; i++) bv[i] = *(const u32x4*)(lb + ob[i] + k);
-#pragma unroll
-                for (int i = 0; i < FM; i++)
-                    if (KS == 1 || i == grp) {
-                        dv[i][0] = *(const f32x4*)(p.ad_d + od[i] + k);
-                        dv[i][1] = *(const f32x4*)(p.ad_d + od[i] + k + 4);
+                    for (int sl = 0; sl < 2; sl++) {
+                        const int c = 2 * sl + h;  // the 32 ranks' first halves are pieces 0 .. 3, the second ones 4 .. 7
+                        hi[sl] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(zd + ((c ^ (l32 & 7)) << 4)));
+                        lo[sl] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(zd + (((c + 4) ^ (l32 & 7)) << 4)));
                     }
-                bf16x8 hi[FM], lo[FM];
+                    if (mine == ~(uint64_t)0) {
 #pragma unroll
-                for (int i = 0; i < FM; i++)
-                    if (KS == 1 || i == grp) split8(dv[i][0], dv[i][1], in_r && id[i] == a, hi[i], lo[i]);
+                        for (int sl = 0; sl < 2; sl++)  // past r: zeros
 #pragma unroll
-                for (int i = 0; i < FN; i++) {
-                    const bf16x8 ol = __builtin_bit_cast(bf16x8, in_r ? bv[i] : u32x4{0u, 0u, 0u, 0u});
+                            for (int in = 0; in < FN; in++) {
+                                const bf16x8 ol = b_at(in, sl);
+                                acc[in][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[sl], acc[in][im], 0, 0, 0);
+                                acc[in][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[sl], acc[in][im], 0, 0, 0);
+                            }
+                    } else {
+                        // rows that do not share it keep their sums by selection, not by
+                        // products with zeros: its values may be infinite or NaN
 #pragma unroll
-                    for (int im = 0; im < FM; im++) {
-                        if (KS == 2 && im != grp) continue;
-                        if (all) {
-                            acc[i][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[im], acc[i][im], 0, 0, 0);
-                            acc[i][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[im], acc[i][im], 0, 0, 0);
-                        } else {
+                        for (int in = 0; in < FN; in++) {
                             f32x16 z;
 #pragma unroll
                             for (int v = 0; v < 16; v++) z[v] = 0.0f;
-                            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[im], z, 0, 0, 0);
-                            z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[im], z, 0, 0, 0);
 #pragma unroll
-                            for (int v = 0; v < 16; v++) acc[i][im][v] += id[im] == a ? z[v] : 0.0f;
+                            for (int sl = 0; sl < 2; sl++) {
+                                const bf16x8 ol = b_at(in, sl);
+                                z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[sl], z, 0, 0, 0);
+                                z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[sl], z, 0, 0, 0);
+                            }
+#pragma unroll
+                            for (int v = 0; v < 16; v++) acc[in][im][v] += id[im] == a ? z[v] : 0.0f;
                         }
                     }
                 }
+                a = next;
             }
+        }
+        if constexpr (KS == 2) {
+#pragma unroll
+            for (int in = 0; in < FN; in++) acc[in][1] = acc[in][0];
         }
     }
 
@@ -703,7 +740,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
 #pragma unroll
     for (int im = 0; im < FM; im++) {
         if (KS == 2 && im != grp) continue;  // the other K group stores this fragment row
-        const float alpha = EPI == EPI_ADAPT && row_adapter(p, m0 + wm * WM + im * 32 + l32) >= 0 ? 1.0f : alpha_e;
+        const float alpha = EPI == EPI_ADAPT && ids[EPI == EPI_ADAPT ? wm * WM + im * 32 + l32 : 0] >= 0 ? 1.0f : alpha_e;
         // lane (l32, h) of fragment in: row l32, columns in*32 + 8g + 4h .. +3
 #pragma unroll
         for (int in = 0; in < FN; in++) {
@@ -1045,8 +1082,9 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
                 bf16x8 hi = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u}), lo = hi, ol = hi;
                 if (kr + g * 8 < p.r) {
                     ol = __builtin_bit_cast(bf16x8, *(const u32x4*)(p.ad_b + ((int64_t)a * p.N + brow) * p.r + kr + g * 8));
-                    const float* const d = p.ad_d + (id == a ? m0 + r : 0) * p.r + kr + g * 8;
-                    split8(*(const f32x4*)d, *(const f32x4*)(d + 4), id == a, hi, lo);
+                    const uint16_t* const d = p.ad_d + (id == a ? m0 + r : 0) * 2 * p.r + kr + g * 8;
+                    hi = __builtin_bit_cast(bf16x8, *(const u32x4*)d);
+                    lo = __builtin_bit_cast(bf16x8, *(const u32x4*)(d + p.r));
                 }
                 f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, acc, 0, 0, 0);
                 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, t, 0, 0, 0);

@@ -42,8 +42,8 @@ struct GParams {
     // split-tail schedule (persistent K-split launch)
     float* part;         // fp32 partial tiles of the split tail tiles, or null (no split)
     int sk_grid;         // workgroups of the persistent launch
-    // adapter epilogue (EPI_ADAPT): d [M, r] fp32, adapters' B [L, N, r], ids [M]
-    const float* ad_d;
+    // adapter epilogue (EPI_ADAPT): d [M, 2, r], adapters' B [L, N, r], ids [M]
+    const uint16_t* ad_d;
     const uint16_t* ad_b;
     const int32_t* ad_ids;
     int ad_n;            // L
