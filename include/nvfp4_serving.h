@@ -38,7 +38,7 @@ enum nvfp4_route_score {
     (4 * (int64_t)(t) * (int64_t)(top_k) * (int64_t)(inter) + 4096 + (4096 * 4 + 1) * (((int64_t)(h) + 127) / 128 * 32))
 
 /*
- * A whole mixture-of-experts layer for a few tokens, in two launches.
+ * A whole mixture-of-experts layer for a few tokens, in two or three launches.
  * Routing, for each token i: the experts are ordered by logit, largest first,
  * equal logits by the lower index first; the first top_k of them whose logit is
  * neither NaN nor -inf are chosen.  Slot j of the token holds the j-th of them,

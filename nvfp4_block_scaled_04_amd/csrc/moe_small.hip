@@ -1,5 +1,5 @@
 // moe_small.hip -- a whole mixture-of-experts layer for a few tokens in two
-// launches, on NVFP4 expert weights and bf16 tokens.
+// launches (three beyond 32 tokens), on NVFP4 expert weights and bf16 tokens.
 //
 // What is computed (tokens x, router logits, E experts of H -> I -> H):
 //   chosen(i) = the top_k experts by (logit descending, index ascending) among
@@ -18,8 +18,9 @@
 // a share of the K axis, which is the chosen experts' I axes laid end to end.  Its
 // waves walk the same chunks and share the activations in LDS; each adds an
 // expert's product into the fp32 sums of its own columns, and of the several
-// workgroups of a column tile the last to finish adds their sums in the order of
-// the shares: no atomic sums, the same result on every call.
+// workgroups of a column tile the last to finish (beyond 32 tokens, a launch of its
+// own) adds their sums in the order of the shares: no atomic sums, the same result
+// on every call.
 //
 // Bound: the chosen experts' weights are read once (9/16 byte an element), the
 // rest is small; the kernels are built to keep weight loads in flight.
@@ -39,8 +40,8 @@ typedef W4Ring<2, 3> UpRing;       // with x and the tables, LDS for two workgro
 
 // Second launch: up to 32 tokens, two workgroups of 8 waves share a CU; beyond, the
 // sums take the LDS, and one workgroup of 16 waves has a CU where there are enough
-// columns for that (64 tokens over 32 experts of 4096 x 2048: 67 us, 77 with 8
-// waves; 61 tokens over 60 of 2064 x 1104, too few: 66 us, 50 with 8 waves).
+// columns for that (64 tokens over 32 experts of 4096 x 2048: 53 us, 67 with 8
+// waves; 61 tokens over 60 of 2064 x 1104, too few: 53 us, 41 with 8 waves).
 template <int NW>
 struct DownShape {
     typedef W4Ring<1, NW == 8 ? 4 : 3> Ring;
@@ -355,6 +356,17 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
 #endif
 }
 
+// Shares of the second launch's K axis, of 12 chunks at least (4 tokens over 128
+// experts of 2048 x 768: 17.9 us, of 4, 8 or 16 chunks at least 21.3, 20.4, 21.4).
+constexpr int kShareChunks = 12;
+__device__ __forceinline__ int shares_of(int total, int most) {
+    return total >= kShareChunks * most ? most : total < kShareChunks ? 1 : total / kShareChunks;
+}
+// Tokens up to which k_moe_down adds the shares itself (16 tokens of 8 experts of
+// 5120 x 8192: 50.3 us, with a launch of its own 52.8; 64 tokens of 32 experts of
+// 4096 x 2048: 66 us, 59.2).
+constexpr int kOwnSum = 32;
+
 // Workgroup (16 NW output columns, share of the K axis): a wave has 16 columns to
 // itself, and all walk the same (expert, chunk) range.
 template <int NW, bool WHOLE>
@@ -381,8 +393,7 @@ __global__ __launch_bounds__(64 * NW, 4) void k_moe_down(EParams p) {
     const int rowb = p.I / 2, cpa4 = (p.I / 16 + 3) / 4;
     const int nch = (p.I + kChunk - 1) / kChunk;
     const int total = nact * nch;
-    // shares of at least 4 chunks; the rest of the workgroups has nothing to do
-    const int shares = total < 4 * p.shares ? (total < 4 ? 1 : total / 4) : p.shares;
+    const int shares = shares_of(total, p.shares);  // the rest of the workgroups has nothing to do
     const int share = blockIdx.y;
     if (share >= shares) return;
     const int tile = blockIdx.x * NW + wave;  // the wave's 16 columns: band_row(tile, 0 .. 15)
@@ -503,16 +514,19 @@ __global__ __launch_bounds__(64 * NW, 4) void k_moe_down(EParams p) {
         for (int i = lane; i < p.T * 4; i += 64) put(i, mine(i));
         return;
     }
-    // several workgroups have these columns: each leaves its sums in memory, and
-    // the wave that finds the others done adds them, in the order of the shares.
-    // Device-scope stores and loads (sc1) pass by the XCDs' own L2s, so no cache
-    // is written back or dropped; the stores are waited for before the count.
+    // several workgroups have these columns: each leaves its sums in memory.  Up to
+    // kOwnSum tokens the wave that finds the others done adds them, in the order of
+    // the shares; beyond, k_moe_sum does, since one wave would take 13 us to (64
+    // tokens, 16 shares).  Device-scope stores and loads (sc1) pass by the XCDs' own
+    // L2s, so no cache is written back or dropped; the stores are waited for before
+    // the count.
     constexpr int kDevice = 16;
     const int n16 = p.T * 64;  // bytes of a share's sums of this tile
     const __amdgpu_buffer_rsrc_t part = make_rsrc(p.part + (int64_t)tile * p.shares * p.T * 16, (uint32_t)(shares * n16));
     for (int i = lane; i < p.T * 4; i += 64) {
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, mine(i)), part, i * 16, share * n16, kDevice);
     }
+    if (p.T > kOwnSum) return;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     int before = 0;
     if (lane == 0) before = __hip_atomic_fetch_add(&p.arrived[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -534,6 +548,30 @@ __global__ __launch_bounds__(64 * NW, 4) void k_moe_down(EParams p) {
 #endif
 }
 
+// The shares' sums in their order, where k_moe_down leaves them: four columns of a
+// token a thread.
+__global__ __launch_bounds__(256) void k_moe_sum(EParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    const int shares = shares_of(((const Routes*)p.routes)->nact * ((p.I + kChunk - 1) / kChunk), p.shares);
+    if (shares == 1) return;  // written already
+    const int n4 = p.T * 4;  // float4s of a share's sums of a tile
+    const int id = blockIdx.x * 256 + threadIdx.x;
+    const int tile = id / n4, i = id % n4, col = band_row(tile, 4 * (i & 3));
+    if (tile >= (p.H + 127) / 128 * 8 || col >= p.H) return;
+    const f32x4* const P = (const f32x4*)p.part + (int64_t)tile * p.shares * n4 + i;
+    f32x4 s = {0, 0, 0, 0};
+    constexpr int U = 16;  // loads in flight together
+    for (int v0 = 0; v0 < shares; v0 += U) {
+        f32x4 v[U];
+#pragma unroll
+        for (int u = 0; u < U; u++) v[u] = v0 + u < shares ? P[(int64_t)(v0 + u) * n4] : f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < U; u++) s += v[u];
+    }
+    *(u32x2*)(p.out + (int64_t)(i >> 2) * p.H + col) = u32x2{pack_bf16x2(s[0], s[1]), pack_bf16x2(s[2], s[3])};
+#endif
+}
+
 template <int NR>
 void launch_up(const EParams& p, int grid, size_t lds, hipStream_t st) {
     if (p.H % kChunk == 0) k_moe_up<NR, true><<<grid, kThreads, lds, st>>>(p);
@@ -552,6 +590,7 @@ void launch_down(EParams p, int cus, int most_shares, hipStream_t st) {
     const dim3 grid((unsigned)cols, (unsigned)p.shares);
     if (p.I % kChunk == 0) k_moe_down<NW, true><<<grid, 64 * NW, lds, st>>>(p);
     else k_moe_down<NW, false><<<grid, 64 * NW, lds, st>>>(p);
+    if (p.T > kOwnSum && p.shares > 1) k_moe_sum<<<(unsigned)(((p.H + 127) / 128 * 8 * p.T * 4 + 255) / 256), 256, 0, st>>>(p);
 }
 
 }  // namespace
