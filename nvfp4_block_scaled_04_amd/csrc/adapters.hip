@@ -141,8 +141,10 @@ struct RowRing {
 };
 
 // Workgroup (group of 16 RT ranks x, tile of 16 TT rows y, share z of the tile's
-// distinct adapters): K split over NW waves, slices of 32 columns.  Many rows
-// take TT = 2: an adapter's A is then read once per 32 rows.
+// distinct adapters): K split over NW waves, slices of 32 columns.
+// Bound: few rows, the latency of a first read and the adapters' bytes (64 rows, 48
+// adapters of 64 x 8192: 50 MB in 15-17 us, 3 TB/s; one row 6.6 us); many rows, the
+// reads of x and A through L2 (8192 x 5120, rank 32: 84 MB of x in 43 us, 2 TB/s).
 template <int RT, int TT, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
@@ -243,7 +245,9 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 
 // Weight-only product of up to 16 TT rows and 16 weight rows, the K chunks split
 // over the waves, and so are the rows' distinct adapters, whose loads come first
-// (the first weight loads are under way meanwhile).
+// (the first weight loads are under way meanwhile).  Bound: the latency of one step
+// of loads (4096 x 4096, 9.4 MB: one row 7 us, 16 rows with 16 adapters 10 us; 23 rows
+// of 1000 x 2608 9 us), and for more rows every workgroup's own reads of x.
 template <int TT, bool WHOLE>
 __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
@@ -355,8 +359,10 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 // Weight-only product of 16 XT rows and 256 columns, a share of the K axis and of
 // the rows' distinct adapters: a wave has 32 columns to itself (two fragments, 128
 // columns apart), the waves share x in LDS.  Where several workgroups share a tile,
-// each leaves its sums in memory for k_wide_sum (a launch more; the last of them
-// adding all took 12 us for 64 rows of 12 shares).
+// each leaves its sums in memory for k_wide_sum (a launch more, 4.2 us; with the last
+// of them adding all this one took 37.7 us instead of 30).  Bound: the workgroup's
+// share of x into LDS and its dequantization beside the weight's reads (64 rows,
+// 5120 x 8192, 48 adapters of rank 64: 30 us for 58 MB, 1.9 TB/s).
 constexpr int kWideX = 32 << 10;  // LDS for x: 2 chunks of 64 rows; and 64 ranks of d
 constexpr int kWideD = 136;       // bf16 of a row of d there (64 ranks' halves, padded)
 typedef W4Ring<2, 3> WideRing;
@@ -560,27 +566,32 @@ AParams params(const AdapterArgs& a) {
 
 hipError_t launch_adapter_down(const AdapterArgs& a, hipStream_t st) {
     const AParams p = params(a);
-    const unsigned ranks = (unsigned)((a.r + 15) / 16);
+    const unsigned ranks = (unsigned)((a.r + 15) / 16), rows = (unsigned)((a.m + 15) / 16);
+    const int cus = device_cus();
+    if (cus <= 0) return hipErrorInvalidDevice;
     if (a.m <= 64) {
         // few rows: a workgroup per 16 ranks and distinct adapter, since the
-        // adapters' reads are the work
-        k_adapter_down<1, 1, 16, 4><<<dim3(ranks, (unsigned)((a.m + 15) / 16), a.m < 16 ? (unsigned)a.m : 16u), 1024, 0, st>>>(p);
+        // adapters' reads are the work (64 rows of 8192, 12 adapters of rank 64: 11.4
+        // us, with two workgroups for a row tile's adapters 71.8)
+        k_adapter_down<1, 1, 16, 4><<<dim3(ranks, rows, a.m < 16 ? (unsigned)a.m : 16u), 1024, 0, st>>>(p);
         return hipGetLastError();
     }
-    // many rows: up to four tiles of ranks on one read of x, an adapter's A once per
-    // 32 rows where those still give every CU a tile, and two workgroups share a row
-    // tile's adapters (a prompt's end falls inside a tile)
-    const bool wide = (a.m + 31) / 32 >= 256;
-    const unsigned rows = (unsigned)((a.m + (wide ? 31 : 15)) / (wide ? 32 : 16));
-    if (wide) {
-        if (ranks == 1) k_adapter_down<1, 2, 16, 3><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
-        else if (ranks == 2) k_adapter_down<2, 2, 16, 2><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
-        else k_adapter_down<4, 2, 8, 3><<<dim3((ranks + 3) / 4, rows, 2), 512, 0, st>>>(p);
-    } else {
-        if (ranks == 1) k_adapter_down<1, 1, 16, 4><<<dim3(1, rows, 2), 1024, 0, st>>>(p);
-        else if (ranks <= 3) k_adapter_down<2, 1, 16, 3><<<dim3((ranks + 1) / 2, rows, 2), 1024, 0, st>>>(p);
-        else k_adapter_down<3, 1, 16, 2><<<dim3((ranks + 2) / 3, rows, 2), 1024, 0, st>>>(p);
-    }
+    // Many rows: two workgroups share a row tile's adapters (a prompt's end falls
+    // inside a tile), and the tiles are the smallest that leave one workgroup a CU
+    // (its rings fill the LDS): 16 rows and 16 ranks, then two or three tiles of
+    // ranks on one read of x, then 32 rows (half the reads of A).  us, 16 ranks
+    // against more at 16 rows: 128 x 4096 rank 64 7.7 : 11.6, 1024 x 4096 rank 32
+    // 9.2 : 11.0, 2048 x 4096 rank 32 17.0 : 11.4.  16 rows against 32: 1024 x 4096
+    // rank 64 13.8 : 17.4, 2048 x 4096 rank 64 24.7 : 18.5, 4096 x 5120 rank 16
+    // 18.2 : 14.2, 8192 x 5120 rank 32 49.8 : 42.9.
+    const unsigned few = (unsigned)cus / 2;
+    if (rows * ranks <= few) k_adapter_down<1, 1, 16, 4><<<dim3(ranks, rows, 2), 1024, 0, st>>>(p);
+    else if (ranks >= 2 && ranks <= 3 && rows * ((ranks + 1) / 2) <= few)
+        k_adapter_down<2, 1, 16, 3><<<dim3((ranks + 1) / 2, rows, 2), 1024, 0, st>>>(p);
+    else if (ranks >= 4 && rows * ((ranks + 2) / 3) <= few) k_adapter_down<3, 1, 16, 2><<<dim3((ranks + 2) / 3, rows, 2), 1024, 0, st>>>(p);
+    else if (ranks == 1) k_adapter_down<1, 2, 16, 3><<<dim3(1, (rows + 1) / 2, 2), 1024, 0, st>>>(p);
+    else if (ranks == 2) k_adapter_down<2, 2, 16, 2><<<dim3(1, (rows + 1) / 2, 2), 1024, 0, st>>>(p);
+    else k_adapter_down<4, 2, 8, 3><<<dim3((ranks + 3) / 4, (rows + 1) / 2, 2), 512, 0, st>>>(p);
     return hipGetLastError();
 }
 

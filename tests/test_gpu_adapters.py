@@ -78,7 +78,8 @@ DECODE = [  # m, n, k, r, L, ids, scaling, bias
     (8200, 24, 48, 16, 5, "runs", True, False),         # projections of many rows: 32-row tiles
     (8193, 40, 272, 32, 40, "mixed", True, True),
     (8225, 16, 144, 200, 6, "runs", False, False),
-    (300, 40, 336, 56, 9, "each", True, False),         # 16-row tiles, 4 tiles of ranks
+    (300, 40, 336, 56, 9, "each", True, False),         # 16-row tiles of 16 ranks
+    (600, 40, 336, 136, 9, "mixed", True, False),       # and of three tiles of ranks
 ]
 
 
