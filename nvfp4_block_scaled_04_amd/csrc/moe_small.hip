@@ -114,6 +114,11 @@ __device__ __forceinline__ int wave_prefix(int v, int& total) {
 }
 
 // NR: logits a lane holds of a token (E <= 16 NR).
+// Bound: the reads of W13 where there is enough of it (16 tokens of 8 experts of
+// 5120 x 8192, about 333 MB: 88 us, 3.8 TB/s; 64 tokens of 32 experts of 4096 x 2048,
+// 302 MB: 77 us, 3.9 TB/s; a copy of 2 GiB moves 4.9, reads alone 5.2 to 5.9), and the
+// routing, the first loads and the waves' sums otherwise (7 to 8 us of one token's 18.5
+// for 47 MB, and of the 22.4 of 4 tokens over 128 experts of 2048 x 768).
 template <int NR, bool WHOLE>
 __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
@@ -369,6 +374,10 @@ constexpr int kOwnSum = 32;
 
 // Workgroup (16 NW output columns, share of the K axis): a wave has 16 columns to
 // itself, and all walk the same (expert, chunk) range.
+// Bound: the reads of W2 and the step from expert to expert (16 tokens of 8 experts
+// of 5120 x 8192, 167 MB: 50.3 us, 3.3 TB/s; 64 of 32 of 4096 x 2048, 151 MB: 53.4 us,
+// 2.8 TB/s); with few bytes the chain of routes, first weights, sums and their
+// exchange (one token, 24 MB: 14.1 us; 4 tokens over 128 of 2048 x 768, 26 MB: 17.9).
 template <int NW, bool WHOLE>
 __global__ __launch_bounds__(64 * NW, 4) void k_moe_down(EParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
