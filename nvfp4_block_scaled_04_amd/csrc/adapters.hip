@@ -360,9 +360,10 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 // the rows' distinct adapters: a wave has 32 columns to itself (two fragments, 128
 // columns apart), the waves share x in LDS.  Where several workgroups share a tile,
 // each leaves its sums in memory for k_wide_sum (a launch more, 4.2 us; with the last
-// of them adding all this one took 37.7 us instead of 30).  Bound: the workgroup's
-// share of x into LDS and its dequantization beside the weight's reads (64 rows,
-// 5120 x 8192, 48 adapters of rank 64: 30 us for 58 MB, 1.9 TB/s).
+// of them adding all this one took 37.7 us instead of 30).  Bound: three
+// parts in turn, the first loads and the sums, the adapters, the K loop (64 rows, 5120
+// x 8192, 48 adapters of rank 64: 30 us for 58 MB, 1.9 TB/s; 22 without the adapters'
+// part, 20 without the K loop).
 constexpr int kWideX = 32 << 10;  // LDS for x: 2 chunks of 64 rows; and 64 ranks of d
 constexpr int kWideD = 136;       // bf16 of a row of d there (64 ranks' halves, padded)
 typedef W4Ring<2, 3> WideRing;
