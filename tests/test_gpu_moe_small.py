@@ -151,6 +151,75 @@ def test_offsets_past_32_bits(serving):
     check(serving, x, lg, w, 2, "softmax", True)
 
 
+# The second launch's form of 16 waves: t > 32 and wide enough h (sixteen_waves).
+SIXTEEN = [  # t, h, inter, E, k, score, renormalize, logits
+    (33, 2064, 144, 5, 2, "softmax", True, "f32"),        # one share; an odd number of 128-column bands
+    (64, 4112, 1040, 4, 3, "sigmoid", False, "bf16"),     # three shares, about 48 tokens an expert, I % 128 != 0
+    (64, 4096, 2048, 6, 2, "softmax", True, "f32"),       # whole chunks and bands
+    (40, 3088, 512, 40, 8, "softmax", False, "f32"),      # many short experts, 13 shares at most
+    (49, 3200, 656, 3, 1, "sigmoid", True, "f32"),
+]
+
+
+def sixteen_waves(t, h):
+    """Whether the second launch takes workgroups of 16 waves: most shares of the
+    K axis times tiles of 256 columns fill the CUs."""
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    return t > 32 and -(-h // 256) * min(1024 // t, 32) >= cus
+
+
+@pytest.mark.parametrize("t,h,inter,E,k,score,renorm,dt", SIXTEEN)
+def test_layer_of_sixteen_waves(serving, t, h, inter, E, k, score, renorm, dt):
+    say("moe, 16 waves", t, h, inter, E, k, score, renorm, dt)
+    assert sixteen_waves(t, h)
+    x, lg, w = layer(t + h, t, h, inter, E, torch.bfloat16 if dt == "bf16" else torch.float32)
+    check(serving, x, lg, w, k, score, renorm)
+
+
+def test_sixteen_waves_edges(serving):
+    """Empty rows, every token on one expert, no token on any, a token of NaN."""
+    say("moe, 16 waves: edges")
+    t, h, inter, E = 50, 3344, 176, 9
+    assert sixteen_waves(t, h)
+    x, lg, w = layer(11, t, h, inter, E)
+    lg[::3] = -INF
+    check(serving, x, lg, w, 4, "softmax", True)
+    lg[:] = -INF
+    lg[:, 7] = 1.0
+    good = check(serving, x, lg, w, 2, "softmax", True)
+    x[20, 5] = NAN
+    out, _, _ = serving.nvfp4_moe_small(x, lg, *w.values(), 2)
+    assert out[20].isnan().all() and torch.equal(out[:20], good[:20]) and torch.equal(out[21:], good[21:])
+    assert not check(serving, x.nan_to_num(), torch.full_like(lg, -INF), w, 2, "softmax", True).any()
+
+
+def test_sixteen_waves_repeats_and_graph(serving):
+    """The same bits on a second call and on three replays of a captured graph,
+    the workspace and the outputs overwritten in between."""
+    say("moe, 16 waves: repeats, graph")
+    t, h, inter, k = 64, 4112, 1040, 3
+    assert sixteen_waves(t, h)
+    x, lg, w = layer(12, t, h, inter, 4)
+    ws = torch.full((serving.moe_small_ws_bytes(t, k, h, inter),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = torch.empty(t, h, dtype=torch.bfloat16, device="cuda")
+    go = lambda: serving.nvfp4_moe_small(x, lg, *w.values(), k, out=out, workspace=ws)
+    go()
+    want = out.clone()
+    graph = torch.cuda.CUDAGraph()
+    for replay in range(4):
+        out.fill_(3)
+        ws.fill_(0xFF)
+        if replay:
+            graph.replay()
+        else:
+            go()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        if replay == 0:
+            with torch.cuda.graph(graph):
+                go()
+
+
 def test_repeats_streams_and_graph(serving):
     """The same bits on a second call, on another stream, and on three replays of
     a captured graph with the workspace and the outputs overwritten in between."""
