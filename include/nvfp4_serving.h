@@ -75,8 +75,8 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
                     int64_t workspace_bytes, void *stream);
 
 /* Bytes of workspace the adapter calls need: the rows' projections onto their
- * adapters' r ranks, in two bf16 halves.  With NVFP4_GEMM_WS_BYTES (nvfp4.h) more
- * they spread a product over more workgroups, whose partial sums go there. */
+ * adapters' r ranks, fp32.  With NVFP4_GEMM_WS_BYTES (nvfp4.h) more they spread a
+ * product over more workgroups, whose partial sums go there. */
 #define NVFP4_ADAPTERS_WS_BYTES(m, r) (((int64_t)(m) * (int64_t)(r) * 4 + 255) / 256 * 256)
 
 /* Largest adapter rank (NVFP4_BAD_RANK beyond it). */
@@ -90,9 +90,10 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
  * the adapter's term left out where adapter[i] is outside [0, n_adapters) (-1
  * by custom).  Rows may use any adapters in any order; each distinct adapter of
  * 16 consecutive rows (64 beyond 32 rows) is read once for them.  The projection
- * onto the ranks is summed in fp32 and enters the second product as two bf16 halves
- * (2^-16 of it).  Results are the same on every call (no atomic sums).
- * Non-finite values of a row or an adapter reach the rows that hold or use them.
+ * onto the ranks is summed and held in fp32 and enters the second product whole, as
+ * three bf16 parts.  Results are the same on every call (no atomic sums).
+ * Non-finite values of a row or an adapter reach the rows that hold or use them (an
+ * infinity in lora_b as NaN: it meets parts that are 0).
  *   x: [m, k] bf16; b: [n, k/2]; b_sf: swizzled scales; alpha: [1] fp32.
  *   lora_a: [n_adapters, r, k] bf16; lora_b: [n_adapters, n, r] bf16 (adapters of
  *   lower rank padded with zeros); adapter: [m] int32; scaling: NULL (1.0) or

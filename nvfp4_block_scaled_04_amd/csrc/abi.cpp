@@ -467,7 +467,7 @@ static nvfp4::AdapterArgs adapter_args(const void* x, const void* lora_a, const 
                                        int64_t k, int64_t r, int64_t n_adapters, void* workspace) {
     nvfp4::AdapterArgs a{};
     a.x = (const uint16_t*)x; a.lora_a = (const uint16_t*)lora_a; a.lora_b = (const uint16_t*)lora_b;
-    a.adapter = adapter; a.scaling = scaling; a.d = (uint16_t*)workspace;
+    a.adapter = adapter; a.scaling = scaling; a.d = (float*)workspace;
     a.m = m; a.n = n; a.k = k; a.r = r; a.n_adapters = n_adapters;
     return a;
 }

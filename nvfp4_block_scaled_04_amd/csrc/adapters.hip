@@ -12,9 +12,9 @@
 // rows that share it are served together.  So an adapter is read once per tile of
 // rows, whatever the order, and rows without one cost nothing.  The other rows of
 // the tile are multiplied beside them and their products left out by selection (an
-// adapter's values may be infinite).  d is summed in fp32 and kept as two bf16
-// halves (2^-16 of d, no more bytes than fp32, and the second product takes them as
-// they are); the adapters' own bf16 values are exact.
+// adapter's values may be infinite).  d is a sum and kept in fp32; it enters
+// the second product as three bf16 parts that add up to it (split_bf16x3), beside the
+// adapters' own bf16 values.
 //
 // Bound: for decode the weight and the adapters that the batch uses, each read
 // once; the projections are short, so their parts are spread over as many waves
@@ -40,7 +40,7 @@ struct AParams {
     const float* scaling;      // [L] or null
     const uint16_t* bias;      // [N] or null
     uint16_t* out;             // [M, N]
-    uint16_t* d;               // [M, 2, R]
+    float* d;                  // [M, R]
     int64_t M, N, K;
     int R, L;
     int cpa4, nblk;
@@ -71,10 +71,16 @@ __device__ __forceinline__ void store4(const AParams& p, int64_t m, int64_t n, f
     }
 }
 
-// Eight bf16 of d, or zeros.
-__device__ __forceinline__ bf16x8 d8(const uint16_t* d, bool on) {
-    const u32x4 v = *(const u32x4*)d;
+// Eight bf16 values, or zeros.
+__device__ __forceinline__ bf16x8 b8(const uint16_t* b, bool on) {
+    const u32x4 v = *(const u32x4*)b;
     return __builtin_bit_cast(bf16x8, on ? v : u32x4{0u, 0u, 0u, 0u});
+}
+
+// Eight values of d in their three parts, or zeros.
+__device__ __forceinline__ void d8(const float* d, bool on, bf16x8 (&part)[3]) {
+    const f32x4 zero = {0, 0, 0, 0}, lo = *(const f32x4*)d, hi = *(const f32x4*)(d + 4);
+    split_bf16x3(on ? lo : zero, on ? hi : zero, part);
 }
 
 // A wave's ring of slices in LDS: NT tiles of 16 bf16 rows, 32 columns (64 bytes)
@@ -171,8 +177,8 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 #pragma unroll
         for (int i = 0; i < TT; i++)
             if (m0 + 16 * i + r < p.M && id[i] < 0)
-                for (int c = p0 + 8 * (g >> 1); c < p0 + 16 * RT && c < p.R; c += 16)
-                    *(u32x4*)(p.d + ((m0 + 16 * i + r) * 2 + (g & 1)) * p.R + c) = u32x4{0u, 0u, 0u, 0u};
+                for (int c = p0 + 4 * g; c < p0 + 16 * RT && c < p.R; c += 16)
+                    *(f32x4*)(p.d + (m0 + 16 * i + r) * p.R + c) = f32x4{0, 0, 0, 0};
     }
     Ring ring;
     ring.init(rings + wave * Ring::BYTES, lane);
@@ -231,12 +237,7 @@ __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
             const bool mine = (TT == 2 && q ? id[TT - 1] : id[0]) == a;
             if (mine && c < p.R) {  // R % 8 == 0
                 s *= p.scaling ? p.scaling[a] : 1.0f;
-                uint32_t hi[2], lo[2];
-                split_bf16x2(s[0], s[1], hi[0], lo[0]);
-                split_bf16x2(s[2], s[3], hi[1], lo[1]);
-                uint16_t* const dst = p.d + (m0 + 16 * q + r) * 2 * p.R + c;
-                *(u32x2*)dst = u32x2{hi[0], hi[1]};
-                *(u32x2*)(dst + p.R) = u32x2{lo[0], lo[1]};
+                *(f32x4*)(p.d + (m0 + 16 * q + r) * p.R + c) = s;
             }
         }
     }
@@ -301,15 +302,16 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
             rem &= ~(uint32_t)__ballot(mine);
             if (turn % kAdWaves != wave) continue;
             const uint16_t* const LB = p.lb + ((int64_t)a * p.N + brow) * p.R;
-            const uint16_t* const D = p.d + (mine ? 16 * i + r : 0) * 2 * p.R;
+            const float* const D = p.d + (mine ? 16 * i + r : 0) * p.R;
             for (int k0 = 0; k0 < p.R; k0 += 32) {
                 const bool in = k0 + 8 * g < p.R;
                 const int k = in ? k0 + 8 * g : 0;
-                const u32x4 bv = *(const u32x4*)(LB + k);
-                const bf16x8 hi = d8(D + k, in && mine), lo = d8(D + p.R + k, in && mine);
-                const bf16x8 ol = __builtin_bit_cast(bf16x8, in ? bv : u32x4{0, 0, 0, 0});
-                f32x4 z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, f32x4{0, 0, 0, 0}, 0, 0, 0);
-                z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, z, 0, 0, 0);
+                const bf16x8 ol = b8(LB + k, in);
+                bf16x8 dv[3];
+                d8(D + k, in && mine, dv);
+                f32x4 z = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < 3; j++) z = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, dv[j], z, 0, 0, 0);
 #pragma unroll
                 for (int v = 0; v < 4; v++) ad[i][v] += mine ? z[v] : 0.0f;
             }
@@ -365,7 +367,7 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 // x 8192, 48 adapters of rank 64: 30 us for 58 MB, 1.9 TB/s; 22 without the adapters'
 // part, 20 without the K loop).
 constexpr int kWideX = 32 << 10;  // LDS for x: 2 chunks of 64 rows; and 64 ranks of d
-constexpr int kWideD = 136;       // bf16 of a row of d there (64 ranks' halves, padded)
+constexpr int kWideD = 200;       // bf16 of a row of d there (64 ranks' three parts, padded)
 typedef W4Ring<2, 3> WideRing;
 
 template <int XT, bool WHOLE>
@@ -416,10 +418,12 @@ __global__ __launch_bounds__(64 * kAdWaves, 2) void k_w4_wide(AParams p) {
     for (int k0 = 0; some && k0 < p.R; k0 += 64) {
         uint16_t* const ds = (uint16_t*)xs;
         __syncthreads();
-        for (int i = t; i < nr * 16; i += kThreads) {
-            const int q = i & 15, k = k0 + (q & 7) * 8;  // a row's 8 pieces of the first halves, 8 of the second
-            *(u32x4*)(ds + (i >> 4) * kWideD + q * 8) =
-                k < p.R ? *(const u32x4*)(p.d + ((m0 + (i >> 4)) * 2 + (q >> 3)) * p.R + k) : u32x4{0u, 0u, 0u, 0u};
+        for (int i = t; i < nr * 8; i += kThreads) {  // 8 ranks of a row
+            const int q = i & 7, k = k0 + q * 8;
+            bf16x8 dv[3];
+            d8(p.d + (m0 + (i >> 3)) * p.R + (k < p.R ? k : 0), k < p.R, dv);
+#pragma unroll
+            for (int j = 0; j < 3; j++) *(bf16x8*)(ds + (i >> 3) * kWideD + j * 64 + q * 8) = dv[j];
         }
         __syncthreads();
         // this share's adapters in turn, the next one's B under way
@@ -455,12 +459,14 @@ __global__ __launch_bounds__(64 * kAdWaves, 2) void k_w4_wide(AParams p) {
                 for (int s = 0; s < 2; s++) {
                     const bool in = k0 + 32 * s + 8 * g < p.R;
                     const uint16_t* const d = ds + (16 * i + r) * kWideD + 32 * s + 8 * g;
-                    const bf16x8 hi = d8(d, on && in), lo = d8(d + 64, on && in);
 #pragma unroll
-                    for (int f = 0; f < 2; f++) {
-                        const bf16x8 ol = __builtin_bit_cast(bf16x8, in ? bv[buf][f][s] : u32x4{0u, 0u, 0u, 0u});
-                        z[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, z[f], 0, 0, 0);
-                        z[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, z[f], 0, 0, 0);
+                    for (int j = 0; j < 3; j++) {
+                        const bf16x8 dv = b8(d + 64 * j, on && in);
+#pragma unroll
+                        for (int f = 0; f < 2; f++) {
+                            const bf16x8 ol = __builtin_bit_cast(bf16x8, in ? bv[buf][f][s] : u32x4{0u, 0u, 0u, 0u});
+                            z[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, dv, z[f], 0, 0, 0);
+                        }
                     }
                 }
 #pragma unroll

@@ -45,7 +45,6 @@
 #include "gemm_common.h"
 #include "internal.h"
 #include "quant_block.h"
-#include "skinny_w4.h"
 
 namespace nvfp4 {
 
@@ -563,7 +562,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
         // are, so they come out as the plain GEMM's, bit for bit.  The tile's
         // rows are served adapter by adapter: the first row not yet served names
         // one, and the rows that share it take part together.  32 ranks at a time
-        // come through LDS (the pipeline's, free now): d's halves once, the adapters' B in
+        // come through LDS (the pipeline's, free now): d once, the adapters' B in
         // two buffers, the next one's on its way while one is used.  Bound: the adapters
         // in turn, each a barrier, LDS reads and a few products (31 prompts, 1003 x 2056 x
         // 2000, rank 40: 37.5 us, 26.4 without the term; three buffers 38.5); with long
@@ -578,6 +577,9 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
         const float al = p.alpha[e];
         // the wave's fragment rows (a K group holds one, kept as the first here)
         constexpr int NM = KS == 2 ? 1 : FM;
+        // the small tiles keep d's parts in registers from adapter to adapter, on the
+        // others they are formed for each (they would spill 16 to 115 registers)
+        constexpr bool KEEP = NM * FN <= 4;
         if constexpr (KS == 2) {
 #pragma unroll
             for (int in = 0; in < FN; in++) acc[in][0] = grp ? acc[in][1] : acc[in][0];
@@ -623,18 +625,31 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
             int a = find();
             if (a < 0) break;
             barrier();  // the pipeline, or the previous ranks, are consumed
-            const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.ad_d + m0 * 2 * p.r, (uint32_t)(rows * p.r * 4));
+            const __amdgpu_buffer_rsrc_t rd = make_rsrc(p.ad_d + m0 * p.r, (uint32_t)(rows * p.r * 4));
 #pragma unroll
-            for (int i = 0; i < BM / 8 / NWT; i++) {
-                const int j = i * NWT + wave_wg, row = j * 8 + (lane >> 3), q = (lane & 7) ^ (row & 7), c = k0 + 8 * (q & 3);
+            for (int i = 0; i < BM / 8 / NWT; i++) {  // eight ranks lie together, group q of a row in place q ^ (row / 2 % 4)
+                const int j = i * NWT + wave_wg, row = j * 8 + (lane >> 3), c = k0 + 8 * ((lane >> 1 & 3) ^ (row >> 1 & 3)) + 4 * (lane & 1);
                 __builtin_amdgcn_raw_ptr_buffer_load_lds(rd, (__attribute__((address_space(3))) void*)(zs + j * 1024), 16,
-                                                         row < rows && c < p.r ? (uint32_t)((2 * row + (q >> 2)) * p.r + c) * 2 : kNothing, 0, 0, 0);
+                                                         row < rows && c < p.r ? (uint32_t)(row * p.r + c) * 4 : kNothing, 0, 0, 0);
             }
             static_assert((BM / 8) % NWT == 0, "whole rounds of d");
             load_b(a, 0);
-            for (int buf = 0; a >= 0; buf ^= 1) {
-                wait_vmcnt<0>();
-                barrier();  // this one's B is there, and the other buffer is free
+            wait_vmcnt<0>();
+            barrier();  // d and the first one's B are there
+            bf16x8 dv[NM][2][3];  // the wave's rows of d, in parts
+            auto read_d = [&](int im) {
+                const lds_u8* const zd = zs + (row0(im) + l32) * 128;
+#pragma unroll
+                for (int sl = 0; sl < 2; sl++) {
+                    const auto d = (const __attribute__((address_space(3))) f32x4*)(zd + ((2 * sl + h) ^ (l32 >> 1 & 3)) * 32);
+                    split_bf16x3(d[0], d[1], dv[im][sl]);
+                }
+            };
+            if constexpr (KEEP) {
+#pragma unroll
+                for (int im = 0; im < NM; im++) read_d(im);
+            }
+            for (int buf = 0;; buf ^= 1) {
                 const int next = find();
                 if (next >= 0) load_b(next, buf ^ 1);
                 const lds_u8* const zb = zs + OFF_Z + buf * ZB + (wn * WN + l32) * 64;
@@ -645,22 +660,16 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
                 for (int im = 0; im < NM; im++) {
                     const uint64_t mine = __ballot(id[im] == a);
                     if (!mine) continue;
-                    const lds_u8* const zd = zs + (row0(im) + l32) * 128;
-                    bf16x8 hi[2], lo[2];
-#pragma unroll
-                    for (int sl = 0; sl < 2; sl++) {
-                        const int c = 2 * sl + h;  // the 32 ranks' first halves are pieces 0 .. 3, the second ones 4 .. 7
-                        hi[sl] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(zd + ((c ^ (l32 & 7)) << 4)));
-                        lo[sl] = __builtin_bit_cast(bf16x8, *(const __attribute__((address_space(3))) u32x4*)(zd + (((c + 4) ^ (l32 & 7)) << 4)));
-                    }
+                    if constexpr (!KEEP) read_d(im);
                     if (mine == ~(uint64_t)0) {
 #pragma unroll
                         for (int sl = 0; sl < 2; sl++)  // past r: zeros
 #pragma unroll
                             for (int in = 0; in < FN; in++) {
                                 const bf16x8 ol = b_at(in, sl);
-                                acc[in][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[sl], acc[in][im], 0, 0, 0);
-                                acc[in][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[sl], acc[in][im], 0, 0, 0);
+#pragma unroll
+                                for (int j = 0; j < 3; j++)
+                                    acc[in][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, dv[im][sl][j], acc[in][im], 0, 0, 0);
                             }
                     } else {
                         // rows that do not share it keep their sums by selection, not by
@@ -673,15 +682,18 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
 #pragma unroll
                             for (int sl = 0; sl < 2; sl++) {
                                 const bf16x8 ol = b_at(in, sl);
-                                z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, hi[sl], z, 0, 0, 0);
-                                z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, lo[sl], z, 0, 0, 0);
+#pragma unroll
+                                for (int j = 0; j < 3; j++) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, dv[im][sl][j], z, 0, 0, 0);
                             }
 #pragma unroll
                             for (int v = 0; v < 16; v++) acc[in][im][v] += id[im] == a ? z[v] : 0.0f;
                         }
                     }
                 }
+                if (next < 0) break;
                 a = next;
+                wait_vmcnt<0>();
+                barrier();  // the next one's B is there, and this one's buffer is free
             }
         }
         if constexpr (KS == 2) {
@@ -1083,15 +1095,17 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
             rem &= ~(uint32_t)__ballot(id == a);
             if (turn % kSkinnyWaves != wave) continue;
             for (int kr = 0; kr < p.r; kr += 32) {
-                bf16x8 hi = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u}), lo = hi, ol = hi;
+                bf16x8 ol = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u}), dv[3];
+                f32x4 d0 = {0, 0, 0, 0}, d1 = d0, t = acc;
                 if (kr + g * 8 < p.r) {
                     ol = __builtin_bit_cast(bf16x8, *(const u32x4*)(p.ad_b + ((int64_t)a * p.N + brow) * p.r + kr + g * 8));
-                    const uint16_t* const d = p.ad_d + (id == a ? m0 + r : 0) * 2 * p.r + kr + g * 8;
-                    hi = __builtin_bit_cast(bf16x8, *(const u32x4*)d);
-                    lo = __builtin_bit_cast(bf16x8, *(const u32x4*)(d + p.r));
+                    const float* const d = p.ad_d + (id == a ? m0 + r : 0) * p.r + kr + g * 8;
+                    d0 = *(const f32x4*)d;
+                    d1 = *(const f32x4*)(d + 4);
                 }
-                f32x4 t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, hi, acc, 0, 0, 0);
-                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, lo, t, 0, 0, 0);
+                split_bf16x3(d0, d1, dv);
+#pragma unroll
+                for (int j = 0; j < 3; j++) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, dv[j], t, 0, 0, 0);
 #pragma unroll
                 for (int v = 0; v < 4; v++) acc[v] = id == a ? t[v] : acc[v];  // the others' by selection
             }

@@ -42,8 +42,8 @@ struct GParams {
     // split-tail schedule (persistent K-split launch)
     float* part;         // fp32 partial tiles of the split tail tiles, or null (no split)
     int sk_grid;         // workgroups of the persistent launch
-    // adapter epilogue (EPI_ADAPT): d [M, 2, r], adapters' B [L, N, r], ids [M]
-    const uint16_t* ad_d;
+    // adapter epilogue (EPI_ADAPT): d [M, r], adapters' B [L, N, r], ids [M]
+    const float* ad_d;
     const uint16_t* ad_b;
     const int32_t* ad_ids;
     int ad_n;            // L
@@ -73,6 +73,29 @@ __device__ __forceinline__ bf16x8 dequant8_bf16(uint32_t w, float s) {
     const bf16x2 h2 = __builtin_convertvector(f32x2{v2[0] * s, v2[1] * s}, bf16x2);
     const bf16x2 h3 = __builtin_convertvector(f32x2{v3[0] * s, v3[1] * s}, bf16x2);
     return bf16x8{h0[0], h0[1], h1[0], h1[1], h2[0], h2[1], h3[0], h3[1]};
+}
+
+// Eight fp32 values f, each as three bf16 ones that add up to it: every part takes
+// the next eight of the 24 significant bits by truncation, so that none rounds up to
+// an infinity (exact but for bits below bf16's least value).  A non-finite f is whole
+// in the first part, the others are finite then and of its sign.
+__device__ __forceinline__ void split_bf16x3(const f32x4& f0, const f32x4& f1, bf16x8 (&part)[3]) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) f[i] = i < 4 ? f0[i & 3] : f1[i & 3];
+#pragma unroll
+    for (int j = 0; j < 3; j++) {
+        u32x4 w;
+#pragma unroll
+        for (int i = 0; i < 4; i++)  // the upper halves of two values
+            w[i] = __builtin_amdgcn_perm(f_bits(f[2 * i + 1]), f_bits(f[2 * i]), 0x07060302);
+        part[j] = __builtin_bit_cast(bf16x8, w);
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (j == 0) f[i] = __builtin_amdgcn_fmed3f(f[i], -kFp32Max, kFp32Max);
+            f[i] -= bits_f(f_bits(f[i]) & 0xFFFF0000u);
+        }
+    }
 }
 
 __device__ __forceinline__ uint32_t word(const u32x4& v, int j) {

@@ -60,9 +60,8 @@ struct GemmArgs {
     uint16_t* out;         // [E, m, n]
     int64_t E, m, n, k, r;
     float* ws = nullptr;   // kGemmWsSlots partial 128x256 fp32 tiles for the split-tail schedule, or null
-    // adapter epilogue (E = 1): row i gets (ad_d[i, 0] + ad_d[i, 1]) @ ad_b[adapter[i]]^T,
-    // unscaled by alpha
-    const uint16_t* ad_d = nullptr;      // [m, 2, r] bf16, or null: no adapters
+    // adapter epilogue (E = 1): row i gets ad_d[i] @ ad_b[adapter[i]]^T, unscaled by alpha
+    const float* ad_d = nullptr;         // [m, r], or null: no adapters
     const uint16_t* ad_b = nullptr;      // [n_adapters, n, r]
     const int32_t* adapter = nullptr;    // [m]
     int64_t n_adapters = 0;
@@ -139,9 +138,7 @@ struct AdapterArgs {
     const uint16_t* lora_b;
     const int32_t* adapter;
     const float* scaling;    // [n_adapters] or null
-    // scaling * x @ lora_a[adapter]^T (0 without one) as two bf16 halves, the sum
-    // within 2^-16 of it, [m, 2, r]
-    uint16_t* d;
+    float* d;                // [m, r]: scaling * x @ lora_a[adapter]^T (0 without one)
     int64_t m, n, k, r, n_adapters;
 };
 // Bytes of the decode product's partial sums.

@@ -1,6 +1,5 @@
 // skinny_w4.h -- pieces of the kernels that stream NVFP4 weight rows against a
-// few bf16 rows (weight-only products for decode), and the split of an fp32
-// value into two bf16 halves.
+// few bf16 rows (weight-only products for decode).
 //
 // A wave works on fragments of 16 weight rows and 16 activation rows.  Lane l
 // (row r = l % 16, group g = l / 16) holds, per chunk of 128 columns, columns
@@ -37,14 +36,6 @@ constexpr uint32_t kNoRow = 0x80000000u;  // offset of what is not there: reads 
 
 __device__ __forceinline__ u32x4 buf_load16(__amdgpu_buffer_rsrc_t rs, uint32_t vo, int so) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, (int)vo, so, 0));
-}
-
-// f = hi + lo + (at most 2^-16 of f): two bf16 values, each rounded to nearest
-// even.  A non-finite f keeps its value in hi and a zero in lo.
-__device__ __forceinline__ void split_bf16x2(float a, float b, uint32_t& hi, uint32_t& lo) {
-    hi = pack_bf16x2(a, b);
-    const float ra = a - bf16_lo(hi), rb = b - bf16_hi(hi);
-    lo = pack_bf16x2(ra == ra ? ra : 0.0f, rb == rb ? rb : 0.0f);
 }
 
 typedef __attribute__((address_space(3))) uint8_t lds_byte;

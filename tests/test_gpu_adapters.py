@@ -293,3 +293,92 @@ def test_non_finite_adapter_stays_with_its_rows(mods, m):
         out = f()
         assert torch.equal(out[rows], want[rows])
         assert out[p["adapter"] == 2][:, 5].isnan().all() and not out[p["adapter"] == 4].isfinite().any()
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 32, 64), (40, 260, 4240), (100, 48, 64)])
+def test_projection_past_the_largest_bf16(mods, m, n, k):
+    """A row's projection that is finite in fp32 but rounds to an infinity in bf16
+    stays finite; one that is infinite stays infinite, with its sign."""
+    serving, _ = mods
+    say("adapters: projection past the largest bf16", m, n, k)
+    g = gen(m)
+    b, b_sf = torch.zeros(n, k // 2, dtype=torch.uint8, device="cuda"), R.rand_sf(g, n, k)   # the shared product is 0
+    x = torch.zeros(m, k, dtype=torch.bfloat16, device="cuda")
+    x[:, 0], x[:, 1], x[:, 3] = 2.0 ** 128 - 2.0 ** 120, 1.5 * 2.0 ** 119, 1.0    # 2^128 - 2^118 together; and 1
+    x[1::3] = -x[1::3]
+    la = torch.zeros(1, 8, k, dtype=torch.bfloat16, device="cuda")
+    la[0, 2, :2] = 1.0
+    la[0, 5, 3] = 3.0
+    lb = torch.full((1, n, 8), 0.0, dtype=torch.bfloat16, device="cuda")
+    lb[0, :, 2], lb[0, :, 5] = 2.0 ** -100, torch.randn(n, device="cuda", generator=g).bfloat16()
+    ids = torch.zeros(m, dtype=torch.int32, device="cuda")
+    alpha = torch.ones(1, device="cuda")
+    zero = torch.zeros(m, n, dtype=torch.float64, device="cuda")
+    calls = [lambda: serving.nvfp4_linear_adapters(x, b, b_sf, alpha, la, lb, ids),
+             lambda: serving.nvfp4_gemm_adapters(torch.zeros(m, k // 2, dtype=torch.uint8, device="cuda"), b, R.rand_sf(g, m, k), b_sf,
+                                                 alpha, x, la, lb, ids)]
+    ref, bound = R.adapters(zero, zero, k, x, la, lb, ids, None, None)
+    assert bool(ref.isfinite().all())
+    for f in calls:
+        assert R.worst(f(), ref, bound) <= 1.0
+    la[0, 2, 0] = 4.0   # the sum is past fp32's largest
+    lb[0, :, 5] = 0.0
+    sign = torch.where(x[:, :1] > 0, 1.0, -1.0).double()
+    for f in calls:
+        assert torch.equal(f().double(), (sign * float("inf")).expand(m, n))
+
+
+def near_pairs(g, m, n, k, r, L):
+    """Rows and adapters whose projections are integers of 24 bits (times a power of
+    two of the row), two and two a small step apart; column c of the output is the
+    step of pair c % (r / 2), exact in every order of the sums.  Returns x, lora_a,
+    lora_b, adapter and the output, with a shared product of 0."""
+    x = torch.zeros(m, k, device="cuda")
+    s = 2.0 ** (torch.arange(m, device="cuda") % 5 - 2)
+    cols = [0, k // 2, k - 1]
+    for c, v in zip(cols, (65536.0, 256.0, 1.0)):
+        x[:, c] = s * v
+    step = torch.randint(1, 256, (L, r // 2), device="cuda", generator=g)
+    low = torch.randint(2 ** 23, 2 ** 24 - 256, (L, r // 2), device="cuda", generator=g)
+    d = torch.stack([low, low + step], -1).view(L, r)
+    la = torch.zeros(L, r, k, device="cuda")
+    for c, shift in zip(cols, (16, 8, 0)):
+        la[:, :, c] = (d >> shift & 255).float()
+    pair = torch.arange(n, device="cuda") % (r // 2)
+    lb = torch.zeros(L, n, r, device="cuda")
+    at = torch.arange(n, device="cuda")
+    lb[:, at, 2 * pair], lb[:, at, 2 * pair + 1] = -1.0, 1.0
+    ids = torch.randint(-1, L, (m,), device="cuda", generator=g, dtype=torch.int32)
+    out = torch.where(ids[:, None] >= 0, s[:, None] * step[ids.clamp(min=0).long()][:, pair], torch.zeros(m, n, device="cuda"))
+    return x.bfloat16(), la.bfloat16(), lb.bfloat16(), ids, out.bfloat16()
+
+
+@pytest.mark.parametrize("m,n,k,r", [(1, 32, 64, 8), (17, 100, 272, 16), (50, 48, 640, 40), (16, 8210, 400, 8), (24, 4100, 256, 72),
+                                     (40, 260, 4240, 24), (100, 48, 64, 256)])
+def test_projection_keeps_its_fp32_bits_decode(mods, m, n, k, r):
+    """The projection onto the ranks is a sum, held in fp32."""
+    serving, _ = mods
+    say("adapters: fp32 projection, decode", m, n, k, r)
+    g = gen(m + n)
+    x, la, lb, ids, want = near_pairs(g, m, n, k, r, 5)
+    b, sf = torch.zeros(n, k // 2, dtype=torch.uint8, device="cuda"), R.rand_sf(g, n, k)
+    for split in (False, True):
+        out = serving.nvfp4_linear_adapters(x, b, sf, torch.ones(1, device="cuda"), la, lb, ids, out=fresh(m, n),
+                                            workspace=workspace(serving.adapters_ws_bytes(m, r, split)))
+        assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("m,n,k,r,split", [(20, 64, 272, 40, False), (300, 520, 128, 24, False), (2000, 1928, 256, 16, False),
+                                           (2048, 4104, 896, 40, False), (4000, 3480, 272, 32, False),
+                                           (4096, 8200, 144, 40, False), (3968, 2560, 1008, 72, True)])
+def test_projection_keeps_its_fp32_bits_prefill(mods, m, n, k, r, split):
+    serving, _ = mods
+    say("adapters: fp32 projection, prefill", m, n, k, r)
+    g = gen(m + n)
+    x, la, lb, ids, want = near_pairs(g, m, n, k, r, 3)
+    ids[: m // 2] = ids[0]   # fragments that share an adapter, and mixed ones
+    want[: m // 2] = want[0] * (2.0 ** (torch.arange(m // 2, device="cuda") % 5))[:, None].bfloat16()
+    a, b = (torch.zeros(v, k // 2, dtype=torch.uint8, device="cuda") for v in (m, n))
+    out = serving.nvfp4_gemm_adapters(a, b, R.rand_sf(g, m, k), R.rand_sf(g, n, k), torch.ones(1, device="cuda"), x, la, lb, ids,
+                                      out=fresh(m, n), workspace=workspace(serving.adapters_ws_bytes(m, r, split)))
+    assert torch.equal(out, want)
