@@ -91,7 +91,8 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
  * by custom).  Rows may use any adapters in any order; each distinct adapter of
  * 16 consecutive rows (64 beyond 32 rows) is read once for them.  The projection
  * onto the ranks is summed and held in fp32 and enters the second product whole, as
- * three bf16 parts.  Results are the same on every call (no atomic sums).
+ * three bf16 parts.  Results are the same on every call (no atomic sums); the order of
+ * the fp32 sums depends on m and on the list of adapters.
  * Non-finite values of a row or an adapter reach the rows that hold or use them (an
  * infinity in lora_b as NaN: it meets parts that are 0).
  *   x: [m, k] bf16; b: [n, k/2]; b_sf: swizzled scales; alpha: [1] fp32.
@@ -119,7 +120,8 @@ int nvfp4_linear_adapters(const void *x, const uint8_t *b, const uint8_t *b_sf, 
  *                    + scaling[t] * (x[i] @ lora_a[t]^T) @ lora_b[t]^T (+ bias)),
  * t = adapter[i].  The adapters' term is added to the GEMM's fp32 accumulators
  * before the output is written; a row without an adapter comes out as
- * nvfp4_gemm's (nvfp4_gemm_ws's), bit for bit.
+ * nvfp4_gemm's (nvfp4_gemm_ws's), bit for bit, and a row's bits do not depend on the
+ * adapters of the rows beside it.
  *   a: [m, k/2], a_sf: its scales; alpha: [1] fp32 = 1 / (gs_a * gs_b); the rest,
  *   and the limits, as nvfp4_linear_adapters.
  *   workspace: as there; with NVFP4_ADAPTERS_WS_BYTES(m, r) + NVFP4_GEMM_WS_BYTES

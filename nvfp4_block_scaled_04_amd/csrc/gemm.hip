@@ -658,36 +658,23 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
                 };
 #pragma unroll
                 for (int im = 0; im < NM; im++) {
-                    const uint64_t mine = __ballot(id[im] == a);
-                    if (!mine) continue;
+                    const bool mine = id[im] == a;
+                    if (!__ballot(mine)) continue;
                     if constexpr (!KEEP) read_d(im);
-                    if (mine == ~(uint64_t)0) {
+                    // rows that do not share it keep their sums by selection, not by products
+                    // with zeros: its values may be infinite or NaN.  (The same for a fragment
+                    // whose rows all share it, so a row's bits do not depend on its neighbours.)
 #pragma unroll
-                        for (int sl = 0; sl < 2; sl++)  // past r: zeros
+                    for (int in = 0; in < FN; in++) {
+                        f32x16 z = acc[in][im];
 #pragma unroll
-                            for (int in = 0; in < FN; in++) {
-                                const bf16x8 ol = b_at(in, sl);
+                        for (int sl = 0; sl < 2; sl++) {  // past r: zeros
+                            const bf16x8 ol = b_at(in, sl);
 #pragma unroll
-                                for (int j = 0; j < 3; j++)
-                                    acc[in][im] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, dv[im][sl][j], acc[in][im], 0, 0, 0);
-                            }
-                    } else {
-                        // rows that do not share it keep their sums by selection, not by
-                        // products with zeros: its values may be infinite or NaN
-#pragma unroll
-                        for (int in = 0; in < FN; in++) {
-                            f32x16 z;
-#pragma unroll
-                            for (int v = 0; v < 16; v++) z[v] = 0.0f;
-#pragma unroll
-                            for (int sl = 0; sl < 2; sl++) {
-                                const bf16x8 ol = b_at(in, sl);
-#pragma unroll
-                                for (int j = 0; j < 3; j++) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, dv[im][sl][j], z, 0, 0, 0);
-                            }
-#pragma unroll
-                            for (int v = 0; v < 16; v++) acc[in][im][v] += id[im] == a ? z[v] : 0.0f;
+                            for (int j = 0; j < 3; j++) z = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ol, dv[im][sl][j], z, 0, 0, 0);
                         }
+#pragma unroll
+                        for (int v = 0; v < 16; v++) acc[in][im][v] = mine ? z[v] : acc[in][im][v];
                     }
                 }
                 if (next < 0) break;
@@ -1084,19 +1071,23 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
             }
         }
     }
+    int id = -1;  // adapter of the lane's row
+    __shared__ f32x4 term[EPI == EPI_ADAPT ? 64 : 1];
     if constexpr (EPI == EPI_ADAPT) {
-        // the rank-r term of each row's own adapter (as in k_gemm), the tile's
-        // distinct adapters dealt to the waves
-        const int id = row_adapter(p, m0 + r);
-        acc *= id >= 0 ? p.alpha[0] : 1.0f;
+        // the rank-r term of each row's own adapter, the tile's distinct adapters dealt to
+        // the waves; apart from the waves' sums, so that it does not matter which had it
+        id = row_adapter(p, m0 + r);
+        f32x4 ad = {0, 0, 0, 0};
+        bool mine = false;
         uint32_t rem = (uint32_t)(__ballot(id >= 0) & 0xFFFF);
         for (int turn = 0; rem; turn++) {
             const int a = __builtin_amdgcn_readlane(id, __builtin_ctz(rem));
             rem &= ~(uint32_t)__ballot(id == a);
             if (turn % kSkinnyWaves != wave) continue;
+            mine |= id == a;
             for (int kr = 0; kr < p.r; kr += 32) {
                 bf16x8 ol = __builtin_bit_cast(bf16x8, u32x4{0u, 0u, 0u, 0u}), dv[3];
-                f32x4 d0 = {0, 0, 0, 0}, d1 = d0, t = acc;
+                f32x4 d0 = {0, 0, 0, 0}, d1 = d0, t = ad;
                 if (kr + g * 8 < p.r) {
                     ol = __builtin_bit_cast(bf16x8, *(const u32x4*)(p.ad_b + ((int64_t)a * p.N + brow) * p.r + kr + g * 8));
                     const float* const d = p.ad_d + (id == a ? m0 + r : 0) * p.r + kr + g * 8;
@@ -1107,9 +1098,10 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
 #pragma unroll
                 for (int j = 0; j < 3; j++) t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ol, dv[j], t, 0, 0, 0);
 #pragma unroll
-                for (int v = 0; v < 4; v++) acc[v] = id == a ? t[v] : acc[v];  // the others' by selection
+                for (int v = 0; v < 4; v++) ad[v] = id == a ? t[v] : ad[v];  // the others' by selection
             }
         }
+        if (mine) term[lane] = ad;
     }
     if constexpr (EPI == EPI_LORA) {
         if (wave == 0) {  // rank-r bf16 correction, once, into wave 0's partial
@@ -1131,7 +1123,11 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void k_gemm_skinny(GParams p) {
     // lane: output row m0 + r, columns n0 + 4g .. n0 + 4g + 3
     const int64_t m = m0 + r;
     if (m >= valid) return;
-    const float alpha = EPI == EPI_ADAPT && row_adapter(p, m) >= 0 ? 1.0f : p.alpha[e];
+    float alpha = p.alpha[e];
+    if (EPI == EPI_ADAPT && id >= 0) {
+        acc = acc * alpha + term[EPI == EPI_ADAPT ? lane : 0];
+        alpha = 1.0f;
+    }
     uint16_t* O = p.out + (int64_t)e * p.M * p.N + m * p.N;
     const int64_t n = n0 + 4 * g;
     float y[4];

@@ -382,3 +382,21 @@ def test_projection_keeps_its_fp32_bits_prefill(mods, m, n, k, r, split):
     out = serving.nvfp4_gemm_adapters(a, b, R.rand_sf(g, m, k), R.rand_sf(g, n, k), torch.ones(1, device="cuda"), x, la, lb, ids,
                                       out=fresh(m, n), workspace=workspace(serving.adapters_ws_bytes(m, r, split)))
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("m,n,k,r", [(40, 1040, 272, 24), (300, 1040, 272, 24), (2000, 1928, 256, 16), (4000, 3480, 272, 40),
+                                     (4096, 8200, 144, 32)])
+def test_prefill_row_does_not_depend_on_its_neighbours(mods, m, n, k, r):
+    """A row comes out the same bit for bit whichever adapters the rows beside it use."""
+    serving, _ = mods
+    say("gemm_adapters: neighbours", m, n, k, r)
+    g = gen(m + r)
+    p = pool(g, m, n, k, r, 5, "one")
+    a, a_sf, b, b_sf = R.rand_fp4(g, m, k=k), R.rand_sf(g, m, k), R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    alpha = torch.full((1,), 3e-4, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    go = lambda ids: serving.nvfp4_gemm_adapters(a, b, a_sf, b_sf, alpha, x, p["lora_a"], p["lora_b"], ids, scaling=p["scaling"])
+    one = p["adapter"]
+    mixed = torch.where(torch.rand(m, device="cuda", generator=g) < 0.5, one, torch.randint_like(one, -1, 4))
+    rows = mixed == one
+    assert torch.equal(go(one)[rows], go(mixed)[rows])
