@@ -452,7 +452,8 @@ static int adapters_check(const void* x, const void* lora_a, const void* lora_b,
     if (r < 8 || r % 8 != 0 || r > NVFP4_ADAPTERS_MAX_RANK) return NVFP4_BAD_RANK;
     if (!dim_ok(m) || !dim_ok(n) || !dim_ok(n_adapters) || k < 16 || k % 16 != 0 || k > kMaxDim)
         return NVFP4_BAD_SHAPE;
-    if ((m + 15) / 16 > 65535) return NVFP4_BAD_SHAPE;
+    // the grids hold that many: workgroups of 16 rows are taken for few tiles only
+    if (m > (int64_t)1 << 20) return NVFP4_BAD_SHAPE;
     // 32-bit offsets into one adapter's B, and into 64 rows of x, A or the weight
     if (n * r >= (int64_t)1 << 32 || k > ((int64_t)1 << 23)) return NVFP4_UNSUPPORTED;
     if (workspace_bytes < NVFP4_ADAPTERS_WS_BYTES(m, r)) return NVFP4_BAD_SHAPE;

@@ -400,3 +400,21 @@ def test_prefill_row_does_not_depend_on_its_neighbours(mods, m, n, k, r):
     mixed = torch.where(torch.rand(m, device="cuda", generator=g) < 0.5, one, torch.randint_like(one, -1, 4))
     rows = mixed == one
     assert torch.equal(go(one)[rows], go(mixed)[rows])
+
+
+def test_most_rows(mods):
+    """2^20 rows, the most that are taken."""
+    serving, _ = mods
+    say("adapters: 2^20 rows")
+    g = gen(20)
+    m, n, k, r, L = 1 << 20, 24, 16, 24, 6
+    p = pool(g, m, n, k, r, L, "runs")
+    a, a_sf, b, b_sf = R.rand_fp4(g, m, k=k), R.rand_sf(g, m, k), R.rand_fp4(g, n, k=k), R.rand_sf(g, n, k)
+    alpha = torch.full((1,), 0.02, device="cuda")
+    x = torch.randn(m, k, device="cuda", generator=g).bfloat16()
+    lora = (p["lora_a"], p["lora_b"], p["adapter"])
+    w = R.dequant(b, b_sf)
+    for left, f in ((x.double(), lambda out: serving.nvfp4_linear_adapters(x, b, b_sf, alpha, *lora, out=out)),
+                    (R.dequant(a, a_sf), lambda out: serving.nvfp4_gemm_adapters(a, b, a_sf, b_sf, alpha, x, *lora, out=out))):
+        ref, bound = R.adapters(left @ w.t() * alpha.double(), left.abs() @ w.abs().t() * alpha.double(), k, x, *lora, None, None)
+        assert R.worst(f(fresh(m, n)), ref, bound) <= 1.0

@@ -77,6 +77,15 @@ def test_gemm_adapters_validation(serving, change, status):
     assert serving._lib.nvfp4_gemm_adapters(*{**GEMM, **change}.values()) == status
 
 
+@pytest.mark.parametrize("call,base", [("nvfp4_linear_adapters", LIN), ("nvfp4_gemm_adapters", GEMM)])
+def test_adapters_row_limit(serving, call, base):
+    """Any m up to 2^20 (checked before the misaligned weight), none beyond."""
+    f, big = getattr(serving._lib, call), {"wsb": 1 << 40, "n": 16, "k": 16, "r": 8}
+    for m in (1048560, 1048561, 1 << 20):
+        assert f(*{**base, **big, "m": m, "b": P + 8}.values()) == MISAL
+    assert f(*{**base, **big, "m": (1 << 20) + 1, "b": P + 8}.values()) == SHAPE
+
+
 def test_workspace_sizes(serving, tmp_path):
     shapes = [(1, 1, 16), (64, 16, 8192), (7, 3, 48)]   # (t, top_k, h), inter = 2 h; (m, ., r)
     src = tmp_path / "ws.c"
