@@ -50,9 +50,11 @@ enum nvfp4_route_score {
  *   [g, u]    = alpha13[e] * x[i] @ W13[e]^T
  *   a         = g / (1 + exp(-g)) * u
  *   out[i, :] = bf16(sum over the chosen e of topk_weights * alpha2[e] * a @ W2[e]^T).
- * A token that chose no expert gets zeros.  Sums and a are formed in fp32, a enters
- * the second product as two fp16 values (2^-20 of a), the dequantized weights are
- * exact.  Results are the same on every call (no atomic sums).
+ * A token that chose no expert gets zeros.  Sums and a are formed in fp32, the
+ * dequantized weights are exact.  x and a enter the products as fp16 values scaled by
+ * 128 columns, x as one (exact, but off by up to 2^-38 of the largest of those columns
+ * where it is below 2^-29 of it), a as two (off by 2^-20 of itself, or by 2^-38 of the
+ * largest).  Results are the same on every call (no atomic sums).
  *   x: [t, h] bf16; logits: [t, E], bf16 (logits_dtype 0) or fp32 (1).
  *   w13: [E, 2*inter, h/2] packed e2m1, gate rows [0, inter) then up rows;
  *   w13_sf: [E, pad_up(2*inter,128)*pad_up(h/16,4)] ue4m3, swizzled;
@@ -89,7 +91,8 @@ int nvfp4_moe_small(const void *x, int64_t t, int64_t h, const void *logits, int
  *                    + scaling[a] * (x[i] @ lora_a[a]^T) @ lora_b[a]^T (+ bias)),
  * the adapter's term left out where adapter[i] is outside [0, n_adapters) (-1
  * by custom).  Rows may use any adapters in any order; each distinct adapter of
- * 16 consecutive rows (64 beyond 32 rows) is read once for them.  The projection
+ * 16 consecutive rows is read once for them (lora_b of up to 64 rows where the weight is
+ * large, lora_a of up to 32 where there are many rows).  The projection
  * onto the ranks is summed and held in fp32 and enters the second product whole, as
  * three bf16 parts.  Results are the same on every call (no atomic sums); the order of
  * the fp32 sums depends on m and on the list of adapters.

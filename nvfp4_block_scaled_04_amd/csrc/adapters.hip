@@ -16,9 +16,10 @@
 // the second product as three bf16 parts that add up to it (split_bf16x3), beside the
 // adapters' own bf16 values.
 //
-// Bound: for decode the weight and the adapters that the batch uses, each read
-// once; the projections are short, so their parts are spread over as many waves
-// as there are and every load of a step is under way at once.
+// Bound: for decode the weight and the adapters that the batch uses; the projections
+// are short, so their parts are spread over as many waves as there are and every load
+// of a step is under way at once.  The projection runs before the product, though only
+// the product's last step needs d: its time (6.5 to 17 us for up to 64 rows) is added.
 #include "device_common.h"
 #include "gemm_common.h"
 #include "internal.h"
@@ -150,7 +151,9 @@ struct RowRing {
 // distinct adapters): K split over NW waves, slices of 32 columns.
 // Bound: few rows, the latency of a first read and the adapters' bytes (64 rows, 48
 // adapters of 64 x 8192: 50 MB in 15-17 us, 3 TB/s; one row 6.6 us); many rows, the
-// reads of x and A through L2 (8192 x 5120, rank 32: 84 MB of x in 43 us, 2 TB/s).
+// reads of x and A through L2 (8192 x 5120, rank 32: 84 MB of x in 38 to 50 us, 2 TB/s;
+// 128 rows of 4096 with 8 adapters of rank 16 in any order: 20 us, the two workgroups of
+// a row tile serve four adapters each in turn).
 template <int RT, int TT, int NW, int D>
 __global__ __launch_bounds__(64 * NW) void k_adapter_down(AParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
@@ -365,7 +368,7 @@ __global__ __launch_bounds__(64 * kAdWaves) void k_w4a16_adapters(AParams p) {
 // of them adding all this one took 37.7 us instead of 30).  Bound: three
 // parts in turn, the first loads and the sums, the adapters, the K loop (64 rows, 5120
 // x 8192, 48 adapters of rank 64: 30 us for 58 MB, 1.9 TB/s; 22 without the adapters'
-// part, 20 without the K loop).
+// part, 20 without the K loop; beyond 64 rows 128 x 4096 x 4096 21 us, 256 29).
 constexpr int kWideX = 32 << 10;  // LDS for x: 2 chunks of 64 rows; and 64 ranks of d
 constexpr int kWideD = 200;       // bf16 of a row of d there (64 ranks' three parts, padded)
 typedef W4Ring<2, 3> WideRing;

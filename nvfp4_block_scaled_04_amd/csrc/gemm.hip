@@ -563,11 +563,12 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS, (KS == 2 ? 2 : kWavesPerEU<BM 
         // rows are served adapter by adapter: the first row not yet served names
         // one, and the rows that share it take part together.  32 ranks at a time
         // come through LDS (the pipeline's, free now): d once, the adapters' B in
-        // two buffers, the next one's on its way while one is used.  Bound: the adapters
-        // in turn, each a barrier, LDS reads and a few products (31 prompts, 1003 x 2056 x
-        // 2000, rank 40: 37.5 us, 26.4 without the term; three buffers 38.5); with long
-        // prompts little (12 prompts, 8192 x 16384 x 5120, rank 32: 1079 us, 1041 without;
-        // 8 prompts, 2048 x 4096 x 4096, rank 16: 62.6, 60.8).
+        // two buffers.  (The next one's load is issued before one is used, but the
+        // compiler waits for it before the first read of B, so every adapter pays a
+        // memory latency.)  Bound: the adapters in turn, each that latency, a barrier, LDS
+        // reads and a few products (31 prompts, 1003 x 2056 x 2000, rank 40: 38 us, 26
+        // without the term); with long prompts little (12 prompts, 8192 x 16384 x 5120,
+        // rank 32: 1064 to 1120 us, 1041 without; 8 prompts, 2048 x 4096 x 4096, rank 16: 63, 61).
         constexpr int OFF_Z = BM * 128, ZB = BN * 64;  // d: 128 bytes a row; a buffer of B
         static_assert(OFF_Z + 2 * ZB <= KS * NST * STAGE && BM % 64 == 0, "d and B fit in the pipeline's LDS");
         constexpr int NWT = NW * KS;

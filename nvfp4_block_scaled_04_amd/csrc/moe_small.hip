@@ -22,8 +22,11 @@
 // own) adds their sums in the order of the shares: no atomic sums, the same result
 // on every call.
 //
-// Bound: the chosen experts' weights are read once (9/16 byte an element), the
-// rest is small; the kernels are built to keep weight loads in flight.
+// Bound: the chosen experts' weights (9/16 byte an element), the rest is small.  They
+// are read once where up to 32 tokens (second launch: 16) chose an expert, and again
+// for every 32 (16) more, from the caches if they fit there: 64 tokens that all choose
+// the same 4 experts of 4096 x 2048 take 59 + 81 us and read 78 + 41 MB past the L2s,
+// for 38 + 19 MB of weights.
 #include "device_common.h"
 #include "gemm_common.h"
 #include "internal.h"
@@ -118,7 +121,12 @@ __device__ __forceinline__ int wave_prefix(int v, int& total) {
 // 5120 x 8192, about 333 MB: 88 us, 3.8 TB/s; 64 tokens of 32 experts of 4096 x 2048,
 // 302 MB: 77 us, 3.9 TB/s; a copy of 2 GiB moves 4.9, reads alone 5.2 to 5.9), and the
 // routing, the first loads and the waves' sums otherwise (7 to 8 us of one token's 18.5
-// for 47 MB, and of the 22.4 of 4 tokens over 128 experts of 2048 x 768).
+// for 47 MB, and of the 22.4 of 4 tokens over 128 experts of 2048 x 768).  Items are dealt
+// whole, so a grid that they do not fill or just exceed waits for the last: 61 tokens
+// over 60 experts of 2064 x 1104 are 540 items for 512 workgroups, 154 MB in 69 us, and
+// about 174 items of 256 workgroups leave a third of them idle in the case of 4 tokens.
+// 20 registers spill at four waves a SIMD (25 where H % 128 != 0), which shows as 6 to 25
+// MB written a call, up to 2 of them the activations.
 template <int NR, bool WHOLE>
 __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)  // the host pass only needs the launch stub
@@ -134,7 +142,8 @@ __global__ __launch_bounds__(kThreads, 4) void k_moe_up(EParams p) {
     const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
 
     // 1. routing: 16 lanes a token, its logits in registers (the first tokens' are on
-    //    their way while the counts are cleared)
+    //    their way while the counts are cleared; bf16 ones the compiler loads one after
+    //    another, 2 us of 28 at 256 experts)
     const int l16 = lane & 15;
     auto load_logits = [&](int tok, float (&lg)[NR]) {
 #pragma unroll
@@ -378,6 +387,9 @@ constexpr int kOwnSum = 32;
 // of 5120 x 8192, 167 MB: 50.3 us, 3.3 TB/s; 64 of 32 of 4096 x 2048, 151 MB: 53.4 us,
 // 2.8 TB/s); with few bytes the chain of routes, first weights, sums and their
 // exchange (one token, 24 MB: 14.1 us; 4 tokens over 128 of 2048 x 768, 26 MB: 17.9).
+// The compiler holds the ring's state per lane, since both pass forms share it: the
+// weight loads of a chunk sit in loops over distinct lane values (one turn each), which
+// costs VALU instructions (22 to 31 an MFMA, 14 to 24 in k_moe_up), and 14 registers spill.
 template <int NW, bool WHOLE>
 __global__ __launch_bounds__(64 * NW, 4) void k_moe_down(EParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)

@@ -14,14 +14,17 @@
 // when they are put into LDS, scaled by a power of two per row and chunk that
 // brings the largest of the 128 columns to [2^14, 2^15): a bf16 value keeps all
 // its bits down to 2^-29 of that largest one, and what lies below is off by less
-// than 2^-39 of it, far under the fp32 sums' own rounding.  The chunk's product
-// is scaled back as it is added to the fp32 accumulators.
+// than 2^-38 of it (a truncation at fp16's least value, 2^-24), far under the fp32
+// sums' own rounding.  The chunk's product is scaled back as it is added to the fp32
+// accumulators.
 //
 // The weights come through LDS: every wave has a ring of K chunks of its own, into
 // which buffer loads write directly (no registers, no address arithmetic: the
 // lane's row is a 32-bit offset that never changes, the chunk a scalar one).  A
 // load instruction takes 64 contiguous bytes of 16 rows, lane by lane; the
-// fragment is read from LDS in the matrix instruction's order.
+// fragment is read from LDS in the matrix instruction's order.  A ring runs empty
+// where a block of activations is put into LDS: its loads are older than the ring's,
+// in a loop, so the compiler's wait for them is for every load under way.
 #pragma once
 
 #include <type_traits>
@@ -173,9 +176,9 @@ __device__ __forceinline__ int band_row(int tile, int r) { return (tile >> 3) * 
 // NF fragments of 16 weight rows, D chunks in LDS.  `aim` points the loads at a
 // matrix and rows, `issue` starts the load of a chunk into the next free slot,
 // `take` waits for the oldest one, and run through `consume` multiplies it.  The
-// reads of a slot and their wait are one piece of assembly, so that they wait for
-// the slot's own loads (by the count of loads issued since) and not, as the
-// compiler would have it, for every load into LDS.
+// reads of a slot and their wait are one piece of assembly, so that between two
+// blocks of activations they wait for the slot's own loads (by the count of loads
+// issued since) and not, as the compiler would have it, for every load into LDS.
 template <int NF, int D>
 struct W4Ring {
     static_assert(NF == 1 || NF == 2, "one scale load covers two fragments");
