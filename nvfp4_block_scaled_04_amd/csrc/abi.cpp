@@ -1,10 +1,11 @@
-// abi.cpp -- the extern "C" entry points declared in include/nvfp4.h and
-// include/nvfp4_serving.h: argument validation (before anything is enqueued) and dispatch to the
+// abi.cpp -- the extern "C" entry points declared in include/nvfp4.h,
+// include/nvfp4_serving.h and include/nvfp4_attention.h: argument validation (before anything is enqueued) and dispatch to the
 // kernel launchers.  The library allocates no memory and keeps no state.
 #include <hip/hip_runtime.h>
 
 #include "../../include/nvfp4.h"
 #include "../../include/nvfp4_serving.h"
+#include "../../include/nvfp4_attention.h"
 #include "internal.h"
 
 namespace {
@@ -515,6 +516,129 @@ int nvfp4_gemm_adapters(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf,
     if (e != hipSuccess) return launch_status(e);
     g.r = r; g.ad_d = ad.d; g.ad_b = ad.lora_b; g.adapter = adapter; g.n_adapters = n_adapters;
     return launch_status(nvfp4::launch_gemm(g, (hipStream_t)stream));
+}
+
+static_assert(nvfp4::kRopeAxes == NVFP4_ROPE_MAX_AXES && 2 * nvfp4::kAttnParts == NVFP4_ATTENTION_MAX_SLOTS,
+              "the header's limits are the kernels'");
+
+// Rows of heads [t, heads, d] with a stride from token to token, in elements.
+static bool rows_ok(int64_t t, int64_t heads, int64_t d, int64_t stride) {
+    return dim_ok(t) && dim_ok(heads) && dim_ok(d) && heads * d <= NVFP4_ATTENTION_MAX_STRIDE && stride >= heads * d &&
+           stride <= NVFP4_ATTENTION_MAX_STRIDE && stride % 8 == 0;
+}
+
+int rope_axes(const void* x, int64_t x_stride, void* out, int64_t out_stride, int64_t t, int64_t heads, int64_t d,
+              const int32_t* positions, const float* inv_freq, const int32_t* sections, int axes, int interleaved,
+              void* stream) {
+    if (!x || !out || !positions || !inv_freq || !sections) return NVFP4_NULL_POINTER;
+    if (!rows_ok(t, heads, d, x_stride) || !rows_ok(t, heads, d, out_stride) || d % 16 != 0) return NVFP4_BAD_SHAPE;
+    if (axes < 1) return NVFP4_BAD_SHAPE;
+    if (axes > NVFP4_ROPE_MAX_AXES || d > NVFP4_ROPE_MAX_DIM) return NVFP4_UNSUPPORTED;
+    nvfp4::RopeArgs a{};
+    int64_t pairs = 0;
+    for (int i = 0; i < axes; i++) {
+        if (sections[i] < 0) return NVFP4_BAD_SHAPE;
+        a.sections[i] = sections[i];
+        pairs += sections[i];
+    }
+    if (pairs < 8 || pairs % 8 != 0 || 2 * pairs > d) return NVFP4_BAD_SHAPE;
+    if (!aligned16(x) || !aligned16(out) || ((uintptr_t)positions & 3u) || ((uintptr_t)inv_freq & 3u))
+        return NVFP4_MISALIGNED;
+    a.x = (const uint16_t*)x; a.out = (uint16_t*)out; a.positions = positions; a.inv_freq = inv_freq;
+    a.t = t; a.heads = heads; a.d = d; a.rot = 2 * pairs; a.x_stride = x_stride; a.out_stride = out_stride;
+    a.axes = axes; a.interleaved = interleaved != 0;
+    return launch_status(nvfp4::launch_rope_axes(a, (hipStream_t)stream));
+}
+
+// The cache's own sizes.
+static int cache_check(int64_t heads, int64_t d, int64_t pages, int64_t page) {
+    if (!dim_ok(heads) || !dim_ok(pages) || d < 32 || d % 32 != 0) return NVFP4_BAD_SHAPE;
+    if (page < 16 || (page & (page - 1)) != 0) return NVFP4_BAD_SHAPE;
+    if (d > NVFP4_KV_MAX_DIM || page > NVFP4_KV_MAX_PAGE || heads * d > NVFP4_ATTENTION_MAX_STRIDE) return NVFP4_UNSUPPORTED;
+    return NVFP4_OK;
+}
+
+static int kv_rows(bool read, const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t t,
+                   int64_t heads, int64_t d, const int32_t* slots, const float* kv_gs, uint8_t* kv, uint8_t* kv_sf,
+                   int64_t pages, int64_t page, void* stream) {
+    if (!k || !v || !slots || !kv_gs || !kv || !kv_sf) return NVFP4_NULL_POINTER;
+    const int st = cache_check(heads, d, pages, page);
+    if (st != NVFP4_OK) return st;
+    if (!rows_ok(t, heads, d, k_stride) || !rows_ok(t, heads, d, v_stride)) return NVFP4_BAD_SHAPE;
+    if (t * heads > ((int64_t)1 << 39) / d) return NVFP4_UNSUPPORTED;  // the grid: a thread per 16 elements of both
+    if (!aligned16(k) || !aligned16(v) || !aligned16(kv) || !aligned16(kv_sf) || ((uintptr_t)slots & 3u) ||
+        ((uintptr_t)kv_gs & 3u))
+        return NVFP4_MISALIGNED;
+    nvfp4::KvRowsArgs a{};
+    a.read = read;
+    a.k = (const uint16_t*)k; a.v = (const uint16_t*)v; a.k_out = (uint16_t*)k; a.v_out = (uint16_t*)v;
+    a.slots = slots; a.kv_gs = kv_gs; a.kv = kv; a.kv_sf = kv_sf;
+    a.t = t; a.heads = heads; a.d = d; a.pages = pages; a.page = page; a.k_stride = k_stride; a.v_stride = v_stride;
+    return launch_status(nvfp4::launch_kv_rows(a, (hipStream_t)stream));
+}
+
+int nvfp4_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t t, int64_t heads,
+                    int64_t d, const int32_t* slots, const float* kv_gs, uint8_t* kv, uint8_t* kv_sf, int64_t pages,
+                    int64_t page, void* stream) {
+    return kv_rows(false, k, k_stride, v, v_stride, t, heads, d, slots, kv_gs, kv, kv_sf, pages, page, stream);
+}
+
+int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, int64_t pages, int64_t page,
+                  const int32_t* slots, int64_t t, int64_t heads, int64_t d, void* k, int64_t k_stride, void* v,
+                  int64_t v_stride, void* stream) {
+    return kv_rows(true, k, k_stride, v, v_stride, t, heads, d, slots, kv_gs, (uint8_t*)kv, (uint8_t*)kv_sf, pages,
+                   page, stream);
+}
+
+static bool scale_ok(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
+
+int nvfp4_attention_decode(const void* q, int64_t b, int64_t t, int64_t q_heads, const uint8_t* kv,
+                           const uint8_t* kv_sf, const float* kv_gs, int64_t heads, int64_t d, int64_t pages,
+                           int64_t page, const int32_t* block_table, int64_t table_pages, const int32_t* lengths,
+                           float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
+                           void* stream) {
+    if (!q || !kv || !kv_sf || !kv_gs || !block_table || !lengths || !out || !workspace) return NVFP4_NULL_POINTER;
+    const int st = cache_check(heads, d, pages, page);
+    if (st != NVFP4_OK) return st;
+    if (!dim_ok(b) || !dim_ok(t) || !dim_ok(q_heads) || !dim_ok(table_pages) || q_heads % heads != 0)
+        return NVFP4_BAD_SHAPE;
+    if (!scale_ok(scale) || b > NVFP4_ATTENTION_MAX_BATCH || t > NVFP4_ATTENTION_MAX_TOKENS ||
+        q_heads * d > NVFP4_ATTENTION_MAX_STRIDE || table_pages > (((int64_t)1 << 30) / page))
+        return NVFP4_UNSUPPORTED;
+    const int64_t tiles = (t * (q_heads / heads) + 15) / 16;
+    if (b * heads * tiles > (int64_t)1 << 30) return NVFP4_UNSUPPORTED;  // the grid
+    if (workspace_bytes < NVFP4_ATTENTION_WS_BYTES(b, d)) return NVFP4_BAD_SHAPE;
+    if (!aligned16(q) || !aligned16(kv) || !aligned16(kv_sf) || !aligned16(out) || !aligned16(workspace) ||
+        ((uintptr_t)kv_gs & 3u) || ((uintptr_t)block_table & 3u) || ((uintptr_t)lengths & 3u) || ((uintptr_t)lse & 3u))
+        return NVFP4_MISALIGNED;
+    nvfp4::AttnDecodeArgs a{};
+    a.q = (const uint16_t*)q; a.kv = kv; a.kv_sf = kv_sf; a.kv_gs = kv_gs; a.block_table = block_table;
+    a.lengths = lengths; a.out = (uint16_t*)out; a.lse = lse; a.ws = workspace;
+    a.b = b; a.t = t; a.q_heads = q_heads; a.heads = heads; a.d = d; a.pages = pages; a.page = page;
+    a.table_pages = table_pages; a.scale = scale;
+    return launch_status(nvfp4::launch_attention_decode(a, (hipStream_t)stream));
+}
+
+int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t d,
+                      const int32_t* cu_q, const int32_t* cu_k, int64_t b, float scale, int causal, void* out,
+                      int64_t out_stride, float* lse, void* stream) {
+    if (!q || !k || !v || !cu_q || !cu_k || !out) return NVFP4_NULL_POINTER;
+    if (d < 16 || d % 16 != 0 || !rows_ok(tq, q_heads, d, q_stride) || !rows_ok(tk, heads, d, k_stride) ||
+        !rows_ok(tk, heads, d, v_stride) || !rows_ok(tq, q_heads, d, out_stride) || !dim_ok(b) || q_heads % heads != 0)
+        return NVFP4_BAD_SHAPE;
+    if (!scale_ok(scale) || d > NVFP4_KV_MAX_DIM || b > NVFP4_ATTENTION_MAX_BATCH ||
+        (tq / 32 + b) * q_heads > (int64_t)1 << 30)
+        return NVFP4_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)cu_q & 3u) ||
+        ((uintptr_t)cu_k & 3u) || ((uintptr_t)lse & 3u))
+        return NVFP4_MISALIGNED;
+    nvfp4::AttnPrefillArgs a{};
+    a.q = (const uint16_t*)q; a.k = (const uint16_t*)k; a.v = (const uint16_t*)v; a.out = (uint16_t*)out; a.lse = lse;
+    a.cu_q = cu_q; a.cu_k = cu_k; a.b = b; a.tq = tq; a.tk = tk; a.q_heads = q_heads; a.heads = heads; a.d = d;
+    a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.out_stride = out_stride;
+    a.scale = scale; a.causal = causal != 0;
+    return launch_status(nvfp4::launch_attention_prefill(a, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,364 @@
+// attention_prefill.hip -- attention of whole prompts, packed one after the
+// other: grouped heads, causal or full, keys that reach further back than the queries.
+//
+// For a query row i of a sequence, over the keys j that it sees:
+//   s_j = q_i . k_j, p_j = 2^(s_j * c - m), out_i = sum p_j v_j / sum p_j,
+// c = scale * log2(e), one pass over the keys with the running maximum m and sum.
+//
+// A workgroup of four waves takes 128 or 256 rows of one head, a wave 32 or 64 of them.
+// 64 keys and values at a time go straight from memory into LDS (two buffers), swizzled
+// at their source so that neither product's reads collide in the banks.  Both products run
+// on 32x32x16 bf16 MFMAs, transposed:
+//   S^T[key, row] = K Q^T: a lane owns one row (and half of the keys), so the softmax
+//   needs one exchange between lanes, and only where the maximum moves;
+//   O^T[column, row] = V^T P^T: V^T comes from transposing LDS reads, in the order of
+//   keys in which a lane holds its column of S^T, so P stays where it is.
+// Sums, maximum and both products' sums are fp32; P is rounded to bf16 (V's range is
+// bf16's), off by 2^-8 of itself at most, as the output is.
+#include "gemm_common.h"
+#include "internal.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kKeys = 64;  // keys of a tile
+
+struct PParams {
+    const uint16_t *q, *k, *v;
+    uint16_t* out;
+    float* lse;                // [tq, Hq] or null
+    const int32_t *cu_q, *cu_k;
+    int64_t q_stride, k_stride, v_stride, out_stride;
+    float c;                   // scale * log2(e)
+    int b, tq, tk, Hq, H, G, d, causal, units;
+};
+
+__device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
+
+__device__ __forceinline__ int clamp_to(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// A sequence's rows and keys; offsets that do not ascend or leave the tensors are clamped.
+struct Seq {
+    int q0, nq, k0, nk;
+};
+
+__device__ __forceinline__ Seq seq_at(const PParams& p, int i) {
+    Seq s;
+    s.q0 = clamp_to(p.cu_q[i], 0, p.tq);
+    s.nq = clamp_to(p.cu_q[i + 1], s.q0, p.tq) - s.q0;
+    s.k0 = clamp_to(p.cu_k[i], 0, p.tk);
+    s.nk = clamp_to(p.cu_k[i + 1], s.k0, p.tk) - s.k0;
+    return s;
+}
+
+// The sequence and tile of rows of unit `unit`; a sequence's last tiles, which have the
+// most keys, come first.
+template <int ROWS>
+__device__ __forceinline__ bool find_tile(const PParams& p, int unit, Seq& s, int& tile) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    for (int base = 0; base < p.b; base += 64) {
+        const int i = base + lane;
+        Seq mine = {};
+        if (i < p.b) mine = seq_at(p, i);
+        const int n = (mine.nq + ROWS - 1) / ROWS;
+        int sum = n;
+#pragma unroll
+        for (int o = 1; o < 64; o *= 2) {
+            const int a = __shfl_up(sum, o);
+            if (lane >= o) sum += a;
+        }
+        const uint64_t hit = __ballot(before + sum > unit);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            s.q0 = __builtin_amdgcn_readlane(mine.q0, l);
+            s.nq = __builtin_amdgcn_readlane(mine.nq, l);
+            s.k0 = __builtin_amdgcn_readlane(mine.k0, l);
+            s.nk = __builtin_amdgcn_readlane(mine.nk, l);
+            tile = before + __builtin_amdgcn_readlane(sum, l) - 1 - unit;
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
+}
+
+// 16-byte chunk c of row r of a staged tile lies in chunk c ^ swizzle(r): K so that 16
+// consecutive rows put one chunk into 16 bank groups, V so that four rows put
+// 64 bytes into four.
+template <int D>
+__device__ __forceinline__ int swizzle_k(int r) { return D == 64 ? (r >> 1) & 7 : r & 15; }
+template <int D>
+__device__ __forceinline__ int swizzle_v(int r) { return D == 64 ? (r & 2) << 1 : (r & 3) << 2; }
+
+// QT: tiles of 32 rows of a wave.
+template <int D, int QT>
+__global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int CH = D / 8;                   // chunks of a row
+    constexpr int TILE = kKeys * D * 2;         // bytes of a tile of K (of V)
+    constexpr int LOADS = kKeys * CH / kThreads;  // of a lane, of K (of V)
+    constexpr int ROWS = kWaves * QT * 32;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l32 = lane & 31, hi = lane >> 5;
+
+    // Workgroups are dealt to the 8 XCDs in turn: where the heads split evenly, an XCD
+    // has KV heads of its own, whose keys and values stay in its L2.
+    int head, unit;
+    if (p.H % 8 == 0) {
+        const int per = p.Hq / 8, r = blockIdx.x >> 3;
+        head = (blockIdx.x & 7) * per + r % per;
+        unit = r / per;
+    } else {
+        head = blockIdx.x % p.Hq;
+        unit = blockIdx.x / p.Hq;
+    }
+    Seq sq;
+    int tile;
+    if (!find_tile<ROWS>(p, unit, sq, tile)) return;
+    const int kv = head / p.G;
+    const int back = sq.nk - sq.nq;             // row i sees the keys up to i + back
+    const int row0 = tile * ROWS;
+    int keys = sq.nk;                           // that any row of the tile sees
+    if (p.causal) {
+        const int last = row0 + ROWS < sq.nq ? row0 + ROWS : sq.nq;
+        keys = clamp_to(last + back, 0, sq.nk);
+    }
+
+    const uint16_t* const kb = p.k + (int64_t)sq.k0 * p.k_stride + kv * p.d;
+    const uint16_t* const vb = p.v + (int64_t)sq.k0 * p.v_stride + kv * p.d;
+    auto stage = [&](int key0, int buf) {
+        const int rows = sq.nk - key0 < kKeys ? sq.nk - key0 : kKeys;  // at least 1; later rows come as zeros
+        const __amdgpu_buffer_rsrc_t rk = make_rsrc(kb + (int64_t)key0 * p.k_stride, (uint32_t)(((rows - 1) * p.k_stride + p.d) * 2));
+        const __amdgpu_buffer_rsrc_t rv = make_rsrc(vb + (int64_t)key0 * p.v_stride, (uint32_t)(((rows - 1) * p.v_stride + p.d) * 2));
+        lds_u8* const st = (lds_u8*)smem + buf * 2 * TILE;
+#pragma unroll
+        for (int i = 0; i < LOADS; i++) {
+            const int piece = (i * kWaves + wave) * 64 + lane;
+            const int r = piece / CH, at = piece % CH;
+            const int ck = at ^ swizzle_k<D>(r), cv = at ^ swizzle_v<D>(r);
+            const uint32_t ok = ck * 8 < p.d && r < rows ? (uint32_t)(r * (int)p.k_stride + ck * 8) * 2u : 0xFFFFFFF0u;
+            const uint32_t ov = cv * 8 < p.d && r < rows ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (__attribute__((address_space(3))) void*)(st + (i * kWaves + wave) * 1024), 16, ok, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (__attribute__((address_space(3))) void*)(st + TILE + (i * kWaves + wave) * 1024), 16, ov, 0, 0, 0);
+        }
+    };
+    if (keys > 0) stage(0, 0);
+
+    // the wave's queries, and what each row sees
+    const int first = row0 + wave * QT * 32;
+    bf16x8 q[QT][D / 16];
+    int end[QT];                                // keys below it are seen
+#pragma unroll
+    for (int t = 0; t < QT; t++) {
+        const int i = first + t * 32 + l32;
+        end[t] = i >= sq.nq ? 0 : p.causal ? clamp_to(i + back + 1, 0, sq.nk) : sq.nk;
+        const uint16_t* const src = p.q + (int64_t)(sq.q0 + (i < sq.nq ? i : 0)) * p.q_stride + head * p.d;
+#pragma unroll
+        for (int s = 0; s < D / 16; s++) {
+            u32x4 w = {};
+            if (i < sq.nq && 16 * s + 8 * hi < p.d) w = *(const u32x4*)(src + 16 * s + 8 * hi);
+            q[t][s] = __builtin_bit_cast(bf16x8, w);
+        }
+    }
+    // keys that all rows of the wave see, and that any sees (rows past the sequence count as its last)
+    int all = sq.nk, any = sq.nk;
+    if (p.causal) {
+        all = clamp_to(first + back + 1, 0, sq.nk);
+        any = clamp_to((first + QT * 32 < sq.nq ? first + QT * 32 : sq.nq) + back, 0, sq.nk);
+    }
+    if (first >= sq.nq) any = 0;
+
+    f32x16 o[QT][D / 32];
+    float m[QT], l[QT];
+#pragma unroll
+    for (int t = 0; t < QT; t++) {
+        m[t] = neg_inf();
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; i++) o[t][i] = f32x16{};
+    }
+
+    // a lane's addresses in the tiles: K rows l32 (+ 32), V rows 4 hi + (lane & 15) / 4 (+ 8 i)
+    const int vr = (lane & 15) >> 2;
+    int vat[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; i++) {
+        const int c = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+        vat[i] = (4 * hi + vr) * D * 2 + (c ^ swizzle_v<D>(vr)) * 16 + (lane & 1) * 8;
+    }
+
+    for (int key0 = 0, buf = 0; key0 < keys; key0 += kKeys, buf ^= 1) {
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the tile is there, the other buffer has been read
+        if (key0 + kKeys < keys) stage(key0 + kKeys, buf ^ 1);
+        if (key0 >= any) continue;
+        lds_u8* const kt = (lds_u8*)smem + buf * 2 * TILE;
+        lds_u8* const vt = kt + TILE;
+        const bool masked = key0 + kKeys > all;
+
+        f32x16 s[QT][2];
+#pragma unroll
+        for (int j = 0; j < 2; j++) {
+#pragma unroll
+            for (int t = 0; t < QT; t++) s[t][j] = f32x16{};
+#pragma unroll
+            for (int i = 0; i < D / 16; i++) {
+                const int r = 32 * j + l32;
+                const bf16x8 a = *(const __attribute__((address_space(3))) bf16x8*)(kt + r * D * 2 + ((2 * i + hi) ^ swizzle_k<D>(r)) * 16);
+#pragma unroll
+                for (int t = 0; t < QT; t++) s[t][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[t][i], s[t][j], 0, 0, 0);
+            }
+        }
+        bf16x8 pf[QT][4];
+#pragma unroll
+        for (int t = 0; t < QT; t++) {
+            if (masked) {
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        if (key0 + 32 * j + 8 * (e >> 2) + 4 * hi + (e & 3) >= end[t]) s[t][j][e] = neg_inf();
+            }
+            float top = s[t][0][0];
+#pragma unroll
+            for (int e = 1; e < 32; e++) top = __builtin_fmaxf(top, s[t][e >> 4][e & 15]);
+            top *= p.c;
+            // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the
+            // row alone, so that its bits do not depend on the rows beside it)
+            if (__any(top > m[t] + 8.0f)) {
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+                const float to = top > m[t] + 8.0f ? top : m[t];
+                const float a = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m[t] - to);
+                m[t] = to;
+                l[t] *= a;
+#pragma unroll
+                for (int i = 0; i < D / 32; i++) o[t][i] *= a;
+            }
+            const float base = m[t] == neg_inf() ? 0.0f : m[t];
+            float sum = 0.0f;
+#pragma unroll
+            for (int f = 0; f < 4; f++) {
+                u32x4 w;
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][f >> 1][8 * (f & 1) + 2 * e], p.c, -base));
+                    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][f >> 1][8 * (f & 1) + 2 * e + 1], p.c, -base));
+                    sum += p0 + p1;
+                    w[e] = pack_bf16x2(p0, p1);
+                }
+                pf[t][f] = __builtin_bit_cast(bf16x8, w);
+            }
+            l[t] += sum;
+        }
+
+        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+        auto v_frag = [&](int f, int i) {  // keys 16 f .. 16 f + 15, columns 32 i ..
+            typedef short s16x4 __attribute__((ext_vector_type(4)));
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + 16 * f * D * 2));
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + (16 * f + 8) * D * 2));
+            const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
+            return bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        };
+        bool odd = false;  // a value that is not finite behind a mask: 0 times it would not be 0
+        if (masked && p.causal) {
+            u16x2 big = {};
+#pragma unroll 1
+            for (int i = lane; i < TILE / 16; i += 64) {
+                const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i * 16);
+#pragma unroll
+                for (int e = 0; e < 4; e++) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, w[e] & 0x7FFF7FFFu));
+            }
+            odd = __any((big[0] > big[1] ? big[0] : big[1]) >= 0x7F80);
+        }
+        if (!odd) {
+#pragma unroll
+            for (int f = 0; f < 4; f++)
+#pragma unroll
+                for (int i = 0; i < D / 32; i++) {
+                    const bf16x8 a = v_frag(f, i);
+#pragma unroll
+                    for (int t = 0; t < QT; t++) o[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pf[t][f], o[t][i], 0, 0, 0);
+                }
+        } else {
+            // finite values through the product; the others go to the rows that see them
+#pragma unroll 1
+            for (int f = 0; f < 4; f++)
+#pragma unroll
+                for (int i = 0; i < D / 32; i++) {
+                    u32x4 w = __builtin_bit_cast(u32x4, v_frag(f, i));
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                        if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+                    }
+#pragma unroll
+                    for (int t = 0; t < QT; t++) {
+                        bf16x8 pv = pf[t][0];
+                        pv = f == 1 ? pf[t][1] : f == 2 ? pf[t][2] : f == 3 ? pf[t][3] : pv;
+                        o[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), pv, o[t][i], 0, 0, 0);
+                    }
+                }
+#pragma unroll 1
+            for (int r = 0; r < kKeys; r++)
+#pragma unroll
+                for (int i = 0; i < D / 32; i++)
+#pragma unroll
+                    for (int e = 0; e < 16; e++) {
+                        const int col = 32 * i + 8 * (e >> 2) + 4 * hi + (e & 3);
+                        const uint16_t bits = *(const __attribute__((address_space(3))) uint16_t*)(
+                            vt + r * D * 2 + ((col >> 3) ^ swizzle_v<D>(r)) * 16 + (col & 7) * 2);
+#pragma unroll
+                        for (int t = 0; t < QT; t++)
+                            if ((bits & 0x7F80) == 0x7F80 && key0 + r < end[t]) o[t][i][e] += bits_f((uint32_t)bits << 16);
+                    }
+        }
+    }
+
+#pragma unroll
+    for (int t = 0; t < QT; t++) {
+        const int i = first + t * 32 + l32;
+        const float den = l[t] + __shfl_xor(l[t], 32);
+        const float by = den == 0.0f ? 0.0f : 1.0f / den;
+        if (i >= sq.nq) continue;
+        uint16_t* const dst = p.out + (int64_t)(sq.q0 + i) * p.out_stride + head * p.d;
+#pragma unroll
+        for (int c = 0; c < D / 32; c++)
+#pragma unroll
+            for (int e = 0; e < 16; e += 4) {
+                const int col = 32 * c + 2 * e + 4 * hi;
+                if (col < p.d)
+                    *(u32x2*)(dst + col) = u32x2{pack_bf16x2(o[t][c][e] * by, o[t][c][e + 1] * by),
+                                                 pack_bf16x2(o[t][c][e + 2] * by, o[t][c][e + 3] * by)};
+            }
+        if (p.lse && hi == 0) p.lse[(int64_t)(sq.q0 + i) * p.Hq + head] = (m[t] + __builtin_log2f(den)) * 0.69314718055994530942f;
+    }
+#endif
+}
+
+template <int D, int QT>
+hipError_t launch(PParams& p, hipStream_t st) {
+    constexpr int ROWS = kWaves * QT * 32;
+    p.units = p.tq / ROWS + p.b;  // tiles that no sequence has return at once
+    k_attn_prefill<D, QT><<<dim3((unsigned)((int64_t)p.units * p.Hq)), kThreads, 4 * kKeys * D * 2, st>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
+    PParams p{};
+    p.q = a.q; p.k = a.k; p.v = a.v; p.out = a.out; p.lse = a.lse; p.cu_q = a.cu_q; p.cu_k = a.cu_k;
+    p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride; p.out_stride = a.out_stride;
+    p.c = a.scale * 1.44269504088896340736f;
+    p.b = (int)a.b; p.tq = (int)a.tq; p.tk = (int)a.tk; p.Hq = (int)a.q_heads; p.H = (int)a.heads;
+    p.G = p.Hq / p.H; p.d = (int)a.d; p.causal = a.causal;
+    if (a.d <= 64) return launch<64, 1>(p, st);
+    if (a.d <= 128) return launch<128, 1>(p, st);
+    return launch<256, 1>(p, st);
+}
+
+}  // namespace nvfp4

@@ -150,6 +150,61 @@ hipError_t launch_adapter_down(const AdapterArgs& a, hipStream_t st);
 hipError_t launch_w4a16_adapters(const AdapterArgs& a, const uint8_t* b, const uint8_t* b_sf, const float* alpha,
                                  const uint16_t* bias, uint16_t* out, float* part, hipStream_t st);
 
+// Rotary positions with several axes.
+constexpr int kRopeAxes = 4;
+struct RopeArgs {
+    const uint16_t* x;         // [t, heads, d], x_stride elements from token to token
+    uint16_t* out;             // the same shape (may be x)
+    const int32_t* positions;  // [axes, t]
+    const float* inv_freq;     // [rot / 2]
+    int64_t t, heads, d, rot, x_stride, out_stride;
+    int axes;
+    int sections[kRopeAxes];   // pairs of an axis
+    bool interleaved;
+};
+hipError_t launch_rope_axes(const RopeArgs& a, hipStream_t st);
+
+// Rows of the paged NVFP4 cache: kv [pages, 2, heads, page, d/2], kv_sf [pages, 2, heads, d/16, page].
+struct KvRowsArgs {
+    bool read;                 // cache -> k_out, v_out, else k, v -> cache
+    const uint16_t *k, *v;     // [t, heads, d], strides in elements from token to token
+    uint16_t *k_out, *v_out;
+    const int32_t* slots;      // [t]
+    const float* kv_gs;        // [2]
+    uint8_t *kv, *kv_sf;
+    int64_t t, heads, d, pages, page, k_stride, v_stride;
+};
+hipError_t launch_kv_rows(const KvRowsArgs& a, hipStream_t st);
+
+// Attention of t tokens a sequence over the paged NVFP4 cache.
+constexpr int64_t kAttnParts = 512;    // parts that the tokens of all sequences are split into, about
+constexpr int64_t kAttnMinPart = 256;  // fewest tokens of a part
+struct AttnDecodeArgs {
+    const uint16_t* q;         // [b, t, q_heads, d]
+    const uint8_t *kv, *kv_sf;
+    const float* kv_gs;        // [2]
+    const int32_t* block_table;  // [b, table_pages]
+    const int32_t* lengths;    // [b]
+    uint16_t* out;
+    float* lse;                // [b, t, q_heads] or null
+    void* ws;                  // NVFP4_ATTENTION_WS_BYTES
+    int64_t b, t, q_heads, heads, d, pages, page, table_pages;
+    float scale;
+};
+hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st);
+
+// Attention of packed prompts.
+struct AttnPrefillArgs {
+    const uint16_t *q, *k, *v; // [tq, q_heads, d], [tk, heads, d], strides from token to token
+    uint16_t* out;
+    float* lse;                // [tq, q_heads] or null
+    const int32_t *cu_q, *cu_k;  // [b + 1]
+    int64_t b, tq, tk, q_heads, heads, d, q_stride, k_stride, v_stride, out_stride;
+    float scale;
+    int causal;
+};
+hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st);
+
 // MX setting (32-element blocks, ue8m0 scales, no global scale).
 struct MxQuantizeArgs {
     const void* x;        // [m, k] bf16 or fp32

@@ -1,0 +1,139 @@
+"""Attention of packed prompts against its 64-bit form."""
+import pytest
+import torch
+
+import attention_ref as A
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+HALF_STEP, TINY = 2.0 ** -8, 0.0   # bf16 probabilities
+
+
+@pytest.fixture(scope="module")
+def att():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    from nvfp4_block_scaled_04_amd import attention
+    return attention
+
+
+def starts(lens, first=0):
+    return torch.tensor([first] + list(lens), dtype=torch.int32, device="cuda").cumsum(0).int()
+
+
+def check(q, k, v, cu_q, cu_k, causal, out, lse=None, scale=None):
+    d, q_heads, heads = q.shape[2], q.shape[1], k.shape[1]
+    scale = d ** -0.5 if scale is None else scale
+    a, c = cu_q.tolist(), cu_k.tolist()
+    for i in range(len(a) - 1):
+        n, m = a[i + 1] - a[i], c[i + 1] - c[i]
+        j = torch.arange(m, device="cuda")
+        lim = torch.arange(n, device="cuda") + m - n if causal else torch.full((n,), m, device="cuda")
+        seen = j <= lim[:, None]
+        for h in range(q_heads):
+            kk, vv = (x[c[i]:c[i + 1], h // (q_heads // heads)].double() for x in (k, v))
+            ref, rl, bound, dl = A.attend(q[a[i]:a[i + 1], h].double(), kk, vv, scale, seen, HALF_STEP, TINY)
+            got = out[a[i]:a[i + 1], h]
+            assert bool(got.isfinite().all()), (i, h)
+            assert A.worst(got, ref, bound) <= 1.0, (i, h, n, m, A.worst(got, ref, bound))
+            if lse is not None:
+                assert A.same_lse(lse[a[i]:a[i + 1], h], rl, dl), (i, h)
+
+
+def inputs(lq, lk, q_heads, heads, d, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    tq, tk = max(1, sum(lq)), max(1, sum(lk))
+    r = lambda t, h: torch.randn(t, h, d, device="cuda", generator=g).bfloat16()  # noqa: E731
+    return r(tq, q_heads), r(tk, heads), r(tk, heads), starts(lq), starts(lk)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,q_heads,heads,d", [
+    ((1,), (1,), 1, 1, 16), ((1,), (1,), 32, 8, 128), ((61,), (61,), 32, 8, 128), ((64,), (64,), 4, 2, 64), ((65, 127, 1, 128), (65, 127, 1, 128), 6, 3, 128),
+    ((0, 7, 0, 33), (0, 7, 5, 33), 2, 1, 64), ((5, 9), (0, 9), 2, 2, 128), ((10, 300), (4, 100), 3, 1, 128), ((129, 255, 256, 257), (129, 255, 256, 257), 2, 2, 96),
+    ((1, 1, 40), (700, 129, 1100), 8, 2, 128), ((200,), (1500,), 5, 1, 64), ((70, 3), (70, 259), 2, 1, 256), ((90,), (200,), 2, 2, 224), ((33, 200), (33, 200), 7, 7, 80),
+    ((1000,), (1000,), 10, 2, 128), ((513, 700), (600, 701), 3, 3, 64), ((2500,), (2500,), 2, 1, 128),
+])
+def test_prefill(att, lq, lk, q_heads, heads, d, causal):
+    say("prefill", lq, lk, q_heads, heads, d, causal)
+    q, k, v, cq, ck = inputs(lq, lk, q_heads, heads, d, sum(lk) + d)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    out = att.attention_prefill(q, k, v, cq, ck, causal=causal, lse=lse)
+    check(q, k, v, cq, ck, causal, out, lse)
+    again = torch.full_like(out, float("nan"))
+    att.attention_prefill(q, k, v, cq, ck, causal=causal, out=again)
+    assert torch.equal(out[:sum(lq)], again[:sum(lq)])
+
+
+def test_many_sequences(att):
+    lens = [(i * 29) % 83 for i in range(150)]
+    say("prefill 150 sequences")
+    q, k, v, cq, ck = inputs(lens, lens, 2, 1, 64, 3)
+    check(q, k, v, cq, ck, True, att.attention_prefill(q, k, v, cq))
+
+
+def test_strides_and_rows_outside(att):
+    """q, k, v as parts of one projection's output, sequences that leave rows before and behind."""
+    say("prefill strides")
+    g = torch.Generator(device="cuda").manual_seed(0)
+    qkv = torch.randn(400, 6 + 2 + 2, 128, device="cuda", generator=g).bfloat16()
+    q, k, v = qkv[:, :6], qkv[:, 6:8], qkv[:, 8:]
+    cu = starts((100, 150), first=30)
+    wide = torch.full((400, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = att.attention_prefill(q, k, v, cu, out=wide[:, 1:7])
+    assert out.data_ptr() == wide[:, 1:7].data_ptr()
+    check(q, k, v, cu, cu, True, out)
+    assert bool((wide[:30] == 7).all()) and bool((wide[280:] == 7).all()) and bool((wide[:, 0] == 7).all()) and bool((wide[:, 7] == 7).all())
+
+
+def test_scale_and_peaks(att):
+    say("prefill peaks")
+    q, k, v, cq, ck = inputs((300,), (300,), 4, 2, 128, 8)
+    q[:, 0] *= 30
+    q[:, 1] = 0
+    k[150] *= 20
+    for scale in (0.5, 1e-5):
+        lse = torch.empty(q.shape[:2], device="cuda")
+        check(q, k, v, cq, ck, True, att.attention_prefill(q, k, v, cq, ck, scale=scale, lse=lse), lse, scale=scale)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_values_behind_the_mask_do_not_matter(att, bad):
+    """Rows before a key or value that is not finite, and other sequences, come out as without it."""
+    say("prefill behind the mask", bad)
+    for d in (64, 128, 256):
+        q, k, v, cq, ck = inputs((200, 90), (200, 90), 2, 1, d, 11)
+        clean = att.attention_prefill(q, k, v, cq, ck)
+        at = 133
+        for which in (k, v):
+            x = which.clone()
+            x[at, 0, 7] = bad
+            out = att.attention_prefill(q, x if which is k else k, x if which is v else v, cq, ck)
+            assert torch.equal(out[:at], clean[:at]), (d, which is k)
+            assert torch.equal(out[200:], clean[200:]), (d, which is k)
+            if which is v:
+                assert not bool(out[at:200, :, 7].isfinite().any())
+                keep = torch.ones(d, dtype=torch.bool)
+                keep[7] = False
+                assert torch.equal(out[at:200][..., keep], clean[at:200][..., keep])
+
+
+def test_neighbours_do_not_matter(att):
+    """Keys of the next sequence lie right behind and are all NaN."""
+    say("prefill neighbours")
+    q, k, v, cq, ck = inputs((70, 60), (70, 60), 2, 2, 128, 12)
+    for causal in (True, False):
+        clean = att.attention_prefill(q, k, v, cq, ck, causal=causal)
+        k2, v2 = k.clone(), v.clone()
+        k2[70:], v2[70:] = float("nan"), float("nan")
+        out = att.attention_prefill(q, k2, v2, cq, ck, causal=causal)
+        assert torch.equal(out[:70], clean[:70]) and bool(out[70:].isnan().all())
+
+
+def test_offsets_outside_the_tensors(att):
+    """Starts that leave the tensors are clamped."""
+    say("prefill clamped")
+    q, k, v, cq, ck = inputs((70, 60), (70, 60), 2, 2, 64, 13)
+    want = att.attention_prefill(q, k, v, cq, ck)
+    cq[2], ck[2], cq[0] = 1 << 30, 1000, -5
+    assert torch.equal(att.attention_prefill(q, k, v, cq, ck), want)

@@ -1,0 +1,145 @@
+"""Rotary positions with several axes, and rows written to and read from the NVFP4 cache,
+against 64-bit forms and the framework's own quantizer."""
+import pytest
+import torch
+
+import attention_ref as A
+import serving_ref as R
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def att():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    from nvfp4_block_scaled_04_amd import attention
+    return attention
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def freqs(n, base=1e4):
+    return (base ** -(torch.arange(n, device="cuda", dtype=torch.float64) / n)).float()
+
+
+# The pair's sum has two products and one addition in fp32 (2^-22 of |x1| + |x2|), cos and
+# sin are off by 2^-22 (an angle rounded to fp32 within half a turn, and their own error),
+# then the output's half step.
+def rope_ok(y, x, ref, pos, freq, sections, inter):
+    n = sum(sections)
+    p, q = (slice(0, 2 * n, 2), slice(1, 2 * n, 2)) if inter else (slice(0, n), slice(n, 2 * n))
+    size = torch.zeros_like(ref)
+    both = x[..., p].double().abs() + x[..., q].double().abs()
+    size[..., p], size[..., q] = both, both
+    bound = size * 2.0 ** -20 + (ref.abs() + size * 2.0 ** -20) * 2.0 ** -8 + 1e-38
+    return A.worst(y, ref, bound) <= 1.0
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("t,heads,d,sections", [
+    (1, 1, 16, (8,)), (1, 40, 128, (64,)), (16, 40, 128, (16, 24, 24)), (77, 3, 64, (8, 8)), (5, 7, 80, (10, 15, 15)),
+    (1000, 2, 256, (44, 42, 42)), (333, 24, 128, (22, 21, 21)), (9, 5, 96, (3, 0, 5)), (4099, 1, 64, (5, 9, 10, 8)), (3, 4, 1024, (512,)),
+])
+def test_rope(att, t, heads, d, sections, inter):
+    say("rope", t, heads, d, sections, inter)
+    g = gen(t + d)
+    n = sum(sections)
+    wide = torch.randn(t, heads + 2, d, device="cuda", generator=g).bfloat16()
+    x = wide[:, 1:heads + 1] if d % 8 == 0 else wide
+    pos = torch.randint(-50, 1 << 20, (len(sections), t), device="cuda", generator=g, dtype=torch.int32)
+    freq = freqs(n)
+    ref = A.rope(x, pos, freq, sections, inter)
+    y = att.rope_axes(x, pos, freq, sections, interleaved=inter)
+    assert rope_ok(y, x, ref, pos, freq, sections, inter)
+    assert torch.equal(y[..., 2 * n:], x[..., 2 * n:])
+    # in place, in a part of a wider tensor whose other heads stay as they were
+    kept = wide.clone()
+    assert att.rope_axes(x, pos, freq, sections, interleaved=inter, out=x) is x
+    assert torch.equal(x, y)
+    assert torch.equal(wide[:, 0], kept[:, 0]) and torch.equal(wide[:, heads + 1:], kept[:, heads + 1:])
+
+
+def test_rope_position_zero_and_specials(att):
+    say("rope specials")
+    x = torch.randn(4, 2, 32, device="cuda").bfloat16()
+    x[1, 0, 3] = float("inf")
+    x[2, 1, 20] = float("nan")
+    pos = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    y = att.rope_axes(x, pos, freqs(16), (16,))
+    ok = x.isfinite()
+    ok[1, 0, 19] = False   # inf * sin(0) in the partner
+    ok[2, 1, 4] = False
+    assert torch.equal(y[ok], x[ok])
+    assert not y[2, 1, 20].isfinite() and not y[1, 0, 3].isfinite()
+    far = torch.tensor([[2 ** 31 - 1, -2 ** 31, 1, 0]], dtype=torch.int32, device="cuda")
+    x = torch.randn(4, 2, 32, device="cuda").bfloat16()
+    assert rope_ok(att.rope_axes(x, far, freqs(16), (16,)), x, A.rope(x, far, freqs(16), (16,), False), far, None, (16,), False)
+
+
+def cache(pages, heads, page, d, fill=0xFF):
+    return (torch.full((pages, 2, heads, page, d // 2), fill, dtype=torch.uint8, device="cuda"),
+            torch.full((pages, 2, heads, d // 16, page), fill, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("t,heads,d,page", [(1, 1, 32, 16), (1, 8, 128, 64), (16, 8, 128, 16), (37, 3, 64, 32), (500, 2, 96, 128),
+                                            (1001, 5, 256, 64), (130, 1, 160, 16), (8003, 8, 128, 16)])
+def test_append_and_read(att, t, heads, d, page):
+    from nvfp4_block_scaled_04_amd import ops
+    say("append", t, heads, d, page)
+    g = gen(t * 3 + d)
+    wide = torch.randn(t, 3 * heads, d, device="cuda", generator=g).bfloat16()
+    wide[:, :, 0] *= 50
+    if t > 4:
+        wide[0] = 0
+        wide[1, :, 5] = float("inf")
+        wide[2, :, 17] = float("nan")
+        wide[3] *= 1e-30
+    k, v = wide[:, heads:2 * heads], wide[:, 2 * heads:]
+    gs = torch.tensor([2688 / 200.0, 2688 / 3.7], device="cuda")
+    pages = -(-t // page) + 2
+    slots = torch.randperm(pages * page, device="cuda", generator=g)[:t].int()
+    dead = torch.zeros(t, dtype=torch.bool, device="cuda")
+    dead[t // 2::7] = t > 1
+    slots[dead] = torch.tensor([-1, pages * page, -2 ** 31, 2 ** 31 - 1], dtype=torch.int32, device="cuda").repeat(t)[:int(dead.sum())]
+    kv, sf = cache(pages, heads, page, d)
+    att.nvfp4_kv_append(k, v, slots, gs, kv, sf)
+    live = (~dead).nonzero()[:, 0]
+    touched = torch.zeros(pages * page, dtype=torch.bool, device="cuda")
+    touched[slots[live].long()] = True
+    for which, x in enumerate((k, v)):
+        fp4, swz, _ = ops.nvfp4_quantize(x.reshape(t * heads, d).contiguous(), global_scale=gs[which:which + 1].clone(), gs_mode=ops.GS_STATIC)
+        want = fp4.view(t, heads, d // 2)
+        want_sf = swz[R.sf_index(t * heads, d)].view(t, heads, d // 16)
+        at, off = slots[live].long() // page, slots[live].long() % page
+        assert torch.equal(kv[at, which, :, off], want[live])
+        assert torch.equal(sf[at, which, :, :, off], want_sf[live])
+        # nothing else was written
+        rest = (~touched).nonzero()[:, 0]
+        assert bool((kv[rest // page, which, :, rest % page] == 0xFF).all()) and bool((sf[rest // page, which, :, :, rest % page] == 0xFF).all())
+    out = torch.full((t, 2 * heads, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    ko, vo = att.nvfp4_kv_read(slots, gs, kv, sf, k=out[:, :heads], v=out[:, heads:])
+    for which, o in enumerate((ko, vo)):
+        want = (A.rows(kv, sf, which, slots[live]).float() / gs[which]).bfloat16()
+        assert torch.equal(o[live], want)
+        assert bool((o[dead] == 7).all())
+    ko, vo = att.nvfp4_kv_read(slots, gs, kv, sf)
+    assert torch.equal(ko[live], out[live, :heads]) and bool((ko[dead] == 0).all()) and bool((vo[dead] == 0).all())
+
+
+def test_read_division_is_rounded(att):
+    """bf16 of the correctly rounded fp32 quotient, for every code and scale and many gs."""
+    say("read all codes")
+    kv, sf = cache(16, 1, 16, 32, 0)
+    flat, fsf = kv.view(16, 2, 16, 16), sf.view(16, 2, 2, 16)
+    flat[:] = torch.arange(16, dtype=torch.uint8, device="cuda").repeat(16).view(16, 16) * 16 + torch.arange(16, dtype=torch.uint8, device="cuda")
+    fsf[:] = torch.arange(512, device="cuda").remainder(127).to(torch.uint8).view(16, 2, 16).unsqueeze(1)
+    slots = torch.arange(256, dtype=torch.int32, device="cuda")
+    for i in range(40):
+        gs = (torch.rand(2, device="cuda", generator=gen(i)) * 10.0 ** (i % 9 - 3)) + 1e-3
+        k, v = att.nvfp4_kv_read(slots, gs, kv, sf)
+        for which, o in enumerate((k, v)):
+            assert torch.equal(o, (A.rows(kv, sf, which, slots).float() / gs[which]).bfloat16())
