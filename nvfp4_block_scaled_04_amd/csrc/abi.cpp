@@ -606,7 +606,7 @@ int nvfp4_attention_decode(const void* q, int64_t b, int64_t t, int64_t q_heads,
         q_heads * d > NVFP4_ATTENTION_MAX_STRIDE || table_pages > (((int64_t)1 << 30) / page))
         return NVFP4_UNSUPPORTED;
     const int64_t tiles = (t * (q_heads / heads) + 15) / 16;
-    if (b * heads * tiles > (int64_t)1 << 30) return NVFP4_UNSUPPORTED;  // the grid
+    if (b * heads * tiles > (int64_t)1 << 30 || b * t * q_heads > (int64_t)1 << 30) return NVFP4_UNSUPPORTED;  // the grids
     if (workspace_bytes < NVFP4_ATTENTION_WS_BYTES(b, d)) return NVFP4_BAD_SHAPE;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(kv_sf) || !aligned16(out) || !aligned16(workspace) ||
         ((uintptr_t)kv_gs & 3u) || ((uintptr_t)block_table & 3u) || ((uintptr_t)lengths & 3u) || ((uintptr_t)lse & 3u))

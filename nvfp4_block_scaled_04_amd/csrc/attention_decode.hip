@@ -27,7 +27,6 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kBlock = 64;        // tokens a wave takes at a time
 constexpr int kRows = 16;         // query rows of a workgroup
-constexpr int kStages = 2;
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
@@ -51,16 +50,27 @@ struct Stage {
     static constexpr int CODES = kBlock * D / 2;                // bytes of K (of V)
     static constexpr int SF = D / 16 * kBlock;                  // bytes of K's scales (of V's)
     static constexpr int OFF_V = CODES, OFF_SF = 2 * CODES;
-    static constexpr int LOADS = 2 * CODES / 1024, SF_LOADS = (2 * SF + 1023) / 1024;
+    static constexpr int SF_LOADS = (2 * SF + 1023) / 1024;
     static constexpr int BYTES = 2 * CODES + SF_LOADS * 1024;
-    static constexpr int WAVE = kStages * BYTES + 4 * SF;       // the ring, then the scales as fp16
+    static constexpr int WAVE = BYTES + 2 * SF;                 // the block, then V's scales as fp16
 };
+
+// V's 16-byte chunk c of row r lies in chunk c ^ swizzle(r), so that the 16 rows of a
+// transposing read lie in different banks.
+template <int D>
+__device__ __forceinline__ int swizzle(int r) { return (r / (512 / D)) & (D / 32 - 1); }
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-__device__ __forceinline__ int64_t wave_sum64(int64_t v) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
+// Inclusive prefix sum over a wave, through DPP: 4 shifts within rows of 16, then the
+// rows' last values to the rows behind.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
     return v;
 }
 
@@ -77,39 +87,29 @@ __device__ __forceinline__ int seq_len(const DParams& p, int i) {
     return v < 0 ? 0 : v > p.cap ? p.cap : v;
 }
 
-__device__ __forceinline__ int parts_of(int len, int64_t chunk) {
-    const int n = (int)((len + chunk - 1) / chunk);
-    return n < 1 ? 1 : n;
-}
-
 __device__ __forceinline__ bool find_work(const DParams& p, Work& w) {
     const int lane = threadIdx.x & 63;
     const int hrs = p.H * p.row_tiles;
     const int unit = blockIdx.x / hrs;
     w.hr = blockIdx.x - unit * hrs;
-    int64_t total = 0;
+    int64_t total = 0;  // in blocks; 64 lengths add up to less than 2^31
     int first = 0;
-    for (int i = lane; i < p.b; i += 64) {
-        const int v = seq_len(p, i);
-        if (i == lane) first = v;
-        total += v;
+    for (int base = 0; base < p.b; base += 64) {
+        const int v = base + lane < p.b ? seq_len(p, base + lane) : 0;
+        if (base == 0) first = v;
+        total += __builtin_amdgcn_readlane(wave_scan((v + kBlock - 1) / kBlock), 63);
     }
-    total = wave_sum64(total);
-    int64_t chunk = (total * hrs + kAttnParts - 1) / kAttnParts;
-    chunk = chunk < kAttnMinPart ? kAttnMinPart : chunk;
-    chunk = (chunk + kBlock - 1) / kBlock * kBlock;
+    int64_t chunk64 = (total * hrs + kAttnParts - 1) / kAttnParts;
+    chunk64 = chunk64 < kAttnMinPart / kBlock ? kAttnMinPart / kBlock : chunk64;
+    const uint32_t chunk = chunk64 > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)chunk64;
     int before = 0, slots = 0;
     for (int base = 0; base < p.b; base += 64) {
         const int i = base + lane;
-        const int len = i < p.b ? (base ? seq_len(p, i) : first) : 0;
-        const int n = i < p.b ? parts_of(len, chunk) : 0;
+        const int len = base == 0 ? first : i < p.b ? seq_len(p, i) : 0;
+        const uint32_t blocks = (uint32_t)(len + kBlock - 1) / kBlock;
+        const int n = i < p.b ? (blocks <= chunk ? 1 : (int)((blocks + chunk - 1) / chunk)) : 0;
         const int m = n > 1 ? n : 0;
-        int sn = n, sm = m;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const int a = __shfl_up(sn, o), c = __shfl_up(sm, o);
-            if (lane >= o) { sn += a; sm += c; }
-        }
+        const int sn = wave_scan(n), sm = wave_scan(m);
         const uint64_t hit = __ballot(before + sn > unit);
         if (hit) {
             const int l = __builtin_ctzll(hit);
@@ -126,69 +126,58 @@ __device__ __forceinline__ bool find_work(const DParams& p, Work& w) {
     return false;
 }
 
-// Pages of a block's four groups of 16 tokens; bits of `bad`: a group behind the part's end
-// or on no page (its loads go to page 0).
-struct Pages {
-    int id[4];
-    uint32_t bad;
-};
-
-__device__ __forceinline__ Pages find_pages(const DParams& p, const int32_t* pages, int tok, int end) {
-    // constant memory to the compiler, so that the uniform reads are scalar ones
-    const auto* const row = (const __attribute__((address_space(4))) int32_t*)pages;
-    Pages g;
-    g.bad = 0;
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int t = tok + 16 * i;
-        const int at = t < end ? t : end - 1;
-        int id = row[at < 0 ? 0 : at >> p.page_log2];
-        if (t >= end || (uint32_t)id >= (uint32_t)p.pages) {
-            g.bad |= 1u << i;
-            id = 0;
-        }
-        g.id[i] = id;
-    }
-    return g;
-}
-
-__device__ __forceinline__ int pick(const int (&id)[4], int i) {
-    const int a = i & 1 ? id[1] : id[0], b = i & 1 ? id[3] : id[2];
-    return i & 2 ? b : a;
-}
-
-template <int D>
-__device__ __forceinline__ void stage_block(const DParams& p, const Pages& g, int tok, int head, lds_u8* st) {
-    using S = Stage<D>;
-    constexpr int CH = D / 32;  // 16-byte chunks of a row
+// The pages of a wave's next 16 blocks: lane 4 k + i has the one of group i (16 tokens) of
+// block k, -1 for a group behind the part's end or on no page.
+__device__ __forceinline__ int load_pages(const DParams& p, const int32_t* row, int tok, int end) {
     const int lane = threadIdx.x & 63;
-    const int rb = p.d >> 1;
+    const int t = tok + (lane >> 2) * (kWaves * kBlock) + 16 * (lane & 3);
+    if (t >= end) return -1;
+    const int id = row[t >> p.page_log2];
+    return (uint32_t)id < (uint32_t)p.pages ? id : -1;
+}
+
+// Starts a block's loads into LDS.  id: its groups' pages (page 0 in the place of none).
+// ONCE: no other workgroup reads the block (one tile of rows), so it passes the caches by
+// (streaming policy): 64 sequences of 16384, 1.2 GB, 244 -> 221 us a call.
+template <int D, bool ONCE>
+__device__ __forceinline__ void stage_block(const DParams& p, const int (&id)[4], int tok, int head, lds_u8* st) {
+    using S = Stage<D>;
+    constexpr int CH = D / 32;             // 16-byte chunks of a row
+    constexpr int ROWS = 64 / CH;          // rows of a load
+    const int lane = threadIdx.x & 63;
+    const uint32_t rb = p.d >> 1;
     const int mask = (1 << p.page_log2) - 1;
+    const uint32_t r = lane / CH, c = lane % CH;
 #pragma unroll
     for (int which = 0; which < 2; which++) {
-        const uint8_t* const base = p.kv + (((int64_t)(which * p.H + head)) << p.page_log2) * rb;
+        const int64_t plane = ((int64_t)(which * p.H + head) << p.page_log2) * rb;
 #pragma unroll
-        for (int j = 0; j < S::LOADS / 2; j++) {
-            const int piece = j * 64 + lane;
-            const int t = piece / CH, c = piece % CH;
-            const int id = pick(g.id, t >> 4);
-            const uint8_t* src = base + id * p.page_codes + (int64_t)(((tok + t) & mask) * rb + (c * 32 < p.d ? c * 16 : 0));
+        for (int j = 0; j < S::CODES / 1024; j++) {
+            // rows j * ROWS .. of the block: within a group, or two groups
+            auto at = [&](int group) { return p.kv + id[group] * p.page_codes + plane + (uint32_t)((tok + 16 * group) & mask) * rb; };
+            uint32_t cc = which ? c ^ swizzle<D>(j * ROWS + r) : c;
+            cc = cc * 32 < (uint32_t)p.d ? cc : 0;
+            const uint8_t* src;
+            if constexpr (D == 64) src = (r < 16 ? at(2 * j) : at(2 * j + 1)) + ((r & 15) * rb + cc * 16);
+            else src = at(j * ROWS / 16) + ((j * ROWS % 16 + r) * rb + cc * 16);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(st + which * S::OFF_V + j * 1024), 16, 0, 0);
+                                             (__attribute__((address_space(3))) void*)(st + which * S::OFF_V + j * 1024), 16, 0, ONCE ? 2 : 0);
         }
     }
     const int blocks = p.d >> 4;
+    auto at = [&](int group) { return p.sf + id[group] * p.page_sf + ((tok + 16 * group) & mask); };
+    const uint8_t* const a = lane & 1 ? at(1) : at(0);
+    const uint8_t* const b = lane & 1 ? at(3) : at(2);
+    const uint8_t* const base = lane & 2 ? b : a;
 #pragma unroll
     for (int j = 0; j < S::SF_LOADS; j++) {
         const int piece = j * 64 + lane;
-        if (piece * 16 < 2 * S::SF) {
+        if (S::SF_LOADS > 1 || D == 128 || lane < 2 * S::SF / 16) {
             const int which = piece * 16 >= S::SF;
-            const int rem = piece - which * (S::SF / 16);
-            const int blk = (rem >> 2) < blocks ? rem >> 2 : 0, grp = rem & 3;
-            const uint8_t* src = p.sf + pick(g.id, grp) * p.page_sf +
-                                 ((((int64_t)(which * p.H + head)) * blocks + blk) << p.page_log2) + ((tok + 16 * grp) & mask);
+            const int blk = (piece - which * (S::SF / 16)) >> 2;
+            const uint8_t* src = base + ((int64_t)((which * p.H + head) * blocks + (blk < blocks ? blk : 0)) << p.page_log2);
             __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                             (__attribute__((address_space(3))) void*)(st + S::OFF_SF + j * 1024), 16, 0, 0);
+                                             (__attribute__((address_space(3))) void*)(st + S::OFF_SF + j * 1024), 16, 0, ONCE ? 2 : 0);
         }
     }
 }
@@ -209,8 +198,31 @@ __device__ __forceinline__ f16x8 dequant8_pairs(uint32_t w, f16x8 s) {
     return f16x8{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
 }
 
-template <int D>
-__global__ __launch_bounds__(kThreads, 2) void k_attn_decode(DParams p) {
+// Transposing reads of N blocks of 16 columns of a lane's row, two to a 16-byte chunk, and
+// the wait for them (the compiler puts a wait for every load under way before its own
+// intrinsic).  sw: the row's swizzle, in bytes.
+template <int D, int OFF, int N>
+__device__ __forceinline__ void read_columns(uint32_t at, uint32_t sw, u32x2 (&v)[N]) {
+    static_assert(N == 4 || N == 8, "");
+    constexpr int BASE = D == 256 && OFF % 128 ? 64 : 0, CONST = OFF - BASE;
+    const uint32_t a0 = at + (BASE ^ sw), a1 = at + ((BASE + 16) ^ sw);
+    if constexpr (N == 4) {
+        asm volatile("ds_read_b64_tr_b4 %0, %4 offset:%6\n\tds_read_b64_tr_b4 %1, %4 offset:%7\n\t"
+                     "ds_read_b64_tr_b4 %2, %5 offset:%6\n\tds_read_b64_tr_b4 %3, %5 offset:%7\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]) : "v"(a0), "v"(a1), "n"(CONST), "n"(CONST + 8) : "memory");
+    } else {
+        const uint32_t a2 = at + ((BASE + 32) ^ sw), a3 = at + ((BASE + 48) ^ sw);
+        asm volatile("ds_read_b64_tr_b4 %0, %8 offset:%12\n\tds_read_b64_tr_b4 %1, %8 offset:%13\n\t"
+                     "ds_read_b64_tr_b4 %2, %9 offset:%12\n\tds_read_b64_tr_b4 %3, %9 offset:%13\n\t"
+                     "ds_read_b64_tr_b4 %4, %10 offset:%12\n\tds_read_b64_tr_b4 %5, %10 offset:%13\n\t"
+                     "ds_read_b64_tr_b4 %6, %11 offset:%12\n\tds_read_b64_tr_b4 %7, %11 offset:%13\n\ts_waitcnt lgkmcnt(0)"
+                     : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5]), "=&v"(v[6]), "=&v"(v[7])
+                     : "v"(a0), "v"(a1), "v"(a2), "v"(a3), "n"(CONST), "n"(CONST + 8) : "memory");
+    }
+}
+
+template <int D, bool ONCE>
+__global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using S = Stage<D>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -251,7 +263,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_decode(DParams p) {
         top = o > top ? o : top;
         o = __shfl_xor(top, 32);
         top = o > top ? o : top;
-        int e = top >> 7;           // the largest one's exponent goes to 14
+        int e = top ? top >> 7 : 127;  // the largest one's exponent goes to 14
         e = e < 15 ? 15 : e > 254 ? 254 : e;
         const float up = bits_f((uint32_t)(268 - e > 254 ? 254 : 268 - e) << 23);
         inv = bits_f((uint32_t)(e - 14) << 23);
@@ -263,13 +275,18 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_decode(DParams p) {
                 q[s][2 * j + 1] = (_Float16)(bf16_hi(raw[s][j]) * up);
             }
     }
-    const float to_x = inv * (p.scale2 / p.gs[0]);
+    const float to_x = __builtin_fmaxf(inv * (p.scale2 / p.gs[0]), 0x1p-126f);  // not 0: -inf times it is -inf
     const int limit = w.len - (p.T - 1 - qt);  // tokens this row sees
 
     uint8_t* const mine = smem + wave * S::WAVE;
-    lds_u8* const ring = (lds_u8*)mine;
-    uint8_t* const ks16 = mine + kStages * S::BYTES;
-    uint8_t* const vs16 = ks16 + 2 * S::SF;
+    lds_u8* const st = (lds_u8*)mine;
+    uint8_t* const vs16 = mine + S::BYTES;
+
+    // a lane's row of 16 values for the transposing reads
+    constexpr int VN = D == 64 ? 4 : 8;
+    const int vrow = 16 * g + n;
+    const uint32_t vat = (uint32_t)(uintptr_t)st + vrow * (D / 2);
+    const uint32_t vsw = swizzle<D>(vrow) * 16;
 
     float m = neg_inf(), l = 0.0f;
     f32x4 o[D / 16];
@@ -278,49 +295,75 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_decode(DParams p) {
 
     const int step = kWaves * kBlock;
     int tok = t0 + wave * kBlock;
-    Pages cur = find_pages(p, row, tok, t1), next = find_pages(p, row, tok + step, t1);
-    if (tok < t1) stage_block<D>(p, cur, tok, head, ring);
-    if (tok + step < t1) stage_block<D>(p, next, tok + step, head, ring + S::BYTES);
-    int s = 0;
-    for (; tok < t1; tok += step, s ^= 1) {
-        const Pages after = find_pages(p, row, tok + 2 * step, t1);
-        if (tok + step < t1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(S::LOADS + S::SF_LOADS) : "memory");
-        else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        const uint8_t* const st = mine + s * S::BYTES;
-        const bool masked = tok + kBlock > w.len - p.T + 1 || tok + kBlock > t1 || cur.bad;
+    int ids = load_pages(p, row, tok, t1), ids_next = load_pages(p, row, tok + 16 * step, t1);
+    int k = 0;          // of the 16 blocks that `ids` knows
+    uint32_t bad = 0;   // groups of the block behind the end or on no page
+    auto start = [&](int at) {  // the loads of the wave's block at `at`, whose pages are those of block k
+        int id[4];
+        bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int v = __builtin_amdgcn_readlane(ids, 4 * k + i);
+            bad |= v < 0 ? 1u << i : 0u;
+            id[i] = v < 0 ? 0 : v;
+        }
+        stage_block<D, ONCE>(p, id, at, head, st);
+    };
+    if (tok < t1) start(tok);
+    for (; tok < t1; tok += step) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        const uint32_t none = bad;
+        const bool masked = tok + kBlock > w.len - p.T + 1 || tok + kBlock > t1 || none;
 
-        // scales to fp16: K's as they lie, V's in the order of a lane's tokens
+        // V's scales to fp16
 #pragma unroll
         for (int j = 0; j < (S::SF + 511) / 512; j++) {
-            const int at = j * 512 + lane * 8;  // 8 tokens of a block
+            const int at = j * 512 + lane * 8;  // 8 tokens of a block of columns
             if (at < S::SF) {
-                const u32x2 kb = *(const u32x2*)(st + S::OFF_SF + at), vb = *(const u32x2*)(st + S::OFF_SF + S::SF + at);
-                f16x4 k0 = scales4(kb[0]), k1 = scales4(kb[1]), v0 = scales4(vb[0]), v1 = scales4(vb[1]);
-                const int t = at & 63, blk = at >> 6;
+                const u32x2 vb = *(const u32x2*)(mine + S::OFF_SF + S::SF + at);
+                f16x4 v0 = scales4(vb[0]), v1 = scales4(vb[1]);
+                const int t = at & 63;
                 if (masked) {
-                    const bool none = (cur.bad >> (t >> 4)) & 1;
+                    const bool gone = (none >> (t >> 4)) & 1;
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        if (none || tok + t + e >= t1) v0[e] = (_Float16)0.0f;
-                        if (none || tok + t + 4 + e >= t1) v1[e] = (_Float16)0.0f;
+                        if (gone || tok + t + e >= t1) v0[e] = (_Float16)0.0f;
+                        if (gone || tok + t + 4 + e >= t1) v1[e] = (_Float16)0.0f;
                     }
                 }
-                if (blk * 16 >= p.d) k0 = k1 = v0 = v1 = f16x4{};
-                *(f16x4*)(ks16 + 2 * at) = k0;
-                *(f16x4*)(ks16 + 2 * at + 8) = k1;
-                uint8_t* const vd = vs16 + 128 * blk + 8 * (t >> 4);
-                *(f16x4*)(vd + 32 * ((t >> 2) & 3)) = v0;
-                *(f16x4*)(vd + 32 * (((t >> 2) & 3) + 1)) = v1;
+                if ((at >> 6) * 16 >= p.d) v0 = v1 = f16x4{};
+                *(f16x8*)(vs16 + 2 * at) = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         }
 
-        // X^T = K Q^T
-        float x[16];
+        // X^T = K Q^T: row n of tile i is token 4 n + i, whose scales of a block of columns are
+        // byte i of a dword
+        f16x2 ksc[4][D / 128 ? D / 128 : 1];  // [i][pair of blocks]
+        {
+            uint32_t kb[D / 64];
+#pragma unroll
+            for (int c = 0; c < D / 64; c++) {
+                kb[c] = *(const uint32_t*)(mine + S::OFF_SF + (g * (D / 64) + c) * kBlock + 4 * n);
+                if ((g * (D / 64) + c) * 16 >= p.d) kb[c] = 0;
+            }
+            if constexpr (D == 64) {
+                const f16x4 v = scales4(kb[0]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) ksc[i][0] = f16x2{v[i], v[i]};
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 128; c++) {
+                    const f16x4 a = scales4(kb[2 * c]), b = scales4(kb[2 * c + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) ksc[i][c] = f16x2{a[i], b[i]};
+                }
+            }
+        }
+        f32x4 x[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             f32x4 acc = {};
-            const uint8_t* const kr = st + (16 * i + n) * (D / 2) + g * (D / 8);
-            const uint8_t* const ksr = ks16 + (g * (D / 64) * kBlock + 16 * i + n) * 2;
+            const uint8_t* const kr = mine + (4 * n + i) * (D / 2) + g * (D / 8);
             uint32_t kw[QW];
             if constexpr (D == 64) {
                 const u32x2 v = *(const u32x2*)kr;
@@ -334,27 +377,37 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_decode(DParams p) {
                 }
             }
 #pragma unroll
-            for (int c = 0; c < QW; c++) {
-                const _Float16 sc = *(const _Float16*)(ksr + (c >> 1) * kBlock * 2);
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(kw[c], sc), q[c], acc, 0, 0, 0);
+            for (int c = 0; c < QW; c++)
+                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(kw[c], ksc[i][c >> 2][(c >> 1) & 1]), q[c], acc, 0, 0, 0);
+            x[i] = acc;
+        }
+        u32x2 vw[D / 16 / VN][VN];
+        read_columns<D, S::OFF_V>(vat, vsw, vw[0]);
+        if constexpr (D == 256) read_columns<D, S::OFF_V + 64>(vat, vsw, vw[1]);
+        // (that waited for every read of the block, so the next one's loads may come)
+        if (tok + step < t1) {
+            if (++k == 16) {
+                k = 0;
+                ids = ids_next;
+                ids_next = load_pages(p, row, tok + 17 * step, t1);
             }
-#pragma unroll
-            for (int e = 0; e < 4; e++) x[4 * i + e] = acc[e] * to_x;
+            start(tok + step);
         }
         if (masked) {
 #pragma unroll
             for (int i = 0; i < 4; i++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const int t = tok + 16 * i + 4 * g + e;
-                    if (t >= limit || t >= t1 || ((cur.bad >> i) & 1)) x[4 * i + e] = neg_inf();
+                    const int t = 16 * g + 4 * e + i;
+                    if (tok + t >= limit || tok + t >= t1 || ((none >> g) & 1)) x[i][e] = neg_inf();
                 }
         }
         // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the row
         // alone, so that its bits do not depend on the rows beside it)
-        float top = x[0];
+        float top = x[0][0];
 #pragma unroll
-        for (int i = 1; i < 16; i++) top = __builtin_fmaxf(top, x[i]);
+        for (int i = 1; i < 16; i++) top = __builtin_fmaxf(top, x[i >> 2][i & 3]);
+        top *= to_x;
         if (__any(top > m + 8.0f)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 16));
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
@@ -366,31 +419,24 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_decode(DParams p) {
             for (int i = 0; i < D / 16; i++) o[i] *= a;
         }
         const float base = m == neg_inf() ? 0.0f : m;
-        f16x8 pf[2];
+        f16x8 pf[2];  // token 16 g + j in place j
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; i++) {
-            const float e = __builtin_amdgcn_exp2f(x[i] - base);
+        for (int j = 0; j < 16; j++) {
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j & 3][j >> 2], to_x, -base));
             sum += e;
-            pf[i >> 3][i & 7] = (_Float16)e;
+            pf[j >> 3][j & 7] = (_Float16)e;
         }
         l += sum;
 
         // O^T += V^T P^T
-        const int vrow = 16 * (n >> 2) + 4 * g + (n & 3);
 #pragma unroll
         for (int b = 0; b < D / 16; b++) {
-            typedef int i32x2 __attribute__((ext_vector_type(2)));
-            const i32x2 vw = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                (__attribute__((address_space(3))) i32x2*)(ring + s * S::BYTES + S::OFF_V + vrow * (D / 2) + 8 * b));
+            const u32x2 v = vw[b / VN][b % VN];
             const f16x8 s0 = *(const f16x8*)(vs16 + 128 * b + 32 * g), s1 = *(const f16x8*)(vs16 + 128 * b + 32 * g + 16);
-            o[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8_pairs((uint32_t)vw[0], s0), pf[0], o[b], 0, 0, 0);
-            o[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8_pairs((uint32_t)vw[1], s1), pf[1], o[b], 0, 0, 0);
+            o[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8_pairs(v[0], s0), pf[0], o[b], 0, 0, 0);
+            o[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8_pairs(v[1], s1), pf[1], o[b], 0, 0, 0);
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the stage has been read
-        if (tok + 2 * step < t1) stage_block<D>(p, after, tok + 2 * step, head, ring + s * S::BYTES);
-        cur = next;
-        next = after;
     }
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -444,60 +490,81 @@ __global__ __launch_bounds__(kThreads, 2) void k_attn_decode(DParams p) {
 #endif
 }
 
-// Joins the parts of the sequences that have several: a workgroup a (sequence, head,
-// row tile), a wave every fourth row.
+// Joins the parts of the sequences that have several: a workgroup a row of the output,
+// its threads side by side over the columns and then over the parts.
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int hrs = p.H * p.row_tiles;
-    const int seq = blockIdx.x / hrs, hr = blockIdx.x - seq * hrs;
+    constexpr int CT = D / 4, GROUPS = kThreads / CT;  // threads of a part's row, parts at a time
+    __shared__ float weight[kAttnParts + 64];
+    __shared__ float red[2 * kWaves];
+    __shared__ __align__(16) float sums[GROUPS * D];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+    const int seq = blockIdx.x / (p.T * p.Hq), rem = blockIdx.x - seq * (p.T * p.Hq);
     const int2 plan = p.plan[seq];
-    if (plan.x <= 1) return;
-    const int rt = hr % p.row_tiles, head = hr / p.row_tiles;
+    const int n = plan.x;
+    if (n <= 1) return;
+    const int tt = rem / p.Hq, qh = rem - tt * p.Hq;
+    const int head = qh / p.G, r = tt * p.G + qh - head * p.G;
+    const int hrs = p.H * p.row_tiles, rt = r / kRows, nn = r - rt * kRows;
     const int64_t stride = (int64_t)hrs * (kRows * (D + 2));
-    const float* const first = p.part + (int64_t)plan.y * stride + (int64_t)hr * (kRows * (D + 2));
-    const float out_scale = 1.0f / p.gs[1];
-    constexpr int E = D / 64;
-    for (int nn = wave; nn < kRows && rt * kRows + nn < p.T * p.G; nn += kWaves) {
-        float top = neg_inf();
-        for (int s = lane; s < plan.x; s += 64) top = __builtin_fmaxf(top, first[s * stride + kRows * D + nn]);
-#pragma unroll
-        for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o));
-        float den = 0.0f, acc[E] = {};
-        for (int s0 = 0; s0 < plan.x; s0 += 64) {
-            float a = 0.0f;
-            if (s0 + lane < plan.x) {
-                const float* const ml = first + (s0 + lane) * stride + kRows * D + nn;
-                a = top == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(ml[0] - top);
-                den += a * ml[kRows];
-            }
-            const int k = plan.x - s0 < 64 ? plan.x - s0 : 64;
-            for (int s = 0; s < k; s++) {
-                const float as = __shfl(a, s);
-                const float* const src = first + (s0 + s) * stride + nn * D + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; e++) acc[e] += as * src[e];
-            }
-        }
-#pragma unroll
-        for (int o = 32; o; o >>= 1) den += __shfl_xor(den, o);
-        const int rr = rt * kRows + nn, tt = rr / p.G;
-        const int64_t orow = ((int64_t)seq * p.T + tt) * p.Hq + head * p.G + rr - tt * p.G;
-        const float by = den == 0.0f ? 0.0f : out_scale / den;
-#pragma unroll
-        for (int e = 0; e < E; e++)
-            if (lane * E + e < p.d) p.out[orow * p.d + lane * E + e] = (uint16_t)f32_to_bf16_rne(acc[e] * by);
-        if (p.lse && lane == 0) p.lse[orow] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
+    const float* const first = p.part + (int64_t)plan.y * stride + (int64_t)(head * p.row_tiles + rt) * (kRows * (D + 2));
+    float top = neg_inf();
+    for (int s = t; s < n; s += kThreads) {
+        const float m = first[s * stride + kRows * D + nn];
+        weight[s] = m;
+        top = __builtin_fmaxf(top, m);
     }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o));
+    if (lane == 0) red[wave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kWaves; v++) top = __builtin_fmaxf(top, red[v]);
+    float den = 0.0f;
+    for (int s = t; s < n; s += kThreads) {
+        const float a = top == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(weight[s] - top);
+        weight[s] = a;
+        den += a * first[s * stride + kRows * D + kRows + nn];
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) den += __shfl_xor(den, o);
+    if (lane == 0) red[kWaves + wave] = den;
+    __syncthreads();
+    den = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kWaves; v++) den += red[kWaves + v];
+    const int c = (t % CT) * 4, grp = t / CT;
+    const float* src = first + (int64_t)grp * stride + nn * D + c;
+    f32x4 acc = {};
+    int s = grp;
+    for (; s + 7 * GROUPS < n; s += 8 * GROUPS, src += 8 * GROUPS * stride) {
+        f32x4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = *(const f32x4*)(src + i * GROUPS * stride);
+#pragma unroll
+        for (int i = 0; i < 8; i++) acc += weight[s + i * GROUPS] * x[i];
+    }
+    for (; s < n; s += GROUPS, src += GROUPS * stride) acc += weight[s] * *(const f32x4*)src;
+    *(f32x4*)(sums + grp * D + c) = acc;
+    __syncthreads();
+    if (t >= CT) return;
+    acc = f32x4{};
+#pragma unroll
+    for (int i = 0; i < GROUPS; i++) acc += *(const f32x4*)(sums + i * D + c);
+    const float by = den == 0.0f ? 0.0f : 1.0f / p.gs[1] / den;
+    const int64_t orow = ((int64_t)seq * p.T + tt) * p.Hq + qh;
+    if (c < p.d) *(u32x2*)(p.out + orow * p.d + c) = u32x2{pack_bf16x2(acc[0] * by, acc[1] * by), pack_bf16x2(acc[2] * by, acc[3] * by)};
+    if (p.lse && t == 0) p.lse[orow] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
 }
 
 template <int D>
 hipError_t launch(const DParams& p, int64_t grid, bool join, hipStream_t st) {
     constexpr int lds = kWaves * Stage<D>::WAVE > kWaves * kRows * (D + 4) * 4 ? kWaves * Stage<D>::WAVE : kWaves * kRows * (D + 4) * 4;
-    k_attn_decode<D><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    if (p.row_tiles == 1) k_attn_decode<D, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    else k_attn_decode<D, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !join) return e;
-    k_attn_join<D><<<dim3((unsigned)(p.b * p.H * p.row_tiles)), kThreads, 0, st>>>(p);
+    k_attn_join<D><<<dim3((unsigned)((int64_t)p.b * p.T * p.Hq)), kThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
