@@ -15,6 +15,8 @@
 //   keys in which a lane holds its column of S^T, so P stays where it is.
 // Sums, maximum and both products' sums are fp32; P is rounded to bf16 (V's range is
 // bf16's), off by 2^-8 of itself at most, as the output is.
+#include <type_traits>
+
 #include "gemm_common.h"
 #include "internal.h"
 
@@ -22,7 +24,6 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kKeys = 64;  // keys of a tile
 
 struct PParams {
@@ -93,14 +94,27 @@ __device__ __forceinline__ int swizzle_k(int r) { return D == 64 ? (r >> 1) & 7 
 template <int D>
 __device__ __forceinline__ int swizzle_v(int r) { return D == 64 ? (r & 2) << 1 : (r & 3) << 2; }
 
-// QT: tiles of 32 rows of a wave.
-template <int D, int QT>
-__global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
+// 16 bytes a lane from a raw buffer into LDS, lane after lane from `lds` on.  In assembly, since
+// behind its own intrinsic the compiler waits for these loads at every LDS read, also of the
+// other buffer.  (It writes no register; the compiler's own waits count it as one load more,
+// which only makes them longer; nothing else here uses m0.)
+__device__ __forceinline__ void load_to_lds(const u32x4& rsrc, uint32_t offset, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(rsrc), "s"(lds) : "memory");
+}
+
+__device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
+    const uint64_t a = (uint64_t)base;
+    return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
+}
+
+// NW: waves of a workgroup; QT: tiles of 32 rows of a wave.
+template <int D, int NW, int QT>
+__global__ __launch_bounds__(64 * NW, QT * D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int CH = D / 8;                   // chunks of a row
     constexpr int TILE = kKeys * D * 2;         // bytes of a tile of K (of V)
-    constexpr int LOADS = kKeys * CH / kThreads;  // of a lane, of K (of V)
-    constexpr int ROWS = kWaves * QT * 32;
+    constexpr int LOADS = kKeys * CH / (64 * NW);  // of a lane, of K (of V)
+    constexpr int ROWS = NW * QT * 32;
     extern __shared__ __align__(16) uint8_t smem[];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -131,20 +145,22 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
 
     const uint16_t* const kb = p.k + (int64_t)sq.k0 * p.k_stride + kv * p.d;
     const uint16_t* const vb = p.v + (int64_t)sq.k0 * p.v_stride + kv * p.d;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
     auto stage = [&](int key0, int buf) {
         const int rows = sq.nk - key0 < kKeys ? sq.nk - key0 : kKeys;  // at least 1; later rows come as zeros
-        const __amdgpu_buffer_rsrc_t rk = make_rsrc(kb + (int64_t)key0 * p.k_stride, (uint32_t)(((rows - 1) * p.k_stride + p.d) * 2));
-        const __amdgpu_buffer_rsrc_t rv = make_rsrc(vb + (int64_t)key0 * p.v_stride, (uint32_t)(((rows - 1) * p.v_stride + p.d) * 2));
-        lds_u8* const st = (lds_u8*)smem + buf * 2 * TILE;
+        const u32x4 rk = raw_buffer(kb + (int64_t)key0 * p.k_stride, (uint32_t)(((rows - 1) * p.k_stride + p.d) * 2));
+        const u32x4 rv = raw_buffer(vb + (int64_t)key0 * p.v_stride, (uint32_t)(((rows - 1) * p.v_stride + p.d) * 2));
+        const uint32_t st = lds0 + buf * 2 * TILE + wave * 1024;
 #pragma unroll
         for (int i = 0; i < LOADS; i++) {
-            const int piece = (i * kWaves + wave) * 64 + lane;
+            const int piece = (i * NW + wave) * 64 + lane;
             const int r = piece / CH, at = piece % CH;
             const int ck = at ^ swizzle_k<D>(r), cv = at ^ swizzle_v<D>(r);
-            const uint32_t ok = ck * 8 < p.d && r < rows ? (uint32_t)(r * (int)p.k_stride + ck * 8) * 2u : 0xFFFFFFF0u;
-            const uint32_t ov = cv * 8 < p.d && r < rows ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rk, (__attribute__((address_space(3))) void*)(st + (i * kWaves + wave) * 1024), 16, ok, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rv, (__attribute__((address_space(3))) void*)(st + TILE + (i * kWaves + wave) * 1024), 16, ov, 0, 0, 0);
+            // a row past the last one ends behind the buffer by itself; a chunk past d must not
+            const uint32_t ok = ck * 8 < p.d ? (uint32_t)(r * (int)p.k_stride + ck * 8) * 2u : 0xFFFFFFF0u;
+            const uint32_t ov = cv * 8 < p.d ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
+            load_to_lds(rk, ok, __builtin_amdgcn_readfirstlane(st + i * NW * 1024));
+            load_to_lds(rv, ov, __builtin_amdgcn_readfirstlane(st + TILE + i * NW * 1024));
         }
     };
     if (keys > 0) stage(0, 0);
@@ -165,6 +181,11 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
             q[t][s] = __builtin_bit_cast(bf16x8, w);
         }
     }
+    // (the queries are waited for here, not at every use in the loop)
+#pragma unroll
+    for (int t = 0; t < QT; t++)
+#pragma unroll
+        for (int s = 0; s < D / 16; s++) asm volatile("" : "+v"(q[t][s]));
     // keys that all rows of the wave see, and that any sees (rows past the sequence count as its last)
     int all = sq.nk, any = sq.nk;
     if (p.causal) {
@@ -175,13 +196,6 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
 
     f32x16 o[QT][D / 32];
     float m[QT], l[QT];
-#pragma unroll
-    for (int t = 0; t < QT; t++) {
-        m[t] = neg_inf();
-        l[t] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 32; i++) o[t][i] = f32x16{};
-    }
 
     // a lane's addresses in the tiles: K rows l32 (+ 32), V rows 4 hi + (lane & 15) / 4 (+ 8 i)
     const int vr = (lane & 15) >> 2;
@@ -192,6 +206,17 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
         vat[i] = (4 * hi + vr) * D * 2 + (c ^ swizzle_v<D>(vr)) * 16 + (lane & 1) * 8;
     }
 
+    // One pass over the keys.  CAREFUL: a value that is not finite behind a mask, which 0 times
+    // it would carry into the rows that do not see it, is kept out of the product and handed to
+    // the rows that do.
+    auto sweep = [&](auto CAREFUL) {
+#pragma unroll
+    for (int t = 0; t < QT; t++) {
+        m[t] = neg_inf();
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 32; i++) o[t][i] = f32x16{};
+    }
     for (int key0 = 0, buf = 0; key0 < keys; key0 += kKeys, buf ^= 1) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the tile is there, the other buffer has been read
         if (key0 + kKeys < keys) stage(key0 + kKeys, buf ^ 1);
@@ -263,8 +288,8 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
             const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
             return bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
         };
-        bool odd = false;  // a value that is not finite behind a mask: 0 times it would not be 0
-        if (masked && p.causal) {
+        bool odd = false;
+        if (CAREFUL && masked && p.causal) {
             u16x2 big = {};
 #pragma unroll 1
             for (int i = lane; i < TILE / 16; i += 64) {
@@ -284,7 +309,6 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
                     for (int t = 0; t < QT; t++) o[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pf[t][f], o[t][i], 0, 0, 0);
                 }
         } else {
-            // finite values through the product; the others go to the rows that see them
 #pragma unroll 1
             for (int f = 0; f < 4; f++)
 #pragma unroll
@@ -317,6 +341,21 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
                     }
         }
     }
+    };
+    sweep(std::false_type{});
+    if (p.causal) {
+        bool bad = false;
+#pragma unroll
+        for (int t = 0; t < QT; t++)
+#pragma unroll
+            for (int i = 0; i < D / 32; i++)
+#pragma unroll
+                for (int e = 0; e < 16; e++) bad |= (f_bits(o[t][i][e]) & 0x7F800000u) == 0x7F800000u;
+        if (__syncthreads_or(bad)) {
+            if (keys > 0) stage(0, 0);
+            sweep(std::true_type{});
+        }
+    }
 
 #pragma unroll
     for (int t = 0; t < QT; t++) {
@@ -339,11 +378,11 @@ __global__ __launch_bounds__(kThreads, QT * D <= 128 ? 2 : 1) void k_attn_prefil
 #endif
 }
 
-template <int D, int QT>
+template <int D, int NW, int QT>
 hipError_t launch(PParams& p, hipStream_t st) {
-    constexpr int ROWS = kWaves * QT * 32;
+    constexpr int ROWS = NW * QT * 32;
     p.units = p.tq / ROWS + p.b;  // tiles that no sequence has return at once
-    k_attn_prefill<D, QT><<<dim3((unsigned)((int64_t)p.units * p.Hq)), kThreads, 4 * kKeys * D * 2, st>>>(p);
+    k_attn_prefill<D, NW, QT><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, 4 * kKeys * D * 2, st>>>(p);
     return hipGetLastError();
 }
 
@@ -356,9 +395,9 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     p.c = a.scale * 1.44269504088896340736f;
     p.b = (int)a.b; p.tq = (int)a.tq; p.tk = (int)a.tk; p.Hq = (int)a.q_heads; p.H = (int)a.heads;
     p.G = p.Hq / p.H; p.d = (int)a.d; p.causal = a.causal;
-    if (a.d <= 64) return launch<64, 1>(p, st);
-    if (a.d <= 128) return launch<128, 1>(p, st);
-    return launch<256, 1>(p, st);
+    if (a.d <= 64) return launch<64, 4, 1>(p, st);
+    if (a.d <= 128) return launch<128, 4, 1>(p, st);
+    return launch<256, 4, 1>(p, st);
 }
 
 }  // namespace nvfp4
