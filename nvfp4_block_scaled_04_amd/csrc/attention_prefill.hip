@@ -107,15 +107,15 @@ __device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
     return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
 }
 
-// NW: waves of a workgroup; QT: tiles of 32 rows of a wave.
-template <int D, int NW, int QT>
-__global__ __launch_bounds__(64 * NW, QT * D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
+// NW: waves of a workgroup, 32 rows each.  Eight waves sit two to a SIMD and take turns (sweep_paired).
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int CH = D / 8;                   // chunks of a row
     constexpr int TILE = kKeys * D * 2;         // bytes of a tile of K (of V)
     constexpr int LOADS = kKeys * CH / (64 * NW);  // of a lane, of K (of V)
-    constexpr int ROWS = NW * QT * 32;
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int ROWS = NW * 32;
+    extern __shared__ __align__(16) uint8_t smem[];  // two tiles of K, two of V
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, hi = lane >> 5;
@@ -145,59 +145,61 @@ __global__ __launch_bounds__(64 * NW, QT * D <= 128 ? 2 : 1) void k_attn_prefill
 
     const uint16_t* const kb = p.k + (int64_t)sq.k0 * p.k_stride + kv * p.d;
     const uint16_t* const vb = p.v + (int64_t)sq.k0 * p.v_stride + kv * p.d;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8*)smem;
-    auto stage = [&](int key0, int buf) {
-        const int rows = sq.nk - key0 < kKeys ? sq.nk - key0 : kKeys;  // at least 1; later rows come as zeros
-        const u32x4 rk = raw_buffer(kb + (int64_t)key0 * p.k_stride, (uint32_t)(((rows - 1) * p.k_stride + p.d) * 2));
-        const u32x4 rv = raw_buffer(vb + (int64_t)key0 * p.v_stride, (uint32_t)(((rows - 1) * p.v_stride + p.d) * 2));
-        const uint32_t st = lds0 + buf * 2 * TILE + wave * 1024;
+    lds_u8* const lds = (lds_u8*)smem;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds + wave * 1024;
+    // a lane's offsets into a tile in memory: a row past the last one ends behind the buffer by
+    // itself, a chunk past d is sent there
+    uint32_t off_k[LOADS], off_v[LOADS];
 #pragma unroll
-        for (int i = 0; i < LOADS; i++) {
-            const int piece = (i * NW + wave) * 64 + lane;
-            const int r = piece / CH, at = piece % CH;
-            const int ck = at ^ swizzle_k<D>(r), cv = at ^ swizzle_v<D>(r);
-            // a row past the last one ends behind the buffer by itself; a chunk past d must not
-            const uint32_t ok = ck * 8 < p.d ? (uint32_t)(r * (int)p.k_stride + ck * 8) * 2u : 0xFFFFFFF0u;
-            const uint32_t ov = cv * 8 < p.d ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
-            load_to_lds(rk, ok, __builtin_amdgcn_readfirstlane(st + i * NW * 1024));
-            load_to_lds(rv, ov, __builtin_amdgcn_readfirstlane(st + TILE + i * NW * 1024));
-        }
+    for (int i = 0; i < LOADS; i++) {
+        const int piece = (i * NW + wave) * 64 + lane;
+        const int r = piece / CH, at = piece % CH;
+        const int ck = at ^ swizzle_k<D>(r), cv = at ^ swizzle_v<D>(r);
+        off_k[i] = ck * 8 < p.d ? (uint32_t)(r * (int)p.k_stride + ck * 8) * 2u : 0xFFFFFFF0u;
+        off_v[i] = cv * 8 < p.d ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
+    }
+    auto stage = [&](const uint16_t* base, int64_t stride, const uint32_t (&off)[LOADS], int key0, uint32_t to) {
+        const int rows = sq.nk - key0 < kKeys ? sq.nk - key0 : kKeys;  // at least 1; later rows come as zeros
+        const u32x4 rs = raw_buffer(base + key0 * stride, (uint32_t)(((rows - 1) * stride + p.d) * 2));
+#pragma unroll
+        for (int i = 0; i < LOADS; i++) load_to_lds(rs, off[i], __builtin_amdgcn_readfirstlane(lds0 + to + i * NW * 1024));
     };
-    if (keys > 0) stage(0, 0);
+    auto stage_k = [&](int n) { stage(kb, p.k_stride, off_k, n * kKeys, (n & 1) * TILE); };
+    auto stage_v = [&](int n) { stage(vb, p.v_stride, off_v, n * kKeys, (2 + (n & 1)) * TILE); };
+    const int tiles = (keys + kKeys - 1) / kKeys;
+    if (tiles > 0) stage_k(0);
 
     // the wave's queries, and what each row sees
-    const int first = row0 + wave * QT * 32;
-    bf16x8 q[QT][D / 16];
-    int end[QT];                                // keys below it are seen
-#pragma unroll
-    for (int t = 0; t < QT; t++) {
-        const int i = first + t * 32 + l32;
-        end[t] = i >= sq.nq ? 0 : p.causal ? clamp_to(i + back + 1, 0, sq.nk) : sq.nk;
-        const uint16_t* const src = p.q + (int64_t)(sq.q0 + (i < sq.nq ? i : 0)) * p.q_stride + head * p.d;
+    const int first = row0 + wave * 32;
+    const int mine = first + l32;
+    const int end = mine >= sq.nq ? 0 : p.causal ? clamp_to(mine + back + 1, 0, sq.nk) : sq.nk;  // keys below it are seen
+    bf16x8 q[D / 16];
+    {
+        const uint16_t* const src = p.q + (int64_t)(sq.q0 + (mine < sq.nq ? mine : 0)) * p.q_stride + head * p.d;
 #pragma unroll
         for (int s = 0; s < D / 16; s++) {
             u32x4 w = {};
-            if (i < sq.nq && 16 * s + 8 * hi < p.d) w = *(const u32x4*)(src + 16 * s + 8 * hi);
-            q[t][s] = __builtin_bit_cast(bf16x8, w);
+            if (mine < sq.nq && 16 * s + 8 * hi < p.d) w = *(const u32x4*)(src + 16 * s + 8 * hi);
+            q[s] = __builtin_bit_cast(bf16x8, w);
         }
     }
-    // (the queries are waited for here, not at every use in the loop)
+    // (waited for here, not at every use in the loop)
 #pragma unroll
-    for (int t = 0; t < QT; t++)
-#pragma unroll
-        for (int s = 0; s < D / 16; s++) asm volatile("" : "+v"(q[t][s]));
+    for (int s = 0; s < D / 16; s++) asm volatile("" : "+v"(q[s]));
     // keys that all rows of the wave see, and that any sees (rows past the sequence count as its last)
     int all = sq.nk, any = sq.nk;
     if (p.causal) {
         all = clamp_to(first + back + 1, 0, sq.nk);
-        any = clamp_to((first + QT * 32 < sq.nq ? first + QT * 32 : sq.nq) + back, 0, sq.nk);
+        any = clamp_to((first + 32 < sq.nq ? first + 32 : sq.nq) + back, 0, sq.nk);
     }
     if (first >= sq.nq) any = 0;
 
-    f32x16 o[QT][D / 32];
-    float m[QT], l[QT];
+    f32x16 o[D / 32];
+    float m = neg_inf(), l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; i++) o[i] = f32x16{};
 
-    // a lane's addresses in the tiles: K rows l32 (+ 32), V rows 4 hi + (lane & 15) / 4 (+ 8 i)
+    // a lane's V rows: 4 hi + (lane & 15) / 4 (+ 8 i)
     const int vr = (lane & 15) >> 2;
     int vat[D / 32];
 #pragma unroll
@@ -205,184 +207,262 @@ __global__ __launch_bounds__(64 * NW, QT * D <= 128 ? 2 : 1) void k_attn_prefill
         const int c = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
         vat[i] = (4 * hi + vr) * D * 2 + (c ^ swizzle_v<D>(vr)) * 16 + (lane & 1) * 8;
     }
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-    // One pass over the keys.  CAREFUL: a value that is not finite behind a mask, which 0 times
-    // it would carry into the rows that do not see it, is kept out of the product and handed to
-    // the rows that do.
-    auto sweep = [&](auto CAREFUL) {
-#pragma unroll
-    for (int t = 0; t < QT; t++) {
-        m[t] = neg_inf();
-        l[t] = 0.0f;
-#pragma unroll
-        for (int i = 0; i < D / 32; i++) o[t][i] = f32x16{};
-    }
-    for (int key0 = 0, buf = 0; key0 < keys; key0 += kKeys, buf ^= 1) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the tile is there, the other buffer has been read
-        if (key0 + kKeys < keys) stage(key0 + kKeys, buf ^ 1);
-        if (key0 >= any) continue;
-        lds_u8* const kt = (lds_u8*)smem + buf * 2 * TILE;
-        lds_u8* const vt = kt + TILE;
-        const bool masked = key0 + kKeys > all;
-
-        f32x16 s[QT][2];
+    // S^T of tile n: s[j] the keys 32 j .. of it
+    auto scores = [&](int n, f32x16 (&s)[2]) {
+        lds_u8* const kt = lds + (n & 1) * TILE;
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-#pragma unroll
-            for (int t = 0; t < QT; t++) s[t][j] = f32x16{};
+            s[j] = f32x16{};
 #pragma unroll
             for (int i = 0; i < D / 16; i++) {
                 const int r = 32 * j + l32;
                 const bf16x8 a = *(const __attribute__((address_space(3))) bf16x8*)(kt + r * D * 2 + ((2 * i + hi) ^ swizzle_k<D>(r)) * 16);
-#pragma unroll
-                for (int t = 0; t < QT; t++) s[t][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[t][i], s[t][j], 0, 0, 0);
+                s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[i], s[j], 0, 0, 0);
             }
         }
-        bf16x8 pf[QT][4];
-#pragma unroll
-        for (int t = 0; t < QT; t++) {
-            if (masked) {
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-#pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        if (key0 + 32 * j + 8 * (e >> 2) + 4 * hi + (e & 3) >= end[t]) s[t][j][e] = neg_inf();
-            }
-            float top = s[t][0][0];
-#pragma unroll
-            for (int e = 1; e < 32; e++) top = __builtin_fmaxf(top, s[t][e >> 4][e & 15]);
-            top *= p.c;
-            // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the
-            // row alone, so that its bits do not depend on the rows beside it)
-            if (__any(top > m[t] + 8.0f)) {
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                const float to = top > m[t] + 8.0f ? top : m[t];
-                const float a = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m[t] - to);
-                m[t] = to;
-                l[t] *= a;
-#pragma unroll
-                for (int i = 0; i < D / 32; i++) o[t][i] *= a;
-            }
-            const float base = m[t] == neg_inf() ? 0.0f : m[t];
-            float sum = 0.0f;
-#pragma unroll
-            for (int f = 0; f < 4; f++) {
-                u32x4 w;
-#pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][f >> 1][8 * (f & 1) + 2 * e], p.c, -base));
-                    const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][f >> 1][8 * (f & 1) + 2 * e + 1], p.c, -base));
-                    sum += p0 + p1;
-                    w[e] = pack_bf16x2(p0, p1);
-                }
-                pf[t][f] = __builtin_bit_cast(bf16x8, w);
-            }
-            l[t] += sum;
-        }
-
-        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-        auto v_frag = [&](int f, int i) {  // keys 16 f .. 16 f + 15, columns 32 i ..
-            typedef short s16x4 __attribute__((ext_vector_type(4)));
-            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + 16 * f * D * 2));
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + (16 * f + 8) * D * 2));
-            const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
-            return bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        };
-        bool odd = false;
-        if (CAREFUL && masked && p.causal) {
-            u16x2 big = {};
-#pragma unroll 1
-            for (int i = lane; i < TILE / 16; i += 64) {
-                const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i * 16);
-#pragma unroll
-                for (int e = 0; e < 4; e++) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, w[e] & 0x7FFF7FFFu));
-            }
-            odd = __any((big[0] > big[1] ? big[0] : big[1]) >= 0x7F80);
-        }
-        if (!odd) {
-#pragma unroll
-            for (int f = 0; f < 4; f++)
-#pragma unroll
-                for (int i = 0; i < D / 32; i++) {
-                    const bf16x8 a = v_frag(f, i);
-#pragma unroll
-                    for (int t = 0; t < QT; t++) o[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, pf[t][f], o[t][i], 0, 0, 0);
-                }
-        } else {
-#pragma unroll 1
-            for (int f = 0; f < 4; f++)
-#pragma unroll
-                for (int i = 0; i < D / 32; i++) {
-                    u32x4 w = __builtin_bit_cast(u32x4, v_frag(f, i));
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
-                        if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
-                    }
-#pragma unroll
-                    for (int t = 0; t < QT; t++) {
-                        bf16x8 pv = pf[t][0];
-                        pv = f == 1 ? pf[t][1] : f == 2 ? pf[t][2] : f == 3 ? pf[t][3] : pv;
-                        o[t][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), pv, o[t][i], 0, 0, 0);
-                    }
-                }
-#pragma unroll 1
-            for (int r = 0; r < kKeys; r++)
-#pragma unroll
-                for (int i = 0; i < D / 32; i++)
-#pragma unroll
-                    for (int e = 0; e < 16; e++) {
-                        const int col = 32 * i + 8 * (e >> 2) + 4 * hi + (e & 3);
-                        const uint16_t bits = *(const __attribute__((address_space(3))) uint16_t*)(
-                            vt + r * D * 2 + ((col >> 3) ^ swizzle_v<D>(r)) * 16 + (col & 7) * 2);
-#pragma unroll
-                        for (int t = 0; t < QT; t++)
-                            if ((bits & 0x7F80) == 0x7F80 && key0 + r < end[t]) o[t][i][e] += bits_f((uint32_t)bits << 16);
-                    }
-        }
-    }
     };
-    sweep(std::false_type{});
+    // its probabilities: pf[f] the keys 16 f .. of it
+    auto soften = [&](int n, f32x16 (&s)[2], bf16x8 (&pf)[4]) {
+        const int key0 = n * kKeys;
+        if (key0 + kKeys > all) {
+#pragma unroll
+            for (int e = 0; e < 32; e++)
+                if (key0 + 32 * (e >> 4) + 8 * ((e & 15) >> 2) + 4 * hi + (e & 3) >= end) s[e >> 4][e & 15] = neg_inf();
+        }
+        float top = s[0][0];
+#pragma unroll
+        for (int e = 1; e < 32; e++) top = __builtin_fmaxf(top, s[e >> 4][e & 15]);
+        top *= p.c;
+        // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the
+        // row alone, so that its bits do not depend on the rows beside it)
+        if (__any(top > m + 8.0f)) {
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            const float to = top > m + 8.0f ? top : m;
+            const float a = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m - to);
+            m = to;
+            l *= a;
+#pragma unroll
+            for (int i = 0; i < D / 32; i++) o[i] *= a;
+        }
+        const float base = m == neg_inf() ? 0.0f : m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int f = 0; f < 4; f++) {
+            u32x4 w;
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + 2 * e], p.c, -base));
+                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + 2 * e + 1], p.c, -base));
+                sum += p0 + p1;
+                w[e] = pack_bf16x2(p0, p1);
+            }
+            pf[f] = __builtin_bit_cast(bf16x8, w);
+        }
+        l += sum;
+    };
+    auto v_frag = [&](lds_u8* vt, int f, int i) {  // V^T of the keys 16 f .. and the columns 32 i ..
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + 16 * f * D * 2));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + (16 * f + 8) * D * 2));
+        const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
+        return bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+    };
+    auto add_values = [&](int n, const bf16x8 (&pf)[4]) {
+        lds_u8* const vt = lds + (2 + (n & 1)) * TILE;
+#pragma unroll
+        for (int f = 0; f < 4; f++)
+#pragma unroll
+            for (int i = 0; i < D / 32; i++) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_frag(vt, f, i), pf[f], o[i], 0, 0, 0);
+    };
+
+    // One pass over the keys, each wave by itself between the tiles' barriers.  CAREFUL: a value
+    // that is not finite behind a mask, which 0 times it would carry into the rows that do not
+    // see it, is kept out of the product and handed to the rows that do.
+    auto sweep = [&](auto CAREFUL) {
+        if (tiles > 0) stage_v(0);
+        for (int n = 0; n < tiles; n++) {
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the tile is there, the other buffers have been read
+            if (n + 1 < tiles) {
+                stage_k(n + 1);
+                stage_v(n + 1);
+            }
+            const int key0 = n * kKeys;
+            if (key0 >= any) continue;
+            f32x16 s[2];
+            bf16x8 pf[4];
+            scores(n, s);
+            soften(n, s, pf);
+            if constexpr (!CAREFUL) {
+                add_values(n, pf);
+            } else {
+                lds_u8* const vt = lds + (2 + (n & 1)) * TILE;
+#pragma unroll 1
+                for (int f = 0; f < 4; f++)
+#pragma unroll
+                    for (int i = 0; i < D / 32; i++) {
+                        u32x4 w = __builtin_bit_cast(u32x4, v_frag(vt, f, i));
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            if ((w[e] & 0x7F80u) == 0x7F80u) w[e] &= 0xFFFF0000u;
+                            if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
+                        }
+                        bf16x8 pv = pf[0];
+                        pv = f == 1 ? pf[1] : f == 2 ? pf[2] : f == 3 ? pf[3] : pv;
+                        o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), pv, o[i], 0, 0, 0);
+                    }
+                u16x2 big = {};
+#pragma unroll 1
+                for (int i = lane; i < TILE / 16; i += 64) {
+                    const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(vt + i * 16);
+#pragma unroll
+                    for (int e = 0; e < 4; e++) big = __builtin_elementwise_max(big, __builtin_bit_cast(u16x2, w[e] & 0x7FFF7FFFu));
+                }
+                if (__any((big[0] > big[1] ? big[0] : big[1]) >= 0x7F80)) {
+#pragma unroll 1
+                    for (int r = 0; r < kKeys; r++)
+#pragma unroll
+                        for (int i = 0; i < D / 32; i++)
+#pragma unroll
+                            for (int e = 0; e < 16; e++) {
+                                const int col = 32 * i + 8 * (e >> 2) + 4 * hi + (e & 3);
+                                const uint16_t bits = *(const __attribute__((address_space(3))) uint16_t*)(
+                                    vt + r * D * 2 + ((col >> 3) ^ swizzle_v<D>(r)) * 16 + (col & 7) * 2);
+                                if ((bits & 0x7F80) == 0x7F80 && key0 + r < end) o[i][e] += bits_f((uint32_t)bits << 16);
+                            }
+                }
+            }
+        }
+    };
+
+    // The same with two waves of a SIMD in step: while one runs the products of a tile (V of the
+    // one before, then K of this), the other runs the softmax of its own, so that the matrix
+    // pipe is always fed.  A barrier ends each half of a step; the second four waves are half a
+    // step behind.  Step n stages K of n + 1 and V of n, which are read a step later, into buffers
+    // last read in the step before.
+    auto sweep_paired = [&]() {
+        const bool behind = wave >= NW / 2;
+        const int own = (any + kKeys - 1) / kKeys;  // tiles that the wave sees
+        f32x16 s[2];
+        bf16x8 pf[4];
+        auto end_half = [&](auto LANDED) {
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (LANDED) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            else asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto feed = [&](int n) {
+            if (n + 1 < tiles) stage_k(n + 1);
+            if (n < tiles) stage_v(n);
+        };
+        // LDS reads run ahead of the products: the compiler alone puts each right before its use
+        auto products = [&](int n) {
+            add_values(n - 1, pf);
+            scores(n, s);
+            constexpr int NV = D / 32 * 4, NK = D / 8;  // products of each
+            __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
+#pragma unroll
+            for (int i = 0; i < NV - 4; i++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < NK - 8; i++) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+        };
+        // Step n: K of tile n meets the queries, V of tile n - 1 the probabilities.
+        end_half(std::true_type{});  // K of tile 0 is there
+        int n = 0;
+        if (own > 0) {
+            feed(0);
+            if (!behind) {
+                scores(0, s);
+                end_half(std::false_type{});
+                soften(0, s, pf);
+                end_half(std::true_type{});
+                for (n = 1; n < own; n++) {
+                    feed(n);
+                    products(n);
+                    end_half(std::false_type{});
+                    soften(n, s, pf);
+                    end_half(std::true_type{});
+                }
+                feed(n);
+                add_values(n - 1, pf);
+                end_half(std::false_type{});
+            } else {
+                end_half(std::false_type{});
+                scores(0, s);
+                end_half(std::true_type{});
+                for (n = 1; n < own; n++) {
+                    feed(n);
+                    soften(n - 1, s, pf);
+                    end_half(std::false_type{});
+                    products(n);
+                    end_half(std::true_type{});
+                }
+                feed(n);
+                soften(n - 1, s, pf);
+                end_half(std::false_type{});
+                add_values(n - 1, pf);
+            }
+            end_half(std::true_type{});
+            n++;
+        }
+        for (; n <= tiles; n++) {  // tiles that only other waves see
+            feed(n);
+            end_half(std::false_type{});
+            end_half(std::true_type{});
+        }
+    };
+    if constexpr (NW == 8) sweep_paired();
+    else sweep(std::false_type{});
+
     if (p.causal) {
         bool bad = false;
 #pragma unroll
-        for (int t = 0; t < QT; t++)
+        for (int i = 0; i < D / 32; i++)
 #pragma unroll
-            for (int i = 0; i < D / 32; i++)
-#pragma unroll
-                for (int e = 0; e < 16; e++) bad |= (f_bits(o[t][i][e]) & 0x7F800000u) == 0x7F800000u;
+            for (int e = 0; e < 16; e++) bad |= (f_bits(o[i][e]) & 0x7F800000u) == 0x7F800000u;
         if (__syncthreads_or(bad)) {
-            if (keys > 0) stage(0, 0);
+            m = neg_inf();
+            l = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 32; i++) o[i] = f32x16{};
+            if (tiles > 0) stage_k(0);
             sweep(std::true_type{});
         }
     }
 
+    const float den = l + __shfl_xor(l, 32);
+    const float by = den == 0.0f ? 0.0f : 1.0f / den;
+    if (mine >= sq.nq) return;
+    uint16_t* const dst = p.out + (int64_t)(sq.q0 + mine) * p.out_stride + head * p.d;
 #pragma unroll
-    for (int t = 0; t < QT; t++) {
-        const int i = first + t * 32 + l32;
-        const float den = l[t] + __shfl_xor(l[t], 32);
-        const float by = den == 0.0f ? 0.0f : 1.0f / den;
-        if (i >= sq.nq) continue;
-        uint16_t* const dst = p.out + (int64_t)(sq.q0 + i) * p.out_stride + head * p.d;
+    for (int c = 0; c < D / 32; c++)
 #pragma unroll
-        for (int c = 0; c < D / 32; c++)
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-                const int col = 32 * c + 2 * e + 4 * hi;
-                if (col < p.d)
-                    *(u32x2*)(dst + col) = u32x2{pack_bf16x2(o[t][c][e] * by, o[t][c][e + 1] * by),
-                                                 pack_bf16x2(o[t][c][e + 2] * by, o[t][c][e + 3] * by)};
-            }
-        if (p.lse && hi == 0) p.lse[(int64_t)(sq.q0 + i) * p.Hq + head] = (m[t] + __builtin_log2f(den)) * 0.69314718055994530942f;
-    }
+        for (int e = 0; e < 16; e += 4) {
+            const int col = 32 * c + 2 * e + 4 * hi;
+            if (col < p.d)
+                *(u32x2*)(dst + col) = u32x2{pack_bf16x2(o[c][e] * by, o[c][e + 1] * by), pack_bf16x2(o[c][e + 2] * by, o[c][e + 3] * by)};
+        }
+    if (p.lse && hi == 0) p.lse[(int64_t)(sq.q0 + mine) * p.Hq + head] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
 #endif
 }
 
-template <int D, int NW, int QT>
+template <int D, int NW>
 hipError_t launch(PParams& p, hipStream_t st) {
-    constexpr int ROWS = NW * QT * 32;
-    p.units = p.tq / ROWS + p.b;  // tiles that no sequence has return at once
-    k_attn_prefill<D, NW, QT><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, 4 * kKeys * D * 2, st>>>(p);
+    p.units = p.tq / (NW * 32) + p.b;  // tiles that no sequence has return at once
+    k_attn_prefill<D, NW><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, 4 * kKeys * D * 2, st>>>(p);
     return hipGetLastError();
 }
 
@@ -395,9 +475,9 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     p.c = a.scale * 1.44269504088896340736f;
     p.b = (int)a.b; p.tq = (int)a.tq; p.tk = (int)a.tk; p.Hq = (int)a.q_heads; p.H = (int)a.heads;
     p.G = p.Hq / p.H; p.d = (int)a.d; p.causal = a.causal;
-    if (a.d <= 64) return launch<64, 4, 1>(p, st);
-    if (a.d <= 128) return launch<128, 4, 1>(p, st);
-    return launch<256, 4, 1>(p, st);
+    if (a.d <= 64) return launch<64, 4>(p, st);
+    if (a.d <= 128) return launch<128, 8>(p, st);
+    return launch<256, 4>(p, st);
 }
 
 }  // namespace nvfp4
