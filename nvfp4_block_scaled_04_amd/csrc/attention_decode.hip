@@ -239,22 +239,49 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DPar
     const int t1 = w.len - t0 < chunk ? w.len : t0 + chunk;  // may lie before t0
     const int32_t* const row = p.table + (int64_t)w.seq * p.table_pages;
 
-    // the row's queries, scaled to fp16
+    // the row's queries, under way while the first block's pages and loads are worked out
     const int r = rt * kRows + n;
     const bool live = r < p.T * p.G;
     const int qt = live ? r / p.G : 0;
     const int64_t qrow = ((int64_t)w.seq * p.T + qt) * p.Hq + head * p.G + (live ? r - qt * p.G : 0);
     constexpr int QW = D / 32;
+    const int step = kWaves * kBlock;
+    int tok = t0 + wave * kBlock;
+    int ids = load_pages(p, row, tok, t1), ids_next = load_pages(p, row, tok + 16 * step, t1);
+    u32x4 raw[QW];
+#pragma unroll
+    for (int s = 0; s < QW; s++) {
+        const int col = g * (D / 4) + 8 * s;
+        raw[s] = u32x4{};
+        if (live && col < p.d) raw[s] = *(const u32x4*)(p.q + qrow * p.d + col);
+    }
+    const float gs_k = p.gs[0], gs_v = p.gs[1];
+
+    uint8_t* const mine = smem + wave * S::WAVE;
+    lds_u8* const st = (lds_u8*)mine;
+    uint8_t* const vs16 = mine + S::BYTES;
+    int k = 0;          // of the 16 blocks that `ids` knows
+    uint32_t bad = 0;   // groups of the block behind the end or on no page
+    auto start = [&](int at) {  // the loads of the wave's block at `at`, whose pages are those of block k
+        int id[4];
+        bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int v = __builtin_amdgcn_readlane(ids, 4 * k + i);
+            bad |= v < 0 ? 1u << i : 0u;
+            id[i] = v < 0 ? 0 : v;
+        }
+        stage_block<D, ONCE>(p, id, at, head, st);
+    };
+    if (tok < t1) start(tok);
+
+    // scaled to fp16
     f16x8 q[QW];
     float inv;
     {
-        u32x4 raw[QW];
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < QW; s++) {
-            const int col = g * (D / 4) + 8 * s;
-            raw[s] = u32x4{};
-            if (live && col < p.d) raw[s] = *(const u32x4*)(p.q + qrow * p.d + col);
             const uint32_t v[4] = {raw[s][0], raw[s][1], raw[s][2], raw[s][3]};
             const uint32_t a = absmax_bits_bf16x8(v);
             top = a > top ? a : top;
@@ -275,12 +302,8 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DPar
                 q[s][2 * j + 1] = (_Float16)(bf16_hi(raw[s][j]) * up);
             }
     }
-    const float to_x = __builtin_fmaxf(inv * (p.scale2 / p.gs[0]), 0x1p-126f);  // not 0: -inf times it is -inf
+    const float to_x = __builtin_fmaxf(inv * (p.scale2 / gs_k), 0x1p-126f);  // not 0: -inf times it is -inf
     const int limit = w.len - (p.T - 1 - qt);  // tokens this row sees
-
-    uint8_t* const mine = smem + wave * S::WAVE;
-    lds_u8* const st = (lds_u8*)mine;
-    uint8_t* const vs16 = mine + S::BYTES;
 
     // a lane's row of 16 values for the transposing reads
     constexpr int VN = D == 64 ? 4 : 8;
@@ -293,23 +316,6 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DPar
 #pragma unroll
     for (int i = 0; i < D / 16; i++) o[i] = f32x4{};
 
-    const int step = kWaves * kBlock;
-    int tok = t0 + wave * kBlock;
-    int ids = load_pages(p, row, tok, t1), ids_next = load_pages(p, row, tok + 16 * step, t1);
-    int k = 0;          // of the 16 blocks that `ids` knows
-    uint32_t bad = 0;   // groups of the block behind the end or on no page
-    auto start = [&](int at) {  // the loads of the wave's block at `at`, whose pages are those of block k
-        int id[4];
-        bad = 0;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int v = __builtin_amdgcn_readlane(ids, 4 * k + i);
-            bad |= v < 0 ? 1u << i : 0u;
-            id[i] = v < 0 ? 0 : v;
-        }
-        stage_block<D, ONCE>(p, id, at, head, st);
-    };
-    if (tok < t1) start(tok);
     for (; tok < t1; tok += step) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         const uint32_t none = bad;
@@ -450,7 +456,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DPar
     for (int b = 0; b < D / 16; b++) *(f32x4*)(my + 16 * b + 4 * g) = o[b];
     if (g == 0) { my[D] = m; my[D + 1] = l; }
     __syncthreads();
-    const float out_scale = 1.0f / p.gs[1];
+    const float out_scale = 1.0f / gs_v;
     float* const slot = p.part + ((int64_t)(w.slot + w.part) * p.H * p.row_tiles + w.hr) * (kRows * (D + 2));
     if (w.hr == 0 && w.part == 0 && threadIdx.x == 0) p.plan[w.seq] = make_int2(w.parts, w.slot);
     constexpr int CT = D / 4;  // threads of a row, four columns each
@@ -508,6 +514,13 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     const int hrs = p.H * p.row_tiles, rt = r / kRows, nn = r - rt * kRows;
     const int64_t stride = (int64_t)hrs * (kRows * (D + 2));
     const float* const first = p.part + (int64_t)plan.y * stride + (int64_t)(head * p.row_tiles + rt) * (kRows * (D + 2));
+    // the first parts' rows, under way while the weights are worked out
+    constexpr int AHEAD = 8;
+    const int c = (t % CT) * 4, grp = t / CT;
+    const float* src = first + (int64_t)(grp < n ? grp : 0) * stride + nn * D + c;
+    f32x4 x[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; i++) x[i] = *(const f32x4*)(src + (grp + i * GROUPS < n ? i * GROUPS * stride : 0));
     float top = neg_inf();
     for (int s = t; s < n; s += kThreads) {
         const float m = first[s * stride + kRows * D + nn];
@@ -533,18 +546,11 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     den = 0.0f;
 #pragma unroll
     for (int v = 0; v < kWaves; v++) den += red[kWaves + v];
-    const int c = (t % CT) * 4, grp = t / CT;
-    const float* src = first + (int64_t)grp * stride + nn * D + c;
     f32x4 acc = {};
-    int s = grp;
-    for (; s + 7 * GROUPS < n; s += 8 * GROUPS, src += 8 * GROUPS * stride) {
-        f32x4 x[8];
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = *(const f32x4*)(src + i * GROUPS * stride);
-#pragma unroll
-        for (int i = 0; i < 8; i++) acc += weight[s + i * GROUPS] * x[i];
-    }
-    for (; s < n; s += GROUPS, src += GROUPS * stride) acc += weight[s] * *(const f32x4*)src;
+    for (int i = 0; i < AHEAD; i++)
+        if (grp + i * GROUPS < n) acc += weight[grp + i * GROUPS] * x[i];
+    for (int s = grp + AHEAD * GROUPS; s < n; s += GROUPS) acc += weight[s] * *(const f32x4*)(src + (int64_t)(s - grp) * stride);
     *(f32x4*)(sums + grp * D + c) = acc;
     __syncthreads();
     if (t >= CT) return;

@@ -17,6 +17,7 @@ constexpr int kThreads = 256;
 // ---- rotary positions -----------------------------------------------------------
 
 constexpr int kRopeAngles = 2048;  // (cos, sin) pairs of a workgroup's tokens
+constexpr int64_t kRopeStream = (int64_t)128 << 20;
 
 struct RParams {
     const uint16_t* x;
@@ -28,21 +29,22 @@ struct RParams {
     int ends[kRopeAxes];     // first pair past axis a
 };
 
-__device__ __forceinline__ void rotate8(const u32x4& a, const u32x4& b, const float2* cs, bool halves, u32x4& ya,
-                                        u32x4& yb) {
-    // halves: a holds x1 of the pairs 0..7, b x2; else a holds the pairs 0..3, b 4..7
+// 4 dwords of bf16 pairs.  Halves: a holds x1 of eight pairs, b their x2 (cs: the eight).
+// Else a holds four pairs (ca), b four others (cb).
+template <bool HALVES>
+__device__ __forceinline__ void rotate(u32x4& a, u32x4& b, const float2* ca, const float2* cb) {
 #pragma unroll
     for (int j = 0; j < 4; j++) {
-        if (halves) {
-            const float2 c0 = cs[2 * j], c1 = cs[2 * j + 1];
+        if (HALVES) {
+            const float2 c0 = ca[2 * j], c1 = ca[2 * j + 1];
             const float p0 = bf16_lo(a[j]), p1 = bf16_hi(a[j]), q0 = bf16_lo(b[j]), q1 = bf16_hi(b[j]);
-            ya[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, p1 * c1.x - q1 * c1.y);
-            yb[j] = pack_bf16x2(q0 * c0.x + p0 * c0.y, q1 * c1.x + p1 * c1.y);
+            a[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, p1 * c1.x - q1 * c1.y);
+            b[j] = pack_bf16x2(q0 * c0.x + p0 * c0.y, q1 * c1.x + p1 * c1.y);
         } else {
-            const float2 c0 = cs[j], c1 = cs[4 + j];
+            const float2 c0 = ca[j], c1 = cb[j];
             const float p0 = bf16_lo(a[j]), q0 = bf16_hi(a[j]), p1 = bf16_lo(b[j]), q1 = bf16_hi(b[j]);
-            ya[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, q0 * c0.x + p0 * c0.y);
-            yb[j] = pack_bf16x2(p1 * c1.x - q1 * c1.y, q1 * c1.x + p1 * c1.y);
+            a[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, q0 * c0.x + p0 * c0.y);
+            b[j] = pack_bf16x2(p1 * c1.x - q1 * c1.y, q1 * c1.x + p1 * c1.y);
         }
     }
 }
@@ -50,8 +52,10 @@ __device__ __forceinline__ void rotate8(const u32x4& a, const u32x4& b, const fl
 // (x1, x2) -> (x1 cos - x2 sin, x2 cos + x1 sin) in fp32, rounded once to bf16.
 // The angle pos * inv_freq is formed in fp64 turns and reduced to half a turn before
 // it becomes fp32: at position 2^20 an fp32 product would be off by 0.06 radians.  A
-// workgroup makes the angles of its tokens once, for all their heads.
-template <bool HALVES>
+// workgroup makes the angles of its tokens once, for all their heads.  A thread takes two
+// 16-byte pieces, in the same place of the rotated part's halves, so that eight threads
+// cover whole lines.  STREAM: past the caches, where the tensor is larger than they are.
+template <bool HALVES, bool STREAM>
 __global__ __launch_bounds__(kThreads) void k_rope_axes(RParams p) {
     __shared__ float2 cs[kRopeAngles];
     const int t0 = blockIdx.x * p.tokens;
@@ -67,27 +71,32 @@ __global__ __launch_bounds__(kThreads) void k_rope_axes(RParams p) {
         cs[i] = make_float2(cospif(r), sinpif(r));
     }
     __syncthreads();
-    const int units = p.d >> 4, turned = p.rot >> 4;  // 16 elements each; the first `turned` are rotated
+    const int units = p.d >> 4, turned = p.rot >> 4;  // two pieces each; the first `turned` are rotated
     const int per = p.heads * units;
     for (int i = threadIdx.x; i < nt * per; i += kThreads) {
         const int tok = i / per, r = i - tok * per;
         const int head = r / units, u = r - head * units;
         const bool turn = u < turned;
         const int64_t e = (int64_t)head * p.d;
-        // element offsets of the unit's two 16-byte pieces
-        const int o0 = HALVES && turn ? u * 8 : u * 16;
-        const int o1 = HALVES && turn ? half + u * 8 : u * 16 + 8;
+        // element offsets of the unit's pieces
+        const int o0 = turn ? u * 8 : u * 16;
+        const int o1 = turn ? half + u * 8 : u * 16 + 8;
         const uint16_t* const src = p.x + (t0 + tok) * p.x_stride + e;
         uint16_t* const dst = p.out + (t0 + tok) * p.out_stride + e;
-        u32x4 a = *(const u32x4*)(src + o0), b = *(const u32x4*)(src + o1);
+        u32x4 a = STREAM ? __builtin_nontemporal_load((const u32x4*)(src + o0)) : *(const u32x4*)(src + o0);
+        u32x4 b = STREAM ? __builtin_nontemporal_load((const u32x4*)(src + o1)) : *(const u32x4*)(src + o1);
         if (turn) {
-            u32x4 ya, yb;
-            rotate8(a, b, cs + tok * half + u * 8, HALVES, ya, yb);
-            a = ya;
-            b = yb;
+            const float2* const c = cs + tok * half;
+            if (HALVES) rotate<true>(a, b, c + u * 8, nullptr);
+            else rotate<false>(a, b, c + u * 4, c + (half >> 1) + u * 4);
         }
-        *(u32x4*)(dst + o0) = a;
-        *(u32x4*)(dst + o1) = b;
+        if (STREAM) {
+            __builtin_nontemporal_store(a, (u32x4*)(dst + o0));
+            __builtin_nontemporal_store(b, (u32x4*)(dst + o1));
+        } else {
+            *(u32x4*)(dst + o0) = a;
+            *(u32x4*)(dst + o1) = b;
+        }
     }
 }
 
@@ -103,73 +112,84 @@ struct CParams {
     int t, heads, d, page_log2;
 };
 
-// Where block `blk` (16 elements) of a head's row in `slot` has its 8 bytes of codes
-// and its scale, for K (which = 0) or V.
-__device__ __forceinline__ void cache_at(const CParams& p, int slot, int which, int head, int blk, int64_t& code, int64_t& sf) {
-    const int64_t row = ((int64_t)(slot >> p.page_log2) * 2 + which) * p.heads + head;
-    const int off = slot & ((1 << p.page_log2) - 1);
-    code = (((row << p.page_log2) + off) * p.d >> 1) + blk * 8;
-    sf = (((row * (p.d >> 4)) + blk) << p.page_log2) + off;
-}
-
-// One block a thread; consecutive threads take the blocks of a row, then the heads,
-// the tokens, and K before V.
+// One block (16 elements) of a head's row a thread, of K and of V; consecutive threads take the
+// blocks of a row, then the heads, then the tokens.
 template <bool READ>
 __global__ __launch_bounds__(kThreads) void k_kv_rows(CParams p) {
     const int blocks = p.d >> 4;
-    const int64_t per = (int64_t)p.t * p.heads * blocks;
-    int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    if (i >= 2 * per) return;
-    const int which = i >= per;
-    i -= which ? per : 0;
+    const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     const int64_t row = i / blocks;
     const int blk = (int)(i - row * blocks);
-    const int tok = (int)(row / p.heads), head = (int)(row - (int64_t)tok * p.heads);
+    const int64_t tok = row / p.heads;
+    const int head = (int)(row - tok * p.heads);
+    if (tok >= p.t) return;
     const int slot = p.slots[tok];
     if (slot < 0 || slot >= p.nslots) return;
-    const float gs = p.gs[which];
-    int64_t code, sf;
-    cache_at(p, slot, which, head, blk, code, sf);
-    const int64_t at = tok * (which ? p.v_stride : p.k_stride) + head * p.d + blk * 16;
-    if (!READ) {
-        const u32x4* const src = (const u32x4*)((which ? p.v : p.k) + at);
-        const u32x4 r[2] = {src[0], src[1]};
-        const u32x4 none[2] = {};
-        float f[16];
-        const float amax = process_block<V_BF16>(r, none, f);
-        const uint32_t s = ue4m3_encode(div6(amax) * gs);
-        const float ds = ue4m3_decode(s);
-        u32x2 w;
-        uint32_t w0, w1;
-        pack_block(f, ds == 0.0f ? 0.0f : gs / ds, w0, w1);
-        w[0] = w0;
-        w[1] = w1;
-        *(u32x2*)(p.kv + code) = w;
-        p.sf[sf] = (uint8_t)s;
-    } else {
-        const u32x2 w = *(const u32x2*)(p.kv + code);
-        const float s = ue4m3_decode(p.sf[sf]);
-        // code * scale is exact; its quotient by gs, correctly rounded by one correction
-        // step from the reciprocal (Markstein), then rounded to bf16
-        const float rcp = 1.0f / gs;
-        u32x4 y[2];
-        typedef float f32x2 __attribute__((ext_vector_type(2)));
-        auto put = [&](int j, f32x2 v) {
-            const float a = v[0] * s, b = v[1] * s;
-            const float qa = a * rcp, qb = b * rcp;
-            y[j >> 2][j & 3] = pack_bf16x2(__builtin_fmaf(__builtin_fmaf(-qa, gs, a), rcp, qa),
-                                           __builtin_fmaf(__builtin_fmaf(-qb, gs, b), rcp, qb));
-        };
+    // the head's rows of K and of V on the page, and the row's place among them
+    const int64_t plane = (int64_t)(slot >> p.page_log2) * 2 * p.heads + head;
+    const int off = slot & ((1 << p.page_log2) - 1);
+    int64_t code[2], sf[2];
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            put(4 * h + 0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 0));
-            put(4 * h + 1, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 1));
-            put(4 * h + 2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 2));
-            put(4 * h + 3, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w[h], 1.0f, 3));
+    for (int w = 0; w < 2; w++) {
+        const int64_t r = plane + w * p.heads;
+        code[w] = (((r << p.page_log2) + off) * p.d >> 1) + blk * 8;
+        sf[w] = ((r * blocks + blk) << p.page_log2) + off;
+    }
+    const int64_t at[2] = {tok * p.k_stride + head * p.d + blk * 16, tok * p.v_stride + head * p.d + blk * 16};
+    const float gs[2] = {p.gs[0], p.gs[1]};
+    if (!READ) {
+        u32x4 r[2][2];
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            const u32x4* const src = (const u32x4*)((w ? p.v : p.k) + at[w]);
+            r[w][0] = src[0];
+            r[w][1] = src[1];
         }
-        u32x4* const dst = (u32x4*)((which ? p.vo : p.ko) + at);
-        dst[0] = y[0];
-        dst[1] = y[1];
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            const u32x4 none[2] = {};
+            float f[16];
+            const float amax = process_block<V_BF16>(r[w], none, f);
+            const uint32_t s = ue4m3_encode(div6(amax) * gs[w]);
+            const float ds = ue4m3_decode(s);
+            uint32_t w0, w1;
+            pack_block(f, ds == 0.0f ? 0.0f : gs[w] / ds, w0, w1);
+            *(u32x2*)(p.kv + code[w]) = u32x2{w0, w1};
+            p.sf[sf[w]] = (uint8_t)s;
+        }
+    } else {
+        u32x2 c[2];
+        uint8_t s8[2];
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            c[w] = *(const u32x2*)(p.kv + code[w]);
+            s8[w] = p.sf[sf[w]];
+        }
+#pragma unroll
+        for (int w = 0; w < 2; w++) {
+            const float s = ue4m3_decode(s8[w]);
+            // code * scale is exact; its quotient by gs, correctly rounded by one correction
+            // step from the reciprocal (Markstein), then rounded to bf16
+            const float rcp = 1.0f / gs[w];
+            u32x4 y[2];
+            typedef float f32x2 __attribute__((ext_vector_type(2)));
+            auto put = [&](int j, f32x2 v) {
+                const float a = v[0] * s, b = v[1] * s;
+                const float qa = a * rcp, qb = b * rcp;
+                y[j >> 2][j & 3] = pack_bf16x2(__builtin_fmaf(__builtin_fmaf(-qa, gs[w], a), rcp, qa),
+                                               __builtin_fmaf(__builtin_fmaf(-qb, gs[w], b), rcp, qb));
+            };
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                put(4 * h + 0, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[w][h], 1.0f, 0));
+                put(4 * h + 1, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[w][h], 1.0f, 1));
+                put(4 * h + 2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[w][h], 1.0f, 2));
+                put(4 * h + 3, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[w][h], 1.0f, 3));
+            }
+            u32x4* const dst = (u32x4*)((w ? p.vo : p.ko) + at[w]);
+            dst[0] = y[0];
+            dst[1] = y[1];
+        }
     }
 }
 
@@ -193,8 +213,14 @@ hipError_t launch_rope_axes(const RopeArgs& a, hipStream_t st) {
     while (tokens > 1 && (a.t + tokens - 1) / tokens < 1024) tokens >>= 1;
     p.tokens = (int)tokens;
     const dim3 grid((unsigned)((a.t + tokens - 1) / tokens));
-    if (a.interleaved) k_rope_axes<false><<<grid, kThreads, 0, st>>>(p);
-    else k_rope_axes<true><<<grid, kThreads, 0, st>>>(p);
+    const bool stream = a.t * a.heads * a.d * 2 > kRopeStream;
+    if (a.interleaved) {
+        if (stream) k_rope_axes<false, true><<<grid, kThreads, 0, st>>>(p);
+        else k_rope_axes<false, false><<<grid, kThreads, 0, st>>>(p);
+    } else {
+        if (stream) k_rope_axes<true, true><<<grid, kThreads, 0, st>>>(p);
+        else k_rope_axes<true, false><<<grid, kThreads, 0, st>>>(p);
+    }
     return hipGetLastError();
 }
 
@@ -204,7 +230,7 @@ hipError_t launch_kv_rows(const KvRowsArgs& a, hipStream_t st) {
     p.kv = a.kv; p.sf = a.kv_sf; p.k_stride = a.k_stride; p.v_stride = a.v_stride;
     p.nslots = a.pages * a.page; p.t = (int)a.t; p.heads = (int)a.heads; p.d = (int)a.d;
     p.page_log2 = __builtin_ctzll((unsigned long long)a.page);
-    const int64_t n = 2 * a.t * a.heads * (a.d / 16);
+    const int64_t n = a.t * a.heads * (a.d / 16);
     const dim3 grid((unsigned)((n + kThreads - 1) / kThreads));
     if (a.read) k_kv_rows<true><<<grid, kThreads, 0, st>>>(p);
     else k_kv_rows<false><<<grid, kThreads, 0, st>>>(p);
