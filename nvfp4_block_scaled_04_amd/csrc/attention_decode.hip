@@ -27,6 +27,7 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kBlock = 64;        // tokens a wave takes at a time
 constexpr int kRows = 16;         // query rows of a workgroup
+constexpr int kAttnLdsLong = 54272;  // LDS of a workgroup, three of which fit a CU
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
@@ -42,7 +43,7 @@ struct DParams {
     float* part;              // slots of kRows * (D + 2) floats
     int64_t page_codes, page_sf;  // bytes of a page
     float scale2;             // scale * log2(e)
-    int b, T, Hq, H, G, d, pages, table_pages, page_log2, row_tiles, cap;
+    int b, T, Hq, H, G, d, pages, table_pages, page_log2, row_tiles, cap, split;  // split: parts of all, about
 };
 
 template <int D>
@@ -75,7 +76,7 @@ __device__ __forceinline__ int wave_scan(int v) {
 }
 
 // Which sequence, part and (head, row tile) a workgroup has, and how long the parts
-// are: the tokens of all sequences are shared out evenly over about kAttnParts
+// are: the tokens of all sequences are shared out evenly over about p.split
 // workgroups, so that the time does not hang on the longest sequence.  Every wave works it
 // out from the lengths (on the device, so that a captured graph follows them).
 struct Work {
@@ -99,7 +100,7 @@ __device__ __forceinline__ bool find_work(const DParams& p, Work& w) {
         if (base == 0) first = v;
         total += __builtin_amdgcn_readlane(wave_scan((v + kBlock - 1) / kBlock), 63);
     }
-    int64_t chunk64 = (total * hrs + kAttnParts - 1) / kAttnParts;
+    int64_t chunk64 = (int64_t)((uint64_t)(total * hrs + p.split - 1) / (uint32_t)p.split);
     chunk64 = chunk64 < kAttnMinPart / kBlock ? kAttnMinPart / kBlock : chunk64;
     const uint32_t chunk = chunk64 > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)chunk64;
     int before = 0, slots = 0;
@@ -501,7 +502,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DPar
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     constexpr int CT = D / 4, GROUPS = kThreads / CT;  // threads of a part's row, parts at a time
-    __shared__ float weight[kAttnParts + 64];
+    __shared__ float weight[kAttnPartsLong + 64];
     __shared__ float red[2 * kWaves];
     __shared__ __align__(16) float sums[GROUPS * D];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -564,8 +565,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
 }
 
 template <int D>
-hipError_t launch(const DParams& p, int64_t grid, bool join, hipStream_t st) {
-    constexpr int lds = kWaves * Stage<D>::WAVE > kWaves * kRows * (D + 4) * 4 ? kWaves * Stage<D>::WAVE : kWaves * kRows * (D + 4) * 4;
+hipError_t launch(const DParams& p, int64_t grid, bool join, bool large, hipStream_t st) {
+    constexpr int need = kWaves * Stage<D>::WAVE > kWaves * kRows * (D + 4) * 4 ? kWaves * Stage<D>::WAVE : kWaves * kRows * (D + 4) * 4;
+    const int lds = large && need < kAttnLdsLong ? kAttnLdsLong : need;
     if (p.row_tiles == 1) k_attn_decode<D, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
     else k_attn_decode<D, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
     hipError_t e = hipGetLastError();
@@ -590,15 +592,21 @@ hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     p.page_log2 = __builtin_ctzll((unsigned long long)a.page);
     p.row_tiles = (p.T * p.G + kRows - 1) / kRows;
     p.cap = (int)(a.table_pages * a.page);
-    // the most workgroups that lengths up to the table's can ask for
+    // Long parts (by the table's size, the lengths being on the device) are better off with three
+    // workgroups a CU and cut finer, so that the last ones end together; short ones with four,
+    // whose beginnings overlap.  64 sequences to 16384: 122 us against 131; 4 to 131072: 109
+    // against 121; 64 of 16384 each: 203 against 193; 256 to 2048: 93 against 79 (not taken).
     const int64_t hrs = (int64_t)p.H * p.row_tiles;
-    int64_t units = (kAttnParts + hrs - 1) / hrs + p.b;
+    const bool large = p.cap >= 2 * kAttnLong && p.b * hrs * p.cap >= kAttnLong * kAttnParts;
+    p.split = large ? kAttnPartsLong : kAttnParts;
+    // the most workgroups that lengths up to the table's can ask for
+    int64_t units = (p.split + hrs - 1) / hrs + p.b;
     const int64_t each = (p.cap + kAttnMinPart - 1) / kAttnMinPart;
     if (each * p.b < units) units = each * p.b;
     const bool join = each > 1;
-    if (a.d <= 64) return launch<64>(p, units * hrs, join, st);
-    if (a.d <= 128) return launch<128>(p, units * hrs, join, st);
-    return launch<256>(p, units * hrs, join, st);
+    if (a.d <= 64) return launch<64>(p, units * hrs, join, large, st);
+    if (a.d <= 128) return launch<128>(p, units * hrs, join, large, st);
+    return launch<256>(p, units * hrs, join, large, st);
 }
 
 }  // namespace nvfp4
