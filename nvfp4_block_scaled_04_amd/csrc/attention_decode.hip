@@ -63,18 +63,6 @@ __device__ __forceinline__ int swizzle(int r) { return (r / (512 / D)) & (D / 32
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
 
-// Inclusive prefix sum over a wave, through DPP: 4 shifts within rows of 16, then the
-// rows' last values to the rows behind.
-__device__ __forceinline__ int wave_scan(int v) {
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
-    return v;
-}
-
 // Which sequence, part and (head, row tile) a workgroup has, and how long the parts
 // are: the tokens of all sequences are shared out evenly over about p.split
 // workgroups, so that the time does not hang on the longest sequence.  Every wave works it

@@ -65,12 +65,7 @@ __device__ __forceinline__ bool find_tile(const PParams& p, int unit, Seq& s, in
         Seq mine = {};
         if (i < p.b) mine = seq_at(p, i);
         const int n = (mine.nq + ROWS - 1) / ROWS;
-        int sum = n;
-#pragma unroll
-        for (int o = 1; o < 64; o *= 2) {
-            const int a = __shfl_up(sum, o);
-            if (lane >= o) sum += a;
-        }
+        const int sum = wave_scan(n);
         const uint64_t hit = __ballot(before + sum > unit);
         if (hit) {
             const int l = __builtin_ctzll(hit);
@@ -115,7 +110,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     constexpr int TILE = kKeys * D * 2;         // bytes of a tile of K (of V)
     constexpr int LOADS = kKeys * CH / (64 * NW);  // of a lane, of K (of V)
     constexpr int ROWS = NW * 32;
-    extern __shared__ __align__(16) uint8_t smem[];  // two tiles of K, two of V
+    extern __shared__ __align__(16) uint8_t smem[];  // two tiles of K, two of V (with eight waves, their queries)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l32 = lane & 31, hi = lane >> 5;
@@ -169,20 +164,30 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     const int tiles = (keys + kKeys - 1) / kKeys;
     if (tiles > 0) stage_k(0);
 
-    // the wave's queries, and what each row sees
+    // The wave's 32 rows of q go through LDS too, in whole lines (fragments straight from memory
+    // would touch every line four times): behind the tiles, or, with four waves, where
+    // the second tiles of K and V will be.
     const int first = row0 + wave * 32;
-    const int mine = first + l32;
-    const int end = mine >= sq.nq ? 0 : p.causal ? clamp_to(mine + back + 1, 0, sq.nk) : sq.nk;  // keys below it are seen
-    bf16x8 q[D / 16];
+    const uint32_t q_lds = NW == 8 ? 4 * TILE + wave * (TILE / 2) : (wave < 2 ? TILE : 3 * TILE) + (wave & 1) * (TILE / 2);
     {
-        const uint16_t* const src = p.q + (int64_t)(sq.q0 + (mine < sq.nq ? mine : 0)) * p.q_stride + head * p.d;
+        const int rows = sq.nq - first;  // those behind the sequence come as zeros
+        const u32x4 rs = raw_buffer(p.q + (int64_t)(sq.q0 + first) * p.q_stride + head * p.d,
+                                    rows > 0 ? (uint32_t)(((rows < 32 ? rows - 1 : 31) * p.q_stride + p.d) * 2) : 0u);
 #pragma unroll
-        for (int s = 0; s < D / 16; s++) {
-            u32x4 w = {};
-            if (mine < sq.nq && 16 * s + 8 * hi < p.d) w = *(const u32x4*)(src + 16 * s + 8 * hi);
-            q[s] = __builtin_bit_cast(bf16x8, w);
+        for (int i = 0; i < 32 * CH / 64; i++) {
+            const int piece = i * 64 + lane;
+            const int r = piece / CH, c = (piece % CH) ^ swizzle_k<D>(r);
+            load_to_lds(rs, c * 8 < p.d ? (uint32_t)(r * (int)p.q_stride + c * 8) * 2u : 0xFFFFFFF0u,
+                        __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + q_lds + i * 1024));
         }
     }
+    const int mine = first + l32;
+    const int end = mine >= sq.nq ? 0 : p.causal ? clamp_to(mine + back + 1, 0, sq.nk) : sq.nk;  // keys below it are seen
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    bf16x8 q[D / 16];
+#pragma unroll
+    for (int s = 0; s < D / 16; s++)
+        q[s] = *(const __attribute__((address_space(3))) bf16x8*)(lds + q_lds + l32 * D * 2 + ((2 * s + hi) ^ swizzle_k<D>(l32)) * 16);
     // (waited for here, not at every use in the loop)
 #pragma unroll
     for (int s = 0; s < D / 16; s++) asm volatile("" : "+v"(q[s]));
@@ -445,24 +450,30 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
 
     const float den = l + __shfl_xor(l, 32);
     const float by = den == 0.0f ? 0.0f : 1.0f / den;
-    if (mine >= sq.nq) return;
-    uint16_t* const dst = p.out + (int64_t)(sq.q0 + mine) * p.out_stride + head * p.d;
+    if (p.lse && hi == 0 && mine < sq.nq) p.lse[(int64_t)(sq.q0 + mine) * p.Hq + head] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
+    // the rows leave through LDS, in whole lines
+    __syncthreads();
+    lds_u8* const mo = lds + wave * (TILE / 2);
 #pragma unroll
     for (int c = 0; c < D / 32; c++)
 #pragma unroll
-        for (int e = 0; e < 16; e += 4) {
-            const int col = 32 * c + 2 * e + 4 * hi;
-            if (col < p.d)
-                *(u32x2*)(dst + col) = u32x2{pack_bf16x2(o[c][e] * by, o[c][e + 1] * by), pack_bf16x2(o[c][e + 2] * by, o[c][e + 3] * by)};
-        }
-    if (p.lse && hi == 0) p.lse[(int64_t)(sq.q0 + mine) * p.Hq + head] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
+        for (int e = 0; e < 16; e += 4)
+            *(__attribute__((address_space(3))) u32x2*)(mo + l32 * D * 2 + ((4 * c + (e >> 2)) ^ swizzle_k<D>(l32)) * 16 + 8 * hi) =
+                u32x2{pack_bf16x2(o[c][e] * by, o[c][e + 1] * by), pack_bf16x2(o[c][e + 2] * by, o[c][e + 3] * by)};
+#pragma unroll
+    for (int i = 0; i < 32 * CH / 64; i++) {
+        const int piece = i * 64 + lane;
+        const int r = piece / CH, c = piece % CH;
+        const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(mo + r * D * 2 + (c ^ swizzle_k<D>(r)) * 16);
+        if (first + r < sq.nq && c * 8 < p.d) *(u32x4*)(p.out + (int64_t)(sq.q0 + first + r) * p.out_stride + head * p.d + c * 8) = w;
+    }
 #endif
 }
 
 template <int D, int NW>
 hipError_t launch(PParams& p, hipStream_t st) {
     p.units = p.tq / (NW * 32) + p.b;  // tiles that no sequence has return at once
-    k_attn_prefill<D, NW><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, 4 * kKeys * D * 2, st>>>(p);
+    k_attn_prefill<D, NW><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, (NW == 8 ? 8 : 4) * kKeys * D * 2, st>>>(p);
     return hipGetLastError();
 }
 

@@ -65,6 +65,18 @@ __device__ __forceinline__ float xor1(float v) {
     return bits_f((uint32_t)__builtin_amdgcn_mov_dpp((int)f_bits(v), 0xB1, 0xF, 0xF, true));
 }
 
+// Inclusive prefix sum over a wave, through DPP: 4 shifts within rows of 16, then the
+// rows' last values to the rows behind.
+__device__ __forceinline__ int wave_scan(int v) {
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+    return v;
+}
+
 // fp32(x / 6) for x >= 0, correctly rounded, without the division sequence:
 // q0 = x * RN(1/6), then one correction step with the exact FMA residual
 // r = x - q0 * 6 (Markstein's correction for division by a constant).
