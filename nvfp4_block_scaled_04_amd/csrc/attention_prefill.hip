@@ -5,9 +5,9 @@
 //   s_j = q_i . k_j, p_j = 2^(s_j * c - m), out_i = sum p_j v_j / sum p_j,
 // c = scale * log2(e), one pass over the keys with the running maximum m and sum.
 //
-// A workgroup of four waves takes 128 or 256 rows of one head, a wave 32 or 64 of them.
-// 64 keys and values at a time go straight from memory into LDS (two buffers), swizzled
-// at their source so that neither product's reads collide in the banks.  Both products run
+// A workgroup of four or eight waves takes 128 or 256 rows of one head, a wave 32 of them (see
+// launch_attention_prefill).  64 keys and values at a time go straight from memory into LDS (two
+// buffers), swizzled at their source so that neither product's reads collide in the banks.  Both products run
 // on 32x32x16 bf16 MFMAs, transposed:
 //   S^T[key, row] = K Q^T: a lane owns one row (and half of the keys), so the softmax
 //   needs one exchange between lanes, and only where the maximum moves;
@@ -102,17 +102,21 @@ __device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
     return u32x4{(uint32_t)a, (uint32_t)(a >> 32) & 0xFFFFu, bytes, 0x00020000u};
 }
 
-// NW: waves of a workgroup, 32 rows each.  Eight waves sit two to a SIMD and take turns (sweep_paired).
-template <int D, int NW>
+// NW: waves of a workgroup.  Eight waves sit two to a SIMD and take turns (sweep_paired).
+// SPLIT: 1: each wave has 32 rows of its own; 2: the second four waves have the rows of
+// the first, which take every other tile of keys, and the halves are joined at the end.
+template <int D, int NW, int SPLIT>
 __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int CH = D / 8;                   // chunks of a row
     constexpr int TILE = kKeys * D * 2;         // bytes of a tile of K (of V)
-    constexpr int LOADS = kKeys * CH / (64 * NW);  // of a lane, of K (of V)
-    constexpr int ROWS = NW * 32;
-    extern __shared__ __align__(16) uint8_t smem[];  // two tiles of K, two of V (with eight waves, their queries)
+    constexpr int GW = NW / SPLIT;              // waves of a group, which share tiles
+    constexpr int LOADS = kKeys * CH / (64 * GW);  // of a lane, of K (of V)
+    constexpr int ROWS = GW * 32;
+    extern __shared__ __align__(16) uint8_t smem[];  // two tiles of K, two of V a group (and the queries of a group of eight)
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int grp = SPLIT == 1 ? 0 : wave / GW, gw = SPLIT == 1 ? wave : wave % GW;
     const int l32 = lane & 31, hi = lane >> 5;
 
     // Workgroups are dealt to the 8 XCDs in turn: where the heads split evenly, an XCD
@@ -140,35 +144,38 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
 
     const uint16_t* const kb = p.k + (int64_t)sq.k0 * p.k_stride + kv * p.d;
     const uint16_t* const vb = p.v + (int64_t)sq.k0 * p.v_stride + kv * p.d;
-    lds_u8* const lds = (lds_u8*)smem;
-    const uint32_t lds0 = (uint32_t)(uintptr_t)lds + wave * 1024;
+    lds_u8* const lds = (lds_u8*)smem + grp * 4 * TILE;  // the group's tiles
+    const uint32_t lds0 = (uint32_t)(uintptr_t)lds + gw * 1024;
     // a lane's offsets into a tile in memory: a row past the last one ends behind the buffer by
     // itself, a chunk past d is sent there
     uint32_t off_k[LOADS], off_v[LOADS];
 #pragma unroll
     for (int i = 0; i < LOADS; i++) {
-        const int piece = (i * NW + wave) * 64 + lane;
+        const int piece = (i * GW + gw) * 64 + lane;
         const int r = piece / CH, at = piece % CH;
         const int ck = at ^ swizzle_k<D>(r), cv = at ^ swizzle_v<D>(r);
         off_k[i] = ck * 8 < p.d ? (uint32_t)(r * (int)p.k_stride + ck * 8) * 2u : 0xFFFFFFF0u;
         off_v[i] = cv * 8 < p.d ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
     }
+    // the group's n-th tile of keys
+    auto key_of = [&](int n) { return (n * SPLIT + grp) * kKeys; };
     auto stage = [&](const uint16_t* base, int64_t stride, const uint32_t (&off)[LOADS], int key0, uint32_t to) {
         const int rows = sq.nk - key0 < kKeys ? sq.nk - key0 : kKeys;  // at least 1; later rows come as zeros
         const u32x4 rs = raw_buffer(base + key0 * stride, (uint32_t)(((rows - 1) * stride + p.d) * 2));
 #pragma unroll
-        for (int i = 0; i < LOADS; i++) load_to_lds(rs, off[i], __builtin_amdgcn_readfirstlane(lds0 + to + i * NW * 1024));
+        for (int i = 0; i < LOADS; i++) load_to_lds(rs, off[i], __builtin_amdgcn_readfirstlane(lds0 + to + i * GW * 1024));
     };
-    auto stage_k = [&](int n) { stage(kb, p.k_stride, off_k, n * kKeys, (n & 1) * TILE); };
-    auto stage_v = [&](int n) { stage(vb, p.v_stride, off_v, n * kKeys, (2 + (n & 1)) * TILE); };
-    const int tiles = (keys + kKeys - 1) / kKeys;
+    auto stage_k = [&](int n) { stage(kb, p.k_stride, off_k, key_of(n), (n & 1) * TILE); };
+    auto stage_v = [&](int n) { stage(vb, p.v_stride, off_v, key_of(n), (2 + (n & 1)) * TILE); };
+    auto tiles_of = [&](int upto) { return (upto + kKeys * (SPLIT - grp) - 1) / (kKeys * SPLIT); };  // of the group, of the keys below
+    const int tiles = tiles_of(keys), steps = (keys + kKeys * SPLIT - 1) / (kKeys * SPLIT);
     if (tiles > 0) stage_k(0);
 
     // The wave's 32 rows of q go through LDS too, in whole lines (fragments straight from memory
-    // would touch every line four times): behind the tiles, or, with four waves, where
-    // the second tiles of K and V will be.
-    const int first = row0 + wave * 32;
-    const uint32_t q_lds = NW == 8 ? 4 * TILE + wave * (TILE / 2) : (wave < 2 ? TILE : 3 * TILE) + (wave & 1) * (TILE / 2);
+    // would touch every line four times): behind the tiles, or, with four waves a
+    // group, where its second tiles of K and V will be.
+    const int first = row0 + gw * 32;
+    const uint32_t q_lds = GW == 8 ? 4 * TILE + gw * (TILE / 2) : (gw < 2 ? TILE : 3 * TILE) + (gw & 1) * (TILE / 2);
     {
         const int rows = sq.nq - first;  // those behind the sequence come as zeros
         const u32x4 rs = raw_buffer(p.q + (int64_t)(sq.q0 + first) * p.q_stride + head * p.d,
@@ -231,7 +238,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     };
     // its probabilities: pf[f] the keys 16 f .. of it
     auto soften = [&](int n, f32x16 (&s)[2], bf16x8 (&pf)[4]) {
-        const int key0 = n * kKeys;
+        const int key0 = key_of(n);
         if (key0 + kKeys > all) {
 #pragma unroll
             for (int e = 0; e < 32; e++)
@@ -287,13 +294,13 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     // see it, is kept out of the product and handed to the rows that do.
     auto sweep = [&](auto CAREFUL) {
         if (tiles > 0) stage_v(0);
-        for (int n = 0; n < tiles; n++) {
+        for (int n = 0; n < steps; n++) {
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the tile is there, the other buffers have been read
             if (n + 1 < tiles) {
                 stage_k(n + 1);
                 stage_v(n + 1);
             }
-            const int key0 = n * kKeys;
+            const int key0 = key_of(n);
             if (key0 >= any) continue;
             f32x16 s[2];
             bf16x8 pf[4];
@@ -348,7 +355,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     // last read in the step before.
     auto sweep_paired = [&]() {
         const bool behind = wave >= NW / 2;
-        const int own = (any + kKeys - 1) / kKeys;  // tiles that the wave sees
+        const int own = tiles_of(any);  // tiles that the wave sees
         f32x16 s[2];
         bf16x8 pf[4];
         auto end_half = [&](auto LANDED) {
@@ -423,7 +430,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
             end_half(std::true_type{});
             n++;
         }
-        for (; n <= tiles; n++) {  // tiles that only other waves see
+        for (; n <= steps; n++) {  // tiles that only other waves see
             feed(n);
             end_half(std::false_type{});
             end_half(std::true_type{});
@@ -448,12 +455,39 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         }
     }
 
+    __syncthreads();  // the tiles have been read
+    if constexpr (SPLIT == 2) {  // the second group's sums to the first, lane by lane
+        lds_u8* const all_lds = (lds_u8*)smem;
+        __attribute__((address_space(3))) f32x4* const sums = (__attribute__((address_space(3))) f32x4*)(all_lds + (4 + gw) * TILE) + lane;
+        __attribute__((address_space(3))) float* const stats = (__attribute__((address_space(3))) float*)(all_lds + 2 * TILE + gw * 512) + lane;
+        if (grp == 1) {
+#pragma unroll
+            for (int i = 0; i < D / 32; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sums[(4 * i + e) * 64] = f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+            stats[0] = m;
+            stats[64] = l;
+        }
+        __syncthreads();
+        if (grp == 1) return;
+        const float m1 = stats[0], to = __builtin_fmaxf(m, m1);
+        const float a0 = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m - to), a1 = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m1 - to);
+        l = l * a0 + stats[64] * a1;
+        m = to;
+#pragma unroll
+        for (int i = 0; i < D / 32; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const f32x4 v = sums[(4 * i + e) * 64];
+#pragma unroll
+                for (int j = 0; j < 4; j++) o[i][4 * e + j] = o[i][4 * e + j] * a0 + v[j] * a1;
+            }
+    }
     const float den = l + __shfl_xor(l, 32);
     const float by = den == 0.0f ? 0.0f : 1.0f / den;
     if (p.lse && hi == 0 && mine < sq.nq) p.lse[(int64_t)(sq.q0 + mine) * p.Hq + head] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
     // the rows leave through LDS, in whole lines
-    __syncthreads();
-    lds_u8* const mo = lds + wave * (TILE / 2);
+    lds_u8* const mo = lds + gw * (TILE / 2);
 #pragma unroll
     for (int c = 0; c < D / 32; c++)
 #pragma unroll
@@ -470,10 +504,10 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
 #endif
 }
 
-template <int D, int NW>
+template <int D, int NW, int SPLIT>
 hipError_t launch(PParams& p, hipStream_t st) {
-    p.units = p.tq / (NW * 32) + p.b;  // tiles that no sequence has return at once
-    k_attn_prefill<D, NW><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, (NW == 8 ? 8 : 4) * kKeys * D * 2, st>>>(p);
+    p.units = p.tq / (NW / SPLIT * 32) + p.b;  // tiles that no sequence has return at once
+    k_attn_prefill<D, NW, SPLIT><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, NW * kKeys * D * 2, st>>>(p);
     return hipGetLastError();
 }
 
@@ -486,9 +520,24 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     p.c = a.scale * 1.44269504088896340736f;
     p.b = (int)a.b; p.tq = (int)a.tq; p.tk = (int)a.tk; p.Hq = (int)a.q_heads; p.H = (int)a.heads;
     p.G = p.Hq / p.H; p.d = (int)a.d; p.causal = a.causal;
-    if (a.d <= 64) return launch<64, 4>(p, st);
-    if (a.d <= 128) return launch<128, 8>(p, st);
-    return launch<256, 4>(p, st);
+    // The workgroup, by the average sequence (the lengths themselves are on the device), measured
+    // with 32 heads of 128:
+    //   * few tiles of rows for the CUs, or few and of unequal work (causal, no long prefix): 128
+    //     rows, the keys split (1 prompt of 1024: 21.9 us, 27.8 unsplit; of 2048: 44.6, 53.2; 16
+    //     rows behind 8000 keys: 94, 153; but 4 of 512: 27.9, 24.4; 4 of 300 behind 2000: 68, 66);
+    //   * long ones: 256 rows (2 of 2048: 73.5 us, 80.2 with 128 rows; 4 of 300 behind 2000: 58,
+    //     66; but 64 of 256: 126, 103);
+    //   * others: 128 rows.  (Heads of 64, bound by the softmax's arithmetic, gain nothing from
+    //     256 rows: 32 of 1500: 582 us, 421.)
+    const int64_t nq = a.tq / a.b, nk = a.tk / a.b, tiles = a.b * ((nq + 127) / 128) * a.q_heads;
+    const bool split = (tiles <= 256 && nk >= 128) ||
+                       (tiles <= 512 && nk >= 1024 && nq >= 128 && a.causal && 2 * a.tk <= 3 * a.tq);
+    if (a.d <= 64) return split ? launch<64, 8, 2>(p, st) : launch<64, 4, 1>(p, st);
+    if (a.d <= 128) {
+        if (split) return launch<128, 8, 2>(p, st);
+        return nq >= 256 && nk >= 1024 ? launch<128, 8, 1>(p, st) : launch<128, 4, 1>(p, st);
+    }
+    return launch<256, 4, 1>(p, st);
 }
 
 }  // namespace nvfp4

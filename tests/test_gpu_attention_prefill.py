@@ -53,6 +53,9 @@ def inputs(lq, lk, q_heads, heads, d, seed):
     ((0, 7, 0, 33), (0, 7, 5, 33), 2, 1, 64), ((5, 9), (0, 9), 2, 2, 128), ((10, 300), (4, 100), 3, 1, 128), ((129, 255, 256, 257), (129, 255, 256, 257), 2, 2, 96),
     ((1, 1, 40), (700, 129, 1100), 8, 2, 128), ((200,), (1500,), 5, 1, 64), ((70, 3), (70, 259), 2, 1, 256), ((90,), (200,), 2, 2, 224), ((33, 200), (33, 200), 7, 7, 80),
     ((1000,), (1000,), 10, 2, 128), ((513, 700), (600, 701), 3, 3, 64), ((2500,), (2500,), 2, 1, 128),
+    # many tiles: 256 rows a workgroup (long), 128 (short), heads of 64, 96 and 256
+    ((2300, 1900), (2300, 1900), 16, 2, 128), ((1100, 1, 1990), (1190, 1500, 1990), 24, 4, 96), ((300,) * 9, (300,) * 9, 16, 8, 128), ((257, 2, 900), (257, 2, 900), 64, 8, 64),
+    ((513, 320), (513, 1320), 40, 8, 128), ((200, 300), (200, 300), 8, 4, 256), ((7, 16), (5000, 3111), 8, 2, 128), ((1,), (4097,), 16, 4, 64),
 ])
 def test_prefill(att, lq, lk, q_heads, heads, d, causal):
     say("prefill", lq, lk, q_heads, heads, d, causal)
@@ -98,24 +101,27 @@ def test_scale_and_peaks(att):
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_values_behind_the_mask_do_not_matter(att, bad):
+@pytest.mark.parametrize("lens,q_heads,heads,d", [((200, 90), 2, 1, 64), ((200, 90), 2, 1, 128), ((200, 90), 2, 1, 256), ((200, 90), 136, 2, 128),
+                                                  ((200, 90), 136, 2, 64), ((1100, 1060), 32, 2, 128)])
+def test_values_behind_the_mask_do_not_matter(att, bad, lens, q_heads, heads, d):
     """Rows before a key or value that is not finite, and other sequences, come out as without it."""
-    say("prefill behind the mask", bad)
-    for d in (64, 128, 256):
-        q, k, v, cq, ck = inputs((200, 90), (200, 90), 2, 1, d, 11)
-        clean = att.attention_prefill(q, k, v, cq, ck)
-        at = 133
-        for which in (k, v):
-            x = which.clone()
-            x[at, 0, 7] = bad
-            out = att.attention_prefill(q, x if which is k else k, x if which is v else v, cq, ck)
-            assert torch.equal(out[:at], clean[:at]), (d, which is k)
-            assert torch.equal(out[200:], clean[200:]), (d, which is k)
-            if which is v:
-                assert not bool(out[at:200, :, 7].isfinite().any())
-                keep = torch.ones(d, dtype=torch.bool)
-                keep[7] = False
-                assert torch.equal(out[at:200][..., keep], clean[at:200][..., keep])
+    say("prefill behind the mask", bad, lens, q_heads, heads, d)
+    q, k, v, cq, ck = inputs(lens, lens, q_heads, heads, d, 11)
+    clean = att.attention_prefill(q, k, v, cq, ck)
+    at, n = lens[0] - 67, lens[0]
+    for which in (k, v):
+        x = which.clone()
+        x[at, 0, 7] = bad
+        out = att.attention_prefill(q, x if which is k else k, x if which is v else v, cq, ck)
+        assert torch.equal(out[:at], clean[:at]), which is k
+        assert torch.equal(out[n:], clean[n:]), which is k
+        if which is v:
+            mine = slice(0, q_heads // heads)
+            assert not bool(out[at:n, mine, 7].isfinite().any())
+            keep = torch.ones(d, dtype=torch.bool)
+            keep[7] = False
+            assert torch.equal(out[at:n][..., keep], clean[at:n][..., keep])
+            assert torch.equal(out[:, q_heads // heads:], clean[:, q_heads // heads:])
 
 
 def test_neighbours_do_not_matter(att):
