@@ -86,7 +86,7 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
 
 /* Parts of split sequences that the workspace holds: 16 rows of d (rounded up to 64, 128 or
  * 256) fp32 sums, their maximum and sum each. */
-#define NVFP4_ATTENTION_MAX_SLOTS 1536
+#define NVFP4_ATTENTION_MAX_SLOTS 2048
 #define NVFP4_ATTENTION_WS_BYTES(b, d)                 \
     ((8 * (int64_t)(b) + 255) / 256 * 256 +            \
      (int64_t)NVFP4_ATTENTION_MAX_SLOTS * 64 * (((d) <= 64 ? 64 : (d) <= 128 ? 128 : 256) + 2))

@@ -16,7 +16,7 @@ from .ops import BF16, BYTES, F32, I32, _check, _dev
 
 EXPORTS = ("rope_axes", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_attention_decode", "attention_prefill")
 
-MAX_SLOTS = 1536  # NVFP4_ATTENTION_MAX_SLOTS
+MAX_SLOTS = 2048  # NVFP4_ATTENTION_MAX_SLOTS
 MAX_AXES = 4      # NVFP4_ROPE_MAX_AXES
 _Sections = ctypes.c_int32 * MAX_AXES
 

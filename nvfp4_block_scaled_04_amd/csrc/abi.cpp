@@ -518,7 +518,7 @@ int nvfp4_gemm_adapters(const uint8_t* a, const uint8_t* b, const uint8_t* a_sf,
     return launch_status(nvfp4::launch_gemm(g, (hipStream_t)stream));
 }
 
-static_assert(nvfp4::kRopeAxes == NVFP4_ROPE_MAX_AXES && 2 * nvfp4::kAttnPartsLong == NVFP4_ATTENTION_MAX_SLOTS,
+static_assert(nvfp4::kRopeAxes == NVFP4_ROPE_MAX_AXES && 2 * nvfp4::kAttnPartsNarrow == NVFP4_ATTENTION_MAX_SLOTS,
               "the header's limits are the kernels'");
 
 // Rows of heads [t, heads, d] with a stride from token to token, in elements.

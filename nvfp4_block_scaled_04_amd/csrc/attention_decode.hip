@@ -211,7 +211,7 @@ __device__ __forceinline__ void read_columns(uint32_t at, uint32_t sw, u32x2 (&v
 }
 
 template <int D, bool ONCE>
-__global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DParams p) {
+__global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_attn_decode(DParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using S = Stage<D>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -490,7 +490,7 @@ __global__ __launch_bounds__(kThreads, D <= 128 ? 4 : 2) void k_attn_decode(DPar
 template <int D>
 __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     constexpr int CT = D / 4, GROUPS = kThreads / CT;  // threads of a part's row, parts at a time
-    __shared__ float weight[kAttnPartsLong + 64];
+    __shared__ float weight[kAttnPartsNarrow + 64];
     __shared__ float red[2 * kWaves];
     __shared__ __align__(16) float sums[GROUPS * D];
     const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
@@ -555,7 +555,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
 template <int D>
 hipError_t launch(const DParams& p, int64_t grid, bool join, bool large, hipStream_t st) {
     constexpr int need = kWaves * Stage<D>::WAVE > kWaves * kRows * (D + 4) * 4 ? kWaves * Stage<D>::WAVE : kWaves * kRows * (D + 4) * 4;
-    const int lds = large && need < kAttnLdsLong ? kAttnLdsLong : need;
+    const int lds = D > 64 && large && need < kAttnLdsLong ? kAttnLdsLong : need;
     if (p.row_tiles == 1) k_attn_decode<D, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
     else k_attn_decode<D, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
     hipError_t e = hipGetLastError();
@@ -584,9 +584,11 @@ hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     // workgroups a CU and cut finer, so that the last ones end together; short ones with four,
     // whose beginnings overlap.  64 sequences to 16384: 122 us against 131; 4 to 131072: 109
     // against 121; 64 of 16384 each: 203 against 193; 256 to 2048: 93 against 79 (not taken).
+    // Heads of 64 have half the bytes a wave, so five workgroups a CU and more parts: 32 of 8192:
+    // 43 us with 1024 parts, 49 with 512, 47 with 2048.
     const int64_t hrs = (int64_t)p.H * p.row_tiles;
     const bool large = p.cap >= 2 * kAttnLong && p.b * hrs * p.cap >= kAttnLong * kAttnParts;
-    p.split = large ? kAttnPartsLong : kAttnParts;
+    p.split = a.d <= 64 ? kAttnPartsNarrow : large ? kAttnPartsLong : kAttnParts;
     // the most workgroups that lengths up to the table's can ask for
     int64_t units = (p.split + hrs - 1) / hrs + p.b;
     const int64_t each = (p.cap + kAttnMinPart - 1) / kAttnMinPart;

@@ -179,6 +179,7 @@ hipError_t launch_kv_rows(const KvRowsArgs& a, hipStream_t st);
 // Attention of t tokens a sequence over the paged NVFP4 cache.
 constexpr int64_t kAttnParts = 512;       // parts that the tokens of all sequences are split into, about
 constexpr int64_t kAttnPartsLong = 768;   // the same where they are long
+constexpr int64_t kAttnPartsNarrow = 1024;  // the same for heads of up to 64
 constexpr int64_t kAttnLong = 4096;       // tokens of a long part, of a sequence twice as long
 constexpr int64_t kAttnMinPart = 256;     // fewest tokens of a part
 struct AttnDecodeArgs {

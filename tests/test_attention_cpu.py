@@ -80,7 +80,7 @@ DEC = dict(q=P, b=2, t=1, hq=16, kv=P, sf=P, gs=P, heads=4, d=128, pages=10, pag
     ({"hq": 0}, SHAPE), ({"per": 0}, SHAPE), ({"t": 65}, UNSUP), ({"b": 65537}, UNSUP), ({"scale": 0.0}, UNSUP), ({"scale": -1.0}, UNSUP),
     ({"scale": float("nan")}, UNSUP), ({"scale": float("inf")}, UNSUP), ({"per": (1 << 24) + 1}, UNSUP), ({"hq": 1 << 16}, UNSUP),
     ({"b": 65536, "t": 64, "hq": 16384, "heads": 8192}, UNSUP),
-    ({"wsb": 256 + 1536 * 64 * 130 - 1}, SHAPE), ({"q": P + 8}, MISAL), ({"out": P + 4}, MISAL), ({"ws": P + 8}, MISAL), ({"table": P + 1}, MISAL),
+    ({"wsb": 256 + 2048 * 64 * 130 - 1}, SHAPE), ({"q": P + 8}, MISAL), ({"out": P + 4}, MISAL), ({"ws": P + 8}, MISAL), ({"table": P + 1}, MISAL),
     ({"lens": P + 2}, MISAL), ({"lse": P + 2}, MISAL),
 ])
 def test_decode_validation(att, change, status):
