@@ -101,7 +101,7 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
  * exact; q enters the products as fp16 scaled by a power of two per head (exact, but off by up to
  * 2^-39 of the head's largest where it is below 2^-28 of it), the probabilities as fp16;
  * sums are fp32.  The tokens of long sequences are split over workgroups, whose parts a
- * second launch joins; how, depends on all lengths, which are read on the device (a
+ * second launch joins; how, depends on the lengths, which are read on the device (a
  * captured graph follows them).  Results are the same on every call.
  *   q: [b, t, q_heads, d] bf16; block_table: [b, table_pages] int32 (entries past a
  *   sequence's last page are not read); lengths: [b] int32; out: [b, t, q_heads, d] bf16;

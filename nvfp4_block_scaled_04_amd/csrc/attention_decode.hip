@@ -26,7 +26,7 @@ namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kBlock = 64;        // tokens a wave takes at a time
-constexpr int kRows = 16;         // query rows of a workgroup
+constexpr int kRows = 16;         // query rows of a matrix product
 constexpr int kAttnLdsLong = 54272;  // LDS of a workgroup, three of which fit a CU
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -210,8 +210,9 @@ __device__ __forceinline__ void read_columns(uint32_t at, uint32_t sw, u32x2 (&v
     }
 }
 
-template <int D, bool ONCE>
-__global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_attn_decode(DParams p) {
+// NT: products' worths of query rows of a workgroup, which share the dequantized keys and values.
+template <int D, int NT, bool ONCE>
+__global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_attn_decode(DParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using S = Stage<D>;
     extern __shared__ __align__(16) uint8_t smem[];
@@ -229,20 +230,26 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
     const int32_t* const row = p.table + (int64_t)w.seq * p.table_pages;
 
     // the row's queries, under way while the first block's pages and loads are worked out
-    const int r = rt * kRows + n;
-    const bool live = r < p.T * p.G;
-    const int qt = live ? r / p.G : 0;
-    const int64_t qrow = ((int64_t)w.seq * p.T + qt) * p.Hq + head * p.G + (live ? r - qt * p.G : 0);
+    constexpr int ROWS = NT * kRows;
     constexpr int QW = D / 32;
+    int limit[NT];  // tokens a row sees
     const int step = kWaves * kBlock;
     int tok = t0 + wave * kBlock;
     int ids = load_pages(p, row, tok, t1), ids_next = load_pages(p, row, tok + 16 * step, t1);
-    u32x4 raw[QW];
+    u32x4 raw[NT][QW];
 #pragma unroll
-    for (int s = 0; s < QW; s++) {
-        const int col = g * (D / 4) + 8 * s;
-        raw[s] = u32x4{};
-        if (live && col < p.d) raw[s] = *(const u32x4*)(p.q + qrow * p.d + col);
+    for (int t = 0; t < NT; t++) {
+        const int r = rt * ROWS + t * kRows + n;
+        const bool live = r < p.T * p.G;
+        const int qt = live ? r / p.G : 0;
+        const int64_t qrow = ((int64_t)w.seq * p.T + qt) * p.Hq + head * p.G + (live ? r - qt * p.G : 0);
+        limit[t] = w.len - (p.T - 1 - qt);
+#pragma unroll
+        for (int s = 0; s < QW; s++) {
+            const int col = g * (D / 4) + 8 * s;
+            raw[t][s] = u32x4{};
+            if (live && col < p.d) raw[t][s] = *(const u32x4*)(p.q + qrow * p.d + col);
+        }
     }
     const float gs_k = p.gs[0], gs_v = p.gs[1];
 
@@ -265,13 +272,14 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
     if (tok < t1) start(tok);
 
     // scaled to fp16
-    f16x8 q[QW];
-    float inv;
-    {
+    f16x8 q[NT][QW];
+    float to_x[NT];
+#pragma unroll
+    for (int t = 0; t < NT; t++) {
         uint32_t top = 0;
 #pragma unroll
         for (int s = 0; s < QW; s++) {
-            const uint32_t v[4] = {raw[s][0], raw[s][1], raw[s][2], raw[s][3]};
+            const uint32_t v[4] = {raw[t][s][0], raw[t][s][1], raw[t][s][2], raw[t][s][3]};
             const uint32_t a = absmax_bits_bf16x8(v);
             top = a > top ? a : top;
         }
@@ -282,17 +290,16 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
         int e = top ? top >> 7 : 127;  // the largest one's exponent goes to 14
         e = e < 15 ? 15 : e > 254 ? 254 : e;
         const float up = bits_f((uint32_t)(268 - e > 254 ? 254 : 268 - e) << 23);
-        inv = bits_f((uint32_t)(e - 14) << 23);
+        const float inv = bits_f((uint32_t)(e - 14) << 23);
+        to_x[t] = __builtin_fmaxf(inv * (p.scale2 / gs_k), 0x1p-126f);  // not 0: -inf times it is -inf
 #pragma unroll
         for (int s = 0; s < QW; s++)
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                q[s][2 * j] = (_Float16)(bf16_lo(raw[s][j]) * up);
-                q[s][2 * j + 1] = (_Float16)(bf16_hi(raw[s][j]) * up);
+                q[t][s][2 * j] = (_Float16)(bf16_lo(raw[t][s][j]) * up);
+                q[t][s][2 * j + 1] = (_Float16)(bf16_hi(raw[t][s][j]) * up);
             }
     }
-    const float to_x = __builtin_fmaxf(inv * (p.scale2 / gs_k), 0x1p-126f);  // not 0: -inf times it is -inf
-    const int limit = w.len - (p.T - 1 - qt);  // tokens this row sees
 
     // a lane's row of 16 values for the transposing reads
     constexpr int VN = D == 64 ? 4 : 8;
@@ -300,10 +307,15 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
     const uint32_t vat = (uint32_t)(uintptr_t)st + vrow * (D / 2);
     const uint32_t vsw = swizzle<D>(vrow) * 16;
 
-    float m = neg_inf(), l = 0.0f;
-    f32x4 o[D / 16];
+    float m[NT], l[NT];
+    f32x4 o[NT][D / 16];
 #pragma unroll
-    for (int i = 0; i < D / 16; i++) o[i] = f32x4{};
+    for (int t = 0; t < NT; t++) {
+        m[t] = neg_inf();
+        l[t] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < D / 16; i++) o[t][i] = f32x4{};
+    }
 
     for (; tok < t1; tok += step) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -354,10 +366,11 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
                 }
             }
         }
-        f32x4 x[4];
+        f32x4 x[NT][4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            f32x4 acc = {};
+#pragma unroll
+            for (int t = 0; t < NT; t++) x[t][i] = f32x4{};
             const uint8_t* const kr = mine + (4 * n + i) * (D / 2) + g * (D / 8);
             uint32_t kw[QW];
             if constexpr (D == 64) {
@@ -372,9 +385,11 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
                 }
             }
 #pragma unroll
-            for (int c = 0; c < QW; c++)
-                acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8(kw[c], ksc[i][c >> 2][(c >> 1) & 1]), q[c], acc, 0, 0, 0);
-            x[i] = acc;
+            for (int c = 0; c < QW; c++) {
+                const f16x8 kf = dequant8(kw[c], ksc[i][c >> 2][(c >> 1) & 1]);
+#pragma unroll
+                for (int t = 0; t < NT; t++) x[t][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[t][c], x[t][i], 0, 0, 0);
+            }
         }
         u32x2 vw[D / 16 / VN][VN];
         read_columns<D, S::OFF_V>(vat, vsw, vw[0]);
@@ -388,82 +403,92 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
             }
             start(tok + step);
         }
-        if (masked) {
+        f16x8 pf[NT][2];  // token 16 g + j in place j
 #pragma unroll
-            for (int i = 0; i < 4; i++)
+        for (int t = 0; t < NT; t++) {
+            if (masked) {
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    const int t = 16 * g + 4 * e + i;
-                    if (tok + t >= limit || tok + t >= t1 || ((none >> g) & 1)) x[i][e] = neg_inf();
-                }
+                for (int i = 0; i < 4; i++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int at = tok + 16 * g + 4 * e + i;
+                        if (at >= limit[t] || at >= t1 || ((none >> g) & 1)) x[t][i][e] = neg_inf();
+                    }
+            }
+            // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the row
+            // alone, so that its bits do not depend on the rows beside it)
+            float top = x[t][0][0];
+#pragma unroll
+            for (int i = 1; i < 16; i++) top = __builtin_fmaxf(top, x[t][i >> 2][i & 3]);
+            top *= to_x[t];
+            if (__any(top > m[t] + 8.0f)) {
+                top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+                const float to = top > m[t] + 8.0f ? top : m[t];
+                const float a = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m[t] - to);
+                m[t] = to;
+                l[t] *= a;
+#pragma unroll
+                for (int i = 0; i < D / 16; i++) o[t][i] *= a;
+            }
+            const float base = m[t] == neg_inf() ? 0.0f : m[t];
+            float sum = 0.0f;
+#pragma unroll
+            for (int j = 0; j < 16; j++) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][j & 3][j >> 2], to_x[t], -base));
+                sum += e;
+                pf[t][j >> 3][j & 7] = (_Float16)e;
+            }
+            l[t] += sum;
         }
-        // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the row
-        // alone, so that its bits do not depend on the rows beside it)
-        float top = x[0][0];
-#pragma unroll
-        for (int i = 1; i < 16; i++) top = __builtin_fmaxf(top, x[i >> 2][i & 3]);
-        top *= to_x;
-        if (__any(top > m + 8.0f)) {
-            top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-            const float to = top > m + 8.0f ? top : m;
-            const float a = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m - to);
-            m = to;
-            l *= a;
-#pragma unroll
-            for (int i = 0; i < D / 16; i++) o[i] *= a;
-        }
-        const float base = m == neg_inf() ? 0.0f : m;
-        f16x8 pf[2];  // token 16 g + j in place j
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 16; j++) {
-            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[j & 3][j >> 2], to_x, -base));
-            sum += e;
-            pf[j >> 3][j & 7] = (_Float16)e;
-        }
-        l += sum;
 
         // O^T += V^T P^T
 #pragma unroll
         for (int b = 0; b < D / 16; b++) {
             const u32x2 v = vw[b / VN][b % VN];
             const f16x8 s0 = *(const f16x8*)(vs16 + 128 * b + 32 * g), s1 = *(const f16x8*)(vs16 + 128 * b + 32 * g + 16);
-            o[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8_pairs(v[0], s0), pf[0], o[b], 0, 0, 0);
-            o[b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(dequant8_pairs(v[1], s1), pf[1], o[b], 0, 0, 0);
+            const f16x8 v0 = dequant8_pairs(v[0], s0), v1 = dequant8_pairs(v[1], s1);
+#pragma unroll
+            for (int t = 0; t < NT; t++) {
+                o[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[t][0], o[t][b], 0, 0, 0);
+                o[t][b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[t][1], o[t][b], 0, 0, 0);
+            }
         }
     }
-    l += __shfl_xor(l, 16);
-    l += __shfl_xor(l, 32);
 
     // the waves' parts, through LDS: [wave][n][D + 4], the last four: m, l
     constexpr int PITCH = D + 4;
     __syncthreads();
     float* const all = (float*)smem;
-    float* const my = all + (wave * kRows + n) * PITCH;
 #pragma unroll
-    for (int b = 0; b < D / 16; b++) *(f32x4*)(my + 16 * b + 4 * g) = o[b];
-    if (g == 0) { my[D] = m; my[D + 1] = l; }
+    for (int t = 0; t < NT; t++) {
+        l[t] += __shfl_xor(l[t], 16);
+        l[t] += __shfl_xor(l[t], 32);
+        float* const my = all + (wave * ROWS + t * kRows + n) * PITCH;
+#pragma unroll
+        for (int b = 0; b < D / 16; b++) *(f32x4*)(my + 16 * b + 4 * g) = o[t][b];
+        if (g == 0) { my[D] = m[t]; my[D + 1] = l[t]; }
+    }
     __syncthreads();
     const float out_scale = 1.0f / gs_v;
-    float* const slot = p.part + ((int64_t)(w.slot + w.part) * p.H * p.row_tiles + w.hr) * (kRows * (D + 2));
+    float* const slot = p.part + ((int64_t)(w.slot + w.part) * p.H * p.row_tiles + w.hr) * (ROWS * (D + 2));
     if (w.hr == 0 && w.part == 0 && threadIdx.x == 0) p.plan[w.seq] = make_int2(w.parts, w.slot);
     constexpr int CT = D / 4;  // threads of a row, four columns each
-    for (int i = threadIdx.x; i < kRows * CT; i += kThreads) {
+    for (int i = threadIdx.x; i < ROWS * CT; i += kThreads) {
         const int nn = i / CT, c = (i - nn * CT) * 4;
-        const int rr = rt * kRows + nn;
+        const int rr = rt * ROWS + nn;
         if (rr >= p.T * p.G) continue;
         float mm[kWaves], top = neg_inf();
 #pragma unroll
         for (int v = 0; v < kWaves; v++) {
-            mm[v] = all[(v * kRows + nn) * PITCH + D];
+            mm[v] = all[(v * ROWS + nn) * PITCH + D];
             top = __builtin_fmaxf(top, mm[v]);
         }
         f32x4 sum = {};
         float den = 0.0f;
 #pragma unroll
         for (int v = 0; v < kWaves; v++) {
-            const float* const src = all + (v * kRows + nn) * PITCH;
+            const float* const src = all + (v * ROWS + nn) * PITCH;
             const float a = top == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(mm[v] - top);
             den += a * src[D + 1];
             sum += a * *(const f32x4*)(src + c);
@@ -471,8 +496,8 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
         if (w.parts > 1) {
             *(f32x4*)(slot + nn * D + c) = sum;
             if (c == 0) {
-                slot[kRows * D + nn] = top;
-                slot[kRows * D + kRows + nn] = den;
+                slot[ROWS * D + nn] = top;
+                slot[ROWS * D + ROWS + nn] = den;
             }
         } else {
             const int tt = rr / p.G;
@@ -487,8 +512,9 @@ __global__ __launch_bounds__(kThreads, D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_at
 
 // Joins the parts of the sequences that have several: a workgroup a row of the output,
 // its threads side by side over the columns and then over the parts.
-template <int D>
+template <int D, int NT>
 __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
+    constexpr int ROWS = NT * kRows;
     constexpr int CT = D / 4, GROUPS = kThreads / CT;  // threads of a part's row, parts at a time
     __shared__ float weight[kAttnPartsNarrow + 64];
     __shared__ float red[2 * kWaves];
@@ -500,9 +526,9 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     if (n <= 1) return;
     const int tt = rem / p.Hq, qh = rem - tt * p.Hq;
     const int head = qh / p.G, r = tt * p.G + qh - head * p.G;
-    const int hrs = p.H * p.row_tiles, rt = r / kRows, nn = r - rt * kRows;
-    const int64_t stride = (int64_t)hrs * (kRows * (D + 2));
-    const float* const first = p.part + (int64_t)plan.y * stride + (int64_t)(head * p.row_tiles + rt) * (kRows * (D + 2));
+    const int hrs = p.H * p.row_tiles, rt = r / ROWS, nn = r - rt * ROWS;
+    const int64_t stride = (int64_t)hrs * (ROWS * (D + 2));
+    const float* const first = p.part + (int64_t)plan.y * stride + (int64_t)(head * p.row_tiles + rt) * (ROWS * (D + 2));
     // the first parts' rows, under way while the weights are worked out
     constexpr int AHEAD = 8;
     const int c = (t % CT) * 4, grp = t / CT;
@@ -512,7 +538,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     for (int i = 0; i < AHEAD; i++) x[i] = *(const f32x4*)(src + (grp + i * GROUPS < n ? i * GROUPS * stride : 0));
     float top = neg_inf();
     for (int s = t; s < n; s += kThreads) {
-        const float m = first[s * stride + kRows * D + nn];
+        const float m = first[s * stride + ROWS * D + nn];
         weight[s] = m;
         top = __builtin_fmaxf(top, m);
     }
@@ -526,7 +552,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     for (int s = t; s < n; s += kThreads) {
         const float a = top == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(weight[s] - top);
         weight[s] = a;
-        den += a * first[s * stride + kRows * D + kRows + nn];
+        den += a * first[s * stride + ROWS * D + ROWS + nn];
     }
 #pragma unroll
     for (int o = 32; o; o >>= 1) den += __shfl_xor(den, o);
@@ -552,15 +578,16 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     if (p.lse && t == 0) p.lse[orow] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
 }
 
-template <int D>
+template <int D, int NT>
 hipError_t launch(const DParams& p, int64_t grid, bool join, bool large, hipStream_t st) {
-    constexpr int need = kWaves * Stage<D>::WAVE > kWaves * kRows * (D + 4) * 4 ? kWaves * Stage<D>::WAVE : kWaves * kRows * (D + 4) * 4;
+    constexpr int merge = kWaves * NT * kRows * (D + 4) * 4;
+    constexpr int need = kWaves * Stage<D>::WAVE > merge ? kWaves * Stage<D>::WAVE : merge;
     const int lds = D > 64 && large && need < kAttnLdsLong ? kAttnLdsLong : need;
-    if (p.row_tiles == 1) k_attn_decode<D, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
-    else k_attn_decode<D, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    if (p.row_tiles == 1) k_attn_decode<D, NT, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    else k_attn_decode<D, NT, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !join) return e;
-    k_attn_join<D><<<dim3((unsigned)((int64_t)p.b * p.T * p.Hq)), kThreads, 0, st>>>(p);
+    k_attn_join<D, NT><<<dim3((unsigned)((int64_t)p.b * p.T * p.Hq)), kThreads, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -578,7 +605,12 @@ hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     p.b = (int)a.b; p.T = (int)a.t; p.H = (int)a.heads; p.Hq = (int)a.q_heads; p.G = p.Hq / p.H; p.d = (int)a.d;
     p.pages = (int)a.pages; p.table_pages = (int)a.table_pages;
     p.page_log2 = __builtin_ctzll((unsigned long long)a.page);
-    p.row_tiles = (p.T * p.G + kRows - 1) / kRows;
+    // More rows than one product takes: two share a read of the cache where that is much (by the
+    // table's size; heads of 256 have no registers for it).  4 x 8 rows over 32 sequences of
+    // 8192: 79 us, 114 apart; 3 x 7 rows over 7 to 2001: 12.8, 10.8 (not taken).
+    const bool two = p.T * p.G > kRows && a.d <= 128 && a.b * a.heads * a.table_pages * a.page >= kAttnShared;
+    const int rows = two ? 2 * kRows : kRows;
+    p.row_tiles = (p.T * p.G + rows - 1) / rows;
     p.cap = (int)(a.table_pages * a.page);
     // Long parts (by the table's size, the lengths being on the device) are better off with three
     // workgroups a CU and cut finer, so that the last ones end together; short ones with four,
@@ -588,15 +620,15 @@ hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     // 43 us with 1024 parts, 49 with 512, 47 with 2048.
     const int64_t hrs = (int64_t)p.H * p.row_tiles;
     const bool large = p.cap >= 2 * kAttnLong && p.b * hrs * p.cap >= kAttnLong * kAttnParts;
-    p.split = a.d <= 64 ? kAttnPartsNarrow : large ? kAttnPartsLong : kAttnParts;
+    p.split = two ? kAttnParts : a.d <= 64 ? kAttnPartsNarrow : large ? kAttnPartsLong : kAttnParts;  // (two: slots twice as large)
     // the most workgroups that lengths up to the table's can ask for
     int64_t units = (p.split + hrs - 1) / hrs + p.b;
     const int64_t each = (p.cap + kAttnMinPart - 1) / kAttnMinPart;
     if (each * p.b < units) units = each * p.b;
     const bool join = each > 1;
-    if (a.d <= 64) return launch<64>(p, units * hrs, join, large, st);
-    if (a.d <= 128) return launch<128>(p, units * hrs, join, large, st);
-    return launch<256>(p, units * hrs, join, large, st);
+    if (a.d <= 64) return two ? launch<64, 2>(p, units * hrs, join, large, st) : launch<64, 1>(p, units * hrs, join, large, st);
+    if (a.d <= 128) return two ? launch<128, 2>(p, units * hrs, join, large, st) : launch<128, 1>(p, units * hrs, join, large, st);
+    return launch<256, 1>(p, units * hrs, join, large, st);
 }
 
 }  // namespace nvfp4

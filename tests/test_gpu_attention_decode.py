@@ -92,6 +92,19 @@ def test_decode(att, lens, new, q_heads, heads, d, page):
     assert torch.equal(out, again)
 
 
+@pytest.mark.parametrize("lens,new,q_heads,heads,d,page", [((600, 33, 1, 0, 2000), 4, 64, 8, 128, 64), ((70, 1025), 3, 21, 3, 64, 32), ((40, 3), 17, 8, 4, 96, 64),
+                                                           ((513,), 5, 40, 8, 256, 64)])
+def test_rows_that_share_a_read(att, lens, new, q_heads, heads, d, page):
+    """Tables wide enough that several tiles of rows are taken together."""
+    say("decode shared", lens, new, q_heads, heads, d, page)
+    s = setup(att, lens, new, q_heads, heads, d, page, seed=new)
+    wide = torch.full((len(lens), (1 << 20) // page), -7, dtype=torch.int32, device="cuda")
+    wide[:, : s["block_table"].shape[1]] = s["block_table"]
+    s["block_table"] = wide
+    lse = torch.empty(s["q"].shape[:3], device="cuda")
+    check(s, att.nvfp4_attention_decode(**s, lse=lse), lse)
+
+
 def test_many_sequences(att):
     lens = [(i * 37) % 401 for i in range(300)] + [5000, 0, 1]
     say("decode 303 sequences")
