@@ -43,7 +43,8 @@ struct DParams {
     float* part;              // slots of kRows * (D + 2) floats
     int64_t page_codes, page_sf;  // bytes of a page
     float scale2;             // scale * log2(e)
-    int b, T, Hq, H, G, d, pages, table_pages, page_log2, row_tiles, cap, split;  // split: parts of all, about
+    int b, T, Hq, H, G, d, pages, table_pages, page_log2, row_tiles, cap;
+    int split, least;  // parts of all sequences, about; fewest blocks of a part
 };
 
 template <int D>
@@ -89,7 +90,7 @@ __device__ __forceinline__ bool find_work(const DParams& p, Work& w) {
         total += __builtin_amdgcn_readlane(wave_scan((v + kBlock - 1) / kBlock), 63);
     }
     int64_t chunk64 = (int64_t)((uint64_t)(total * hrs + p.split - 1) / (uint32_t)p.split);
-    chunk64 = chunk64 < kAttnMinPart / kBlock ? kAttnMinPart / kBlock : chunk64;
+    chunk64 = chunk64 < p.least ? p.least : chunk64;
     const uint32_t chunk = chunk64 > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)chunk64;
     int before = 0, slots = 0;
     for (int base = 0; base < p.b; base += 64) {
@@ -623,7 +624,11 @@ hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     p.split = two ? kAttnParts : a.d <= 64 ? kAttnPartsNarrow : large ? kAttnPartsLong : kAttnParts;  // (two: slots twice as large)
     // the most workgroups that lengths up to the table's can ask for
     int64_t units = (p.split + hrs - 1) / hrs + p.b;
-    const int64_t each = (p.cap + kAttnMinPart - 1) / kAttnMinPart;
+    // Sequences of up to kAttnWhole stay whole, which saves the second launch (16 of 1000: 12.6 us
+    // against 15.0; one alone: 11.9 against 10.7, and 3 us less of the host).
+    const int64_t least = p.cap <= kAttnWhole ? kAttnWhole : kAttnMinPart;
+    p.least = (int)(least / kBlock);
+    const int64_t each = (p.cap + least - 1) / least;
     if (each * p.b < units) units = each * p.b;
     const bool join = each > 1;
     if (a.d <= 64) return two ? launch<64, 2>(p, units * hrs, join, large, st) : launch<64, 1>(p, units * hrs, join, large, st);
