@@ -94,7 +94,7 @@ class Attention:
         request = torch.arange(len(x), device="cuda")
         attention.nvfp4_kv_append(k, v, cache.slots(request, position), cache.kv_gs, cache.kv, cache.kv_sf)
         cache.lengths += 1
-        out = attention.nvfp4_attention_decode(q[:, None].contiguous(), cache.kv, cache.kv_sf, cache.kv_gs, cache.block_table,
+        out = attention.nvfp4_attention_decode(q[:, None], cache.kv, cache.kv_sf, cache.kv_gs, cache.block_table,
                                                cache.lengths, workspace=self.workspace)
         return x + narrow(out.view(len(x), -1), self.wo, self.wo_sf, self.gs_o)
 

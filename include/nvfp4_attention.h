@@ -103,7 +103,7 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
  * sums are fp32.  The tokens of long sequences are split over workgroups, whose parts a
  * second launch joins; how, depends on the lengths, which are read on the device (a
  * captured graph follows them).  Results are the same on every call.
- *   q: [b, t, q_heads, d] bf16; block_table: [b, table_pages] int32 (entries past a
+ *   q: [b, t, q_heads, d] bf16 with q_stride from token to token; block_table: [b, table_pages] int32 (entries past a
  *   sequence's last page are not read); lengths: [b] int32; out: [b, t, q_heads, d] bf16;
  *   lse: NULL or [b, t, q_heads] fp32, log(sum exp(scale * q . K_p)).
  *   workspace: workspace_bytes >= NVFP4_ATTENTION_WS_BYTES(b, d), 16-byte aligned; contents
@@ -112,7 +112,7 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
  * NVFP4_ATTENTION_MAX_TOKENS, b at most NVFP4_ATTENTION_MAX_BATCH, table_pages * page at
  * most 2^30.
  */
-int nvfp4_attention_decode(const void* q, int64_t b, int64_t t, int64_t q_heads, const uint8_t* kv,
+int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t, int64_t q_heads, const uint8_t* kv,
                            const uint8_t* kv_sf, const float* kv_gs, int64_t heads, int64_t d, int64_t pages,
                            int64_t page, const int32_t* block_table, int64_t table_pages, const int32_t* lengths,
                            float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,

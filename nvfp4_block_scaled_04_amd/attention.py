@@ -28,7 +28,7 @@ def _load():
         "rope_axes": [vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, i32, i32, vp],
         "nvfp4_kv_append": [vp, i64, vp, i64, i64, i64, i64, vp, vp, vp, vp, i64, i64, vp],
         "nvfp4_kv_read": [vp, vp, vp, i64, i64, vp, i64, i64, i64, vp, i64, vp, i64, vp],
-        "nvfp4_attention_decode": [vp, i64, i64, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, f32, vp, vp, vp, i64,
+        "nvfp4_attention_decode": [vp, i64, i64, i64, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, f32, vp, vp, vp, i64,
                                    vp],
         "attention_prefill": [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, i64, f32, i32, vp, i64, vp, vp],
     }
@@ -82,14 +82,17 @@ def _at(t, name, dtype, numel, i):
 
 
 def _bytes(t, name, numel, i):
-    if t.get_device() == i and t.element_size() == 1 and t.is_contiguous() and t.numel() >= numel:
-        return t.data_ptr()
+    try:
+        if t.get_device() == i and t.element_size() == 1 and t.is_contiguous() and t.numel() >= numel:
+            return t.data_ptr()
+    except AttributeError:
+        pass
     return _dev(t, name, BYTES, numel, torch.device("cuda", i)).data_ptr()
 
 
 def _shaped(out, name, shape):
-    if out.shape != shape:
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(out.shape)}")
+    if getattr(out, "shape", None) != shape:
+        raise ValueError(f"{name} must be {tuple(shape)}, got {getattr(out, 'shape', type(out))}")
 
 
 _device, _stream_of = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
@@ -174,15 +177,23 @@ def nvfp4_kv_read(slots, kv_gs, kv, kv_sf, k=None, v=None):
 
 def nvfp4_attention_decode(q, kv, kv_sf, kv_gs, block_table, lengths, scale=None, out=None, lse=None, workspace=None):
     """Attention of t new tokens a sequence over the cache, which holds them already.  q: [b, t,
-    q_heads, d] bf16; block_table: [b, pages of a sequence] int32; lengths: [b] int32, the new
+    q_heads, d] bf16 (any stride from token to token); block_table: [b, pages of a sequence] int32; lengths: [b] int32, the new
     tokens included; scale: d ** -0.5 when None; lse: None or [b, t, q_heads] fp32, written.
     Token j sees the positions below lengths - (t - 1 - j).  workspace: attention_ws_bytes(b, d)
     bytes.  Returns out [b, t, q_heads, d] bf16."""
     i, pages, heads, page, d, kv_at, sf_at, gs_at = _cache(kv, kv_sf, kv_gs)
-    q_at = _at(q, "q", BF16, 0, i)
-    if q.dim() != 4 or q.shape[3] != d or heads < 1 or q.shape[2] % heads:
-        raise ValueError(f"q must be [b, t, a multiple of {heads}, {d}], got {tuple(q.shape)}")
+    if _gpu(q, "q") != i or q.dtype is not BF16[0] or q.dim() != 4 or q.shape[3] != d or heads < 1 or q.shape[2] % heads:
+        raise ValueError(f"q must be bf16 [b, t, a multiple of {heads}, {d}] on GPU {i}, got {q.dtype} {tuple(q.shape)} on {q.device}")
     b, t, q_heads, _ = q.shape
+    if q.is_contiguous():
+        stride = q_heads * d
+    else:
+        s0, s1, s2, s3 = q.stride()
+        stride = s1 if t > 1 else s0
+        if s3 != 1 or (q_heads > 1 and s2 != d) or (t > 1 and b > 1 and s0 != t * s1):
+            raise ValueError(f"q must have its heads one after the other and its tokens in even steps, got strides {q.stride()}")
+        if b * t == 1:
+            stride = q_heads * d
     table_at = _at(block_table, "block_table", I32, 0, i)
     if block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError(f"block_table must be [{b}, pages], got {tuple(block_table.shape)}")
@@ -193,7 +204,7 @@ def nvfp4_attention_decode(q, kv, kv_sf, kv_gs, block_table, lengths, scale=None
     need = attention_ws_bytes(b, d)
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    _call(_lib.nvfp4_attention_decode, "nvfp4_attention_decode", i, q_at, b, t, q_heads, kv_at, sf_at, gs_at, heads, d,
+    _call(_lib.nvfp4_attention_decode, "nvfp4_attention_decode", i, q.data_ptr(), stride, b, t, q_heads, kv_at, sf_at, gs_at, heads, d,
           pages, page, table_at, block_table.shape[1], _at(lengths, "lengths", I32, b, i), d ** -0.5 if scale is None else scale,
           _at(out, "out", BF16, 0, i), None if lse is None else _at(lse, "lse", F32, b * t * q_heads, i),
           _bytes(workspace, "workspace", need, i), workspace.numel())

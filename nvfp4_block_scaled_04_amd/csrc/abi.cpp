@@ -592,7 +592,7 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
 
 static bool scale_ok(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
 
-int nvfp4_attention_decode(const void* q, int64_t b, int64_t t, int64_t q_heads, const uint8_t* kv,
+int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t, int64_t q_heads, const uint8_t* kv,
                            const uint8_t* kv_sf, const float* kv_gs, int64_t heads, int64_t d, int64_t pages,
                            int64_t page, const int32_t* block_table, int64_t table_pages, const int32_t* lengths,
                            float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
@@ -602,6 +602,7 @@ int nvfp4_attention_decode(const void* q, int64_t b, int64_t t, int64_t q_heads,
     if (st != NVFP4_OK) return st;
     if (!dim_ok(b) || !dim_ok(t) || !dim_ok(q_heads) || !dim_ok(table_pages) || q_heads % heads != 0)
         return NVFP4_BAD_SHAPE;
+    if (q_stride < q_heads * d || q_stride % 8 != 0 || q_stride > NVFP4_ATTENTION_MAX_STRIDE) return NVFP4_BAD_SHAPE;
     if (!scale_ok(scale) || b > NVFP4_ATTENTION_MAX_BATCH || t > NVFP4_ATTENTION_MAX_TOKENS ||
         q_heads * d > NVFP4_ATTENTION_MAX_STRIDE || table_pages > (((int64_t)1 << 30) / page))
         return NVFP4_UNSUPPORTED;
@@ -615,7 +616,7 @@ int nvfp4_attention_decode(const void* q, int64_t b, int64_t t, int64_t q_heads,
     a.q = (const uint16_t*)q; a.kv = kv; a.kv_sf = kv_sf; a.kv_gs = kv_gs; a.block_table = block_table;
     a.lengths = lengths; a.out = (uint16_t*)out; a.lse = lse; a.ws = workspace;
     a.b = b; a.t = t; a.q_heads = q_heads; a.heads = heads; a.d = d; a.pages = pages; a.page = page;
-    a.table_pages = table_pages; a.scale = scale;
+    a.table_pages = table_pages; a.q_stride = q_stride; a.scale = scale;
     return launch_status(nvfp4::launch_attention_decode(a, (hipStream_t)stream));
 }
 

@@ -32,7 +32,7 @@ constexpr int kAttnLdsLong = 54272;  // LDS of a workgroup, three of which fit a
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
 struct DParams {
-    const uint16_t* q;        // [b, T, Hq, d]
+    const uint16_t* q;        // [b, T, Hq, d], q_stride from token to token
     const uint8_t *kv, *sf;
     const float* gs;
     const int32_t* table;     // [b, table_pages]
@@ -42,6 +42,7 @@ struct DParams {
     int2* plan;               // [b] parts and first slot of a sequence
     float* part;              // slots of kRows * (D + 2) floats
     int64_t page_codes, page_sf;  // bytes of a page
+    int64_t q_stride;
     float scale2;             // scale * log2(e)
     int b, T, Hq, H, G, d, pages, table_pages, page_log2, row_tiles, cap;
     int split, least;  // parts of all sequences, about; fewest blocks of a part
@@ -243,13 +244,13 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
         const int r = rt * ROWS + t * kRows + n;
         const bool live = r < p.T * p.G;
         const int qt = live ? r / p.G : 0;
-        const int64_t qrow = ((int64_t)w.seq * p.T + qt) * p.Hq + head * p.G + (live ? r - qt * p.G : 0);
+        const uint16_t* const src = p.q + ((int64_t)w.seq * p.T + qt) * p.q_stride + (head * p.G + (live ? r - qt * p.G : 0)) * p.d;
         limit[t] = w.len - (p.T - 1 - qt);
 #pragma unroll
         for (int s = 0; s < QW; s++) {
             const int col = g * (D / 4) + 8 * s;
             raw[t][s] = u32x4{};
-            if (live && col < p.d) raw[t][s] = *(const u32x4*)(p.q + qrow * p.d + col);
+            if (live && col < p.d) raw[t][s] = *(const u32x4*)(src + col);
         }
     }
     const float gs_k = p.gs[0], gs_v = p.gs[1];
@@ -597,7 +598,7 @@ hipError_t launch(const DParams& p, int64_t grid, bool join, bool large, hipStre
 hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     DParams p{};
     p.q = a.q; p.kv = a.kv; p.sf = a.kv_sf; p.gs = a.kv_gs; p.table = a.block_table; p.lengths = a.lengths;
-    p.out = a.out; p.lse = a.lse;
+    p.out = a.out; p.lse = a.lse; p.q_stride = a.q_stride;
     p.plan = (int2*)a.ws;
     p.part = (float*)((char*)a.ws + (a.b * 8 + 255) / 256 * 256);
     p.page_codes = a.page * a.heads * a.d;

@@ -185,7 +185,7 @@ constexpr int64_t kAttnMinPart = 256;     // fewest tokens of a part
 constexpr int64_t kAttnWhole = 1024;      // tokens of a sequence (by the table) that is not split
 constexpr int64_t kAttnShared = (int64_t)1 << 20;  // tokens times KV heads from which rows share a read
 struct AttnDecodeArgs {
-    const uint16_t* q;         // [b, t, q_heads, d]
+    const uint16_t* q;         // [b, t, q_heads, d], q_stride elements from token to token
     const uint8_t *kv, *kv_sf;
     const float* kv_gs;        // [2]
     const int32_t* block_table;  // [b, table_pages]
@@ -193,7 +193,7 @@ struct AttnDecodeArgs {
     uint16_t* out;
     float* lse;                // [b, t, q_heads] or null
     void* ws;                  // NVFP4_ATTENTION_WS_BYTES
-    int64_t b, t, q_heads, heads, d, pages, page, table_pages;
+    int64_t b, t, q_heads, heads, d, pages, page, table_pages, q_stride;
     float scale;
 };
 hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st);

@@ -71,15 +71,15 @@ def test_rows_validation(att, call, base, change, status):
     assert getattr(att._lib, call)(*{**base, **change}.values()) == status
 
 
-DEC = dict(q=P, b=2, t=1, hq=16, kv=P, sf=P, gs=P, heads=4, d=128, pages=10, page=64, table=P, per=5, lens=P, scale=0.1, out=P, lse=None,
+DEC = dict(q=P, qs=2048, b=2, t=1, hq=16, kv=P, sf=P, gs=P, heads=4, d=128, pages=10, page=64, table=P, per=5, lens=P, scale=0.1, out=P, lse=None,
            ws=P, wsb=1 << 30, stream=None)
 
 
 @pytest.mark.parametrize("change,status", [
     *[({n: None}, NULLP) for n in ("q", "kv", "sf", "gs", "table", "lens", "out", "ws")], *CACHE, ({"b": 0}, SHAPE), ({"t": 0}, SHAPE), ({"hq": 18}, SHAPE),
-    ({"hq": 0}, SHAPE), ({"per": 0}, SHAPE), ({"t": 65}, UNSUP), ({"b": 65537}, UNSUP), ({"scale": 0.0}, UNSUP), ({"scale": -1.0}, UNSUP),
-    ({"scale": float("nan")}, UNSUP), ({"scale": float("inf")}, UNSUP), ({"per": (1 << 24) + 1}, UNSUP), ({"hq": 1 << 16}, UNSUP),
-    ({"b": 65536, "t": 64, "hq": 16384, "heads": 8192}, UNSUP),
+    ({"hq": 0}, SHAPE), ({"qs": 2040}, SHAPE), ({"qs": 2052}, SHAPE), ({"qs": (1 << 22) + 8}, SHAPE), ({"per": 0}, SHAPE), ({"t": 65}, UNSUP), ({"b": 65537}, UNSUP), ({"scale": 0.0}, UNSUP), ({"scale": -1.0}, UNSUP),
+    ({"scale": float("nan")}, UNSUP), ({"scale": float("inf")}, UNSUP), ({"per": (1 << 24) + 1}, UNSUP), ({"hq": 1 << 16, "qs": 1 << 22}, SHAPE),
+    ({"b": 65536, "t": 64, "hq": 16384, "heads": 8192, "qs": 1 << 21}, UNSUP),
     ({"wsb": 256 + 2048 * 64 * 130 - 1}, SHAPE), ({"q": P + 8}, MISAL), ({"out": P + 4}, MISAL), ({"ws": P + 8}, MISAL), ({"table": P + 1}, MISAL),
     ({"lens": P + 2}, MISAL), ({"lse": P + 2}, MISAL),
 ])

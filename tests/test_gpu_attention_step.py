@@ -89,7 +89,7 @@ def test_prompts_then_steps_then_a_prefix(att, lens, q_heads, heads, d, page):
         att.nvfp4_kv_append(k, v, slots, s.gs, s.kv, s.sf)
         held += 1
         s.lens = held.tolist()
-        out = att.nvfp4_attention_decode(q[:, None].contiguous(), s.kv, s.sf, s.gs, s.table, held, workspace=ws)
+        out = att.nvfp4_attention_decode(q[:, None], s.kv, s.sf, s.gs, s.table, held, workspace=ws)
         for i, n in enumerate(s.lens):
             seen = torch.ones(1, n, dtype=torch.bool, device="cuda")
             s.check(q[i:i + 1], s.cached(i, 0), s.cached(i, 1), out[i], seen, 2.0 ** -11, 2.0 ** -25)
