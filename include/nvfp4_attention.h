@@ -68,7 +68,8 @@ int rope_axes(const void* x, int64_t x_stride, void* out, int64_t out_stride, in
  * nvfp4_quantize in STATIC mode with kv_gs, goes to slots[i].  A slot outside
  * [0, pages * page) (-1 by custom: a row of padding) is passed over.  Slots of one call
  * are distinct; other bytes of the cache keep their values.
- *   k, v: [t, heads, d] bf16 with k_stride, v_stride; slots: [t] int32.
+ *   k, v: [t, heads, d] bf16 with k_stride, v_stride, at most 2^35 elements each;
+ *   slots: [t] int32.
  */
 int nvfp4_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t t, int64_t heads,
                     int64_t d, const int32_t* slots, const float* kv_gs, uint8_t* kv, uint8_t* kv_sf, int64_t pages,
@@ -78,7 +79,7 @@ int nvfp4_kv_append(const void* k, int64_t k_stride, const void* v, int64_t v_st
  * The rows of slots[i] as bf16: bf16((e2m1 * ue4m3) / kv_gs), the quotient rounded to fp32
  * first.  For a cached prefix that a prompt's attention reads.  Rows of slots outside
  * [0, pages * page) are left as they were.
- *   k, v: [t, heads, d] bf16 with k_stride, v_stride, written.
+ *   k, v: [t, heads, d] bf16 with k_stride, v_stride, at most 2^35 elements each, written.
  */
 int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, int64_t pages, int64_t page,
                   const int32_t* slots, int64_t t, int64_t heads, int64_t d, void* k, int64_t k_stride, void* v,

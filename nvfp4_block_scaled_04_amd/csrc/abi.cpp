@@ -565,7 +565,7 @@ static int kv_rows(bool read, const void* k, int64_t k_stride, const void* v, in
     const int st = cache_check(heads, d, pages, page);
     if (st != NVFP4_OK) return st;
     if (!rows_ok(t, heads, d, k_stride) || !rows_ok(t, heads, d, v_stride)) return NVFP4_BAD_SHAPE;
-    if (t * heads > ((int64_t)1 << 39) / d) return NVFP4_UNSUPPORTED;  // the grid: a thread per 16 elements of both
+    if (t * heads > ((int64_t)1 << 35) / d) return NVFP4_UNSUPPORTED;  // the grid: a thread per 16 elements of both
     if (!aligned16(k) || !aligned16(v) || !aligned16(kv) || !aligned16(kv_sf) || ((uintptr_t)slots & 3u) ||
         ((uintptr_t)kv_gs & 3u))
         return NVFP4_MISALIGNED;

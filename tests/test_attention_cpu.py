@@ -65,7 +65,7 @@ READ = dict(kv=P, sf=P, gs=P, pages=10, page=64, slots=P, t=4, heads=4, d=128, k
 @pytest.mark.parametrize("call,base", [("nvfp4_kv_append", APPEND), ("nvfp4_kv_read", READ)])
 @pytest.mark.parametrize("change,status", [
     *[({n: None}, NULLP) for n in ("k", "v", "slots", "gs", "kv", "sf")], *CACHE, ({"t": 0}, SHAPE), ({"ks": 500}, SHAPE), ({"vs": 516}, SHAPE),
-    ({"t": 1 << 30, "heads": 512, "ks": 1 << 16, "vs": 1 << 16}, UNSUP), ({"k": P + 8}, MISAL), ({"v": P + 2}, MISAL), ({"slots": P + 2}, MISAL),
+    ({"t": 1 << 30, "heads": 512, "ks": 1 << 16, "vs": 1 << 16}, UNSUP), ({"t": (1 << 26) + 1}, UNSUP), ({"k": P + 8}, MISAL), ({"v": P + 2}, MISAL), ({"slots": P + 2}, MISAL),
 ])
 def test_rows_validation(att, call, base, change, status):
     assert getattr(att._lib, call)(*{**base, **change}.values()) == status
