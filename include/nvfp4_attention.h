@@ -57,7 +57,7 @@ extern "C" {
  *   positions: [axes, t] int32; inv_freq: [pairs] fp32 (radians a position).
  *   sections: `axes` numbers of pairs, in HOST memory, read before the call returns.
  * Requires 1 <= axes <= 4, sections >= 0, their sum a positive multiple of 8 and at most
- * d / 2, d a multiple of 16.
+ * d / 2, d a multiple of 16, t * heads * d at most 2^36.
  */
 int rope_axes(const void* x, int64_t x_stride, void* out, int64_t out_stride, int64_t t, int64_t heads, int64_t d,
               const int32_t* positions, const float* inv_freq, const int32_t* sections, int axes, int interleaved,
@@ -100,18 +100,19 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
  * A token that sees nothing gets zeros (and lse = -inf).  Pages outside [0, pages) are
  * passed over as if their positions were not seen.  The keys and values are
  * exact; q enters the products as fp16 scaled by a power of two per head (exact, but off by up to
- * 2^-39 of the head's largest where it is below 2^-28 of it), the probabilities as fp16;
- * sums are fp32.  The tokens of long sequences are split over workgroups, whose parts a
+ * 2^-39 of the head's largest where it is below 2^-28 of it), the probabilities as fp16 (off by
+ * 2^-11 of themselves, or by 2^-25 of the largest); sums are fp32.  The tokens of long sequences are split over workgroups, whose parts a
  * second launch joins; how, depends on the lengths, which are read on the device (a
  * captured graph follows them).  Results are the same on every call.
- *   q: [b, t, q_heads, d] bf16 with q_stride from token to token; block_table: [b, table_pages] int32 (entries past a
- *   sequence's last page are not read); lengths: [b] int32; out: [b, t, q_heads, d] bf16;
- *   lse: NULL or [b, t, q_heads] fp32, log(sum exp(scale * q . K_p)).
+ *   q: [b, t, q_heads, d] bf16 with q_stride from token to token; block_table:
+ *   [b, table_pages] int32 (entries past a sequence's last page are not read); lengths: [b]
+ *   int32; out: [b, t, q_heads, d] bf16; lse: NULL or [b, t, q_heads] fp32,
+ *   log(sum exp(scale * q . K_p)).
  *   workspace: workspace_bytes >= NVFP4_ATTENTION_WS_BYTES(b, d), 16-byte aligned; contents
  *   ignored on entry, undefined on exit; calls that share one must not overlap.
- * Requires q_heads a multiple of heads, scale > 0 and finite, t at most
- * NVFP4_ATTENTION_MAX_TOKENS, b at most NVFP4_ATTENTION_MAX_BATCH, table_pages * page at
- * most 2^30.
+ * Requires q_heads a multiple of heads, 0 < scale <= 2e38, t at most
+ * NVFP4_ATTENTION_MAX_TOKENS, b at most NVFP4_ATTENTION_MAX_BATCH, b * t * q_heads at most
+ * 2^23, table_pages * page at most 2^30.
  */
 int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t, int64_t q_heads, const uint8_t* kv,
                            const uint8_t* kv_sf, const float* kv_gs, int64_t heads, int64_t d, int64_t pages,
@@ -131,8 +132,9 @@ int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t
  *   q: [tq, q_heads, d], k, v: [tk, heads, d], out: [tq, q_heads, d], bf16, each with its
  *   stride; cu_q, cu_k: [b + 1] int32 on the device, ascending (values outside the tensors
  *   are clamped); lse: NULL or [tq, q_heads] fp32.
- * Requires q_heads a multiple of heads, d a multiple of 16 up to NVFP4_KV_MAX_DIM, scale >
- * 0 and finite.  Results are the same on every call.
+ * Requires q_heads a multiple of heads, d a multiple of 16 up to NVFP4_KV_MAX_DIM, 0 < scale
+ * <= 2e38, b at most NVFP4_ATTENTION_MAX_BATCH, (tq / 128 + b) * q_heads below 2^23.  Results
+ * are the same on every call.
  */
 int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t d,

@@ -534,6 +534,7 @@ int rope_axes(const void* x, int64_t x_stride, void* out, int64_t out_stride, in
     if (!rows_ok(t, heads, d, x_stride) || !rows_ok(t, heads, d, out_stride) || d % 16 != 0) return NVFP4_BAD_SHAPE;
     if (axes < 1) return NVFP4_BAD_SHAPE;
     if (axes > NVFP4_ROPE_MAX_AXES || d > NVFP4_ROPE_MAX_DIM) return NVFP4_UNSUPPORTED;
+    if (t * heads > ((int64_t)1 << 36) / d) return NVFP4_UNSUPPORTED;  // the grid: at most a thread per 32 elements
     nvfp4::RopeArgs a{};
     int64_t pairs = 0;
     for (int i = 0; i < axes; i++) {
@@ -590,7 +591,8 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
                    page, stream);
 }
 
-static bool scale_ok(float scale) { return scale > 0.0f && scale <= 3.0e38f; }
+// (times log2(e) it is finite)
+static bool scale_ok(float scale) { return scale > 0.0f && scale <= 2.0e38f; }
 
 int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t, int64_t q_heads, const uint8_t* kv,
                            const uint8_t* kv_sf, const float* kv_gs, int64_t heads, int64_t d, int64_t pages,
@@ -606,8 +608,7 @@ int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t
     if (!scale_ok(scale) || b > NVFP4_ATTENTION_MAX_BATCH || t > NVFP4_ATTENTION_MAX_TOKENS ||
         q_heads * d > NVFP4_ATTENTION_MAX_STRIDE || table_pages > (((int64_t)1 << 30) / page))
         return NVFP4_UNSUPPORTED;
-    const int64_t tiles = (t * (q_heads / heads) + 15) / 16;
-    if (b * heads * tiles > (int64_t)1 << 30 || b * t * q_heads > (int64_t)1 << 30) return NVFP4_UNSUPPORTED;  // the grids
+    if (b * t * q_heads > (int64_t)1 << 23) return NVFP4_UNSUPPORTED;  // the grids: below 2^32 threads
     if (workspace_bytes < NVFP4_ATTENTION_WS_BYTES(b, d)) return NVFP4_BAD_SHAPE;
     if (!aligned16(q) || !aligned16(kv) || !aligned16(kv_sf) || !aligned16(out) || !aligned16(workspace) ||
         ((uintptr_t)kv_gs & 3u) || ((uintptr_t)block_table & 3u) || ((uintptr_t)lengths & 3u) || ((uintptr_t)lse & 3u))
@@ -629,7 +630,7 @@ int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_
         !rows_ok(tk, heads, d, v_stride) || !rows_ok(tq, q_heads, d, out_stride) || !dim_ok(b) || q_heads % heads != 0)
         return NVFP4_BAD_SHAPE;
     if (!scale_ok(scale) || d > NVFP4_KV_MAX_DIM || b > NVFP4_ATTENTION_MAX_BATCH ||
-        (tq / 32 + b) * q_heads > (int64_t)1 << 30)
+        (tq / 128 + b) * q_heads >= (int64_t)1 << 23)  // the grid: below 2^32 threads
         return NVFP4_UNSUPPORTED;
     if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)cu_q & 3u) ||
         ((uintptr_t)cu_k & 3u) || ((uintptr_t)lse & 3u))

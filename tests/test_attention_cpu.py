@@ -47,7 +47,7 @@ ROPE = dict(x=P, xs=512, out=P, outs=512, t=4, heads=4, d=128, pos=P, freq=P, se
     ({"xs": 516}, SHAPE), ({"xs": (1 << 22) + 8}, SHAPE), ({"axes": 0}, SHAPE), ({"axes": 5, "sections": sec(8, 8, 8, 8, 8)}, UNSUP),
     ({"heads": 1, "d": 1040, "xs": 1040, "outs": 1040}, UNSUP), ({"sections": sec(24, 20, 28)}, SHAPE), ({"sections": sec(24, 20, 19)}, SHAPE),
     ({"sections": sec(24, -8, 8)}, SHAPE), ({"sections": sec(0, 0, 0)}, SHAPE), ({"x": P + 8}, MISAL), ({"out": P + 2}, MISAL),
-    ({"pos": P + 2}, MISAL), ({"freq": P + 1}, MISAL),
+    ({"pos": P + 2}, MISAL), ({"freq": P + 1}, MISAL), ({"t": (1 << 27) + 1}, UNSUP),
 ])
 def test_rope_validation(att, change, status):
     assert att._lib.rope_axes(*{**ROPE, **change}.values()) == status
@@ -79,7 +79,7 @@ DEC = dict(q=P, qs=2048, b=2, t=1, hq=16, kv=P, sf=P, gs=P, heads=4, d=128, page
     *[({n: None}, NULLP) for n in ("q", "kv", "sf", "gs", "table", "lens", "out", "ws")], *CACHE, ({"b": 0}, SHAPE), ({"t": 0}, SHAPE), ({"hq": 18}, SHAPE),
     ({"hq": 0}, SHAPE), ({"qs": 2040}, SHAPE), ({"qs": 2052}, SHAPE), ({"qs": (1 << 22) + 8}, SHAPE), ({"per": 0}, SHAPE), ({"t": 65}, UNSUP), ({"b": 65537}, UNSUP), ({"scale": 0.0}, UNSUP), ({"scale": -1.0}, UNSUP),
     ({"scale": float("nan")}, UNSUP), ({"scale": float("inf")}, UNSUP), ({"per": (1 << 24) + 1}, UNSUP), ({"hq": 1 << 16, "qs": 1 << 22}, SHAPE),
-    ({"b": 65536, "t": 64, "hq": 16384, "heads": 8192, "qs": 1 << 21}, UNSUP),
+    ({"scale": 2.1e38}, UNSUP), ({"b": 65536, "t": 1, "hq": 132, "qs": 132 * 128}, UNSUP), ({"b": 65536, "t": 64, "hq": 16384, "heads": 8192, "qs": 1 << 21}, UNSUP),
     ({"wsb": 256 + 2048 * 64 * 130 - 1}, SHAPE), ({"q": P + 8}, MISAL), ({"out": P + 4}, MISAL), ({"ws": P + 8}, MISAL), ({"table": P + 1}, MISAL),
     ({"lens": P + 2}, MISAL), ({"lse": P + 2}, MISAL),
 ])
@@ -93,8 +93,8 @@ PRE = dict(q=P, qs=2048, k=P, ks=512, v=P, vs=512, tq=9, tk=9, hq=16, heads=4, d
 @pytest.mark.parametrize("change,status", [
     *[({n: None}, NULLP) for n in ("q", "k", "v", "cq", "ck", "out")], ({"tq": 0}, SHAPE), ({"tk": 0}, SHAPE), ({"hq": 18}, SHAPE), ({"heads": 0}, SHAPE),
     ({"d": 0}, SHAPE), ({"d": 120}, SHAPE), ({"b": 0}, SHAPE), ({"qs": 2040}, SHAPE), ({"ks": 508}, SHAPE), ({"vs": 516}, SHAPE), ({"outs": 0}, SHAPE),
-    ({"d": 272, "qs": 1 << 14, "ks": 1 << 14, "vs": 1 << 14, "outs": 1 << 14}, UNSUP), ({"scale": 0.0}, UNSUP), ({"scale": float("nan")}, UNSUP), ({"b": 65537}, UNSUP),
-    ({"tq": 1 << 30, "hq": 64, "qs": 8192, "outs": 8192}, UNSUP), ({"q": P + 2}, MISAL), ({"k": P + 8}, MISAL), ({"v": P + 4}, MISAL), ({"out": P + 8}, MISAL), ({"cq": P + 2}, MISAL),
+    ({"d": 272, "qs": 1 << 14, "ks": 1 << 14, "vs": 1 << 14, "outs": 1 << 14}, UNSUP), ({"scale": 0.0}, UNSUP), ({"scale": float("nan")}, UNSUP), ({"b": 65537}, UNSUP), ({"scale": 2.1e38}, UNSUP),
+    ({"b": 65536, "hq": 128, "qs": 1 << 14, "outs": 1 << 14}, UNSUP), ({"tq": 1 << 30, "hq": 64, "qs": 8192, "outs": 8192}, UNSUP), ({"q": P + 2}, MISAL), ({"k": P + 8}, MISAL), ({"v": P + 4}, MISAL), ({"out": P + 8}, MISAL), ({"cq": P + 2}, MISAL),
     ({"ck": P + 1}, MISAL), ({"lse": P + 2}, MISAL),
 ])
 def test_prefill_validation(att, change, status):

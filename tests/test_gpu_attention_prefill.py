@@ -143,3 +143,19 @@ def test_offsets_outside_the_tensors(att):
     want = att.attention_prefill(q, k, v, cq, ck)
     cq[2], ck[2], cq[0] = 1 << 30, 1000, -5
     assert torch.equal(att.attention_prefill(q, k, v, cq, ck), want)
+
+
+def test_rows_past_4_gib(att):
+    """q, k, v and out as parts of rows whose offsets pass 32 bits: 5 GB."""
+    say("prefill large strides")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    wide = torch.empty(40000, 512, 128, dtype=torch.bfloat16, device="cuda")
+    lens, first = (130, 1, 200), 40000 - 331
+    wide[first:] = torch.randn(331, 512, 128, device="cuda", generator=g).bfloat16()
+    q, k, v, out = wide[:, 500:504], wide[:, 7:9], wide[:, 100:102], wide[:, 300:304]
+    cu = starts(lens, first=first)
+    kept = wide[first:].clone()
+    att.attention_prefill(q, k, v, cu, out=out)
+    check(q, k, v, cu, cu, True, out)
+    kept[:, 300:304] = out[first:]
+    assert torch.equal(wide[first:], kept)

@@ -43,6 +43,7 @@ def rope_ok(y, x, ref, pos, freq, sections, inter):
 @pytest.mark.parametrize("t,heads,d,sections", [
     (1, 1, 16, (8,)), (1, 40, 128, (64,)), (16, 40, 128, (16, 24, 24)), (77, 3, 64, (8, 8)), (5, 7, 80, (10, 15, 15)),
     (1000, 2, 256, (44, 42, 42)), (333, 24, 128, (22, 21, 21)), (9, 5, 96, (3, 0, 5)), (4099, 1, 64, (5, 9, 10, 8)), (3, 4, 1024, (512,)),
+    (8200, 64, 128, (16, 24, 24)), (300000, 4, 64, (7, 9)),   # larger than the caches
 ])
 def test_rope(att, t, heads, d, sections, inter):
     say("rope", t, heads, d, sections, inter)
