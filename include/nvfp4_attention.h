@@ -22,7 +22,7 @@
  *          e2m1 * ue4m3 / kv_gs.
  * A slot is (page index) * page + (position within the page).  A sequence's position i
  * lies on page block_table[i / page].  page is a power of two from 16 to
- * NVFP4_KV_MAX_PAGE, d a multiple of 32 up to NVFP4_KV_MAX_DIM.  Bytes no call has
+ * NVFP4_KV_MAX_PAGE, d a multiple of 16 up to NVFP4_KV_MAX_DIM.  Bytes no call has
  * written are never used: a cache need not be cleared.
  */
 #ifndef NVFP4_ATTENTION_H
@@ -56,7 +56,7 @@ extern "C" {
  *   the same stride), but may not overlap it otherwise.
  *   positions: [axes, t] int32; inv_freq: [pairs] fp32 (radians a position).
  *   sections: `axes` numbers of pairs, in HOST memory, read before the call returns.
- * Requires 1 <= axes <= 4, sections >= 0, their sum a positive multiple of 8 and at most
+ * Requires 1 <= axes <= 4, sections >= 0, their sum positive, even and at most
  * d / 2, d a multiple of 16, t * heads * d at most 2^36.
  */
 int rope_axes(const void* x, int64_t x_stride, void* out, int64_t out_stride, int64_t t, int64_t heads, int64_t d,

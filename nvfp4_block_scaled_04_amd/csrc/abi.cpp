@@ -542,7 +542,7 @@ int rope_axes(const void* x, int64_t x_stride, void* out, int64_t out_stride, in
         a.sections[i] = sections[i];
         pairs += sections[i];
     }
-    if (pairs < 8 || pairs % 8 != 0 || 2 * pairs > d) return NVFP4_BAD_SHAPE;
+    if (pairs < 2 || pairs % 2 != 0 || 2 * pairs > d) return NVFP4_BAD_SHAPE;
     if (!aligned16(x) || !aligned16(out) || ((uintptr_t)positions & 3u) || ((uintptr_t)inv_freq & 3u))
         return NVFP4_MISALIGNED;
     a.x = (const uint16_t*)x; a.out = (uint16_t*)out; a.positions = positions; a.inv_freq = inv_freq;
@@ -553,7 +553,7 @@ int rope_axes(const void* x, int64_t x_stride, void* out, int64_t out_stride, in
 
 // The cache's own sizes.
 static int cache_check(int64_t heads, int64_t d, int64_t pages, int64_t page) {
-    if (!dim_ok(heads) || !dim_ok(pages) || d < 32 || d % 32 != 0) return NVFP4_BAD_SHAPE;
+    if (!dim_ok(heads) || !dim_ok(pages) || d < 16 || d % 16 != 0) return NVFP4_BAD_SHAPE;
     if (page < 16 || (page & (page - 1)) != 0) return NVFP4_BAD_SHAPE;
     if (d > NVFP4_KV_MAX_DIM || page > NVFP4_KV_MAX_PAGE || heads * d > NVFP4_ATTENTION_MAX_STRIDE) return NVFP4_UNSUPPORTED;
     return NVFP4_OK;

@@ -134,24 +134,50 @@ __device__ __forceinline__ int load_pages(const DParams& p, const int32_t* row, 
 // Starts a block's loads into LDS.  id: its groups' pages (page 0 in the place of none).
 // ONCE: no other workgroup reads the block (one tile of rows), so it passes the caches by
 // (streaming policy): 64 sequences of 16384, 1.2 GB, 244 -> 221 us a call.
-template <int D, bool ONCE>
+// PACKED: rows lie in LDS as they do in memory, where the 16 rows of a group are 8 d bytes in one
+// piece, for a d that is no multiple of 32 (a row alone does not begin on 16 bytes) or half of D
+// (32 sequences of 8192, heads of 32: 33 us, 39 with rows of D; but of 96, 64 of up to 8192: 72, 67).
+template <int D, bool ONCE, bool PACKED>
 __device__ __forceinline__ void stage_block(const DParams& p, const int (&id)[4], int tok, int head, lds_u8* st) {
     using S = Stage<D>;
     constexpr int CH = D / 32;             // 16-byte chunks of a row
     constexpr int ROWS = 64 / CH;          // rows of a load
     const int lane = threadIdx.x & 63;
-    const uint32_t rb = p.d >> 1;
+    const int d = p.d;
+    const uint32_t rb = d >> 1;
     const int mask = (1 << p.page_log2) - 1;
     const uint32_t r = lane / CH, c = lane % CH;
+    if constexpr (PACKED) {
+        const int per = d >> 1;  // 16-byte pieces of a group
+        const int64_t plane = ((int64_t)head << p.page_log2) * rb, to_v = ((int64_t)p.H << p.page_log2) * rb;
+        uint64_t at[4];  // of a group's first piece, less the pieces before it
 #pragma unroll
-    for (int which = 0; which < 2; which++) {
+        for (int i = 0; i < 4; i++)
+            at[i] = (uint64_t)(p.kv + id[i] * p.page_codes + plane + (uint32_t)((tok + 16 * i) & mask) * rb) - i * per * 16;
+#pragma unroll
+        for (int j = 0; j < S::CODES / 1024; j++) {
+            if (j * 64 >= 4 * per) break;
+            // (a lane past the last piece repeats it, behind the rows)
+            const int piece = j * 64 + lane < 4 * per ? j * 64 + lane : 4 * per - 1;
+            uint64_t from = at[0];
+#pragma unroll
+            for (int i = 1; i < 4; i++) from = piece >= i * per ? at[i] : from;
+            const uint8_t* const src = (const uint8_t*)from + piece * 16;
+#pragma unroll
+            for (int which = 0; which < 2; which++)
+                __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)(src + (which ? to_v : 0)),
+                                                 (__attribute__((address_space(3))) void*)(st + which * S::OFF_V + j * 1024), 16, 0, ONCE ? 2 : 0);
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < (PACKED ? 0 : 2); which++) {
         const int64_t plane = ((int64_t)(which * p.H + head) << p.page_log2) * rb;
 #pragma unroll
         for (int j = 0; j < S::CODES / 1024; j++) {
             // rows j * ROWS .. of the block: within a group, or two groups
             auto at = [&](int group) { return p.kv + id[group] * p.page_codes + plane + (uint32_t)((tok + 16 * group) & mask) * rb; };
             uint32_t cc = which ? c ^ swizzle<D>(j * ROWS + r) : c;
-            cc = cc * 32 < (uint32_t)p.d ? cc : 0;
+            cc = cc * 32 < (uint32_t)d ? cc : 0;
             const uint8_t* src;
             if constexpr (D == 64) src = (r < 16 ? at(2 * j) : at(2 * j + 1)) + ((r & 15) * rb + cc * 16);
             else src = at(j * ROWS / 16) + ((j * ROWS % 16 + r) * rb + cc * 16);
@@ -159,7 +185,7 @@ __device__ __forceinline__ void stage_block(const DParams& p, const int (&id)[4]
                                              (__attribute__((address_space(3))) void*)(st + which * S::OFF_V + j * 1024), 16, 0, ONCE ? 2 : 0);
         }
     }
-    const int blocks = p.d >> 4;
+    const int blocks = d >> 4;
     auto at = [&](int group) { return p.sf + id[group] * p.page_sf + ((tok + 16 * group) & mask); };
     const uint8_t* const a = lane & 1 ? at(1) : at(0);
     const uint8_t* const b = lane & 1 ? at(3) : at(2);
@@ -217,11 +243,15 @@ __device__ __forceinline__ void read_columns(uint32_t at, uint32_t sw, u32x2 (&v
 }
 
 // NT: products' worths of query rows of a workgroup, which share the dequantized keys and values.
-template <int D, int NT, bool ONCE>
-__global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5 : D <= 128 ? 4 : 2) void k_attn_decode(DParams p) {
+// (PACKED: a workgroup of a CU fewer, for the registers of its addresses: spilled, whose reloads
+// wait for the loads in flight, 64 sequences of up to 8192 with heads of 96 took 113 us, 72 so.)
+template <int D, int NT, bool ONCE, bool PACKED>
+__global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? (PACKED ? 4 : 5) : D <= 128 ? (PACKED ? 3 : 4) : 2) void k_attn_decode(DParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     using S = Stage<D>;
     extern __shared__ __align__(16) uint8_t smem[];
+    const int d = p.d;
+    const int pitch = PACKED ? d >> 1 : D / 2;  // bytes of a row in LDS
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -248,13 +278,13 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
         const int r = rt * ROWS + t * kRows + n;
         const bool live = r < p.T * p.G;
         const int qt = live ? r / p.G : 0;
-        const uint16_t* const src = p.q + ((int64_t)w.seq * p.T + qt) * p.q_stride + (head * p.G + (live ? r - qt * p.G : 0)) * p.d;
+        const uint16_t* const src = p.q + ((int64_t)w.seq * p.T + qt) * p.q_stride + (head * p.G + (live ? r - qt * p.G : 0)) * d;
         limit[t] = w.len - (p.T - 1 - qt);
 #pragma unroll
         for (int s = 0; s < QW; s++) {
             const int col = g * (D / 4) + 8 * s;
             raw[t][s] = u32x4{};
-            if (live && col < p.d) raw[t][s] = *(const u32x4*)(src + col);
+            if (live && col < d) raw[t][s] = *(const u32x4*)(src + col);
         }
     }
     const float gs_k = p.gs[0], gs_v = p.gs[1];
@@ -273,7 +303,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
             bad |= v < 0 ? 1u << i : 0u;
             id[i] = v < 0 ? 0 : v;
         }
-        stage_block<D, ONCE>(p, id, at, head, st);
+        stage_block<D, ONCE, PACKED>(p, id, at, head, st);
     };
     if (tok < t1) start(tok);
 
@@ -310,8 +340,8 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
     // a lane's row of 16 values for the transposing reads
     constexpr int VN = D == 64 ? 4 : 8;
     const int vrow = 16 * g + n;
-    const uint32_t vat = (uint32_t)(uintptr_t)st + vrow * (D / 2);
-    const uint32_t vsw = swizzle<D>(vrow) * 16;
+    const uint32_t vat = (uint32_t)(uintptr_t)st + vrow * pitch;
+    const uint32_t vsw = PACKED ? 0 : swizzle<D>(vrow) * 16;
 
     float m[NT], l[NT];
     f32x4 o[NT][D / 16];
@@ -344,7 +374,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
                         if (gone || tok + t + 4 + e >= t1) v1[e] = (_Float16)0.0f;
                     }
                 }
-                if ((at >> 6) * 16 >= p.d) v0 = v1 = f16x4{};
+                if ((at >> 6) * 16 >= d) v0 = v1 = f16x4{};
                 *(f16x8*)(vs16 + 2 * at) = __builtin_shufflevector(v0, v1, 0, 1, 2, 3, 4, 5, 6, 7);
             }
         }
@@ -357,7 +387,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
 #pragma unroll
             for (int c = 0; c < D / 64; c++) {
                 kb[c] = *(const uint32_t*)(mine + S::OFF_SF + (g * (D / 64) + c) * kBlock + 4 * n);
-                if ((g * (D / 64) + c) * 16 >= p.d) kb[c] = 0;
+                if ((g * (D / 64) + c) * 16 >= d) kb[c] = 0;
             }
             if constexpr (D == 64) {
                 const f16x4 v = scales4(kb[0]);
@@ -377,7 +407,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
         for (int i = 0; i < 4; i++) {
 #pragma unroll
             for (int t = 0; t < NT; t++) x[t][i] = f32x4{};
-            const uint8_t* const kr = mine + (4 * n + i) * (D / 2) + g * (D / 8);
+            const uint8_t* const kr = mine + (4 * n + i) * pitch + g * (D / 8);
             uint32_t kw[QW];
             if constexpr (D == 64) {
                 const u32x2 v = *(const u32x2*)kr;
@@ -385,7 +415,13 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
             } else {
 #pragma unroll
                 for (int c = 0; c < QW / 4; c++) {
-                    const u32x4 v = *(const u32x4*)(kr + 16 * c);
+                    u32x4 v;
+                    if constexpr (PACKED) {
+                        const u32x2 a = *(const u32x2*)(kr + 16 * c), b = *(const u32x2*)(kr + 16 * c + 8);
+                        v = u32x4{a[0], a[1], b[0], b[1]};
+                    } else {
+                        v = *(const u32x4*)(kr + 16 * c);
+                    }
 #pragma unroll
                     for (int j = 0; j < 4; j++) kw[4 * c + j] = v[j];
                 }
@@ -509,7 +545,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? 5
             const int tt = rr / p.G;
             const int64_t orow = ((int64_t)w.seq * p.T + tt) * p.Hq + head * p.G + rr - tt * p.G;
             const float by = den == 0.0f ? 0.0f : out_scale / den;
-            if (c < p.d) *(u32x2*)(p.out + orow * p.d + c) = u32x2{pack_bf16x2(sum[0] * by, sum[1] * by), pack_bf16x2(sum[2] * by, sum[3] * by)};
+            if (c < d) *(u32x2*)(p.out + orow * d + c) = u32x2{pack_bf16x2(sum[0] * by, sum[1] * by), pack_bf16x2(sum[2] * by, sum[3] * by)};
             if (p.lse && c == 0) p.lse[orow] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
         }
     }
@@ -589,8 +625,11 @@ hipError_t launch(const DParams& p, int64_t grid, bool join, bool large, hipStre
     constexpr int merge = kWaves * NT * kRows * (D + 4) * 4;
     constexpr int need = kWaves * Stage<D>::WAVE > merge ? kWaves * Stage<D>::WAVE : merge;
     const int lds = D > 64 && large && need < kAttnLdsLong ? kAttnLdsLong : need;
-    if (p.row_tiles == 1) k_attn_decode<D, NT, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
-    else k_attn_decode<D, NT, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    const bool once = p.row_tiles == 1, packed = p.d % 32 != 0 || 2 * p.d <= D;
+    if (once && !packed) k_attn_decode<D, NT, true, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    else if (once) k_attn_decode<D, NT, true, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    else if (!packed) k_attn_decode<D, NT, false, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    else k_attn_decode<D, NT, false, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || !join) return e;
     k_attn_join<D, NT><<<dim3((unsigned)((int64_t)p.b * p.T * p.Hq)), kThreads, 0, st>>>(p);

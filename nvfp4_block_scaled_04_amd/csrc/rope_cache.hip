@@ -34,22 +34,35 @@ struct RParams {
     int ends[kRopeAxes];     // first pair past axis a
 };
 
-// 4 dwords of bf16 pairs.  Halves: a holds x1 of eight pairs, b their x2 (cs: the eight).
-// Else a holds four pairs (ca), b four others (cb).
-template <bool HALVES>
-__device__ __forceinline__ void rotate(u32x4& a, u32x4& b, const float2* ca, const float2* cb) {
+// A piece: W elements of bf16.
+template <int W>
+struct Piece { typedef uint32_t type __attribute__((ext_vector_type(W / 2))); };
+template <>
+struct Piece<2> { typedef uint32_t type; };
+__device__ __forceinline__ uint32_t dword(uint32_t v, int) { return v; }
+__device__ __forceinline__ void set_dword(uint32_t& v, int, uint32_t to) { v = to; }
+template <typename V>
+__device__ __forceinline__ uint32_t dword(const V& v, int j) { return v[j]; }
+template <typename V>
+__device__ __forceinline__ void set_dword(V& v, int j, uint32_t to) { v[j] = to; }
+
+// Two pieces.  Halves: a holds x1 of W pairs, b their x2 (ca: the W).  Else a holds
+// W / 2 pairs (ca), b as many others (cb).
+template <bool HALVES, int W>
+__device__ __forceinline__ void rotate(typename Piece<W>::type& a, typename Piece<W>::type& b, const float2* ca, const float2* cb) {
 #pragma unroll
-    for (int j = 0; j < 4; j++) {
+    for (int j = 0; j < W / 2; j++) {
+        const uint32_t aj = dword(a, j), bj = dword(b, j);
         if (HALVES) {
             const float2 c0 = ca[2 * j], c1 = ca[2 * j + 1];
-            const float p0 = bf16_lo(a[j]), p1 = bf16_hi(a[j]), q0 = bf16_lo(b[j]), q1 = bf16_hi(b[j]);
-            a[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, p1 * c1.x - q1 * c1.y);
-            b[j] = pack_bf16x2(q0 * c0.x + p0 * c0.y, q1 * c1.x + p1 * c1.y);
+            const float p0 = bf16_lo(aj), p1 = bf16_hi(aj), q0 = bf16_lo(bj), q1 = bf16_hi(bj);
+            set_dword(a, j, pack_bf16x2(p0 * c0.x - q0 * c0.y, p1 * c1.x - q1 * c1.y));
+            set_dword(b, j, pack_bf16x2(q0 * c0.x + p0 * c0.y, q1 * c1.x + p1 * c1.y));
         } else {
             const float2 c0 = ca[j], c1 = cb[j];
-            const float p0 = bf16_lo(a[j]), q0 = bf16_hi(a[j]), p1 = bf16_lo(b[j]), q1 = bf16_hi(b[j]);
-            a[j] = pack_bf16x2(p0 * c0.x - q0 * c0.y, q0 * c0.x + p0 * c0.y);
-            b[j] = pack_bf16x2(p1 * c1.x - q1 * c1.y, q1 * c1.x + p1 * c1.y);
+            const float p0 = bf16_lo(aj), q0 = bf16_hi(aj), p1 = bf16_lo(bj), q1 = bf16_hi(bj);
+            set_dword(a, j, pack_bf16x2(p0 * c0.x - q0 * c0.y, q0 * c0.x + p0 * c0.y));
+            set_dword(b, j, pack_bf16x2(p1 * c1.x - q1 * c1.y, q1 * c1.x + p1 * c1.y));
         }
     }
 }
@@ -58,9 +71,10 @@ __device__ __forceinline__ void rotate(u32x4& a, u32x4& b, const float2* ca, con
 // The angle pos * inv_freq is formed in fp64 turns and reduced to half a turn before
 // it becomes fp32: at position 2^20 an fp32 product would be off by 0.06 radians.  A
 // workgroup makes the angles of its tokens once, for all their heads.  A thread takes two
-// 16-byte pieces, in the same place of the rotated part's halves, so that eight threads
-// cover whole lines.  STREAM: past the caches, where the tensor is larger than they are.
-template <bool HALVES, bool STREAM>
+// pieces of W elements, in the same place of the rotated part's halves, so that eight threads
+// cover whole lines.  W: 8, or what divides the pairs, so that the second half begins on a piece.
+// STREAM: past the caches, where the tensor is larger than they are.
+template <bool HALVES, bool STREAM, int W>
 __global__ __launch_bounds__(rope_threads(STREAM)) void k_rope_axes(RParams p) {
     constexpr int kThreads = rope_threads(STREAM);
     __shared__ float2 cs[kRopeAngles];
@@ -77,7 +91,8 @@ __global__ __launch_bounds__(rope_threads(STREAM)) void k_rope_axes(RParams p) {
         cs[i] = make_float2(cospif(r), sinpif(r));
     }
     __syncthreads();
-    const int units = p.d >> 4, turned = p.rot >> 4;  // two pieces each; the first `turned` are rotated
+    typedef typename Piece<W>::type piece;
+    const int units = p.d / (2 * W), turned = p.rot / (2 * W);  // two pieces each; the first `turned` are rotated
     const int per = p.heads * units;
     for (int i = threadIdx.x; i < nt * per; i += kThreads) {
         const int tok = i / per, r = i - tok * per;
@@ -85,23 +100,23 @@ __global__ __launch_bounds__(rope_threads(STREAM)) void k_rope_axes(RParams p) {
         const bool turn = u < turned;
         const int64_t e = (int64_t)head * p.d;
         // element offsets of the unit's pieces
-        const int o0 = turn ? u * 8 : u * 16;
-        const int o1 = turn ? half + u * 8 : u * 16 + 8;
+        const int o0 = turn ? u * W : u * 2 * W;
+        const int o1 = turn ? half + u * W : u * 2 * W + W;
         const uint16_t* const src = p.x + (t0 + tok) * p.x_stride + e;
         uint16_t* const dst = p.out + (t0 + tok) * p.out_stride + e;
-        u32x4 a = STREAM ? __builtin_nontemporal_load((const u32x4*)(src + o0)) : *(const u32x4*)(src + o0);
-        u32x4 b = STREAM ? __builtin_nontemporal_load((const u32x4*)(src + o1)) : *(const u32x4*)(src + o1);
+        piece a = STREAM ? __builtin_nontemporal_load((const piece*)(src + o0)) : *(const piece*)(src + o0);
+        piece b = STREAM ? __builtin_nontemporal_load((const piece*)(src + o1)) : *(const piece*)(src + o1);
         if (turn) {
             const float2* const c = cs + tok * half;
-            if (HALVES) rotate<true>(a, b, c + u * 8, nullptr);
-            else rotate<false>(a, b, c + u * 4, c + (half >> 1) + u * 4);
+            if (HALVES) rotate<true, W>(a, b, c + u * W, nullptr);
+            else rotate<false, W>(a, b, c + u * (W / 2), c + (half >> 1) + u * (W / 2));
         }
         if (STREAM) {
-            __builtin_nontemporal_store(a, (u32x4*)(dst + o0));
-            __builtin_nontemporal_store(b, (u32x4*)(dst + o1));
+            __builtin_nontemporal_store(a, (piece*)(dst + o0));
+            __builtin_nontemporal_store(b, (piece*)(dst + o1));
         } else {
-            *(u32x4*)(dst + o0) = a;
-            *(u32x4*)(dst + o1) = b;
+            *(piece*)(dst + o0) = a;
+            *(piece*)(dst + o1) = b;
         }
     }
 }
@@ -208,6 +223,18 @@ __global__ __launch_bounds__(kRowThreadsMany) void k_kv_rows(CParams p) {
 
 }  // namespace
 
+template <int W>
+static void rope(const RParams& p, bool interleaved, bool stream, dim3 grid, hipStream_t st) {
+    const int threads = rope_threads(stream);
+    if (interleaved) {
+        if (stream) k_rope_axes<false, true, W><<<grid, threads, 0, st>>>(p);
+        else k_rope_axes<false, false, W><<<grid, threads, 0, st>>>(p);
+    } else {
+        if (stream) k_rope_axes<true, true, W><<<grid, threads, 0, st>>>(p);
+        else k_rope_axes<true, false, W><<<grid, threads, 0, st>>>(p);
+    }
+}
+
 hipError_t launch_rope_axes(const RopeArgs& a, hipStream_t st) {
     RParams p{};
     p.x = a.x; p.out = a.out; p.pos = a.positions; p.inv_freq = a.inv_freq;
@@ -221,20 +248,17 @@ hipError_t launch_rope_axes(const RopeArgs& a, hipStream_t st) {
     // a few pieces a thread, while the workgroups still fill the card several times
     const bool stream = a.t * a.heads * a.d * 2 > kRopeStream;
     const int threads = rope_threads(stream);
-    const int64_t per = a.heads * (a.d / 16);
+    const int64_t per = a.heads * (a.d / 16);  // (pairs of 16-byte pieces)
     int64_t tokens = per >= 4 * threads ? 1 : 4 * threads / per;
     const int64_t most = kRopeAngles / (a.rot / 2);
     if (tokens > most) tokens = most;
     while (tokens > 1 && (a.t + tokens - 1) / tokens < 1024) tokens >>= 1;
     p.tokens = (int)tokens;
     const dim3 grid((unsigned)((a.t + tokens - 1) / tokens));
-    if (a.interleaved) {
-        if (stream) k_rope_axes<false, true><<<grid, threads, 0, st>>>(p);
-        else k_rope_axes<false, false><<<grid, threads, 0, st>>>(p);
-    } else {
-        if (stream) k_rope_axes<true, true><<<grid, threads, 0, st>>>(p);
-        else k_rope_axes<true, false><<<grid, threads, 0, st>>>(p);
-    }
+    const int64_t pairs = a.rot / 2;
+    if (pairs % 8 == 0) rope<8>(p, a.interleaved, stream, grid, st);
+    else if (pairs % 4 == 0) rope<4>(p, a.interleaved, stream, grid, st);
+    else rope<2>(p, a.interleaved, stream, grid, st);
     return hipGetLastError();
 }
 

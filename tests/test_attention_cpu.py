@@ -55,7 +55,7 @@ def test_rope_validation(att, change, status):
 
 CACHE = [
     ({"pages": 0}, SHAPE), ({"page": 8}, SHAPE), ({"page": 48}, SHAPE), ({"page": 8192}, UNSUP), ({"page": 0}, SHAPE), ({"page": -16}, SHAPE),
-    ({"d": 16}, SHAPE), ({"d": 80}, SHAPE), ({"d": 288}, UNSUP), ({"heads": 0}, SHAPE), ({"heads": 1 << 20}, UNSUP),
+    ({"d": 8}, SHAPE), ({"d": 0}, SHAPE), ({"d": 88}, SHAPE), ({"d": 272}, UNSUP), ({"heads": 0}, SHAPE), ({"heads": 1 << 20}, UNSUP),
     ({"kv": P + 8}, MISAL), ({"sf": P + 4}, MISAL), ({"gs": P + 2}, MISAL),
 ]
 APPEND = dict(k=P, ks=512, v=P, vs=512, t=4, heads=4, d=128, slots=P, gs=P, kv=P, sf=P, pages=10, page=64, stream=None)

@@ -39,7 +39,7 @@ def test_rope(att):
         refused(att.rope_axes, *bad)
     refused(att.rope_axes, x, pos, f, (8, 8), out=z(4, 2, 48))
     refused(att.rope_axes, x, pos, f, (8, 8), out=z(4, 2, 32, dtype=torch.float16))
-    refused(att.rope_axes, x, pos, f, (8, 4), error=RuntimeError)
+    refused(att.rope_axes, x, pos, f, (8, 5), error=RuntimeError)
     refused(att.rope_axes, x, i32(0, 4), f, (), error=(ValueError, RuntimeError))
     refused(att.rope_axes, z(4, 2, 24), pos, f, (4, 4), error=RuntimeError)
     refused(att.rope_axes, z(0, 2, 32), i32(2, 0), f, (8, 8), error=RuntimeError)
@@ -55,7 +55,7 @@ def test_cache_rows(att):
                 (k, k, slots, gs, kv, None), (k, k, None, gs, kv, sf), (k.transpose(1, 2).contiguous().transpose(1, 2), k, slots, gs, kv, sf)):
         refused(att.nvfp4_kv_append, *bad)
     refused(att.nvfp4_kv_append, z(5, 2, 64), z(5, 2, 64), slots, gs, u8(3, 2, 2, 48, 32), u8(3, 2, 2, 4, 48), error=RuntimeError)
-    refused(att.nvfp4_kv_append, z(5, 2, 80), z(5, 2, 80), slots, gs, u8(3, 2, 2, 16, 40), u8(3, 2, 2, 5, 16), error=RuntimeError)
+    refused(att.nvfp4_kv_append, z(5, 2, 272), z(5, 2, 272), slots, gs, u8(3, 2, 2, 16, 136), u8(3, 2, 2, 17, 16), error=RuntimeError)
     att.nvfp4_kv_read(slots, gs, kv, sf)
     refused(att.nvfp4_kv_read, slots, gs, kv, sf, k=z(4, 2, 64))
     refused(att.nvfp4_kv_read, slots, gs, kv, sf, v=z(5, 2, 64, dtype=torch.float16))

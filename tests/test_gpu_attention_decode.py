@@ -79,6 +79,8 @@ def check(s, out, lse=None, scale=None, gone=()):
     ((333, 1024), 1, 21, 3, 96, 32), ((513, 40), 1, 10, 2, 256, 64), ((90, 777), 1, 5, 5, 160, 16), ((4000, 17), 1, 71, 1, 64, 64),
     ((5, 2, 1, 0, 600), 4, 12, 4, 128, 16), ((1000, 3), 7, 48, 2, 64, 32), ((259, 258, 257), 3, 8, 8, 256, 16), ((40,), 64, 2, 1, 128, 64),
     ((9000, 12000, 64), 1, 8, 8, 128, 256), ((20000,), 2, 4, 1, 128, 4096), ((3000,) * 3, 1, 3, 3, 192, 64), ((70,), 1, 7, 7, 224, 16),
+    ((1, 300, 0, 77), 1, 8, 2, 80, 16), ((3000, 65), 1, 21, 3, 80, 64), ((500,), 3, 40, 4, 48, 32), ((200, 18), 1, 5, 5, 16, 16), ((31, 1200), 2, 6, 2, 112, 64),
+    ((700, 2), 1, 9, 3, 144, 16), ((100, 400), 5, 16, 2, 240, 128), ((257,), 1, 2, 2, 208, 32), ((1100, 7), 1, 64, 4, 32, 16),
 ])
 def test_decode(att, lens, new, q_heads, heads, d, page):
     say("decode", lens, new, q_heads, heads, d, page)
@@ -93,7 +95,7 @@ def test_decode(att, lens, new, q_heads, heads, d, page):
 
 
 @pytest.mark.parametrize("lens,new,q_heads,heads,d,page", [((600, 33, 1, 0, 2000), 4, 64, 8, 128, 64), ((70, 1025), 3, 21, 3, 64, 32), ((40, 3), 17, 8, 4, 96, 64),
-                                                           ((513,), 5, 40, 8, 256, 64)])
+                                                           ((513,), 5, 40, 8, 256, 64), ((300, 17, 1400), 5, 24, 4, 80, 16), ((90, 700), 2, 40, 4, 48, 32)])
 def test_rows_that_share_a_read(att, lens, new, q_heads, heads, d, page):
     """Tables wide enough that several tiles of rows are taken together."""
     say("decode shared", lens, new, q_heads, heads, d, page)

@@ -42,7 +42,7 @@ def rope_ok(y, x, ref, pos, freq, sections, inter):
 @pytest.mark.parametrize("inter", [False, True])
 @pytest.mark.parametrize("t,heads,d,sections", [
     (1, 1, 16, (8,)), (1, 40, 128, (64,)), (16, 40, 128, (16, 24, 24)), (77, 3, 64, (8, 8)), (5, 7, 80, (10, 15, 15)),
-    (1000, 2, 256, (44, 42, 42)), (333, 24, 128, (22, 21, 21)), (9, 5, 96, (3, 0, 5)), (4099, 1, 64, (5, 9, 10, 8)), (3, 4, 1024, (512,)),
+    (1000, 2, 256, (44, 42, 42)), (333, 24, 128, (22, 21, 21)), (9, 5, 96, (3, 0, 5)), (4099, 1, 64, (5, 9, 10, 8)), (3, 4, 1024, (512,)), (100, 6, 80, (6, 7, 7)), (7, 3, 80, (10,)), (65, 9, 64, (1, 1)), (19, 2, 128, (13, 0, 37)),
     (8200, 64, 128, (16, 24, 24)), (300000, 4, 64, (7, 9)),   # larger than the caches
 ])
 def test_rope(att, t, heads, d, sections, inter):
@@ -87,7 +87,7 @@ def cache(pages, heads, page, d, fill=0xFF):
 
 
 @pytest.mark.parametrize("t,heads,d,page", [(1, 1, 32, 16), (1, 8, 128, 64), (16, 8, 128, 16), (37, 3, 64, 32), (500, 2, 96, 128),
-                                            (1001, 5, 256, 64), (130, 1, 160, 16), (8003, 8, 128, 16)])
+                                            (1001, 5, 256, 64), (77, 3, 80, 16), (300, 2, 16, 32), (4500, 6, 240, 64), (130, 1, 160, 16), (8003, 8, 128, 16)])
 def test_append_and_read(att, t, heads, d, page):
     from nvfp4_block_scaled_04_amd import ops
     say("append", t, heads, d, page)
@@ -97,7 +97,7 @@ def test_append_and_read(att, t, heads, d, page):
     if t > 4:
         wide[0] = 0
         wide[1, :, 5] = float("inf")
-        wide[2, :, 17] = float("nan")
+        wide[2, :, 17 % d] = float("nan")
         wide[3] *= 1e-30
     k, v = wide[:, heads:2 * heads], wide[:, 2 * heads:]
     gs = torch.tensor([2688 / 200.0, 2688 / 3.7], device="cuda")
