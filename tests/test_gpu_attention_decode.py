@@ -114,6 +114,16 @@ def test_many_sequences(att):
     check(s, att.nvfp4_attention_decode(**s))
 
 
+@pytest.mark.parametrize("q_heads,heads,d,new", [(32, 2, 256, 1), (40, 1, 128, 1), (26, 2, 80, 1), (16, 16, 64, 2)])
+def test_many_rows_and_parts(att, q_heads, heads, d, new):
+    """A thousand rows and more, some of sequences in many parts."""
+    lens = [(i * 53) % 700 for i in range(40)] + [9000, 0, 4500]
+    say("decode many rows", q_heads, heads, d, new)
+    s = setup(att, lens, new, q_heads, heads, d, 32, seed=d)
+    lse = torch.empty(s["q"].shape[:3], device="cuda")
+    check(s, att.nvfp4_attention_decode(**s, lse=lse), lse)
+
+
 def test_scale_and_peaks(att):
     """Scores far apart (one key takes all), a scale of its own, queries of very different size."""
     say("decode peaks")
