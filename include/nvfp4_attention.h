@@ -120,6 +120,10 @@ int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t
                            float scale, void* out, float* lse, void* workspace, int64_t workspace_bytes,
                            void* stream);
 
+/* A workspace of attention_prefill that suffices for all sizes. */
+#define NVFP4_ATTENTION_PREFILL_WS_BYTES(d) \
+    ((int64_t)512 * 129 * 4 * (((d) <= 64 ? 64 : (d) <= 128 ? 128 : 256) + 4))
+
 /*
  * Attention of whole prompts, packed one after the other: sequence i has the rows
  * cu_q[i] .. cu_q[i + 1] - 1 of q and the keys cu_k[i] .. cu_k[i + 1] - 1, which may reach
@@ -135,11 +139,15 @@ int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t
  * Requires q_heads a multiple of heads, d a multiple of 16 up to NVFP4_KV_MAX_DIM, 0 < scale
  * <= 2e38, b at most NVFP4_ATTENTION_MAX_BATCH, (tq / 128 + b) * q_heads below 2^23.  Results
  * are the same on every call.
+ *   workspace: NULL, or workspace_bytes >= NVFP4_ATTENTION_PREFILL_WS_BYTES(d) (16-byte
+ *   aligned, contents ignored on entry, undefined on exit, not shared by calls that overlap).
+ *   With one, few rows behind many keys have the keys split over workgroups, whose sums, fp32,
+ *   a second launch joins.  Less than that is taken where it suffices for the sizes at hand.
  */
 int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t d,
                       const int32_t* cu_q, const int32_t* cu_k, int64_t b, float scale, int causal, void* out,
-                      int64_t out_stride, float* lse, void* stream);
+                      int64_t out_stride, float* lse, void* workspace, int64_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -30,7 +30,7 @@ def _load():
         "nvfp4_kv_read": [vp, vp, vp, i64, i64, vp, i64, i64, i64, vp, i64, vp, i64, vp],
         "nvfp4_attention_decode": [vp, i64, i64, i64, i64, vp, vp, vp, i64, i64, i64, i64, vp, i64, vp, f32, vp, vp, vp, i64,
                                    vp],
-        "attention_prefill": [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, i64, f32, i32, vp, i64, vp, vp],
+        "attention_prefill": [vp, i64, vp, i64, vp, i64, i64, i64, i64, i64, i64, vp, vp, i64, f32, i32, vp, i64, vp, vp, i64, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
@@ -45,6 +45,14 @@ _lib = _load()
 def attention_ws_bytes(b, d):
     """NVFP4_ATTENTION_WS_BYTES: workspace bytes of nvfp4_attention_decode."""
     return (8 * b + 255) // 256 * 256 + MAX_SLOTS * 64 * ((64 if d <= 64 else 128 if d <= 128 else 256) + 2)
+
+
+def attention_prefill_ws_bytes(tq, tk, q_heads, b, d):
+    """Workspace bytes that attention_prefill takes with these sizes: 0 where it needs none."""
+    most, keys = 512 // (b * ((max(1, tq // b) + 127) // 128) * q_heads), tk // b
+    if most < 4 or keys < 1536:
+        return 0
+    return min(keys // 256, most, 64) * tq * q_heads * ((64 if d <= 64 else 128 if d <= 128 else 256) + 4) * 4
 
 
 def _rows(x, name, i):
@@ -211,12 +219,12 @@ def nvfp4_attention_decode(q, kv, kv_sf, kv_gs, block_table, lengths, scale=None
     return out
 
 
-def attention_prefill(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, lse=None):
+def attention_prefill(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=None, lse=None, workspace=None):
     """Attention of packed prompts.  q: [tq, q_heads, d], k, v: [tk, heads, d] bf16, any strides from
     token to token; cu_q, cu_k: [b + 1] int32, where each sequence's rows and keys start (cu_k =
     cu_q when None); causal: row r of n rows and m keys sees the keys up to r + m - n, else all;
-    scale: d ** -0.5 when None; lse: None or [tq, q_heads] fp32, written.  Returns out [tq, q_heads,
-    d] bf16; rows outside all sequences are left as they were (zeros in an out allocated here)."""
+    scale: d ** -0.5 when None; lse: None or [tq, q_heads] fp32, written; workspace:
+    attention_prefill_ws_bytes bytes, where few rows meet many keys.  Returns out [tq, q_heads, d] bf16; rows outside all sequences are left as they were (zeros in an out allocated here)."""
     i = _gpu(q, "q")
     qs, ks, vs = _rows(q, "q", i), _rows(k, "k", i), _rows(v, "v", i)
     tq, q_heads, d = q.shape
@@ -230,7 +238,13 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=Non
         out = torch.zeros(tq, q_heads, d, dtype=torch.bfloat16, device=q.device)
     else:
         _shaped(out, "out", q.shape)
+    ws, need = None, attention_prefill_ws_bytes(tq, tk, q_heads, b, d) if b > 0 and q_heads > 0 else 0
+    if need:
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws, need = _bytes(workspace, "workspace", need, i), workspace.numel()
     _call(_lib.attention_prefill, "attention_prefill", i, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, tq, tk, q_heads,
           heads, d, cu_at, cu_at if cu_k is None else _at(cu_k, "cu_k", I32, b + 1, i), b, d ** -0.5 if scale is None else scale,
-          1 if causal else 0, out.data_ptr(), _rows(out, "out", i), None if lse is None else _at(lse, "lse", F32, tq * q_heads, i))
+          1 if causal else 0, out.data_ptr(), _rows(out, "out", i), None if lse is None else _at(lse, "lse", F32, tq * q_heads, i),
+          ws, need)
     return out

@@ -624,7 +624,7 @@ int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t
 int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t d,
                       const int32_t* cu_q, const int32_t* cu_k, int64_t b, float scale, int causal, void* out,
-                      int64_t out_stride, float* lse, void* stream) {
+                      int64_t out_stride, float* lse, void* workspace, int64_t workspace_bytes, void* stream) {
     if (!q || !k || !v || !cu_q || !cu_k || !out) return NVFP4_NULL_POINTER;
     if (d < 16 || d % 16 != 0 || !rows_ok(tq, q_heads, d, q_stride) || !rows_ok(tk, heads, d, k_stride) ||
         !rows_ok(tk, heads, d, v_stride) || !rows_ok(tq, q_heads, d, out_stride) || !dim_ok(b) || q_heads % heads != 0)
@@ -632,12 +632,17 @@ int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_
     if (!scale_ok(scale) || d > NVFP4_KV_MAX_DIM || b > NVFP4_ATTENTION_MAX_BATCH ||
         (tq / 128 + b) * q_heads >= (int64_t)1 << 23)  // the grid: below 2^32 threads
         return NVFP4_UNSUPPORTED;
-    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || ((uintptr_t)cu_q & 3u) ||
-        ((uintptr_t)cu_k & 3u) || ((uintptr_t)lse & 3u))
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || !aligned16(workspace) ||
+        ((uintptr_t)cu_q & 3u) || ((uintptr_t)cu_k & 3u) || ((uintptr_t)lse & 3u))
         return NVFP4_MISALIGNED;
+    if (workspace) {
+        const int64_t parts = nvfp4::prefill_parts(tq, tk, q_heads, b);
+        if (parts > 1 && workspace_bytes < parts * tq * q_heads * ((d <= 64 ? 64 : d <= 128 ? 128 : 256) + 4) * 4)
+            return NVFP4_BAD_SHAPE;
+    }
     nvfp4::AttnPrefillArgs a{};
     a.q = (const uint16_t*)q; a.k = (const uint16_t*)k; a.v = (const uint16_t*)v; a.out = (uint16_t*)out; a.lse = lse;
-    a.cu_q = cu_q; a.cu_k = cu_k; a.b = b; a.tq = tq; a.tk = tk; a.q_heads = q_heads; a.heads = heads; a.d = d;
+    a.ws = workspace; a.cu_q = cu_q; a.cu_k = cu_k; a.b = b; a.tq = tq; a.tk = tk; a.q_heads = q_heads; a.heads = heads; a.d = d;
     a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride; a.out_stride = out_stride;
     a.scale = scale; a.causal = causal != 0;
     return launch_status(nvfp4::launch_attention_prefill(a, (hipStream_t)stream));

@@ -13,6 +13,10 @@
 //   needs one exchange between lanes, and only where the maximum moves;
 //   O^T[column, row] = V^T P^T: V^T comes from transposing LDS reads, in the order of
 //   keys in which a lane holds its column of S^T, so P stays where it is.
+// What bounds it: a prompt of 8192, 40 heads of 128, 620 us, 1.11 PFLOP/s: the card's power (on zeros
+// 480 us; the library's product of 8192^3 runs at 1.24-1.32 on such data, 1.76 on zeros); heads of 64
+// the softmax's arithmetic; short prompts the chain of a tile's keys.  Where few rows meet many
+// keys, workgroups share the keys (prefill_parts).
 // Sums, maximum and both products' sums are fp32; P is rounded to bf16 (V's range is
 // bf16's), off by 2^-8 of itself at most, as the output is.
 #include <type_traits>
@@ -30,10 +34,11 @@ struct PParams {
     const uint16_t *q, *k, *v;
     uint16_t* out;
     float* lse;                // [tq, Hq] or null
+    float* part;               // [parts, tq, Hq, D + 4] sums, maximum, sum of the probabilities
     const int32_t *cu_q, *cu_k;
     int64_t q_stride, k_stride, v_stride, out_stride;
     float c;                   // scale * log2(e)
-    int b, tq, tk, Hq, H, G, d, causal, units;
+    int b, tq, tk, Hq, H, G, d, causal, units, parts;
 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -106,7 +111,8 @@ __device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
 // NW: waves of a workgroup.  Eight waves sit two to a SIMD and take turns (sweep_paired).
 // SPLIT: 1: each wave has 32 rows of its own; 2: the second four waves have the rows of
 // the first, which take every other tile of keys, and the halves are joined at the end.
-template <int D, int NW, int SPLIT>
+// PARTS: p.parts workgroups share a tile's keys, in stretches, and k_join_parts joins them.
+template <int D, int NW, int SPLIT, bool PARTS>
 __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int CH = D / 8;                   // chunks of a row
@@ -122,7 +128,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
 
     // Workgroups are dealt to the 8 XCDs in turn: where the heads split evenly, an XCD
     // has KV heads of its own, whose keys and values stay in its L2.
-    int head, unit;
+    int head, unit, part = 0;
     if (p.H % 8 == 0) {
         const int per = p.Hq / 8, r = blockIdx.x >> 3;
         head = (blockIdx.x & 7) * per + r % per;
@@ -130,6 +136,10 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     } else {
         head = blockIdx.x % p.Hq;
         unit = blockIdx.x / p.Hq;
+    }
+    if constexpr (PARTS) {
+        part = unit % p.parts;
+        unit /= p.parts;
     }
     Seq sq;
     int tile;
@@ -159,7 +169,13 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         off_v[i] = cv * 8 < p.d ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
     }
     // the group's n-th tile of keys
-    auto key_of = [&](int n) { return (n * SPLIT + grp) * kKeys; };
+    int tile0 = 0, tile1 = (keys + kKeys - 1) / kKeys;
+    if constexpr (PARTS) {
+        const int all_tiles = tile1;
+        tile0 = (int)((int64_t)all_tiles * part / p.parts);
+        tile1 = (int)((int64_t)all_tiles * (part + 1) / p.parts);
+    }
+    auto key_of = [&](int n) { return PARTS ? (tile0 + n) * kKeys : (n * SPLIT + grp) * kKeys; };
     auto stage = [&](const uint16_t* base, int64_t stride, const uint32_t (&off)[LOADS], int key0, uint32_t to) {
         const int rows = sq.nk - key0 < kKeys ? sq.nk - key0 : kKeys;  // at least 1; later rows come as zeros
         const u32x4 rs = raw_buffer(base + key0 * stride, (uint32_t)(((rows - 1) * stride + p.d) * 2));
@@ -169,7 +185,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     auto stage_k = [&](int n) { stage(kb, p.k_stride, off_k, key_of(n), (n & 1) * TILE); };
     auto stage_v = [&](int n) { stage(vb, p.v_stride, off_v, key_of(n), (2 + (n & 1)) * TILE); };
     auto tiles_of = [&](int upto) { return (upto + kKeys * (SPLIT - grp) - 1) / (kKeys * SPLIT); };  // of the group, of the keys below
-    const int tiles = tiles_of(keys), steps = (keys + kKeys * SPLIT - 1) / (kKeys * SPLIT);
+    const int tiles = PARTS ? tile1 - tile0 : tiles_of(keys), steps = PARTS ? tiles : (keys + kKeys * SPLIT - 1) / (kKeys * SPLIT);
     if (tiles > 0) stage_k(0);
 
     // The wave's 32 rows of q go through LDS too, in whole lines (fragments straight from memory
@@ -485,6 +501,19 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
             }
     }
     const float den = l + __shfl_xor(l, 32);
+    if constexpr (PARTS) {
+        if (mine >= sq.nq) return;
+        float* const to = p.part + (((int64_t)part * p.tq + sq.q0 + mine) * p.Hq + head) * (D + 4);
+#pragma unroll
+        for (int i = 0; i < D / 32; i++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) *(f32x4*)(to + 32 * i + 8 * e + 4 * hi) = f32x4{o[i][4 * e], o[i][4 * e + 1], o[i][4 * e + 2], o[i][4 * e + 3]};
+        if (hi == 0) {
+            to[D] = m;
+            to[D + 1] = den;
+        }
+        return;
+    }
     const float by = den == 0.0f ? 0.0f : 1.0f / den;
     if (p.lse && hi == 0 && mine < sq.nq) p.lse[(int64_t)(sq.q0 + mine) * p.Hq + head] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
     // the rows leave through LDS, in whole lines
@@ -505,10 +534,66 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
 #endif
 }
 
+// Joins the parts of the rows' keys: a wave for a head's row, its lanes side by side over the
+// columns and then over the parts.
+template <int D>
+__global__ __launch_bounds__(256) void k_join_parts(PParams p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int row = (int)(at / p.Hq), head = (int)(at - (int64_t)row * p.Hq);
+    if (row >= p.tq) return;
+    bool live = false;  // rows outside the sequences stay as they are
+    for (int base = 0; base < p.b && !live; base += 64) {
+        const int i = base + lane;
+        Seq s = {};
+        if (i < p.b) s = seq_at(p, i);
+        live = __any(row >= s.q0 && row < s.q0 + s.nq);
+    }
+    if (!live) return;
+    constexpr int CT = D / 4, GROUPS = 64 / CT;
+    const int c = (lane % CT) * 4, grp = lane / CT;
+    const int64_t stride = (int64_t)p.tq * p.Hq * (D + 4);
+    const float* const first = p.part + at * (D + 4);
+    const float own = lane < p.parts ? first[lane * stride + D] : neg_inf();
+    float den = lane < p.parts ? first[lane * stride + D + 1] : 0.0f;
+    float top = own;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) top = __builtin_fmaxf(top, __shfl_xor(top, o));
+    const float weight = top == neg_inf() ? 0.0f : __builtin_amdgcn_exp2f(own - top);
+    den *= weight;
+#pragma unroll
+    for (int o = 32; o; o >>= 1) den += __shfl_xor(den, o);
+    f32x4 acc = {};
+    for (int s0 = 0; s0 < p.parts; s0 += GROUPS) {  // (all lanes, since they hold the weights)
+        const int s = s0 + grp < p.parts ? s0 + grp : p.parts - 1;
+        const float a = __shfl(weight, s);
+        const f32x4 x = *(const f32x4*)(first + s * stride + c);
+        if (s0 + grp < p.parts) acc += a * x;
+    }
+#pragma unroll
+    for (int o = 32; o >= CT; o >>= 1)
+#pragma unroll
+        for (int j = 0; j < 4; j++) acc[j] += __shfl_xor(acc[j], o);
+    const float by = den == 0.0f ? 0.0f : 1.0f / den;
+    if (lane < CT && c < p.d)
+        *(u32x2*)(p.out + row * p.out_stride + head * p.d + c) = u32x2{pack_bf16x2(acc[0] * by, acc[1] * by), pack_bf16x2(acc[2] * by, acc[3] * by)};
+    if (p.lse && lane == 0) p.lse[at] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
+}
+
 template <int D, int NW, int SPLIT>
 hipError_t launch(PParams& p, hipStream_t st) {
     p.units = p.tq / (NW / SPLIT * 32) + p.b;  // tiles that no sequence has return at once
-    k_attn_prefill<D, NW, SPLIT><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, NW * kKeys * D * 2, st>>>(p);
+    k_attn_prefill<D, NW, SPLIT, false><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, NW * kKeys * D * 2, st>>>(p);
+    return hipGetLastError();
+}
+
+template <int D>
+hipError_t launch_parts(PParams& p, hipStream_t st) {
+    p.units = (p.tq / 128 + p.b) * p.parts;
+    k_attn_prefill<D, 4, 1, true><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 256, 4 * kKeys * D * 2, st>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    k_join_parts<D><<<dim3((unsigned)(((int64_t)p.tq * p.Hq + 3) / 4)), 256, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -524,13 +609,18 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     // The workgroup, by the average sequence (the lengths themselves are on the device), measured
     // with 32 heads of 128:
     //   * few tiles of rows for the CUs, or few and of unequal work (causal, no long prefix): 128
-    //     rows, the keys split (1 prompt of 1024: 21.9 us, 27.8 unsplit; of 2048: 44.6, 53.2; 16
-    //     rows behind 8000 keys: 94, 153; but 4 of 512: 27.9, 24.4; 4 of 300 behind 2000: 68, 66);
+    //     rows, the keys split (1 prompt of 1024: 21.9 us, 27.8 unsplit; of 2048: 44.6, 53.2; but 4 of 512: 27.9, 24.4; 4 of 300 behind 2000: 68, 66);
     //   * long ones: 256 rows (2 of 2048: 73.5 us, 80.2 with 128 rows; 4 of 300 behind 2000: 58,
     //     66; but 64 of 256: 126, 103);
     //   * others: 128 rows.  (Heads of 64, bound by the softmax's arithmetic, gain nothing from
     //     256 rows: 32 of 1500: 582 us, 421.)
-    const int64_t nq = a.tq / a.b, nk = a.tk / a.b, tiles = a.b * ((nq + 127) / 128) * a.q_heads;
+    const int64_t nq = a.tq / a.b > 1 ? a.tq / a.b : 1, nk = a.tk / a.b, tiles = a.b * ((nq + 127) / 128) * a.q_heads;
+    p.parts = (int)prefill_parts(a.tq, a.tk, a.q_heads, a.b);
+    p.part = (float*)a.ws;
+    if (p.part && p.parts > 1) {
+        if (a.d <= 64) return launch_parts<64>(p, st);
+        return a.d <= 128 ? launch_parts<128>(p, st) : launch_parts<256>(p, st);
+    }
     const bool split = (tiles <= 256 && nk >= 128) ||
                        (tiles <= 512 && nk >= 1024 && nq >= 128 && a.causal && 2 * a.tk <= 3 * a.tq);
     if (a.d <= 64) return split ? launch<64, 8, 2>(p, st) : launch<64, 4, 1>(p, st);

@@ -204,10 +204,23 @@ struct AttnPrefillArgs {
     uint16_t* out;
     float* lse;                // [tq, q_heads] or null
     const int32_t *cu_q, *cu_k;  // [b + 1]
+    void* ws;                  // prefill_parts sums of the rows, or null (one)
     int64_t b, tq, tk, q_heads, heads, d, q_stride, k_stride, v_stride, out_stride;
     float scale;
     int causal;
 };
+// Workgroups that share the keys of a tile of rows, by the average sequence: two a CU in all, of 256
+// keys or more, where the tiles are few and the keys many.  32 heads of 128, one sequence of 1 row
+// behind 8191 keys: 22.6 us, unshared 95.9; 128 behind 1920: 21.8, 31.1; 512 behind 7680: 87, 110; but
+// 700 behind 1300 (tiles for 192 CUs): 44, 33; 4 of 100 behind 1000: 30, 23 (not taken).
+constexpr int64_t kPrefillGroups = 512, kPrefillKeys = 256, kPrefillLong = 1536;
+inline int64_t prefill_parts(int64_t tq, int64_t tk, int64_t q_heads, int64_t b) {
+    const int64_t nq = tq / b > 1 ? tq / b : 1, nk = tk / b, tiles = b * ((nq + 127) / 128) * q_heads;
+    const int64_t most = kPrefillGroups / tiles, parts = nk / kPrefillKeys;
+    if (most < 4 || nk < kPrefillLong) return 1;
+    const int64_t n = parts < most ? parts : most;
+    return n < 64 ? n : 64;
+}
 hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st);
 
 // MX setting (32-element blocks, ue8m0 scales, no global scale).

@@ -87,7 +87,7 @@ def test_decode_validation(att, change, status):
     assert att._lib.nvfp4_attention_decode(*{**DEC, **change}.values()) == status
 
 
-PRE = dict(q=P, qs=2048, k=P, ks=512, v=P, vs=512, tq=9, tk=9, hq=16, heads=4, d=128, cq=P, ck=P, b=2, scale=0.1, causal=1, out=P, outs=2048, lse=None, stream=None)
+PRE = dict(q=P, qs=2048, k=P, ks=512, v=P, vs=512, tq=9, tk=9, hq=16, heads=4, d=128, cq=P, ck=P, b=2, scale=0.1, causal=1, out=P, outs=2048, lse=None, ws=None, wsb=0, stream=None)
 
 
 @pytest.mark.parametrize("change,status", [
@@ -128,3 +128,28 @@ def test_host_tensors_refused(att):
         att.nvfp4_attention_decode(x[:, None], kv, sf, gs, i.view(2, 1), i[0])
     with pytest.raises(ValueError):
         att.attention_prefill(x, x, x, i[0])
+
+
+def test_prefill_workspace_sizes(att, tmp_path):
+    """The binding asks for what the library checks, and the header's bound holds for it."""
+    src = tmp_path / "w.c"
+    src.write_text('#include <stdio.h>\n#include "nvfp4_attention.h"\n'
+                   'int main(void) { printf("%lld %lld %lld\\n", (long long)NVFP4_ATTENTION_PREFILL_WS_BYTES(64), '
+                   '(long long)NVFP4_ATTENTION_PREFILL_WS_BYTES(80), (long long)NVFP4_ATTENTION_PREFILL_WS_BYTES(256)); return 0; }\n')
+    exe = tmp_path / "w"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
+    bound = dict(zip((64, 80, 256), map(int, subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split())))
+    some = 0
+    for d in (64, 80, 256):
+        for q_heads in (1, 3, 32, 127, 128, 129):
+            for b in (1, 2, 7, 64):
+                for tq in (1, 16, 127, 128, 129, 300, 8191):
+                    for tk in (1, 1535, 1536, 20000, 1 << 20):
+                        need = att.attention_prefill_ws_bytes(tq, tk, q_heads, b, d)
+                        assert 0 <= need <= bound[d]
+                        if need and some < 200:
+                            some += 1
+                            a = {**PRE, "tq": tq, "tk": tk, "hq": q_heads, "heads": 1, "b": b, "d": d, "qs": q_heads * d, "outs": q_heads * d, "ks": d, "vs": d, "ws": P}
+                            assert att._lib.attention_prefill(*{**a, "wsb": need - 1}.values()) == SHAPE
+                            assert att._lib.attention_prefill(*{**a, "ws": P + 8, "wsb": need}.values()) == MISAL
+    assert some == 200

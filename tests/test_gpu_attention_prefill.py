@@ -159,3 +159,44 @@ def test_rows_past_4_gib(att):
     check(q, k, v, cu, cu, True, out)
     kept[:, 300:304] = out[first:]
     assert torch.equal(wide[first:], kept)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,q_heads,heads,d", [
+    ((1,), (8191,), 32, 8, 128), ((61,), (4157,), 6, 2, 64), ((129, 0, 7), (5000, 40, 64), 4, 4, 96), ((16, 1, 30), (2016, 3000, 900), 8, 8, 256), ((300,), (1600,), 16, 2, 80),
+    ((2000,), (2000,), 3, 1, 128), ((5, 3, 0, 2), (9000, 0, 2, 130), 7, 1, 64), ((130,), (16500,), 2, 1, 224),
+])
+def test_few_rows_behind_many_keys(att, lq, lk, q_heads, heads, d, causal):
+    """Keys that several workgroups share."""
+    say("prefill parts", lq, lk, q_heads, heads, d, causal)
+    q, k, v, cq, ck = inputs(lq, lk, q_heads, heads, d, sum(lk) + d)
+    need = att.attention_prefill_ws_bytes(len(q), len(k), q_heads, len(lq), d)
+    assert need > 0
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    out = att.attention_prefill(q, k, v, cq, ck, causal=causal, lse=lse, workspace=ws)
+    check(q, k, v, cq, ck, causal, out, lse)
+    wide = torch.full((len(q) + 9, q_heads + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    more = torch.cat([q[:0].new_zeros(5, q_heads, d), q, q[:0].new_zeros(4, q_heads, d)])
+    att.attention_prefill(more, k, v, cq + 5, ck, causal=causal, out=wide[:, 1:])
+    assert torch.equal(wide[5:len(q) + 5, 1:], out)
+    assert bool((wide[:5] == 7).all()) and bool((wide[len(q) + 5:] == 7).all()) and bool((wide[:, 0] == 7).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_shared_keys_behind_the_mask(att, bad, d):
+    say("prefill parts behind the mask", bad, d)
+    q, k, v, cq, ck = inputs((100, 20), (3000, 2500), 4, 2, d, 21)
+    assert att.attention_prefill_ws_bytes(len(q), len(k), 4, 2, d) > 0
+    clean = att.attention_prefill(q, k, v, cq, ck)
+    at = 2940   # rows up to 39 do not see it
+    for which in (k, v):
+        x = which.clone()
+        x[at, 0, 7] = bad
+        out = att.attention_prefill(q, x if which is k else k, x if which is v else v, cq, ck)
+        assert torch.equal(out[:40], clean[:40]) and torch.equal(out[100:], clean[100:]) and torch.equal(out[:, 2:], clean[:, 2:])
+        if which is v:
+            assert not bool(out[40:100, :2, 7].isfinite().any())
+            keep = torch.arange(d) != 7
+            assert torch.equal(out[40:100][..., keep], clean[40:100][..., keep])

@@ -211,6 +211,30 @@ def test_captured_prefill_replays(att):
         assert torch.equal(out, want), cut
 
 
+def test_captured_prefix_replays(att):
+    """The same where workgroups share the keys."""
+    say("attention prefix graph")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    q = torch.randn(150, 8, 128, device="cuda", generator=g).bfloat16()
+    k, v = (torch.randn(6000, 2, 128, device="cuda", generator=g).bfloat16() for _ in range(2))
+    need = att.attention_prefill_ws_bytes(150, 6000, 8, 2, 128)
+    assert need > 0
+    cu_q, cu_k = (torch.tensor([0, 70, n], dtype=torch.int32, device="cuda") for n in (150, 6000))
+    out, ws = torch.zeros_like(q), torch.empty(need, dtype=torch.uint8, device="cuda")
+    run = lambda: att.attention_prefill(q, k, v, cu_q, cu_k, out=out, workspace=ws)  # noqa: E731
+    graph = capture(run)
+    for a, b in ((70, 3000), (1, 5999), (149, 200), (0, 0), (150, 6000), (64, 1)):
+        cu_q[1], cu_k[1] = a, b
+        out.fill_(float("nan"))
+        run()
+        want = out.clone()
+        out.fill_(float("nan"))
+        ws.fill_(0xFF)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and bool(out.isfinite().all()), (a, b)
+
+
 def test_streams(att):
     """Calls on two streams at once, with a workspace each, and tensors made on another stream."""
     say("attention streams")
