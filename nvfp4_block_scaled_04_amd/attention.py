@@ -47,12 +47,16 @@ def attention_ws_bytes(b, d):
     return (8 * b + 255) // 256 * 256 + MAX_SLOTS * 64 * ((64 if d <= 64 else 128 if d <= 128 else 256) + 2)
 
 
-def attention_prefill_ws_bytes(tq, tk, q_heads, b, d):
+def attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d):
     """Workspace bytes that attention_prefill takes with these sizes: 0 where it needs none."""
-    most, keys = 512 // (b * ((max(1, tq // b) + 127) // 128) * q_heads), tk // b
-    if most < 4 or keys < 1536:
+    keys = tk // b
+    if keys < 1536:
         return 0
-    return min(keys // 256, most, 64) * tq * q_heads * ((64 if d <= 64 else 128 if d <= 128 else 256) + 4) * 4
+    n = max(1, tq // b)
+    tiles, packed = (n + 127) // 128 * q_heads, (n * (q_heads // heads) + 127) // 128 * heads
+    most = 512 // (b * (packed if 2 * packed <= tiles else tiles))
+    parts = min(keys // 256, most, 64, 66048 // (tq * q_heads)) if most >= 4 else 1
+    return 0 if parts < 2 else parts * tq * q_heads * ((64 if d <= 64 else 128 if d <= 128 else 256) + 4) * 4
 
 
 def _rows(x, name, i):
@@ -238,7 +242,7 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=Non
         out = torch.zeros(tq, q_heads, d, dtype=torch.bfloat16, device=q.device)
     else:
         _shaped(out, "out", q.shape)
-    ws, need = None, attention_prefill_ws_bytes(tq, tk, q_heads, b, d) if b > 0 and q_heads > 0 else 0
+    ws, need = None, attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d) if b > 0 and tq > 0 else 0
     if need:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

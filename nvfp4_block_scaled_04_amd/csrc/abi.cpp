@@ -636,7 +636,7 @@ int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_
         ((uintptr_t)cu_q & 3u) || ((uintptr_t)cu_k & 3u) || ((uintptr_t)lse & 3u))
         return NVFP4_MISALIGNED;
     if (workspace) {
-        const int64_t parts = nvfp4::prefill_parts(tq, tk, q_heads, b);
+        const int64_t parts = nvfp4::prefill_parts(tq, tk, q_heads, heads, b);
         if (parts > 1 && workspace_bytes < parts * tq * q_heads * ((d <= 64 ? 64 : d <= 128 ? 128 : 256) + 4) * 4)
             return NVFP4_BAD_SHAPE;
     }

@@ -38,7 +38,7 @@ struct PParams {
     const int32_t *cu_q, *cu_k;
     int64_t q_stride, k_stride, v_stride, out_stride;
     float c;                   // scale * log2(e)
-    int b, tq, tk, Hq, H, G, d, causal, units, parts;
+    int b, tq, tk, Hq, H, G, d, causal, parts;
 };
 
 __device__ __forceinline__ float neg_inf() { return -__builtin_inff(); }
@@ -59,17 +59,17 @@ __device__ __forceinline__ Seq seq_at(const PParams& p, int i) {
     return s;
 }
 
-// The sequence and tile of rows of unit `unit`; a sequence's last tiles, which have the
+// The sequence and tile of rows (`per` heads each) of unit `unit`; a sequence's last tiles, which have the
 // most keys, come first.
 template <int ROWS>
-__device__ __forceinline__ bool find_tile(const PParams& p, int unit, Seq& s, int& tile) {
+__device__ __forceinline__ bool find_tile(const PParams& p, int unit, int per, Seq& s, int& tile) {
     const int lane = threadIdx.x & 63;
     int before = 0;
     for (int base = 0; base < p.b; base += 64) {
         const int i = base + lane;
         Seq mine = {};
         if (i < p.b) mine = seq_at(p, i);
-        const int n = (mine.nq + ROWS - 1) / ROWS;
+        const int n = (mine.nq * per + ROWS - 1) / ROWS;
         const int sum = wave_scan(n);
         const uint64_t hit = __ballot(before + sum > unit);
         if (hit) {
@@ -112,7 +112,9 @@ __device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
 // SPLIT: 1: each wave has 32 rows of its own; 2: the second four waves have the rows of
 // the first, which take every other tile of keys, and the halves are joined at the end.
 // PARTS: p.parts workgroups share a tile's keys, in stretches, and k_join_parts joins them.
-template <int D, int NW, int SPLIT, bool PARTS>
+// PACK: the rows of all heads of a group lie in one tile, one after the other (row n is head n % G of
+// its token n / G), and share the keys that it reads.
+template <int D, int NW, int SPLIT, bool PARTS, bool PACK>
 __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
     constexpr int CH = D / 8;                   // chunks of a row
@@ -128,14 +130,15 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
 
     // Workgroups are dealt to the 8 XCDs in turn: where the heads split evenly, an XCD
     // has KV heads of its own, whose keys and values stay in its L2.
+    const int heads = PACK ? p.H : p.Hq, group = PACK ? p.G : 1;  // (heads of a row)
     int head, unit, part = 0;
     if (p.H % 8 == 0) {
-        const int per = p.Hq / 8, r = blockIdx.x >> 3;
+        const int per = heads / 8, r = blockIdx.x >> 3;
         head = (blockIdx.x & 7) * per + r % per;
         unit = r / per;
     } else {
-        head = blockIdx.x % p.Hq;
-        unit = blockIdx.x / p.Hq;
+        head = blockIdx.x % heads;
+        unit = blockIdx.x / heads;
     }
     if constexpr (PARTS) {
         part = unit % p.parts;
@@ -143,14 +146,17 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     }
     Seq sq;
     int tile;
-    if (!find_tile<ROWS>(p, unit, sq, tile)) return;
-    const int kv = head / p.G;
+    if (!find_tile<ROWS>(p, unit, group, sq, tile)) return;
+    const int kv = PACK ? head : head / p.G;
+    if (PACK) head *= p.G;                      // the row's first
+    const int nrows = sq.nq * group;
+    auto token = [&](int row) { return PACK ? row / p.G : row; };
     const int back = sq.nk - sq.nq;             // row i sees the keys up to i + back
     const int row0 = tile * ROWS;
     int keys = sq.nk;                           // that any row of the tile sees
     if (p.causal) {
-        const int last = row0 + ROWS < sq.nq ? row0 + ROWS : sq.nq;
-        keys = clamp_to(last + back, 0, sq.nk);
+        const int last = row0 + ROWS < nrows ? row0 + ROWS : nrows;
+        keys = clamp_to(token(last - 1) + 1 + back, 0, sq.nk);
     }
 
     const uint16_t* const kb = p.k + (int64_t)sq.k0 * p.k_stride + kv * p.d;
@@ -194,19 +200,21 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     const int first = row0 + gw * 32;
     const uint32_t q_lds = GW == 8 ? 4 * TILE + gw * (TILE / 2) : (gw < 2 ? TILE : 3 * TILE) + (gw & 1) * (TILE / 2);
     {
-        const int rows = sq.nq - first;  // those behind the sequence come as zeros
-        const u32x4 rs = raw_buffer(p.q + (int64_t)(sq.q0 + first) * p.q_stride + head * p.d,
-                                    rows > 0 ? (uint32_t)(((rows < 32 ? rows - 1 : 31) * p.q_stride + p.d) * 2) : 0u);
+        const int rows = nrows - first;  // those behind the sequence come as zeros
+        const int t0 = token(first), t1 = token(first + (rows < 32 ? rows : 32) - 1);
+        const u32x4 rs = raw_buffer(p.q + (int64_t)(sq.q0 + t0) * p.q_stride + head * p.d,
+                                    rows > 0 ? (uint32_t)(((t1 - t0) * p.q_stride + group * p.d) * 2) : 0u);
 #pragma unroll
         for (int i = 0; i < 32 * CH / 64; i++) {
             const int piece = i * 64 + lane;
             const int r = piece / CH, c = (piece % CH) ^ swizzle_k<D>(r);
-            load_to_lds(rs, c * 8 < p.d ? (uint32_t)(r * (int)p.q_stride + c * 8) * 2u : 0xFFFFFFF0u,
+            const int t = PACK ? token(first + r) - t0 : r, h = PACK ? first + r - (t + t0) * p.G : 0;
+            load_to_lds(rs, c * 8 < p.d && (!PACK || r < rows) ? (uint32_t)(t * (int)p.q_stride + h * p.d + c * 8) * 2u : 0xFFFFFFF0u,
                         __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + q_lds + i * 1024));
         }
     }
     const int mine = first + l32;
-    const int end = mine >= sq.nq ? 0 : p.causal ? clamp_to(mine + back + 1, 0, sq.nk) : sq.nk;  // keys below it are seen
+    const int end = mine >= nrows ? 0 : p.causal ? clamp_to(token(mine) + back + 1, 0, sq.nk) : sq.nk;  // keys below it are seen
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     bf16x8 q[D / 16];
 #pragma unroll
@@ -218,10 +226,10 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     // keys that all rows of the wave see, and that any sees (rows past the sequence count as its last)
     int all = sq.nk, any = sq.nk;
     if (p.causal) {
-        all = clamp_to(first + back + 1, 0, sq.nk);
-        any = clamp_to((first + 32 < sq.nq ? first + 32 : sq.nq) + back, 0, sq.nk);
+        all = clamp_to(token(first) + back + 1, 0, sq.nk);
+        any = clamp_to(token((first + 32 < nrows ? first + 32 : nrows) - 1) + 1 + back, 0, sq.nk);
     }
-    if (first >= sq.nq) any = 0;
+    if (first >= nrows) any = 0;
 
     f32x16 o[D / 32];
     float m = neg_inf(), l = 0.0f;
@@ -502,8 +510,9 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     }
     const float den = l + __shfl_xor(l, 32);
     if constexpr (PARTS) {
-        if (mine >= sq.nq) return;
-        float* const to = p.part + (((int64_t)part * p.tq + sq.q0 + mine) * p.Hq + head) * (D + 4);
+        if (mine >= nrows) return;
+        const int t = token(mine);
+        float* const to = p.part + (((int64_t)part * p.tq + sq.q0 + t) * p.Hq + head + (mine - t * group)) * (D + 4);
 #pragma unroll
         for (int i = 0; i < D / 32; i++)
 #pragma unroll
@@ -515,7 +524,8 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         return;
     }
     const float by = den == 0.0f ? 0.0f : 1.0f / den;
-    if (p.lse && hi == 0 && mine < sq.nq) p.lse[(int64_t)(sq.q0 + mine) * p.Hq + head] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
+    if (p.lse && hi == 0 && mine < nrows)
+        p.lse[(int64_t)(sq.q0 + token(mine)) * p.Hq + head + (mine - token(mine) * group)] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
     // the rows leave through LDS, in whole lines
     lds_u8* const mo = lds + gw * (TILE / 2);
 #pragma unroll
@@ -529,7 +539,9 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         const int piece = i * 64 + lane;
         const int r = piece / CH, c = piece % CH;
         const u32x4 w = *(const __attribute__((address_space(3))) u32x4*)(mo + r * D * 2 + (c ^ swizzle_k<D>(r)) * 16);
-        if (first + r < sq.nq && c * 8 < p.d) *(u32x4*)(p.out + (int64_t)(sq.q0 + first + r) * p.out_stride + head * p.d + c * 8) = w;
+        const int t = token(first + r);
+        if (first + r < nrows && c * 8 < p.d)
+            *(u32x4*)(p.out + (int64_t)(sq.q0 + t) * p.out_stride + (head + (first + r - t * group)) * p.d + c * 8) = w;
     }
 #endif
 }
@@ -582,15 +594,23 @@ __global__ __launch_bounds__(256) void k_join_parts(PParams p) {
 
 template <int D, int NW, int SPLIT>
 hipError_t launch(PParams& p, hipStream_t st) {
-    p.units = p.tq / (NW / SPLIT * 32) + p.b;  // tiles that no sequence has return at once
-    k_attn_prefill<D, NW, SPLIT, false><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 64 * NW, NW * kKeys * D * 2, st>>>(p);
+    const int64_t units = p.tq / (NW / SPLIT * 32) + p.b;  // tiles that no sequence has return at once
+    k_attn_prefill<D, NW, SPLIT, false, false><<<dim3((unsigned)(units * p.Hq)), 64 * NW, NW * kKeys * D * 2, st>>>(p);
     return hipGetLastError();
 }
 
+// The groups' rows in one tile (pack), p.parts workgroups to a tile.
 template <int D>
-hipError_t launch_parts(PParams& p, hipStream_t st) {
-    p.units = (p.tq / 128 + p.b) * p.parts;
-    k_attn_prefill<D, 4, 1, true><<<dim3((unsigned)((int64_t)p.units * p.Hq)), 256, 4 * kKeys * D * 2, st>>>(p);
+hipError_t launch_few(PParams& p, bool pack, hipStream_t st) {
+    const int64_t units = ((int64_t)p.tq * (pack ? p.G : 1) / 128 + p.b) * p.parts;
+    const dim3 grid((unsigned)(units * (pack ? p.H : p.Hq)));
+    constexpr int lds = 4 * kKeys * D * 2;
+    if (p.parts == 1) {
+        k_attn_prefill<D, 4, 1, false, true><<<grid, 256, lds, st>>>(p);
+        return hipGetLastError();
+    }
+    if (pack) k_attn_prefill<D, 4, 1, true, true><<<grid, 256, lds, st>>>(p);
+    else k_attn_prefill<D, 4, 1, true, false><<<grid, 256, lds, st>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_join_parts<D><<<dim3((unsigned)(((int64_t)p.tq * p.Hq + 3) / 4)), 256, 0, st>>>(p);
@@ -615,11 +635,17 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     //   * others: 128 rows.  (Heads of 64, bound by the softmax's arithmetic, gain nothing from
     //     256 rows: 32 of 1500: 582 us, 421.)
     const int64_t nq = a.tq / a.b > 1 ? a.tq / a.b : 1, nk = a.tk / a.b, tiles = a.b * ((nq + 127) / 128) * a.q_heads;
-    p.parts = (int)prefill_parts(a.tq, a.tk, a.q_heads, a.b);
+    // The heads of a group share a tile where that halves the tiles, and these are more than the CUs
+    // or the keys are shared too (32 / 8 heads of 128: 128 of 16 rows 20.0 us, 51 apart; 64 of 30
+    // behind 500 keys 39, 81; 16 of 16 behind 4000 60, 99; but one of 61 8.1, 7.2; 8 of 32 behind
+    // 1000 26.6, 21.4: a wave beside it slows the chain of a tile's keys).
+    const bool packs = prefill_packs(a.tq, a.q_heads, a.heads, a.b);
     p.part = (float*)a.ws;
-    if (p.part && p.parts > 1) {
-        if (a.d <= 64) return launch_parts<64>(p, st);
-        return a.d <= 128 ? launch_parts<128>(p, st) : launch_parts<256>(p, st);
+    p.parts = p.part ? (int)prefill_parts(a.tq, a.tk, a.q_heads, a.heads, a.b) : 1;
+    const bool pack = packs && (p.parts > 1 || tiles > 256);
+    if (pack || p.parts > 1) {
+        if (a.d <= 64) return launch_few<64>(p, pack, st);
+        return a.d <= 128 ? launch_few<128>(p, pack, st) : launch_few<256>(p, pack, st);
     }
     const bool split = (tiles <= 256 && nk >= 128) ||
                        (tiles <= 512 && nk >= 1024 && nq >= 128 && a.causal && 2 * a.tk <= 3 * a.tq);

@@ -214,12 +214,23 @@ struct AttnPrefillArgs {
 // behind 8191 keys: 22.6 us, unshared 95.9; 128 behind 1920: 21.8, 31.1; 512 behind 7680: 87, 110; but
 // 700 behind 1300 (tiles for 192 CUs): 44, 33; 4 of 100 behind 1000: 30, 23 (not taken).
 constexpr int64_t kPrefillGroups = 512, kPrefillKeys = 256, kPrefillLong = 1536;
-inline int64_t prefill_parts(int64_t tq, int64_t tk, int64_t q_heads, int64_t b) {
-    const int64_t nq = tq / b > 1 ? tq / b : 1, nk = tk / b, tiles = b * ((nq + 127) / 128) * q_heads;
-    const int64_t most = kPrefillGroups / tiles, parts = nk / kPrefillKeys;
+constexpr int64_t kPrefillRows = 512 * 129;  // of the parts together
+inline int64_t prefill_tiles(int64_t tq, int64_t per, int64_t heads, int64_t b) {
+    return b * (((tq / b > 1 ? tq / b : 1) * per + 127) / 128) * heads;
+}
+// Whether the heads of a group in one tile at least halve the tiles.
+inline bool prefill_packs(int64_t tq, int64_t q_heads, int64_t heads, int64_t b) {
+    return 2 * prefill_tiles(tq, q_heads / heads, heads, b) <= prefill_tiles(tq, 1, q_heads, b);
+}
+inline int64_t prefill_parts(int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t b) {
+    const int64_t nk = tk / b;
+    const int64_t most = kPrefillGroups / (prefill_packs(tq, q_heads, heads, b) ? prefill_tiles(tq, q_heads / heads, heads, b)
+                                                                                : prefill_tiles(tq, 1, q_heads, b));
     if (most < 4 || nk < kPrefillLong) return 1;
-    const int64_t n = parts < most ? parts : most;
-    return n < 64 ? n : 64;
+    int64_t n = nk / kPrefillKeys < most ? nk / kPrefillKeys : most;
+    if (n > 64) n = 64;
+    const int64_t room = kPrefillRows / (tq * q_heads);  // of the workspace
+    return n < room ? n : room > 1 ? room : 1;
 }
 hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st);
 

@@ -141,15 +141,16 @@ def test_prefill_workspace_sizes(att, tmp_path):
     bound = dict(zip((64, 80, 256), map(int, subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split())))
     some = 0
     for d in (64, 80, 256):
-        for q_heads in (1, 3, 32, 127, 128, 129):
+        for q_heads, heads in ((1, 1), (3, 3), (32, 8), (32, 32), (40, 1), (127, 127), (128, 2), (128, 128), (129, 3)):
             for b in (1, 2, 7, 64):
                 for tq in (1, 16, 127, 128, 129, 300, 8191):
                     for tk in (1, 1535, 1536, 20000, 1 << 20):
-                        need = att.attention_prefill_ws_bytes(tq, tk, q_heads, b, d)
+                        need = att.attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d)
                         assert 0 <= need <= bound[d]
                         if need and some < 200:
                             some += 1
-                            a = {**PRE, "tq": tq, "tk": tk, "hq": q_heads, "heads": 1, "b": b, "d": d, "qs": q_heads * d, "outs": q_heads * d, "ks": d, "vs": d, "ws": P}
+                            a = {**PRE, "tq": tq, "tk": tk, "hq": q_heads, "heads": heads, "b": b, "d": d, "qs": q_heads * d, "outs": q_heads * d, "ks": heads * d, "vs": heads * d,
+                                 "ws": P}
                             assert att._lib.attention_prefill(*{**a, "wsb": need - 1}.values()) == SHAPE
                             assert att._lib.attention_prefill(*{**a, "ws": P + 8, "wsb": need}.values()) == MISAL
     assert some == 200

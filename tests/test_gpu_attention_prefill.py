@@ -170,7 +170,7 @@ def test_few_rows_behind_many_keys(att, lq, lk, q_heads, heads, d, causal):
     """Keys that several workgroups share."""
     say("prefill parts", lq, lk, q_heads, heads, d, causal)
     q, k, v, cq, ck = inputs(lq, lk, q_heads, heads, d, sum(lk) + d)
-    need = att.attention_prefill_ws_bytes(len(q), len(k), q_heads, len(lq), d)
+    need = att.attention_prefill_ws_bytes(len(q), len(k), q_heads, heads, len(lq), d)
     assert need > 0
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")
     lse = torch.full(q.shape[:2], 7.0, device="cuda")
@@ -188,7 +188,7 @@ def test_few_rows_behind_many_keys(att, lq, lk, q_heads, heads, d, causal):
 def test_shared_keys_behind_the_mask(att, bad, d):
     say("prefill parts behind the mask", bad, d)
     q, k, v, cq, ck = inputs((100, 20), (3000, 2500), 4, 2, d, 21)
-    assert att.attention_prefill_ws_bytes(len(q), len(k), 4, 2, d) > 0
+    assert att.attention_prefill_ws_bytes(len(q), len(k), 4, 2, 2, d) > 0
     clean = att.attention_prefill(q, k, v, cq, ck)
     at = 2940   # rows up to 39 do not see it
     for which in (k, v):
@@ -200,3 +200,41 @@ def test_shared_keys_behind_the_mask(att, bad, d):
             assert not bool(out[40:100, :2, 7].isfinite().any())
             keep = torch.arange(d) != 7
             assert torch.equal(out[40:100][..., keep], clean[40:100][..., keep])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,q_heads,heads,d", [
+    ((16, 1, 0, 7) * 16, (16, 1, 0, 7) * 16, 32, 8, 128), ((30, 5) * 20, (530, 5) * 20, 21, 3, 64), ((1,) * 64, (1,) * 64, 40, 4, 80), ((33, 20, 61) * 8, (33, 200, 61) * 8, 30, 2, 96),
+    ((3,) * 40, (70,) * 40, 14, 1, 256), ((300,) + (0,) * 60, (300,) + (9,) * 60, 35, 7, 128),
+])
+def test_heads_that_share_a_tile(att, lq, lk, q_heads, heads, d, causal):
+    """Many short sequences with grouped heads."""
+    say("prefill packed", lq[:4], lk[:4], len(lq), q_heads, heads, d, causal)
+    q, k, v, cq, ck = inputs(lq, lk, q_heads, heads, d, sum(lk) + d)
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    wide = torch.full((len(q) + 9, q_heads + 1, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    more = torch.zeros(len(q) + 9, q_heads + 3, d, dtype=torch.bfloat16, device="cuda")
+    more[5:len(q) + 5, 2:-1] = q
+    att.attention_prefill(more[:, 2:-1], k, v, cq + 5, ck, causal=causal, out=wide[:, 1:])
+    out = att.attention_prefill(q, k, v, cq, ck, causal=causal, lse=lse)
+    check(q, k, v, cq, ck, causal, out, lse)
+    assert torch.equal(wide[5:len(q) + 5, 1:], out)
+    assert bool((wide[:5] == 7).all()) and bool((wide[len(q) + 5:] == 7).all()) and bool((wide[:, 0] == 7).all())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_shared_tiles_behind_the_mask(att, bad):
+    say("prefill packed behind the mask", bad)
+    lens = (14,) * 40
+    q, k, v, cq, ck = inputs(lens, lens, 32, 8, 128, 22)
+    clean = att.attention_prefill(q, k, v, cq, ck)
+    at = 14 * 7 + 5
+    for which in (k, v):
+        x = which.clone()
+        x[at, 3, 7] = bad
+        out = att.attention_prefill(q, x if which is k else k, x if which is v else v, cq, ck)
+        keep = torch.ones(560, 32, 128, dtype=torch.bool)
+        keep[at:14 * 8, 12:16, 7 if which is v else slice(None)] = False
+        assert torch.equal(out[keep], clean[keep])
+        if which is v:
+            assert not bool(out[at:14 * 8, 12:16, 7].isfinite().any())

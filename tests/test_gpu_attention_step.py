@@ -217,7 +217,7 @@ def test_captured_prefix_replays(att):
     g = torch.Generator(device="cuda").manual_seed(4)
     q = torch.randn(150, 8, 128, device="cuda", generator=g).bfloat16()
     k, v = (torch.randn(6000, 2, 128, device="cuda", generator=g).bfloat16() for _ in range(2))
-    need = att.attention_prefill_ws_bytes(150, 6000, 8, 2, 128)
+    need = att.attention_prefill_ws_bytes(150, 6000, 8, 2, 2, 128)
     assert need > 0
     cu_q, cu_k = (torch.tensor([0, 70, n], dtype=torch.int32, device="cuda") for n in (150, 6000))
     out, ws = torch.zeros_like(q), torch.empty(need, dtype=torch.uint8, device="cuda")
