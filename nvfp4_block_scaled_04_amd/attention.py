@@ -54,7 +54,7 @@ def attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d):
         return 0
     n = max(1, tq // b)
     tiles, packed = (n + 127) // 128 * q_heads, (n * (q_heads // heads) + 127) // 128 * heads
-    most = 512 // (b * (packed if 2 * packed <= tiles else tiles))
+    most = 512 // (b * (packed if 20 * packed <= 19 * tiles else tiles))
     parts = min(keys // 256, most, 64, 66048 // (tq * q_heads)) if most >= 4 else 1
     return 0 if parts < 2 else parts * tq * q_heads * ((64 if d <= 64 else 128 if d <= 128 else 256) + 4) * 4
 

@@ -635,10 +635,10 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     //   * others: 128 rows.  (Heads of 64, bound by the softmax's arithmetic, gain nothing from
     //     256 rows: 32 of 1500: 582 us, 421.)
     const int64_t nq = a.tq / a.b > 1 ? a.tq / a.b : 1, nk = a.tk / a.b, tiles = a.b * ((nq + 127) / 128) * a.q_heads;
-    // The heads of a group share a tile where that halves the tiles, and these are more than the CUs
-    // or the keys are shared too (32 / 8 heads of 128: 128 of 16 rows 20.0 us, 51 apart; 64 of 30
-    // behind 500 keys 39, 81; 16 of 16 behind 4000 60, 99; but one of 61 8.1, 7.2; 8 of 32 behind
-    // 1000 26.6, 21.4: a wave beside it slows the chain of a tile's keys).
+    // The heads of a group share a tile where that saves tiles, and these are more than the CUs or the
+    // keys are shared too (32 / 8 heads of 128: 128 of 16 rows 20.0 us, 51 apart; 64 of 30 behind
+    // 500 keys 39, 81; 16 of 16 behind 4000 60, 99; 8 of 520 behind 1000 115, 121; but one of 61 8.1,
+    // 7.2; 8 of 32 behind 1000 26.6, 21.4: a wave beside it slows the chain of a tile's keys).
     const bool packs = prefill_packs(a.tq, a.q_heads, a.heads, a.b);
     p.part = (float*)a.ws;
     p.parts = p.part ? (int)prefill_parts(a.tq, a.tk, a.q_heads, a.heads, a.b) : 1;

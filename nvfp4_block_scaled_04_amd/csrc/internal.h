@@ -218,9 +218,9 @@ constexpr int64_t kPrefillRows = 512 * 129;  // of the parts together
 inline int64_t prefill_tiles(int64_t tq, int64_t per, int64_t heads, int64_t b) {
     return b * (((tq / b > 1 ? tq / b : 1) * per + 127) / 128) * heads;
 }
-// Whether the heads of a group in one tile at least halve the tiles.
+// Whether the heads of a group in one tile save one tile in twenty or more.
 inline bool prefill_packs(int64_t tq, int64_t q_heads, int64_t heads, int64_t b) {
-    return 2 * prefill_tiles(tq, q_heads / heads, heads, b) <= prefill_tiles(tq, 1, q_heads, b);
+    return 20 * prefill_tiles(tq, q_heads / heads, heads, b) <= 19 * prefill_tiles(tq, 1, q_heads, b);
 }
 inline int64_t prefill_parts(int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t b) {
     const int64_t nk = tk / b;
