@@ -671,7 +671,7 @@ hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     p.page_log2 = __builtin_ctzll((unsigned long long)a.page);
     // More rows than one product takes: two share a read of the cache where that is much (by the
     // table's size; heads of 256 have no registers for it).  4 x 8 rows over 32 sequences of
-    // 8192: 79 us, 114 apart; 3 x 7 rows over 7 to 2001: 12.8, 10.8 (not taken).
+    // 8192: 79 us, 114 apart; 4 x 8 over 8 of 8192: 29.6, 34.5; 4 x 8 over 16 of 1024: 16.4, 14.3 (not taken).
     const bool two = p.T * p.G > kRows && a.d <= 128 && a.b * a.heads * a.table_pages * a.page >= kAttnShared;
     const int rows = two ? 2 * kRows : kRows;
     p.row_tiles = (p.T * p.G + rows - 1) / rows;

@@ -183,7 +183,7 @@ constexpr int64_t kAttnPartsNarrow = 1024;  // the same for heads of up to 64
 constexpr int64_t kAttnLong = 4096;       // tokens of a long part, of a sequence twice as long
 constexpr int64_t kAttnMinPart = 256;     // fewest tokens of a part
 constexpr int64_t kAttnWhole = 1024;      // tokens of a sequence (by the table) that is not split
-constexpr int64_t kAttnShared = (int64_t)1 << 20;  // tokens times KV heads from which rows share a read
+constexpr int64_t kAttnShared = (int64_t)1 << 18;  // tokens times KV heads from which rows share a read
 struct AttnDecodeArgs {
     const uint16_t* q;         // [b, t, q_heads, d], q_stride elements from token to token
     const uint8_t *kv, *kv_sf;
