@@ -49,9 +49,9 @@ def attention_ws_bytes(b, d):
 
 def attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d):
     """Workspace bytes that attention_prefill takes with these sizes: 0 where it needs none."""
-    keys = tk // b
-    if keys < 1536:
+    if min(tq, q_heads, heads, b) < 1 or tk // b < 1536:
         return 0
+    keys = tk // b
     n = max(1, tq // b)
     tiles, packed = (n + 127) // 128 * q_heads, (n * (q_heads // heads) + 127) // 128 * heads
     most = 512 // (b * (packed if 20 * packed <= 19 * tiles else tiles))
@@ -242,7 +242,7 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=Non
         out = torch.zeros(tq, q_heads, d, dtype=torch.bfloat16, device=q.device)
     else:
         _shaped(out, "out", q.shape)
-    ws, need = None, attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d) if b > 0 and tq > 0 else 0
+    ws, need = None, attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d)
     if need:
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)

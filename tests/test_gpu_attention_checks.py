@@ -98,6 +98,21 @@ def test_decode_takes_rows_of_a_projection(att):
     assert torch.equal(att.nvfp4_attention_decode(one, kv, sf, gs, table[:1], lens[:1]), att.nvfp4_attention_decode(one.contiguous(), kv, sf, gs, table[:1], lens[:1]))
 
 
+def test_prefill_without_rows(att):
+    q, k, cu = z(5, 2, 64), z(5, 2, 64), torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+    refused(att.attention_prefill, z(0, 2, 64), k, k, cu, error=RuntimeError)
+    refused(att.attention_prefill, q, z(0, 2, 64), z(0, 2, 64), cu, error=RuntimeError)
+    refused(att.attention_prefill, z(5, 0, 64), k, k, cu, error=RuntimeError)
+    refused(att.attention_prefill, q, z(5, 0, 64), z(5, 0, 64), cu)
+    refused(att.attention_prefill, q, k, k, cu[:1], error=RuntimeError)
+    long = z(4000, 2, 64)
+    assert att.attention_prefill_ws_bytes(5, 4000, 2, 2, 1, 64) > 0
+    cu_k = torch.tensor([0, 4000], dtype=torch.int32, device="cuda")
+    refused(att.attention_prefill, q, long, long, cu, cu_k, workspace=u8(100))
+    refused(att.attention_prefill, q, long, long, cu, cu_k, workspace=torch.empty(1 << 26, dtype=torch.uint8))
+    refused(att.attention_prefill, q, long, long, cu, cu_k, workspace=u8(1 << 26)[4:], error=RuntimeError)
+
+
 def test_prefill(att):
     q, k, cu = z(6, 4, 64), z(6, 2, 64), torch.tensor([0, 2, 6], dtype=torch.int32, device="cuda")
     att.attention_prefill(q, k, k, cu)
