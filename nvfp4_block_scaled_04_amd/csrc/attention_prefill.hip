@@ -28,7 +28,13 @@ namespace nvfp4 {
 
 namespace {
 
-constexpr int kKeys = 64;  // keys of a tile
+// LDS: two tiles of K and two of V for each of SPLIT groups of waves, the queries behind them where
+// eight waves have rows of their own.  With 32 keys a wave's queries are as large as a tile, and
+// four waves take a tile more.
+template <int D, int KEYS, int NW, int SPLIT>
+constexpr int lds_bytes() {
+    return 4 * SPLIT * KEYS * D * 2 + (NW / SPLIT == 8 ? 8 * 64 * D : KEYS == 32 ? 64 * D : 0);
+}
 
 struct PParams {
     const uint16_t *q, *k, *v;
@@ -114,15 +120,19 @@ __device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
 // PARTS: p.parts workgroups share a tile's keys, in stretches, and k_join_parts joins them.
 // PACK: the rows of all heads of a group lie in one tile, one after the other (row n is head n % G of
 // its token n / G), and share the keys that it reads.
-template <int D, int NW, int SPLIT, bool PARTS, bool PACK>
-__global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PParams p) {
+// KEYS: of a tile.  With 32, two workgroups of heads of 256 share a CU (512 registers and 160 KB),
+// with 64, one has them alone.
+template <int D, int KEYS, int NW, int SPLIT, bool PARTS, bool PACK>
+__global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_prefill(PParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
+    constexpr int NS = KEYS / 32, NP = KEYS / 16;
     constexpr int CH = D / 8;                   // chunks of a row
-    constexpr int TILE = kKeys * D * 2;         // bytes of a tile of K (of V)
+    constexpr int TILE = KEYS * D * 2;          // bytes of a tile of K (of V)
+    constexpr int OWN = 32 * D * 2;             // of a wave's 32 rows
     constexpr int GW = NW / SPLIT;              // waves of a group, which share tiles
-    constexpr int LOADS = kKeys * CH / (64 * GW);  // of a lane, of K (of V)
+    constexpr int LOADS = KEYS * CH / (64 * GW);  // of a lane, of K (of V)
     constexpr int ROWS = GW * 32;
-    extern __shared__ __align__(16) uint8_t smem[];  // two tiles of K, two of V a group (and the queries of a group of eight)
+    extern __shared__ __align__(16) uint8_t smem[];  // lds_bytes
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int grp = SPLIT == 1 ? 0 : wave / GW, gw = SPLIT == 1 ? wave : wave % GW;
@@ -175,30 +185,30 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         off_v[i] = cv * 8 < p.d ? (uint32_t)(r * (int)p.v_stride + cv * 8) * 2u : 0xFFFFFFF0u;
     }
     // the group's n-th tile of keys
-    int tile0 = 0, tile1 = (keys + kKeys - 1) / kKeys;
+    int tile0 = 0, tile1 = (keys + KEYS - 1) / KEYS;
     if constexpr (PARTS) {
         const int all_tiles = tile1;
         tile0 = (int)((int64_t)all_tiles * part / p.parts);
         tile1 = (int)((int64_t)all_tiles * (part + 1) / p.parts);
     }
-    auto key_of = [&](int n) { return PARTS ? (tile0 + n) * kKeys : (n * SPLIT + grp) * kKeys; };
+    auto key_of = [&](int n) { return PARTS ? (tile0 + n) * KEYS : (n * SPLIT + grp) * KEYS; };
     auto stage = [&](const uint16_t* base, int64_t stride, const uint32_t (&off)[LOADS], int key0, uint32_t to) {
-        const int rows = sq.nk - key0 < kKeys ? sq.nk - key0 : kKeys;  // at least 1; later rows come as zeros
+        const int rows = sq.nk - key0 < KEYS ? sq.nk - key0 : KEYS;  // at least 1; later rows come as zeros
         const u32x4 rs = raw_buffer(base + key0 * stride, (uint32_t)(((rows - 1) * stride + p.d) * 2));
 #pragma unroll
         for (int i = 0; i < LOADS; i++) load_to_lds(rs, off[i], __builtin_amdgcn_readfirstlane(lds0 + to + i * GW * 1024));
     };
     auto stage_k = [&](int n) { stage(kb, p.k_stride, off_k, key_of(n), (n & 1) * TILE); };
     auto stage_v = [&](int n) { stage(vb, p.v_stride, off_v, key_of(n), (2 + (n & 1)) * TILE); };
-    auto tiles_of = [&](int upto) { return (upto + kKeys * (SPLIT - grp) - 1) / (kKeys * SPLIT); };  // of the group, of the keys below
-    const int tiles = PARTS ? tile1 - tile0 : tiles_of(keys), steps = PARTS ? tiles : (keys + kKeys * SPLIT - 1) / (kKeys * SPLIT);
+    auto tiles_of = [&](int upto) { return (upto + KEYS * (SPLIT - grp) - 1) / (KEYS * SPLIT); };  // of the group, of the keys below
+    const int tiles = PARTS ? tile1 - tile0 : tiles_of(keys), steps = PARTS ? tiles : (keys + KEYS * SPLIT - 1) / (KEYS * SPLIT);
     if (tiles > 0) stage_k(0);
 
     // The wave's 32 rows of q go through LDS too, in whole lines (fragments straight from memory
     // would touch every line four times): behind the tiles, or, with four waves a
-    // group, where its second tiles of K and V will be.
+    // group, where tiles after the first of K will be.
     const int first = row0 + gw * 32;
-    const uint32_t q_lds = GW == 8 ? 4 * TILE + gw * (TILE / 2) : (gw < 2 ? TILE : 3 * TILE) + (gw & 1) * (TILE / 2);
+    lds_u8* const mine_q = lds + (GW == 8 ? 4 * TILE + gw * OWN : KEYS == 32 ? (1 + gw) * TILE : (gw < 2 ? TILE : 3 * TILE) + (gw & 1) * OWN);
     {
         const int rows = nrows - first;  // those behind the sequence come as zeros
         const int t0 = token(first), t1 = token(first + (rows < 32 ? rows : 32) - 1);
@@ -210,7 +220,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
             const int r = piece / CH, c = (piece % CH) ^ swizzle_k<D>(r);
             const int t = PACK ? token(first + r) - t0 : r, h = PACK ? first + r - (t + t0) * p.G : 0;
             load_to_lds(rs, c * 8 < p.d && (!PACK || r < rows) ? (uint32_t)(t * (int)p.q_stride + h * p.d + c * 8) * 2u : 0xFFFFFFF0u,
-                        __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds + q_lds + i * 1024));
+                        __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)mine_q + i * 1024));
         }
     }
     const int mine = first + l32;
@@ -219,10 +229,12 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     bf16x8 q[D / 16];
 #pragma unroll
     for (int s = 0; s < D / 16; s++)
-        q[s] = *(const __attribute__((address_space(3))) bf16x8*)(lds + q_lds + l32 * D * 2 + ((2 * s + hi) ^ swizzle_k<D>(l32)) * 16);
+        q[s] = *(const __attribute__((address_space(3))) bf16x8*)(mine_q + l32 * D * 2 + ((2 * s + hi) ^ swizzle_k<D>(l32)) * 16);
     // (waited for here, not at every use in the loop)
 #pragma unroll
     for (int s = 0; s < D / 16; s++) asm volatile("" : "+v"(q[s]));
+    // (some lie where the first tile of V goes)
+    if constexpr (KEYS == 32) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     // keys that all rows of the wave see, and that any sees (rows past the sequence count as its last)
     int all = sq.nk, any = sq.nk;
     if (p.causal) {
@@ -238,9 +250,10 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
 
     // a lane's V rows: 4 hi + (lane & 15) / 4 (+ 8 i)
     const int vr = (lane & 15) >> 2;
-    int vat[D / 32];
+    constexpr int VA = D / 32 < 4 ? D / 32 : 4;  // (the swizzle stays within 16 chunks)
+    int vat[VA];
 #pragma unroll
-    for (int i = 0; i < D / 32; i++) {
+    for (int i = 0; i < VA; i++) {
         const int c = 4 * i + 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
         vat[i] = (4 * hi + vr) * D * 2 + (c ^ swizzle_v<D>(vr)) * 16 + (lane & 1) * 8;
     }
@@ -248,30 +261,30 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     typedef short s16x4 __attribute__((ext_vector_type(4)));
 
     // S^T of tile n: s[j] the keys 32 j .. of it
-    auto scores = [&](int n, f32x16 (&s)[2]) {
+    auto scores = [&](int n, f32x16 (&s)[NS]) {
         lds_u8* const kt = lds + (n & 1) * TILE;
 #pragma unroll
-        for (int j = 0; j < 2; j++) {
+        for (int j = 0; j < NS; j++) {
             s[j] = f32x16{};
 #pragma unroll
             for (int i = 0; i < D / 16; i++) {
                 const int r = 32 * j + l32;
-                const bf16x8 a = *(const __attribute__((address_space(3))) bf16x8*)(kt + r * D * 2 + ((2 * i + hi) ^ swizzle_k<D>(r)) * 16);
+                const bf16x8 a = *(const __attribute__((address_space(3))) bf16x8*)(kt + r * D * 2 + ((2 * (i % 8) + hi) ^ swizzle_k<D>(r)) * 16 + i / 8 * 256);
                 s[j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, q[i], s[j], 0, 0, 0);
             }
         }
     };
     // its probabilities: pf[f] the keys 16 f .. of it
-    auto soften = [&](int n, f32x16 (&s)[2], bf16x8 (&pf)[4]) {
+    auto soften = [&](int n, f32x16 (&s)[NS], bf16x8 (&pf)[NP]) {
         const int key0 = key_of(n);
-        if (key0 + kKeys > all) {
+        if (key0 + KEYS > all) {
 #pragma unroll
-            for (int e = 0; e < 32; e++)
+            for (int e = 0; e < 16 * NS; e++)
                 if (key0 + 32 * (e >> 4) + 8 * ((e & 15) >> 2) + 4 * hi + (e & 3) >= end) s[e >> 4][e & 15] = neg_inf();
         }
         float top = s[0][0];
 #pragma unroll
-        for (int e = 1; e < 32; e++) top = __builtin_fmaxf(top, s[e >> 4][e & 15]);
+        for (int e = 1; e < 16 * NS; e++) top = __builtin_fmaxf(top, s[e >> 4][e & 15]);
         top *= p.c;
         // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the
         // row alone, so that its bits do not depend on the rows beside it)
@@ -287,7 +300,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         const float base = m == neg_inf() ? 0.0f : m;
         float sum = 0.0f;
 #pragma unroll
-        for (int f = 0; f < 4; f++) {
+        for (int f = 0; f < NP; f++) {
             u32x4 w;
 #pragma unroll
             for (int e = 0; e < 4; e++) {
@@ -301,15 +314,15 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         l += sum;
     };
     auto v_frag = [&](lds_u8* vt, int f, int i) {  // V^T of the keys 16 f .. and the columns 32 i ..
-        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + 16 * f * D * 2));
-        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i] + (16 * f + 8) * D * 2));
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i % VA] + i / VA * 256 + 16 * f * D * 2));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(vt + vat[i % VA] + i / VA * 256 + (16 * f + 8) * D * 2));
         const bf16x4 x = __builtin_bit_cast(bf16x4, a), y = __builtin_bit_cast(bf16x4, b);
         return bf16x8{x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
     };
-    auto add_values = [&](int n, const bf16x8 (&pf)[4]) {
+    auto add_values = [&](int n, const bf16x8 (&pf)[NP]) {
         lds_u8* const vt = lds + (2 + (n & 1)) * TILE;
 #pragma unroll
-        for (int f = 0; f < 4; f++)
+        for (int f = 0; f < NP; f++)
 #pragma unroll
             for (int i = 0; i < D / 32; i++) o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v_frag(vt, f, i), pf[f], o[i], 0, 0, 0);
     };
@@ -327,8 +340,8 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
             }
             const int key0 = key_of(n);
             if (key0 >= any) continue;
-            f32x16 s[2];
-            bf16x8 pf[4];
+            f32x16 s[NS];
+            bf16x8 pf[NP];
             scores(n, s);
             soften(n, s, pf);
             if constexpr (!CAREFUL) {
@@ -336,7 +349,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
             } else {
                 lds_u8* const vt = lds + (2 + (n & 1)) * TILE;
 #pragma unroll 1
-                for (int f = 0; f < 4; f++)
+                for (int f = 0; f < NP; f++)
 #pragma unroll
                     for (int i = 0; i < D / 32; i++) {
                         u32x4 w = __builtin_bit_cast(u32x4, v_frag(vt, f, i));
@@ -346,7 +359,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
                             if ((w[e] & 0x7F800000u) == 0x7F800000u) w[e] &= 0xFFFFu;
                         }
                         bf16x8 pv = pf[0];
-                        pv = f == 1 ? pf[1] : f == 2 ? pf[2] : f == 3 ? pf[3] : pv;
+                        pv = f == 1 ? pf[1] : f == 2 ? pf[2 % NP] : f == 3 ? pf[3 % NP] : pv;
                         o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, w), pv, o[i], 0, 0, 0);
                     }
                 u16x2 big = {};
@@ -358,7 +371,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
                 }
                 if (__any((big[0] > big[1] ? big[0] : big[1]) >= 0x7F80)) {
 #pragma unroll 1
-                    for (int r = 0; r < kKeys; r++)
+                    for (int r = 0; r < KEYS; r++)
 #pragma unroll
                         for (int i = 0; i < D / 32; i++)
 #pragma unroll
@@ -381,8 +394,8 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     auto sweep_paired = [&]() {
         const bool behind = wave >= NW / 2;
         const int own = tiles_of(any);  // tiles that the wave sees
-        f32x16 s[2];
-        bf16x8 pf[4];
+        f32x16 s[NS];
+        bf16x8 pf[NP];
         auto end_half = [&](auto LANDED) {
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (LANDED) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -397,7 +410,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         auto products = [&](int n) {
             add_values(n - 1, pf);
             scores(n, s);
-            constexpr int NV = D / 32 * 4, NK = D / 8;  // products of each
+            constexpr int NV = D / 32 * NP, NK = D / 16 * NS;  // products of each
             __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);
 #pragma unroll
             for (int i = 0; i < NV - 4; i++) {
@@ -470,7 +483,15 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
         for (int i = 0; i < D / 32; i++)
 #pragma unroll
             for (int e = 0; e < 16; e++) bad |= (f_bits(o[i][e]) & 0x7F800000u) == 0x7F800000u;
-        if (__syncthreads_or(bad)) {
+        __attribute__((address_space(3))) int* const flags = (__attribute__((address_space(3))) int*)smem;
+        bad = __any(bad);
+        __syncthreads();
+        if (lane == 0) flags[wave] = bad;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NW; i++) bad |= flags[i] != 0;
+        if (bad) {
+            __syncthreads();
             m = neg_inf();
             l = 0.0f;
 #pragma unroll
@@ -527,7 +548,7 @@ __global__ __launch_bounds__(64 * NW, D <= 128 ? 2 : 1) void k_attn_prefill(PPar
     if (p.lse && hi == 0 && mine < nrows)
         p.lse[(int64_t)(sq.q0 + token(mine)) * p.Hq + head + (mine - token(mine) * group)] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
     // the rows leave through LDS, in whole lines
-    lds_u8* const mo = lds + gw * (TILE / 2);
+    lds_u8* const mo = lds + gw * OWN;
 #pragma unroll
     for (int c = 0; c < D / 32; c++)
 #pragma unroll
@@ -592,10 +613,10 @@ __global__ __launch_bounds__(256) void k_join_parts(PParams p) {
     if (p.lse && lane == 0) p.lse[at] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
 }
 
-template <int D, int NW, int SPLIT>
+template <int D, int KEYS, int NW, int SPLIT>
 hipError_t launch(PParams& p, hipStream_t st) {
     const int64_t units = p.tq / (NW / SPLIT * 32) + p.b;  // tiles that no sequence has return at once
-    k_attn_prefill<D, NW, SPLIT, false, false><<<dim3((unsigned)(units * p.Hq)), 64 * NW, NW * kKeys * D * 2, st>>>(p);
+    k_attn_prefill<D, KEYS, NW, SPLIT, false, false><<<dim3((unsigned)(units * p.Hq)), 64 * NW, lds_bytes<D, KEYS, NW, SPLIT>(), st>>>(p);
     return hipGetLastError();
 }
 
@@ -604,13 +625,13 @@ template <int D>
 hipError_t launch_few(PParams& p, bool pack, hipStream_t st) {
     const int64_t units = ((int64_t)p.tq * (pack ? p.G : 1) / 128 + p.b) * p.parts;
     const dim3 grid((unsigned)(units * (pack ? p.H : p.Hq)));
-    constexpr int lds = 4 * kKeys * D * 2;
+    constexpr int KEYS = D <= 128 ? 64 : 32, lds = lds_bytes<D, KEYS, 4, 1>();
     if (p.parts == 1) {
-        k_attn_prefill<D, 4, 1, false, true><<<grid, 256, lds, st>>>(p);
+        k_attn_prefill<D, KEYS, 4, 1, false, true><<<grid, 256, lds, st>>>(p);
         return hipGetLastError();
     }
-    if (pack) k_attn_prefill<D, 4, 1, true, true><<<grid, 256, lds, st>>>(p);
-    else k_attn_prefill<D, 4, 1, true, false><<<grid, 256, lds, st>>>(p);
+    if (pack) k_attn_prefill<D, KEYS, 4, 1, true, true><<<grid, 256, lds, st>>>(p);
+    else k_attn_prefill<D, KEYS, 4, 1, true, false><<<grid, 256, lds, st>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_join_parts<D><<<dim3((unsigned)(((int64_t)p.tq * p.Hq + 3) / 4)), 256, 0, st>>>(p);
@@ -649,12 +670,14 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     }
     const bool split = (tiles <= 256 && nk >= 128) ||
                        (tiles <= 512 && nk >= 1024 && nq >= 128 && a.causal && 2 * a.tk <= 3 * a.tq);
-    if (a.d <= 64) return split ? launch<64, 8, 2>(p, st) : launch<64, 4, 1>(p, st);
+    if (a.d <= 64) return split ? launch<64, 64, 8, 2>(p, st) : launch<64, 64, 4, 1>(p, st);
     if (a.d <= 128) {
-        if (split) return launch<128, 8, 2>(p, st);
-        return nq >= 256 && nk >= 1024 ? launch<128, 8, 1>(p, st) : launch<128, 4, 1>(p, st);
+        if (split) return launch<128, 64, 8, 2>(p, st);
+        return nq >= 256 && nk >= 1024 ? launch<128, 64, 8, 1>(p, st) : launch<128, 64, 4, 1>(p, st);
     }
-    return launch<256, 4, 1>(p, st);
+    // Heads of 256: two workgroups a CU where there are more than one (16 / 8 heads: a prompt of 8192
+    // 523 us, 757 with one; 64 of 128 62, 79; but 2 of 66 behind 506, 35 / 7 heads, 37.6, 33.2).
+    return tiles > 256 ? launch<256, 32, 4, 1>(p, st) : launch<256, 64, 4, 1>(p, st);
 }
 
 }  // namespace nvfp4

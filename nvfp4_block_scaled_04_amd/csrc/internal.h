@@ -210,7 +210,7 @@ struct AttnPrefillArgs {
     int causal;
 };
 // Workgroups that share the keys of a tile of rows, by the average sequence: two a CU in all, of 256
-// keys or more, where the tiles are few and the keys many.  32 heads of 128, one sequence of 1 row
+// keys or more, where the tiles are few and the keys many.  32 / 8 heads of 128, one sequence of 1 row
 // behind 8191 keys: 19.3 us, unshared 95.9; 128 behind 1920: 21.8, 31.1; 512 behind 7680: 87, 110; but
 // 700 behind 1300 (tiles for 192 CUs): 44, 33; 4 of 100 behind 1000: 30, 23 (not taken).
 constexpr int64_t kPrefillGroups = 512, kPrefillKeys = 256, kPrefillLong = 1536;

@@ -56,6 +56,7 @@ def inputs(lq, lk, q_heads, heads, d, seed):
     # many tiles: 256 rows a workgroup (long), 128 (short), heads of 64, 96 and 256
     ((2300, 1900), (2300, 1900), 16, 2, 128), ((1100, 1, 1990), (1190, 1500, 1990), 24, 4, 96), ((300,) * 9, (300,) * 9, 16, 8, 128), ((257, 2, 900), (257, 2, 900), 64, 8, 64),
     ((513, 320), (513, 1320), 40, 8, 128), ((200, 300), (200, 300), 8, 4, 256), ((7, 16), (5000, 3111), 8, 2, 128), ((1,), (4097,), 16, 4, 64),
+    ((31, 32, 33, 1), (31, 96, 65, 64), 4, 4, 256), ((700, 129), (1000, 129), 6, 2, 256), ((100,), (3001,), 32, 32, 208), ((1300,), (1300,), 8, 8, 256),
 ])
 def test_prefill(att, lq, lk, q_heads, heads, d, causal):
     say("prefill", lq, lk, q_heads, heads, d, causal)
