@@ -189,10 +189,10 @@ def nvfp4_kv_read(slots, kv_gs, kv, kv_sf, k=None, v=None):
 
 def nvfp4_attention_decode(q, kv, kv_sf, kv_gs, block_table, lengths, scale=None, out=None, lse=None, workspace=None):
     """Attention of t new tokens a sequence over the cache, which holds them already.  q: [b, t,
-    q_heads, d] bf16 (any stride from token to token); block_table: [b, pages of a sequence] int32; lengths: [b] int32, the new
-    tokens included; scale: d ** -0.5 when None; lse: None or [b, t, q_heads] fp32, written.
-    Token j sees the positions below lengths - (t - 1 - j).  workspace: attention_ws_bytes(b, d)
-    bytes.  Returns out [b, t, q_heads, d] bf16."""
+    q_heads, d] bf16 (any stride from token to token); block_table: [b, pages of a sequence] int32;
+    lengths: [b] int32, the new tokens included; scale: d ** -0.5 when None; lse: None or [b, t,
+    q_heads] fp32, written.  Token j sees the positions below lengths - (t - 1 - j).  workspace:
+    attention_ws_bytes(b, d) bytes.  Returns out [b, t, q_heads, d] bf16."""
     i, pages, heads, page, d, kv_at, sf_at, gs_at = _cache(kv, kv_sf, kv_gs)
     if _gpu(q, "q") != i or q.dtype is not BF16[0] or q.dim() != 4 or q.shape[3] != d or heads < 1 or q.shape[2] % heads:
         raise ValueError(f"q must be bf16 [b, t, a multiple of {heads}, {d}] on GPU {i}, got {q.dtype} {tuple(q.shape)} on {q.device}")

@@ -5,10 +5,10 @@
 //   s_j = q_i . k_j, p_j = 2^(s_j * c - m), out_i = sum p_j v_j / sum p_j,
 // c = scale * log2(e), one pass over the keys with the running maximum m and sum.
 //
-// A workgroup of four or eight waves takes 128 or 256 rows of one head, a wave 32 of them (see
-// launch_attention_prefill).  64 keys and values at a time go straight from memory into LDS (two
-// buffers), swizzled at their source so that neither product's reads collide in the banks.  Both products run
-// on 32x32x16 bf16 MFMAs, transposed:
+// A workgroup of four or eight waves takes 128 or 256 rows of one head (or of the heads of a group),
+// a wave 32 of them (see launch_attention_prefill).  64 keys and values at a time (32 for most heads
+// of 256) go straight from memory into LDS (two buffers), swizzled at their source so that neither
+// product's reads collide in the banks.  Both products run on 32x32x16 bf16 MFMAs, transposed:
 //   S^T[key, row] = K Q^T: a lane owns one row (and half of the keys), so the softmax
 //   needs one exchange between lanes, and only where the maximum moves;
 //   O^T[column, row] = V^T P^T: V^T comes from transposing LDS reads, in the order of
