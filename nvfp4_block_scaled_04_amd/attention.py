@@ -60,13 +60,14 @@ def attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d):
 
 
 def _rows(x, name, i):
-    """A bf16 tensor [t, heads, d] on GPU i whose heads lie one after the other: its token stride."""
+    """A bf16 tensor [t, heads, d] on GPU i whose heads lie one after the other: t, heads, d and its
+    token stride."""
     try:
         if x.get_device() == i and x.dtype is BF16[0]:
             t, heads, d = x.shape
             s0, s1, s2 = x.stride()
             if (s2 == 1 or d == 1) and (s1 == d or heads == 1):
-                return s0 if t > 1 else heads * d
+                return t, heads, d, s0 if t > 1 else heads * d
     except (AttributeError, ValueError, TypeError):
         pass
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
@@ -102,6 +103,14 @@ def _bytes(t, name, numel, i):
     return _dev(t, name, BYTES, numel, torch.device("cuda", i)).data_ptr()
 
 
+def _rows_as(x, name, i, shape):
+    """The token stride of such a tensor of that shape."""
+    t, heads, d, stride = _rows(x, name, i)
+    if (t, heads, d) != shape:
+        raise ValueError(f"{name} must be {shape}, got {tuple(x.shape)}")
+    return stride
+
+
 def _shaped(out, name, shape):
     if getattr(out, "shape", None) != shape:
         raise ValueError(f"{name} must be {tuple(shape)}, got {getattr(out, 'shape', type(out))}")
@@ -128,19 +137,17 @@ def rope_axes(x, positions, inv_freq, sections, interleaved=False, out=None):
     each axis; interleaved: pairs are (2i, 2i + 1) instead of (i, i + pairs).  Returns out (x
     itself for in place), with the elements past the pairs copied."""
     i = _gpu(x, "x")
-    stride = _rows(x, "x", i)
-    t, heads, d = x.shape
+    t, heads, d, stride = _rows(x, "x", i)
     axes = len(sections)
     if axes > MAX_AXES:
         raise ValueError(f"at most {MAX_AXES} axes, got {axes}")
     if out is None:
         out = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    elif out is not x:
-        _shaped(out, "out", x.shape)
+    out_stride = stride if out is x else _rows_as(out, "out", i, (t, heads, d))
     pos = _at(positions, "positions", I32, axes * t, i)
     if positions.shape != (axes, t):
         raise ValueError(f"positions must be [{axes}, {t}], got {tuple(positions.shape)}")
-    _call(_lib.rope_axes, "rope_axes", i, x.data_ptr(), stride, out.data_ptr(), _rows(out, "out", i), t, heads, d, pos,
+    _call(_lib.rope_axes, "rope_axes", i, x.data_ptr(), stride, out.data_ptr(), out_stride, t, heads, d, pos,
           _at(inv_freq, "inv_freq", F32, sum(sections), i), _Sections(*sections), axes, 1 if interleaved else 0)
     return out
 
@@ -148,9 +155,10 @@ def rope_axes(x, positions, inv_freq, sections, interleaved=False, out=None):
 def _cache(kv, kv_sf, kv_gs):
     """(GPU, pages, heads, page, d) of a cache and its pointers."""
     i = _gpu(kv, "kv")
-    if kv.dim() != 5 or kv.shape[1] != 2:
-        raise ValueError(f"kv must be [pages, 2, heads, page, d/2], got {tuple(kv.shape)}")
-    pages, _, heads, page, half = kv.shape
+    shape = kv.shape
+    if len(shape) != 5 or shape[1] != 2:
+        raise ValueError(f"kv must be [pages, 2, heads, page, d/2], got {tuple(shape)}")
+    pages, _, heads, page, half = shape
     at = _bytes(kv, "kv", 0, i)
     if not isinstance(kv_sf, torch.Tensor) or kv_sf.shape != (pages, 2, heads, half // 8, page):
         raise ValueError(f"kv_sf must be [{pages}, 2, {heads}, {half // 8}, {page}] beside kv {tuple(kv.shape)}, got "
@@ -163,10 +171,10 @@ def nvfp4_kv_append(k, v, slots, kv_gs, kv, kv_sf):
     kv: [pages, 2, heads, page, d/2] bytes, kv_sf: [pages, 2, heads, d/16, page] bytes, kv_gs: [2]
     fp32 global scales of keys and values."""
     i, pages, heads, page, d, kv_at, sf_at, gs_at = _cache(kv, kv_sf, kv_gs)
-    ks, vs = _rows(k, "k", i), _rows(v, "v", i)
-    t = k.shape[0]
-    _shaped(k, "k", (t, heads, d))
-    _shaped(v, "v", (t, heads, d))
+    t, k_heads, k_d, ks = _rows(k, "k", i)
+    if k_heads != heads or k_d != d:
+        _shaped(k, "k", (t, heads, d))
+    vs = _rows_as(v, "v", i, (t, heads, d))
     _call(_lib.nvfp4_kv_append, "nvfp4_kv_append", i, k.data_ptr(), ks, v.data_ptr(), vs, t, heads, d,
           _at(slots, "slots", I32, t, i), gs_at, kv_at, sf_at, pages, page)
 
@@ -179,9 +187,7 @@ def nvfp4_kv_read(slots, kv_gs, kv, kv_sf, k=None, v=None):
     t = slots.numel()
     k = torch.zeros(t, heads, d, dtype=torch.bfloat16, device=kv.device) if k is None else k
     v = torch.zeros(t, heads, d, dtype=torch.bfloat16, device=kv.device) if v is None else v
-    ks, vs = _rows(k, "k", i), _rows(v, "v", i)
-    _shaped(k, "k", (t, heads, d))
-    _shaped(v, "v", (t, heads, d))
+    ks, vs = _rows_as(k, "k", i, (t, heads, d)), _rows_as(v, "v", i, (t, heads, d))
     _call(_lib.nvfp4_kv_read, "nvfp4_kv_read", i, kv_at, sf_at, gs_at, pages, page, slots_at, t, heads, d, k.data_ptr(),
           ks, v.data_ptr(), vs)
     return k, v
@@ -228,20 +234,20 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=Non
     token to token; cu_q, cu_k: [b + 1] int32, where each sequence's rows and keys start (cu_k =
     cu_q when None); causal: row r of n rows and m keys sees the keys up to r + m - n, else all;
     scale: d ** -0.5 when None; lse: None or [tq, q_heads] fp32, written; workspace:
-    attention_prefill_ws_bytes bytes, where few rows meet many keys.  Returns out [tq, q_heads, d] bf16; rows outside all sequences are left as they were (zeros in an out allocated here)."""
+    attention_prefill_ws_bytes bytes, where few rows meet many keys.  Returns out [tq, q_heads, d]
+    bf16; rows outside all sequences are left as they were (zeros in an out allocated here)."""
     i = _gpu(q, "q")
-    qs, ks, vs = _rows(q, "q", i), _rows(k, "k", i), _rows(v, "v", i)
-    tq, q_heads, d = q.shape
-    tk, heads, dk = k.shape
-    if dk != d or v.shape != k.shape or heads < 1 or q_heads % heads:
+    tq, q_heads, d, qs = _rows(q, "q", i)
+    tk, heads, dk, ks = _rows(k, "k", i)
+    tv, v_heads, dv, vs = _rows(v, "v", i)
+    if dk != d or tv != tk or v_heads != heads or dv != d or heads < 1 or q_heads % heads:
         raise ValueError(f"k / v must be [tk, heads, {d}] with heads a divisor of {q_heads}, got {tuple(k.shape)} / "
                          f"{tuple(v.shape)}")
     cu_at = _at(cu_q, "cu_q", I32, 0, i)
     b = cu_q.numel() - 1
     if out is None:
         out = torch.zeros(tq, q_heads, d, dtype=torch.bfloat16, device=q.device)
-    else:
-        _shaped(out, "out", q.shape)
+    out_stride = _rows_as(out, "out", i, (tq, q_heads, d))
     ws, need = None, attention_prefill_ws_bytes(tq, tk, q_heads, heads, b, d)
     if need:
         if workspace is None:
@@ -249,6 +255,6 @@ def attention_prefill(q, k, v, cu_q, cu_k=None, causal=True, scale=None, out=Non
         ws, need = _bytes(workspace, "workspace", need, i), workspace.numel()
     _call(_lib.attention_prefill, "attention_prefill", i, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, tq, tk, q_heads,
           heads, d, cu_at, cu_at if cu_k is None else _at(cu_k, "cu_k", I32, b + 1, i), b, d ** -0.5 if scale is None else scale,
-          1 if causal else 0, out.data_ptr(), _rows(out, "out", i), None if lse is None else _at(lse, "lse", F32, tq * q_heads, i),
+          1 if causal else 0, out.data_ptr(), out_stride, None if lse is None else _at(lse, "lse", F32, tq * q_heads, i),
           ws, need)
     return out
