@@ -4,7 +4,7 @@
 //
 // All three are bound by their bytes.  A thread reads 32 bytes (16 bf16, of K and of V
 // for the cache), works on them in registers and writes them, neighbours side by side:
-// 20280 tokens of 16 x 128 turn at 6.0 TB/s (read and written, 83 us), 8003 rows of K
+// 20280 tokens of 48 x 128 turn at 6.0 TB/s (read and written, 83 us), 8003 rows of K
 // and V of 8 x 128 are quantized into the cache or read back in 19 us (4.1 TB/s).
 #include "gemm_common.h"
 #include "internal.h"
@@ -20,7 +20,7 @@ constexpr int kRopeAngles = 2048;  // (cos, sin) pairs of a workgroup's tokens
 constexpr int64_t kRopeStream = (int64_t)128 << 20;
 
 // Threads of a workgroup: one that streams has less to wait for at its barrier if it is small
-// (20280 tokens of 16 x 128 at 128 / 256 threads: 82.9 / 86.5 us), where few tokens fill part of
+// (20280 tokens of 48 x 128 at 128 / 256 threads: 82.9 / 86.5 us), where few tokens fill part of
 // the card their angles want more threads (16 tokens: 3.8 / 3.5 us).
 constexpr int rope_threads(bool stream) { return stream ? 128 : 256; }
 
