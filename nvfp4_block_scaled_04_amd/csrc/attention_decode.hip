@@ -474,11 +474,21 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? (
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) o[t][i] *= a;
             }
-            const float base = m[t] == neg_inf() ? 0.0f : m[t];
+            float base = m[t] == neg_inf() ? 0.0f : m[t], by = to_x[t];
+            if (__any(__builtin_fabsf(base) >= kFarScore)) {  // (by the row alone too)
+                const bool far = __builtin_fabsf(base) >= kFarScore;
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const float v = x[t][i >> 2][i & 3];
+                    x[t][i >> 2][i & 3] = far ? far_score(v, by, base) : v;
+                }
+                base = far ? 0.0f : base;
+                by = far ? 1.0f : by;
+            }
             float sum = 0.0f;
 #pragma unroll
             for (int j = 0; j < 16; j++) {
-                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][j & 3][j >> 2], to_x[t], -base));
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][j & 3][j >> 2], by, -base));
                 sum += e;
                 pf[t][j >> 3][j & 7] = (_Float16)e;
             }

@@ -274,8 +274,9 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
             }
         }
     };
-    // its probabilities: pf[f] the keys 16 f .. of it
-    auto soften = [&](int n, f32x16 (&s)[NS], bf16x8 (&pf)[NP]) {
+    // its probabilities: pf[f] the keys 16 f .. of it.  FAR: by far_score in the rows whose scores are
+    // that large.
+    auto soften = [&](auto FAR, int n, f32x16 (&s)[NS], bf16x8 (&pf)[NP]) {
         const int key0 = key_of(n);
         if (key0 + KEYS > all) {
 #pragma unroll
@@ -297,15 +298,22 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
 #pragma unroll
             for (int i = 0; i < D / 32; i++) o[i] *= a;
         }
-        const float base = m == neg_inf() ? 0.0f : m;
+        float base = m == neg_inf() ? 0.0f : m, c = p.c;
+        if constexpr (FAR) {
+            const bool far = __builtin_fabsf(base) >= kFarScore;
+#pragma unroll
+            for (int e = 0; e < 16 * NS; e++) s[e >> 4][e & 15] = far ? far_score(s[e >> 4][e & 15], c, base) : s[e >> 4][e & 15];
+            base = far ? 0.0f : base;
+            c = far ? 1.0f : c;
+        }
         float sum = 0.0f;
 #pragma unroll
         for (int f = 0; f < NP; f++) {
             u32x4 w;
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + 2 * e], p.c, -base));
-                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + 2 * e + 1], p.c, -base));
+                const float p0 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + 2 * e], c, -base));
+                const float p1 = __builtin_amdgcn_exp2f(__builtin_fmaf(s[f >> 1][8 * (f & 1) + 2 * e + 1], c, -base));
                 sum += p0 + p1;
                 w[e] = pack_bf16x2(p0, p1);
             }
@@ -329,7 +337,7 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
 
     // One pass over the keys, each wave by itself between the tiles' barriers.  CAREFUL: a value
     // that is not finite behind a mask, which 0 times it would carry into the rows that do not
-    // see it, is kept out of the product and handed to the rows that do.
+    // see it, is kept out of the product and handed to the rows that do; scores past kFarScore.
     auto sweep = [&](auto CAREFUL) {
         if (tiles > 0) stage_v(0);
         for (int n = 0; n < steps; n++) {
@@ -343,7 +351,7 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
             f32x16 s[NS];
             bf16x8 pf[NP];
             scores(n, s);
-            soften(n, s, pf);
+            soften(CAREFUL, n, s, pf);
             if constexpr (!CAREFUL) {
                 add_values(n, pf);
             } else {
@@ -437,13 +445,13 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
             if (!behind) {
                 scores(0, s);
                 end_half(std::false_type{});
-                soften(0, s, pf);
+                soften(std::false_type{}, 0, s, pf);
                 end_half(std::true_type{});
                 for (n = 1; n < own; n++) {
                     feed(n);
                     products(n);
                     end_half(std::false_type{});
-                    soften(n, s, pf);
+                    soften(std::false_type{}, n, s, pf);
                     end_half(std::true_type{});
                 }
                 feed(n);
@@ -455,13 +463,13 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
                 end_half(std::true_type{});
                 for (n = 1; n < own; n++) {
                     feed(n);
-                    soften(n - 1, s, pf);
+                    soften(std::false_type{}, n - 1, s, pf);
                     end_half(std::false_type{});
                     products(n);
                     end_half(std::true_type{});
                 }
                 feed(n);
-                soften(n - 1, s, pf);
+                soften(std::false_type{}, n - 1, s, pf);
                 end_half(std::false_type{});
                 add_values(n - 1, pf);
             }
@@ -477,28 +485,28 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
     if constexpr (NW == 8) sweep_paired();
     else sweep(std::false_type{});
 
-    if (p.causal) {
-        bool bad = false;
+    // Again, carefully, where an output is not finite or a row's scores are so large that their maximum's
+    // rounding counts (a maximum that was as far below has left nothing, or what is not finite).
+    bool again = m != neg_inf() && __builtin_fabsf(m) >= kFarScore;
 #pragma unroll
-        for (int i = 0; i < D / 32; i++)
+    for (int i = 0; i < D / 32; i++)
 #pragma unroll
-            for (int e = 0; e < 16; e++) bad |= (f_bits(o[i][e]) & 0x7F800000u) == 0x7F800000u;
-        __attribute__((address_space(3))) int* const flags = (__attribute__((address_space(3))) int*)smem;
-        bad = __any(bad);
+        for (int e = 0; e < 16; e++) again |= (f_bits(o[i][e]) & 0x7F800000u) == 0x7F800000u;
+    __attribute__((address_space(3))) int* const flags = (__attribute__((address_space(3))) int*)smem;
+    again = __any(again);
+    __syncthreads();
+    if (lane == 0) flags[wave] = again;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NW; i++) again |= flags[i] != 0;
+    if (again) {
         __syncthreads();
-        if (lane == 0) flags[wave] = bad;
-        __syncthreads();
+        m = neg_inf();
+        l = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NW; i++) bad |= flags[i] != 0;
-        if (bad) {
-            __syncthreads();
-            m = neg_inf();
-            l = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 32; i++) o[i] = f32x16{};
-            if (tiles > 0) stage_k(0);
-            sweep(std::true_type{});
-        }
+        for (int i = 0; i < D / 32; i++) o[i] = f32x16{};
+        if (tiles > 0) stage_k(0);
+        sweep(std::true_type{});
     }
 
     __syncthreads();  // the tiles have been read

@@ -77,6 +77,16 @@ __device__ __forceinline__ int wave_scan(int v) {
     return v;
 }
 
+// Softmax, scores (times log2 e) of this size on: a row's maximum m = fp32(s * c) is rounded, and the
+// fused fma(s, c, -m) shows by how much, up to half a unit in its last place: 2^-4 here, but 2^4 at
+// 2^28 and 2^7 at 2^31, powers of two that leave fp16 and fp32.  Such scores take far_score, whose
+// product is rounded as the maximum's was.
+constexpr float kFarScore = 0x1p20f;
+__device__ __forceinline__ float far_score(float s, float c, float m) {
+#pragma clang fp contract(off)
+    return s * c - m;
+}
+
 // fp32(x / 6) for x >= 0, correctly rounded, without the division sequence:
 // q0 = x * RN(1/6), then one correction step with the exact FMA residual
 // r = x - q0 * 6 (Markstein's correction for division by a constant).

@@ -1,0 +1,84 @@
+"""Attention whose scores, probabilities or values lie many binades apart, against its 64-bit form."""
+import pytest
+import torch
+
+import attention_ref as A
+from gpu_util import say
+from serving_ref import gamma
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def att():
+    if not torch.cuda.is_available():
+        pytest.fail("no GPU visible")
+    from nvfp4_block_scaled_04_amd import attention
+    return attention
+
+
+def one_key_takes_all(q, k, v, scale, seen, out, lse):
+    """Scores so large that fp32 holds them to whole units or worse.  Where the largest (or several equal
+    ones) lead by more than their error, the others' weights are zero and what comes out is the leaders'
+    mean, its probabilities and itself rounded to bf16 at worst (2^-8 each, and 2^-20 of sums); anywhere else it lies among
+    the values.  Returns the number of rows with such a lead."""
+    x = (q @ k.t() * scale).masked_fill(~seen, -float("inf"))
+    dx = (gamma(q.shape[1]) * (q.abs() @ k.abs().t()) * scale + 2.0 ** -21 * x.abs()).masked_fill(~seen, 0).amax(-1)
+    top = x.amax(-1, keepdim=True)
+    first = x >= top * (1 - 2.0 ** -40 * top.sign())   # (equal but for the 64-bit sums' own rounding)
+    lead = top[:, 0] - x.masked_fill(first, -float("inf")).amax(-1) > 2 * dx + 100
+    ref = first.double() @ v / first.sum(-1, keepdim=True)
+    size = first.double() @ v.abs() / first.sum(-1, keepdim=True)
+    assert bool(((out.double() - ref).abs() <= size * (2.0 ** -7 + 2.0 ** -15))[lead].all())
+    assert bool((out.double().abs() <= v.abs().amax(0) * (1 + 2.0 ** -6)).all())
+    assert bool(((lse.double() - (top[:, 0] + first.sum(-1).log())).abs() <= dx + 2.0 ** -21 * top[:, 0].abs() + 1)[lead].all())
+    return int(lead.sum())
+
+
+@pytest.mark.parametrize("power", [20, 27, 31, 60])
+@pytest.mark.parametrize("n,new,q_heads,heads,d", [(900, 1, 8, 2, 128), (3000, 3, 16, 2, 64), (500, 1, 4, 2, 256), (65, 1, 3, 3, 80)])
+def test_decode_with_scores_past_the_units_of_fp32(att, n, new, q_heads, heads, d, power):
+    say("decode large scores", n, new, q_heads, heads, d, power)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    page, b = 16, 2
+    pages = -(-n // page)
+    kv = torch.full((pages, 2, heads, page, d // 2), 0xFF, dtype=torch.uint8, device="cuda")
+    sf = torch.full((pages, 2, heads, d // 16, page), 0xFF, dtype=torch.uint8, device="cuda")
+    gs = torch.tensor([2688 / 6.0, 2688 / 5.0], device="cuda")
+    k, v = (torch.randn(n, heads, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    k[n // 2] = k[n // 3]
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    att.nvfp4_kv_append(k, v, slots, gs, kv, sf)
+    q = (torch.randn(b, new, q_heads, d, device="cuda", generator=g) * 2.0 ** power).bfloat16()
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(b, -1).contiguous()
+    lse = torch.empty(b, new, q_heads, device="cuda")
+    out = att.nvfp4_attention_decode(q, kv, sf, gs, table, torch.full((b,), n, dtype=torch.int32, device="cuda"), lse=lse)
+    assert bool(out.isfinite().all())
+    kk, vv = (A.rows(kv, sf, w, slots) / gs[w].double() for w in (0, 1))
+    seen = torch.arange(n, device="cuda") < (n - (new - 1 - torch.arange(new, device="cuda")))[:, None]
+    led = sum(one_key_takes_all(q[i, :, h].double(), kk[:, h * heads // q_heads], vv[:, h * heads // q_heads], d ** -0.5, seen, out[i, :, h], lse[i, :, h])
+              for i in range(b) for h in range(q_heads))
+    assert led >= 0.8 * b * new * q_heads
+
+
+@pytest.mark.parametrize("power", [20, 31, 33, 60])
+@pytest.mark.parametrize("lq,lk,q_heads,heads,d", [((150, 40), (150, 90), 4, 2, 128), ((700,), (700,), 2, 2, 64), ((60,), (60,), 2, 1, 256), ((5,), (3000,), 4, 1, 128),
+                                                   ((300,) * 9, (300,) * 9, 16, 8, 96)])
+def test_prompts_with_scores_past_the_units_of_fp32(att, lq, lk, q_heads, heads, d, power):
+    say("prefill large scores", lq, lk, q_heads, heads, d, power)
+    g = torch.Generator(device="cuda").manual_seed(sum(lk))
+    q = (torch.randn(sum(lq), q_heads, d, device="cuda", generator=g) * 2.0 ** power).bfloat16()
+    k, v = (torch.randn(sum(lk), heads, d, device="cuda", generator=g).bfloat16() for _ in range(2))
+    k[9] = k[3]
+    cq, ck = (torch.tensor((0,) + n, device="cuda").cumsum(0).int() for n in (lq, lk))
+    for causal in (True, False):
+        lse = torch.empty(q.shape[:2], device="cuda")
+        out = att.attention_prefill(q, k, v, cq, ck, causal=causal, lse=lse)
+        assert bool(out.isfinite().all())
+        led = 0
+        for i, (n, m) in enumerate(zip(lq, lk)):
+            r, c = slice(int(cq[i]), int(cq[i + 1])), slice(int(ck[i]), int(ck[i + 1]))
+            seen = torch.arange(m, device="cuda") <= ((torch.arange(n, device="cuda") + m - n) if causal else torch.full((n,), m, device="cuda"))[:, None]
+            led += sum(one_key_takes_all(q[r, h].double(), k[c, h * heads // q_heads].double(), v[c, h * heads // q_heads].double(), d ** -0.5, seen, out[r, h], lse[r, h])
+                       for h in range(q_heads))
+        assert led >= 0.8 * sum(lq) * q_heads
