@@ -101,9 +101,10 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
  * passed over as if their positions were not seen.  The keys and values are
  * exact; q enters the products as fp16 scaled by a power of two per head (exact, but off by up to
  * 2^-39 of the head's largest where it is below 2^-28 of it), the probabilities as fp16 (off by
- * 2^-11 of themselves, or by 2^-25 of the largest); sums are fp32.  The tokens of long sequences are split over workgroups, whose parts a
- * second launch joins; how, depends on the lengths, which are read on the device (a
- * captured graph follows them).  Results are the same on every call.
+ * 2^-11 of themselves, or, below 2^-26 of the largest, by 2^-37 of it); sums are fp32.  The tokens
+ * of long sequences are split over workgroups, whose parts a second launch joins; how, depends on
+ * the lengths, which are read on the device (a captured graph follows them).  Results are the same
+ * on every call.
  *   q: [b, t, q_heads, d] bf16 with q_stride from token to token; block_table:
  *   [b, table_pages] int32 (entries past a sequence's last page are not read); lengths: [b]
  *   int32; out: [b, t, q_heads, d] bf16; lse: NULL or [b, t, q_heads] fp32,

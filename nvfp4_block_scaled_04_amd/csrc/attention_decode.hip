@@ -19,8 +19,8 @@
 //   tokens of one column, in the order in which its rows of X^T hold them, so P goes
 //   from one product into the other without crossing lanes.
 // e2m1 * ue4m3 is exact in fp16.  q enters as fp16 scaled by a power of two per row (exact
-// down to 2^-28 of the row's largest, off by up to 2^-39 of it below); P is rounded to fp16, off
-// by 2^-11 of itself at most.  Maximum, sum and both products' sums are fp32.
+// down to 2^-28 of the row's largest, off by up to 2^-39 of it below); P is rounded to fp16 (kLag).
+// Maximum, sum and both products' sums are fp32.
 #include "gemm_common.h"
 #include "internal.h"
 
@@ -32,6 +32,14 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kBlock = 64;        // tokens a wave takes at a time
 constexpr int kRows = 16;         // query rows of a matrix product
 constexpr int kJoinMany = 1024;   // rows of the output that are joined by a wave each
+// A row's maximum m, in whole powers of two, is moved where a score exceeds it by more than kLag; a
+// probability is 2^(score - m + kUp), 2^15 at most, which fp16 holds to 2^-11 of itself down to 2^-26
+// of the largest and to 2^-37 of the largest below.  (At m itself with a lag of 8 fp16 ends at 2^-25,
+// and a key 17 above many others, in natural units, took their share away.)  A smaller lag moves more
+// often: 64 sequences of up to 16384 with 0 / 2 / 8: 123 / 121 / 119 us, 4 x 8 rows over 32 of 8192
+// 79.3 / 78.3 / 76.6.
+constexpr int kLag = 2, kUp = 15 - kLag;
+constexpr float kDown = 1.0f / (1 << kUp);
 constexpr int kAttnLdsLong = 54272;  // LDS of a workgroup, three of which fit a CU
 
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
@@ -458,31 +466,31 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? (
                         if (at >= limit[t] || at >= t1 || ((none >> g) & 1)) x[t][i][e] = neg_inf();
                     }
             }
-            // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the row
-            // alone, so that its bits do not depend on the rows beside it)
+            // (moved by the row alone, so that its bits do not depend on the rows beside it)
             float top = x[t][0][0];
 #pragma unroll
             for (int i = 1; i < 16; i++) top = __builtin_fmaxf(top, x[t][i >> 2][i & 3]);
             top *= to_x[t];
-            if (__any(top > m[t] + 8.0f)) {
+            if (__any(top > m[t] + kLag)) {
                 top = __builtin_fmaxf(top, __shfl_xor(top, 16));
                 top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                const float to = top > m[t] + 8.0f ? top : m[t];
+                const float to = top > m[t] + kLag ? __builtin_rintf(top) : m[t];
                 const float a = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m[t] - to);
                 m[t] = to;
                 l[t] *= a;
 #pragma unroll
                 for (int i = 0; i < D / 16; i++) o[t][i] *= a;
             }
-            float base = m[t] == neg_inf() ? 0.0f : m[t], by = to_x[t];
-            if (__any(__builtin_fabsf(base) >= kFarScore)) {  // (by the row alone too)
-                const bool far = __builtin_fabsf(base) >= kFarScore;
+            const float most = m[t] == neg_inf() ? 0.0f : m[t];
+            float base = most - kUp, by = to_x[t];
+            if (__any(__builtin_fabsf(most) >= kFarScore)) {  // (by the row alone too)
+                const bool far = __builtin_fabsf(most) >= kFarScore;
 #pragma unroll
                 for (int i = 0; i < 16; i++) {
                     const float v = x[t][i >> 2][i & 3];
-                    x[t][i >> 2][i & 3] = far ? far_score(v, by, base) : v;
+                    x[t][i >> 2][i & 3] = far ? far_score(v, by, most) : v;
                 }
-                base = far ? 0.0f : base;
+                base = far ? -kUp : base;
                 by = far ? 1.0f : by;
             }
             float sum = 0.0f;
@@ -557,7 +565,7 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? (
             const int64_t orow = ((int64_t)w.seq * p.T + tt) * p.Hq + head * p.G + rr - tt * p.G;
             const float by = den == 0.0f ? 0.0f : out_scale / den;
             if (c < d) *(u32x2*)(p.out + orow * d + c) = u32x2{pack_bf16x2(sum[0] * by, sum[1] * by), pack_bf16x2(sum[2] * by, sum[3] * by)};
-            if (p.lse && c == 0) p.lse[orow] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
+            if (p.lse && c == 0) p.lse[orow] = (top + __builtin_log2f(den * kDown)) * 0.69314718055994530942f;
         }
     }
 #endif
@@ -644,7 +652,7 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     for (int i = 0; i < GROUPS; i++) acc += *(const f32x4*)(sums + i * D + c);
     const float by = den == 0.0f ? 0.0f : 1.0f / p.gs[1] / den;
     if (c < p.d) *(u32x2*)(p.out + (int64_t)orow * p.d + c) = u32x2{pack_bf16x2(acc[0] * by, acc[1] * by), pack_bf16x2(acc[2] * by, acc[3] * by)};
-    if (p.lse && t == 0) p.lse[orow] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
+    if (p.lse && t == 0) p.lse[orow] = (top + __builtin_log2f(den * kDown)) * 0.69314718055994530942f;
 }
 
 template <int D, int NT>

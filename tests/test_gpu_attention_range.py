@@ -82,3 +82,48 @@ def test_prompts_with_scores_past_the_units_of_fp32(att, lq, lk, q_heads, heads,
             led += sum(one_key_takes_all(q[r, h].double(), k[c, h * heads // q_heads].double(), v[c, h * heads // q_heads].double(), d ** -0.5, seen, out[r, h], lse[r, h])
                        for h in range(q_heads))
         assert led >= 0.8 * sum(lq) * q_heads
+
+
+# Probabilities enter the product as fp16: half a step is 2^-11 of themselves, or, in fp16's
+# subnormals, 2^-25, where the largest is at least 2^12.5: 2^-37.5 of the largest.
+HALF_STEP, TINY = 2.0 ** -11, 2.0 ** -37
+
+
+@pytest.mark.parametrize("depth", [9.0, 14.0, 17.5, 18.5])
+@pytest.mark.parametrize("b,n,at,new,q_heads,heads,d,page", [
+    (64, 32768, range(100, 32768, 4096), 1, 8, 8, 128, 64), (64, 32768, range(0, 32768, 2048), 1, 8, 8, 64, 64), (3, 1000, (0,), 1, 8, 2, 128, 16),
+    (3, 1000, (999,), 1, 4, 2, 256, 16), (40, 9000, range(50, 9000, 1000), 1, 6, 6, 80, 32), (2, 70, (1,), 1, 3, 3, 96, 16),
+    (32, 16384, range(16000, 0, -1000), 5, 32, 8, 128, 64), (2, 300, (7, 200), 3, 8, 1, 48, 16),
+])
+def test_few_keys_far_above_the_others(att, depth, b, n, at, new, q_heads, heads, d, page):
+    """Keys `at` score `depth` above all others (which score 0) and hold zeros: what comes out is the
+    others' alone, e^-depth each.  All sequences read the same pages, as ones with a prefix in common do."""
+    say("decode depth", depth, b, n, new, q_heads, heads, d, page)
+    g = torch.Generator(device="cuda").manual_seed(n + d)
+    pages = -(-n // page)
+    kv = torch.full((pages, 2, heads, page, d // 2), 0xFF, dtype=torch.uint8, device="cuda")
+    sf = torch.full((pages, 2, heads, d // 16, page), 0xFF, dtype=torch.uint8, device="cuda")
+    gs = torch.tensor([2688 / 2.0, 2688 / 4.0], device="cuda")
+    k = torch.zeros(n, heads, d, device="cuda")
+    v = 1 + torch.rand(n, heads, d, device="cuda", generator=g)
+    k[list(at)], v[list(at)] = 1.0, 0.0
+    order = torch.randperm(pages, device="cuda", generator=g).int()
+    j = torch.arange(n, device="cuda")
+    slots = (order[j // page] * page + j % page).int()
+    att.nvfp4_kv_append(k.bfloat16(), v.bfloat16(), slots, gs, kv, sf)
+    q = torch.ones(b, new, q_heads, d, device="cuda").bfloat16()
+    table = order.expand(b, -1).contiguous()
+    lengths = torch.full((b,), n, dtype=torch.int32, device="cuda")
+    key = A.rows(kv, sf, 0, slots) / gs[0].double()
+    val = A.rows(kv, sf, 1, slots) / gs[1].double()
+    scale = depth / key[at[0], 0].sum().item()
+    lse = torch.empty(b, new, q_heads, device="cuda")
+    out = att.nvfp4_attention_decode(q, kv, sf, gs, table, lengths, scale=scale, lse=lse)
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+    group = q_heads // heads
+    seen = j < (n - (new - 1 - torch.arange(new, device="cuda")))[:, None]
+    for h in range(q_heads):
+        ref, rl, bound, dl = A.attend(q[0, :, h].double(), key[:, h // group], val[:, h // group], scale, seen, HALF_STEP, TINY)
+        worst = A.worst(out[0, :, h], ref, bound)
+        assert worst <= 1.0, (h, worst, (out[0, :, h].double() / ref).amin().item())
+        assert A.same_lse(lse[0, :, h], rl, dl), h
