@@ -133,7 +133,8 @@ int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t
  *   out = sum_p softmax_p(scale * q . k_p) v_p,
  * zeros (and lse = -inf) for a row that sees nothing.  What a row does not see has no
  * effect on it, whatever its values.  Rows of q outside all sequences are left as they were.
- * Probabilities are rounded to bf16 for their product with v; sums are fp32.
+ * Probabilities, one at most, are rounded to bf16 for their product with v; sums are fp32 (and
+ * divided by the probabilities' sum, that of the unrounded ones, at the end).
  *   q: [tq, q_heads, d], k, v: [tk, heads, d], out: [tq, q_heads, d], bf16, each with its
  *   stride; cu_q, cu_k: [b + 1] int32 on the device, ascending (values outside the tensors
  *   are clamped); lse: NULL or [tq, q_heads] fp32.

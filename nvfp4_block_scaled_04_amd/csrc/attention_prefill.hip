@@ -18,7 +18,8 @@
 // the softmax's arithmetic; short prompts the chain of a tile's keys.  Where few rows meet many
 // keys, workgroups share the keys (prefill_parts).
 // Sums, maximum and both products' sums are fp32; P is rounded to bf16 (V's range is
-// bf16's), off by 2^-8 of itself at most, as the output is.
+// bf16's), off by 2^-8 of itself at most, as the output is.  No P is above one (kLag), so that sums of
+// values near bf16's largest stay within fp32 as far as a softmax in fp32 goes.
 #include <type_traits>
 
 #include "gemm_common.h"
@@ -35,6 +36,11 @@ template <int D, int KEYS, int NW, int SPLIT>
 constexpr int lds_bytes() {
     return 4 * SPLIT * KEYS * D * 2 + (NW / SPLIT == 8 ? 8 * 64 * D : KEYS == 32 ? 64 * D : 0);
 }
+
+// A row's maximum m is moved only where a score exceeds it by more than kLag, to the largest score (on a
+// grid on which m + kLag is exact); a probability is 2^(score - m - kLag), one at most.  (2^kLag times a
+// value of 2^120 would pass fp32.)
+constexpr int kLag = 8;
 
 struct PParams {
     const uint16_t *q, *k, *v;
@@ -287,23 +293,23 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
 #pragma unroll
         for (int e = 1; e < 16 * NS; e++) top = __builtin_fmaxf(top, s[e >> 4][e & 15]);
         top *= p.c;
-        // a row's maximum is moved only where a score exceeds it by more than 2^8 (by the
-        // row alone, so that its bits do not depend on the rows beside it)
-        if (__any(top > m + 8.0f)) {
+        // (moved by the row alone, so that its bits do not depend on the rows beside it)
+        if (__any(top > m + kLag)) {
             top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-            const float to = top > m + 8.0f ? top : m;
+            const float to = top > m + kLag ? (top + kLag) - kLag : m;
             const float a = to == neg_inf() ? 1.0f : __builtin_amdgcn_exp2f(m - to);
             m = to;
             l *= a;
 #pragma unroll
             for (int i = 0; i < D / 32; i++) o[i] *= a;
         }
-        float base = m == neg_inf() ? 0.0f : m, c = p.c;
+        const float most = m == neg_inf() ? 0.0f : m;
+        float base = most + kLag, c = p.c;
         if constexpr (FAR) {
-            const bool far = __builtin_fabsf(base) >= kFarScore;
+            const bool far = __builtin_fabsf(most) >= kFarScore;
 #pragma unroll
-            for (int e = 0; e < 16 * NS; e++) s[e >> 4][e & 15] = far ? far_score(s[e >> 4][e & 15], c, base) : s[e >> 4][e & 15];
-            base = far ? 0.0f : base;
+            for (int e = 0; e < 16 * NS; e++) s[e >> 4][e & 15] = far ? far_score(s[e >> 4][e & 15], c, most) : s[e >> 4][e & 15];
+            base = far ? kLag : base;
             c = far ? 1.0f : c;
         }
         float sum = 0.0f;
@@ -554,7 +560,7 @@ __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_
     }
     const float by = den == 0.0f ? 0.0f : 1.0f / den;
     if (p.lse && hi == 0 && mine < nrows)
-        p.lse[(int64_t)(sq.q0 + token(mine)) * p.Hq + head + (mine - token(mine) * group)] = (m + __builtin_log2f(den)) * 0.69314718055994530942f;
+        p.lse[(int64_t)(sq.q0 + token(mine)) * p.Hq + head + (mine - token(mine) * group)] = (m + __builtin_log2f(den * (1 << kLag))) * 0.69314718055994530942f;
     // the rows leave through LDS, in whole lines
     lds_u8* const mo = lds + gw * OWN;
 #pragma unroll
@@ -618,7 +624,7 @@ __global__ __launch_bounds__(256) void k_join_parts(PParams p) {
     const float by = den == 0.0f ? 0.0f : 1.0f / den;
     if (lane < CT && c < p.d)
         *(u32x2*)(p.out + row * p.out_stride + head * p.d + c) = u32x2{pack_bf16x2(acc[0] * by, acc[1] * by), pack_bf16x2(acc[2] * by, acc[3] * by)};
-    if (p.lse && lane == 0) p.lse[at] = (top + __builtin_log2f(den)) * 0.69314718055994530942f;
+    if (p.lse && lane == 0) p.lse[at] = (top + __builtin_log2f(den * (1 << kLag))) * 0.69314718055994530942f;
 }
 
 template <int D, int KEYS, int NW, int SPLIT>

@@ -127,3 +127,35 @@ def test_few_keys_far_above_the_others(att, depth, b, n, at, new, q_heads, heads
         worst = A.worst(out[0, :, h], ref, bound)
         assert worst <= 1.0, (h, worst, (out[0, :, h].double() / ref).amin().item())
         assert A.same_lse(lse[0, :, h], rl, dl), h
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lq,lk,q_heads,heads,d", [
+    ((200, 70), (200, 70), 4, 2, 128), ((90,), (300,), 2, 2, 64), ((130,), (257,), 2, 1, 256), ((300,) * 9, (300,) * 9, 16, 8, 96), ((3, 20) * 20, (90, 20) * 20, 32, 8, 128),
+    ((7, 16), (5000, 3111), 8, 2, 128), ((5,), (2000,), 3, 3, 64), ((2300, 1900), (2300, 1900), 16, 16, 128), ((200, 300), (200, 300), 64, 64, 256),
+])
+def test_prompts_with_values_near_the_largest(att, lq, lk, q_heads, heads, d, causal):
+    """Values of 2^122, and keys whose scores rise by less than makes the maximum move: the result is an
+    average, and fp32 holds every sum on the way while no probability is above one (about a hundred keys
+    count as much as the largest at most, of random sign).  Bounds as of any prompt: probabilities and
+    outputs in bf16."""
+    say("prefill large values", lq[:4], lk[:4], q_heads, heads, d, causal)
+    g = torch.Generator(device="cuda").manual_seed(sum(lk) + d)
+    r = lambda t, h: torch.randn(t, h, d, device="cuda", generator=g)  # noqa: E731
+    q, k, v = r(sum(lq), q_heads), r(sum(lk), heads) * 0.25, r(sum(lk), heads)
+    cq, ck = (torch.tensor((0,) + n, device="cuda").cumsum(0).int() for n in (lq, lk))
+    q[..., 0] = d ** 0.5
+    at = torch.cat([torch.arange(n, device="cuda") for n in lk])
+    k[..., 0] = (at > 7).float()[:, None]             # past the first keys
+    k[..., 0] += 4.2 * (at % 67 == 66).float()[:, None]   # and now and then a score of 5.2: 2^7.5
+    q, k, v = q.bfloat16(), k.bfloat16(), (v.clamp(-3, 3) * 2.0 ** 120.5).bfloat16()
+    lse = torch.empty(q.shape[:2], device="cuda")
+    out = att.attention_prefill(q, k, v, cq, ck, causal=causal, lse=lse)
+    for i, (n, m) in enumerate(zip(lq, lk)):
+        a, c = slice(int(cq[i]), int(cq[i + 1])), slice(int(ck[i]), int(ck[i + 1]))
+        seen = torch.arange(m, device="cuda") <= ((torch.arange(n, device="cuda") + m - n) if causal else torch.full((n,), m, device="cuda"))[:, None]
+        for h in range(q_heads):
+            ref, rl, bound, dl = A.attend(q[a, h].double(), k[c, h * heads // q_heads].double(), v[c, h * heads // q_heads].double(), d ** -0.5, seen, 2.0 ** -8, 0.0)
+            assert bool(out[a, h].isfinite().all()), (i, h)
+            assert A.worst(out[a, h], ref, bound) <= 1.0, (i, h)
+            assert A.same_lse(lse[a, h], rl, dl), (i, h)
