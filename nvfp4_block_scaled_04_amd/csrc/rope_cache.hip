@@ -200,8 +200,17 @@ __global__ __launch_bounds__(kRowThreadsMany) void k_kv_rows(CParams p) {
             // code * scale is exact; its quotient by gs, correctly rounded by one correction
             // step from the reciprocal (Markstein), then rounded to bf16
             const float rcp = 1.0f / gs[w];
-            u32x4 y[2];
+            u32x4* const dst = (u32x4*)((w ? p.vo : p.ko) + at[w]);
             typedef float f32x2 __attribute__((ext_vector_type(2)));
+            if (!(gs[w] >= 0x1p-112f && gs[w] <= 0x1p112f)) {  // where a step of it could leave fp32's normal numbers
+#pragma unroll 1
+                for (int j = 0; j < 8; j++) {
+                    const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4((j < 4 ? c[w][0] : c[w][1]) >> 8 * (j & 3), 1.0f, 0);
+                    ((uint32_t*)dst)[j] = pack_bf16x2(v[0] * s / gs[w], v[1] * s / gs[w]);
+                }
+                continue;
+            }
+            u32x4 y[2];
             auto put = [&](int j, f32x2 v) {
                 const float a = v[0] * s, b = v[1] * s;
                 const float qa = a * rcp, qb = b * rcp;
@@ -215,7 +224,6 @@ __global__ __launch_bounds__(kRowThreadsMany) void k_kv_rows(CParams p) {
                 put(4 * h + 2, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[w][h], 1.0f, 2));
                 put(4 * h + 3, __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[w][h], 1.0f, 3));
             }
-            u32x4* const dst = (u32x4*)((w ? p.vo : p.ko) + at[w]);
             dst[0] = y[0];
             dst[1] = y[1];
         }

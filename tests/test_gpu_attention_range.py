@@ -159,3 +159,22 @@ def test_prompts_with_values_near_the_largest(att, lq, lk, q_heads, heads, d, ca
             assert bool(out[a, h].isfinite().all()), (i, h)
             assert A.worst(out[a, h], ref, bound) <= 1.0, (i, h)
             assert A.same_lse(lse[a, h], rl, dl), (i, h)
+
+
+@pytest.mark.parametrize("scales", [(7e-36, 1e-36), (3e38, 1e37), (float("inf"), 2.0 ** 126), (1e-39, 2.0 ** -149), (2.0 ** -112, 2.0 ** 112), (2.0 ** -113, 2.0 ** 113),
+                                    (1.1 * 2.0 ** -116, 1.7 * 2.0 ** 120), (2688 / 3.3895e38, 2688 / 1e-38)])
+def test_read_with_any_global_scale(att, scales):
+    """bf16 of the correctly rounded fp32 quotient, infinite and subnormal ones among them, for every
+    code and scale."""
+    say("read scales", scales)
+    kv, sf = torch.zeros(16, 2, 1, 16, 16, dtype=torch.uint8, device="cuda"), torch.zeros(16, 2, 1, 2, 16, dtype=torch.uint8, device="cuda")
+    flat, fsf = kv.view(16, 2, 16, 16), sf.view(16, 2, 2, 16)
+    flat[:] = torch.arange(16, dtype=torch.uint8, device="cuda").repeat(16).view(16, 16) * 16 + torch.arange(16, dtype=torch.uint8, device="cuda")
+    fsf[:] = torch.arange(512, device="cuda").remainder(127).to(torch.uint8).view(16, 2, 16).unsqueeze(1)
+    slots = torch.arange(256, dtype=torch.int32, device="cuda")
+    gs = torch.tensor(scales, dtype=torch.float32, device="cuda")
+    for which, o in enumerate(att.nvfp4_kv_read(slots, gs, kv, sf)):
+        want = (A.rows(kv, sf, which, slots).float().cpu() / gs[which].cpu()).bfloat16()
+        assert not bool(want.isnan().any())
+        same = o.cpu() == want
+        assert bool(same.all()), (which, int((~same).sum()))
