@@ -563,8 +563,8 @@ __global__ __launch_bounds__(kThreads, NT == 2 ? (D <= 64 ? 3 : 2) : D <= 64 ? (
         } else {
             const int tt = rr / p.G;
             const int64_t orow = ((int64_t)w.seq * p.T + tt) * p.Hq + head * p.G + rr - tt * p.G;
-            const float by = den == 0.0f ? 0.0f : out_scale / den;
-            if (c < d) *(u32x2*)(p.out + orow * d + c) = u32x2{pack_bf16x2(sum[0] * by, sum[1] * by), pack_bf16x2(sum[2] * by, sum[3] * by)};
+            const float by = den == 0.0f ? 0.0f : 1.0f / den;  // (times out_scale it may be subnormal)
+            if (c < d) *(u32x2*)(p.out + orow * d + c) = u32x2{pack_bf16x2(sum[0] * by * out_scale, sum[1] * by * out_scale), pack_bf16x2(sum[2] * by * out_scale, sum[3] * by * out_scale)};
             if (p.lse && c == 0) p.lse[orow] = (top + __builtin_log2f(den * kDown)) * 0.69314718055994530942f;
         }
     }
@@ -650,8 +650,8 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
     acc = f32x4{};
 #pragma unroll
     for (int i = 0; i < GROUPS; i++) acc += *(const f32x4*)(sums + i * D + c);
-    const float by = den == 0.0f ? 0.0f : 1.0f / p.gs[1] / den;
-    if (c < p.d) *(u32x2*)(p.out + (int64_t)orow * p.d + c) = u32x2{pack_bf16x2(acc[0] * by, acc[1] * by), pack_bf16x2(acc[2] * by, acc[3] * by)};
+    const float by = den == 0.0f ? 0.0f : 1.0f / den, out_scale = 1.0f / p.gs[1];
+    if (c < p.d) *(u32x2*)(p.out + (int64_t)orow * p.d + c) = u32x2{pack_bf16x2(acc[0] * by * out_scale, acc[1] * by * out_scale), pack_bf16x2(acc[2] * by * out_scale, acc[3] * by * out_scale)};
     if (p.lse && t == 0) p.lse[orow] = (top + __builtin_log2f(den * kDown)) * 0.69314718055994530942f;
 }
 

@@ -178,3 +178,30 @@ def test_read_with_any_global_scale(att, scales):
         assert not bool(want.isnan().any())
         same = o.cpu() == want
         assert bool(same.all()), (which, int((~same).sum()))
+
+
+@pytest.mark.parametrize("size", [1e-35, 1e-34, 1e-30, 1e33, 3e37])
+@pytest.mark.parametrize("lens,q_heads,heads,d", [((900, 40), 8, 2, 128), ((5000,), 4, 4, 64), ((9000, 30), 6, 1, 256)])
+def test_decode_with_very_small_and_large_values(att, size, lens, q_heads, heads, d):
+    """The global scale of values near either end of bf16's range, whole sequences and parts."""
+    say("decode size of values", size, lens, q_heads, heads, d)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    page, most, b = 16, max(lens), len(lens)
+    pages = -(-most // page)
+    kv = torch.full((pages, 2, heads, page, d // 2), 0xFF, dtype=torch.uint8, device="cuda")
+    sf = torch.full((pages, 2, heads, d // 16, page), 0xFF, dtype=torch.uint8, device="cuda")
+    k = torch.randn(most, heads, d, device="cuda", generator=g).bfloat16()
+    v = (torch.randn(most, heads, d, device="cuda", generator=g).clamp(-4, 4) * size).bfloat16()
+    gs = torch.stack([2688 / k.abs().amax().float(), 2688 / v.abs().amax().float()])
+    slots = torch.arange(most, dtype=torch.int32, device="cuda")
+    att.nvfp4_kv_append(k, v, slots, gs, kv, sf)
+    q = torch.randn(b, 1, q_heads, d, device="cuda", generator=g).bfloat16()
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(b, -1).contiguous()
+    out = att.nvfp4_attention_decode(q, kv, sf, gs, table, torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    kk, vv = (A.rows(kv, sf, w, slots) / gs[w].double() for w in (0, 1))
+    for i, n in enumerate(lens):
+        for h in range(q_heads):
+            at = h * heads // q_heads
+            ref, _, bound, _ = A.attend(q[i, :, h].double(), kk[:n, at], vv[:n, at], d ** -0.5, torch.ones(1, n, dtype=torch.bool, device="cuda"), HALF_STEP, TINY)
+            bound = bound - 1e-37 + 1e-41   # (what attend allows around zero is as large as these values)
+            assert A.worst(out[i, :, h], ref, bound) <= 1.0, (i, h, A.worst(out[i, :, h], ref, bound))
