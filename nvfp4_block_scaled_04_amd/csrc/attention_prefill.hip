@@ -109,10 +109,10 @@ __device__ __forceinline__ int swizzle_v(int r) { return D == 64 ? (r & 2) << 1 
 // 16 bytes a lane from a raw buffer into LDS, lane after lane from `lds` on.  In assembly, since
 // behind its own intrinsic the compiler waits for these loads at every LDS read, also of the
 // other buffer.  (It writes no register; the compiler's own waits count it as one load more,
-// which only makes them longer; nothing else here uses m0.  The s_nop covers m0 and a descriptor
-// that a vector instruction has just written.)
+// which only makes them longer.  The s_nop covers m0 and a descriptor that a vector instruction has
+// just written.)
 __device__ __forceinline__ void load_to_lds(const u32x4& rsrc, uint32_t offset, uint32_t lds) {
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(rsrc), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(offset), "s"(rsrc), "s"(lds) : "memory", "m0");
 }
 
 __device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
