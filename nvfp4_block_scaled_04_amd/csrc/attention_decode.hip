@@ -29,9 +29,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr int kBlock = 64;        // tokens a wave takes at a time
-constexpr int kRows = 16;         // query rows of a matrix product
-constexpr int kJoinMany = 1024;   // rows of the output that are joined by a wave each
+constexpr int kBlock = kAttnBlock;  // tokens a wave takes at a time
+constexpr int kRows = kAttnRows;    // query rows of a matrix product
 // A row's maximum m, in whole powers of two, is moved where a score exceeds it by more than kLag; a
 // probability is 2^(score - m + kUp), 2^15 at most, which fp16 holds to 2^-11 of itself down to 2^-26
 // of the largest and to 2^-37 of the largest below.  (At m itself with a lag of 8 fp16 ends at 2^-25,
@@ -656,19 +655,19 @@ __global__ __launch_bounds__(kThreads) void k_attn_join(DParams p) {
 }
 
 template <int D, int NT>
-hipError_t launch(const DParams& p, int64_t grid, bool join, bool large, hipStream_t st) {
+hipError_t launch(const DParams& p, const DecodePlan& plan, hipStream_t st) {
     constexpr int merge = kWaves * NT * kRows * (D + 4) * 4;
     constexpr int need = kWaves * Stage<D>::WAVE > merge ? kWaves * Stage<D>::WAVE : merge;
-    const int lds = D > 64 && large && need < kAttnLdsLong ? kAttnLdsLong : need;
-    const bool once = p.row_tiles == 1, packed = p.d % 32 != 0 || 2 * p.d <= D;
-    if (once && !packed) k_attn_decode<D, NT, true, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
-    else if (once) k_attn_decode<D, NT, true, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
-    else if (!packed) k_attn_decode<D, NT, false, false><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
-    else k_attn_decode<D, NT, false, true><<<dim3((unsigned)grid), kThreads, lds, st>>>(p);
+    const int lds = D > 64 && plan.large && need < kAttnLdsLong ? kAttnLdsLong : need;
+    const dim3 grid((unsigned)(plan.units * p.H * p.row_tiles));
+    if (plan.once && !plan.packed) k_attn_decode<D, NT, true, false><<<grid, kThreads, lds, st>>>(p);
+    else if (plan.once) k_attn_decode<D, NT, true, true><<<grid, kThreads, lds, st>>>(p);
+    else if (!plan.packed) k_attn_decode<D, NT, false, false><<<grid, kThreads, lds, st>>>(p);
+    else k_attn_decode<D, NT, false, true><<<grid, kThreads, lds, st>>>(p);
     hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !join) return e;
+    if (e != hipSuccess || !plan.join) return e;
     const int rows_out = p.b * p.T * p.Hq;
-    if (rows_out < kJoinMany) k_attn_join<D, NT, kWaves><<<dim3((unsigned)rows_out), kThreads, 0, st>>>(p);
+    if (plan.join_waves == kWaves) k_attn_join<D, NT, kWaves><<<dim3((unsigned)rows_out), kThreads, 0, st>>>(p);
     else k_attn_join<D, NT, 1><<<dim3((unsigned)((rows_out + kWaves - 1) / kWaves)), kThreads, 0, st>>>(p);
     return hipGetLastError();
 }
@@ -687,34 +686,14 @@ hipError_t launch_attention_decode(const AttnDecodeArgs& a, hipStream_t st) {
     p.b = (int)a.b; p.T = (int)a.t; p.H = (int)a.heads; p.Hq = (int)a.q_heads; p.G = p.Hq / p.H; p.d = (int)a.d;
     p.pages = (int)a.pages; p.table_pages = (int)a.table_pages;
     p.page_log2 = __builtin_ctzll((unsigned long long)a.page);
-    // More rows than one product takes: two share a read of the cache where that is much (by the
-    // table's size; heads of 256 have no registers for it).  4 x 8 rows over 32 sequences of
-    // 8192: 79 us, 114 apart; 4 x 8 over 8 of 8192: 29.6, 34.5; 4 x 8 over 16 of 1024: 16.4, 14.3 (not taken).
-    const bool two = p.T * p.G > kRows && a.d <= 128 && a.b * a.heads * a.table_pages * a.page >= kAttnShared;
-    const int rows = two ? 2 * kRows : kRows;
-    p.row_tiles = (p.T * p.G + rows - 1) / rows;
     p.cap = (int)(a.table_pages * a.page);
-    // Long parts (by the table's size, the lengths being on the device) are better off with three
-    // workgroups a CU and cut finer, so that the last ones end together; short ones with four,
-    // whose beginnings overlap.  64 sequences to 16384: 122 us against 131; 4 to 131072: 109
-    // against 121; 64 of 16384 each: 203 against 193; 256 to 2048: 93 against 79 (not taken).
-    // Heads of 64 have half the bytes a wave, so five workgroups a CU and more parts: 32 of 8192:
-    // 43 us with 1024 parts, 49 with 512, 47 with 2048.
-    const int64_t hrs = (int64_t)p.H * p.row_tiles;
-    const bool large = p.cap >= 2 * kAttnLong && p.b * hrs * p.cap >= kAttnLong * kAttnParts;
-    p.split = two ? kAttnParts : a.d <= 64 ? kAttnPartsNarrow : large ? kAttnPartsLong : kAttnParts;  // (two: slots twice as large)
-    // the most workgroups that lengths up to the table's can ask for
-    int64_t units = (p.split + hrs - 1) / hrs + p.b;
-    // Sequences of up to kAttnWhole stay whole, which saves the second launch (16 of 1000: 12.6 us
-    // against 15.0; one alone: 11.9 against 10.7, and 3 us less of the host).
-    const int64_t least = p.cap <= kAttnWhole ? kAttnWhole : kAttnMinPart;
-    p.least = (int)(least / kBlock);
-    const int64_t each = (p.cap + least - 1) / least;
-    if (each * p.b < units) units = each * p.b;
-    const bool join = each > 1;
-    if (a.d <= 64) return two ? launch<64, 2>(p, units * hrs, join, large, st) : launch<64, 1>(p, units * hrs, join, large, st);
-    if (a.d <= 128) return two ? launch<128, 2>(p, units * hrs, join, large, st) : launch<128, 1>(p, units * hrs, join, large, st);
-    return launch<256, 1>(p, units * hrs, join, large, st);
+    const DecodePlan plan = decode_plan(a.b, a.t, a.q_heads, a.heads, a.d, p.cap);
+    p.row_tiles = (int)plan.row_tiles;
+    p.split = (int)plan.split;
+    p.least = (int)plan.least;
+    if (plan.width == 64) return plan.two ? launch<64, 2>(p, plan, st) : launch<64, 1>(p, plan, st);
+    if (plan.width == 128) return plan.two ? launch<128, 2>(p, plan, st) : launch<128, 1>(p, plan, st);
+    return launch<256, 1>(p, plan, st);
 }
 
 }  // namespace nvfp4

@@ -6,7 +6,7 @@
 // c = scale * log2(e), one pass over the keys with the running maximum m and sum.
 //
 // A workgroup of four or eight waves takes 128 or 256 rows of one head (or of the heads of a group),
-// a wave 32 of them (see launch_attention_prefill).  64 keys and values at a time (32 for most heads
+// a wave 32 of them (see prefill_plan).  64 keys and values at a time (32 for most heads
 // of 256) go straight from memory into LDS (two buffers), swizzled at their source so that neither
 // product's reads collide in the banks.  Both products run on 32x32x16 bf16 MFMAs, transposed:
 //   S^T[key, row] = K Q^T: a lane owns one row (and half of the keys), so the softmax
@@ -661,37 +661,19 @@ hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st) {
     p.c = a.scale * 1.44269504088896340736f;
     p.b = (int)a.b; p.tq = (int)a.tq; p.tk = (int)a.tk; p.Hq = (int)a.q_heads; p.H = (int)a.heads;
     p.G = p.Hq / p.H; p.d = (int)a.d; p.causal = a.causal;
-    // The workgroup, by the average sequence (the lengths themselves are on the device), measured
-    // with 32 heads of 128:
-    //   * few tiles of rows for the CUs, or few and of unequal work (causal, no long prefix): 128
-    //     rows, the keys split (1 prompt of 1024: 21.9 us, 27.8 unsplit; of 2048: 44.6, 53.2; but 4 of 512: 27.9, 24.4; 4 of 300 behind 2000: 68, 66);
-    //   * long ones: 256 rows (2 of 2048: 73.5 us, 80.2 with 128 rows; 4 of 300 behind 2000: 58,
-    //     66; but 64 of 256: 126, 103);
-    //   * others: 128 rows.  (Heads of 64, bound by the softmax's arithmetic, gain nothing from
-    //     256 rows: 32 of 1500: 582 us, 421.)
-    const int64_t nq = a.tq / a.b > 1 ? a.tq / a.b : 1, nk = a.tk / a.b, tiles = a.b * ((nq + 127) / 128) * a.q_heads;
-    // The heads of a group share a tile where that saves tiles, and these are more than the CUs or the
-    // keys are shared too (32 / 8 heads of 128: 128 of 16 rows 20.0 us, 51 apart; 64 of 30 behind
-    // 500 keys 39, 81; 16 of 16 behind 4000 60, 99; 8 of 520 behind 1000 115, 121; but one of 61 8.1,
-    // 7.2; 8 of 32 behind 1000 26.6, 21.4: a wave beside it slows the chain of a tile's keys).
-    const bool packs = prefill_packs(a.tq, a.q_heads, a.heads, a.b);
     p.part = (float*)a.ws;
-    p.parts = p.part ? (int)prefill_parts(a.tq, a.tk, a.q_heads, a.heads, a.b) : 1;
-    const bool pack = packs && (p.parts > 1 || tiles > 256);
-    if (pack || p.parts > 1) {
-        if (a.d <= 64) return launch_few<64>(p, pack, st);
-        return a.d <= 128 ? launch_few<128>(p, pack, st) : launch_few<256>(p, pack, st);
+    const PrefillPlan plan = prefill_plan(a.tq, a.tk, a.q_heads, a.heads, a.d, a.b, a.causal != 0, a.ws != nullptr);
+    p.parts = (int)plan.parts;
+    if (plan.pack || plan.parts > 1) {
+        if (plan.width == 64) return launch_few<64>(p, plan.pack, st);
+        return plan.width == 128 ? launch_few<128>(p, plan.pack, st) : launch_few<256>(p, plan.pack, st);
     }
-    const bool split = (tiles <= 256 && nk >= 128) ||
-                       (tiles <= 512 && nk >= 1024 && nq >= 128 && a.causal && 2 * a.tk <= 3 * a.tq);
-    if (a.d <= 64) return split ? launch<64, 64, 8, 2>(p, st) : launch<64, 64, 4, 1>(p, st);
-    if (a.d <= 128) {
-        if (split) return launch<128, 64, 8, 2>(p, st);
-        return nq >= 256 && nk >= 1024 ? launch<128, 64, 8, 1>(p, st) : launch<128, 64, 4, 1>(p, st);
+    if (plan.width == 64) return plan.split == 2 ? launch<64, 64, 8, 2>(p, st) : launch<64, 64, 4, 1>(p, st);
+    if (plan.width == 128) {
+        if (plan.split == 2) return launch<128, 64, 8, 2>(p, st);
+        return plan.waves == 8 ? launch<128, 64, 8, 1>(p, st) : launch<128, 64, 4, 1>(p, st);
     }
-    // Heads of 256: two workgroups a CU where there are more than one (16 / 8 heads: a prompt of 8192
-    // 523 us, 757 with one; 64 of 128 62, 79; but 2 of 66 behind 506, 35 / 7 heads, 37.6, 33.2).
-    return tiles > 256 ? launch<256, 32, 4, 1>(p, st) : launch<256, 64, 4, 1>(p, st);
+    return plan.keys == 32 ? launch<256, 32, 4, 1>(p, st) : launch<256, 64, 4, 1>(p, st);
 }
 
 }  // namespace nvfp4

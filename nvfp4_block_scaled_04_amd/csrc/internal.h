@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "attention_plan.h"
+
 namespace nvfp4 {
 
 struct QuantizeArgs {
@@ -177,13 +179,6 @@ struct KvRowsArgs {
 hipError_t launch_kv_rows(const KvRowsArgs& a, hipStream_t st);
 
 // Attention of t tokens a sequence over the paged NVFP4 cache.
-constexpr int64_t kAttnParts = 512;       // parts that the tokens of all sequences are split into, about
-constexpr int64_t kAttnPartsLong = 768;   // the same where they are long
-constexpr int64_t kAttnPartsNarrow = 1024;  // the same for heads of up to 64
-constexpr int64_t kAttnLong = 4096;       // tokens of a long part, of a sequence twice as long
-constexpr int64_t kAttnMinPart = 256;     // fewest tokens of a part
-constexpr int64_t kAttnWhole = 1024;      // tokens of a sequence (by the table) that is not split
-constexpr int64_t kAttnShared = (int64_t)1 << 18;  // tokens times KV heads from which rows share a read
 struct AttnDecodeArgs {
     const uint16_t* q;         // [b, t, q_heads, d], q_stride elements from token to token
     const uint8_t *kv, *kv_sf;
@@ -209,29 +204,6 @@ struct AttnPrefillArgs {
     float scale;
     int causal;
 };
-// Workgroups that share the keys of a tile of rows, by the average sequence: two a CU in all, of 256
-// keys or more, where the tiles are few and the keys many.  32 / 8 heads of 128, one sequence of 1 row
-// behind 8191 keys: 19.3 us, unshared 95.9; 128 behind 1920: 21.8, 31.1; 512 behind 7680: 87, 110; but
-// 700 behind 1300 (tiles for 192 CUs): 44, 33; 4 of 100 behind 1000: 30, 23 (not taken).
-constexpr int64_t kPrefillGroups = 512, kPrefillKeys = 256, kPrefillLong = 1536;
-constexpr int64_t kPrefillRows = 512 * 129;  // of the parts together
-inline int64_t prefill_tiles(int64_t tq, int64_t per, int64_t heads, int64_t b) {
-    return b * (((tq / b > 1 ? tq / b : 1) * per + 127) / 128) * heads;
-}
-// Whether the heads of a group in one tile save one tile in twenty or more.
-inline bool prefill_packs(int64_t tq, int64_t q_heads, int64_t heads, int64_t b) {
-    return 20 * prefill_tiles(tq, q_heads / heads, heads, b) <= 19 * prefill_tiles(tq, 1, q_heads, b);
-}
-inline int64_t prefill_parts(int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t b) {
-    const int64_t nk = tk / b;
-    const int64_t most = kPrefillGroups / (prefill_packs(tq, q_heads, heads, b) ? prefill_tiles(tq, q_heads / heads, heads, b)
-                                                                                : prefill_tiles(tq, 1, q_heads, b));
-    if (most < 4 || nk < kPrefillLong) return 1;
-    int64_t n = nk / kPrefillKeys < most ? nk / kPrefillKeys : most;
-    if (n > 64) n = 64;
-    const int64_t room = kPrefillRows / (tq * q_heads);  // of the workspace
-    return n < room ? n : room > 1 ? room : 1;
-}
 hipError_t launch_attention_prefill(const AttnPrefillArgs& a, hipStream_t st);
 
 // MX setting (32-element blocks, ue8m0 scales, no global scale).

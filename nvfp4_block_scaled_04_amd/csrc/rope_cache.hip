@@ -18,7 +18,6 @@ namespace {
 // ---- rotary positions -----------------------------------------------------------
 
 constexpr int kRopeAngles = 2048;  // (cos, sin) pairs of a workgroup's tokens
-constexpr int64_t kRopeStream = (int64_t)128 << 20;
 
 // Threads of a workgroup: one that streams has less to wait for at its barrier if it is small
 // (20280 tokens of 48 x 128 at 128 / 256 threads: 82.9 / 86.5 us), where few tokens fill part of
@@ -133,11 +132,6 @@ struct CParams {
     int64_t k_stride, v_stride, nslots;
     int t, heads, d, page_log2;
 };
-
-// Threads of a workgroup, by the blocks there are: 8003 rows of 8 x 128 written and read at 256 /
-// 512: 19.8 / 19.0 us, 16 rows: 5.9 / 6.5.
-constexpr int kRowThreads = 256, kRowThreadsMany = 512;
-constexpr int64_t kRowsMany = 256 * kRowThreadsMany;  // a workgroup a CU
 
 // One block (16 elements) of a head's row a thread, of K and of V; consecutive threads take the
 // blocks of a row, then the heads, then the tokens.  At most 2^31 blocks: their index stays in
@@ -255,8 +249,8 @@ hipError_t launch_rope_axes(const RopeArgs& a, hipStream_t st) {
         p.ends[i] = i < a.axes - 1 ? end : 1 << 30;
     }
     // a few pieces a thread, while the workgroups still fill the card several times
-    const bool stream = a.t * a.heads * a.d * 2 > kRopeStream;
-    const int threads = rope_threads(stream);
+    const RopePlan plan = rope_plan(a.t, a.heads, a.d, a.rot / 2);
+    const int threads = rope_threads(plan.stream);
     const int64_t per = a.heads * (a.d / 16);  // (pairs of 16-byte pieces)
     int64_t tokens = per >= 4 * threads ? 1 : 4 * threads / per;
     const int64_t most = kRopeAngles / (a.rot / 2);
@@ -264,10 +258,9 @@ hipError_t launch_rope_axes(const RopeArgs& a, hipStream_t st) {
     while (tokens > 1 && (a.t + tokens - 1) / tokens < 1024) tokens >>= 1;
     p.tokens = (int)tokens;
     const dim3 grid((unsigned)((a.t + tokens - 1) / tokens));
-    const int64_t pairs = a.rot / 2;
-    if (pairs % 8 == 0) rope<8>(p, a.interleaved, stream, grid, st);
-    else if (pairs % 4 == 0) rope<4>(p, a.interleaved, stream, grid, st);
-    else rope<2>(p, a.interleaved, stream, grid, st);
+    if (plan.width == 8) rope<8>(p, a.interleaved, plan.stream, grid, st);
+    else if (plan.width == 4) rope<4>(p, a.interleaved, plan.stream, grid, st);
+    else rope<2>(p, a.interleaved, plan.stream, grid, st);
     return hipGetLastError();
 }
 
@@ -278,7 +271,7 @@ hipError_t launch_kv_rows(const KvRowsArgs& a, hipStream_t st) {
     p.nslots = a.pages * a.page; p.t = (int)a.t; p.heads = (int)a.heads; p.d = (int)a.d;
     p.page_log2 = __builtin_ctzll((unsigned long long)a.page);
     const int64_t n = a.t * a.heads * (a.d / 16);
-    const int threads = n >= kRowsMany ? kRowThreadsMany : kRowThreads;
+    const int threads = kv_rows_threads(n);
     const dim3 grid((unsigned)((n + threads - 1) / threads));
     if (a.read) k_kv_rows<true><<<grid, threads, 0, st>>>(p);
     else k_kv_rows<false><<<grid, threads, 0, st>>>(p);
