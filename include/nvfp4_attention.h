@@ -107,8 +107,9 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
  * 2^-39 of the head's largest where it is below 2^-28 of it), the probabilities as fp16 (off by
  * 2^-11 of themselves, or, below 2^-26 of the largest, by 2^-37 of it); sums are fp32.  The tokens
  * of long sequences are split over workgroups, whose parts a second launch joins; how, depends on
- * the lengths, which are read on the device (a captured graph follows them).  Results are the same
- * on every call.
+ * the lengths, which are read on the device (a captured graph follows them), and on the width of
+ * the table: one far wider than the longest sequence costs up to a quarter (16 of 500 tokens: 9.2
+ * us, with a table for 65536 11.7).  Results are the same on every call.
  *   q: [b, t, q_heads, d] bf16 with q_stride from token to token; block_table:
  *   [b, table_pages] int32 (entries past a sequence's last page are not read); lengths: [b]
  *   int32; out: [b, t, q_heads, d] bf16; lse: NULL or [b, t, q_heads] fp32,
@@ -149,6 +150,8 @@ int nvfp4_attention_decode(const void* q, int64_t q_stride, int64_t b, int64_t t
  *   aligned, contents ignored on entry, undefined on exit, not shared by calls that overlap).
  *   With one, few rows behind many keys have the keys split over workgroups, whose sums, fp32,
  *   a second launch joins.  Less than that is taken where it suffices for the sizes at hand.
+ * The kernel is chosen by the average sequence: a long prompt and many single rows are faster in
+ * two calls (32 / 8 heads of 128: 4096 rows beside 15 of one row behind 2000 keys 194 us, apart 128 + 28).
  */
 int attention_prefill(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, int64_t tq, int64_t tk, int64_t q_heads, int64_t heads, int64_t d,

@@ -7,8 +7,9 @@
 // of the cache (d * 9/8 a token, head and both tensors), so a workgroup serves 16 or 32
 // rows of a KV head with one read, and the tokens of a sequence are split over
 // workgroups where there are few sequences; a second launch joins the parts.  64 sequences
-// of 16384, 8 heads of 128 (1.2 GB): 193 us with 512 parts, 6.2 TB/s, what reads alone reach;
-// 32 heads over one of 32768 (38 MB): 11 us, of which 6 are the bytes'.
+// of up to 16384, 64 / 8 heads of 128 (631 MB): 119 us, 5.3 TB/s, of 16384 each (1.2 GB) 203, 6.0 TB/s,
+// what reads alone reach; 32 heads over one of 32768 (38 MB): 13 us, of which 6 are the bytes', and 4
+// of the join.
 //
 // A wave takes 64 tokens at a time, staged in LDS of its own (16 bytes a lane, straight from
 // memory, no barriers): one block, whose next loads start when the last read of it has
@@ -141,7 +142,7 @@ __device__ __forceinline__ int load_pages(const DParams& p, const int32_t* row, 
 
 // Starts a block's loads into LDS.  id: its groups' pages (page 0 in the place of none).
 // ONCE: no other workgroup reads the block (one tile of rows), so it passes the caches by
-// (streaming policy): 64 sequences of 16384, 1.2 GB, 244 -> 221 us a call.
+// (streaming policy): 64 sequences of 16384, 1.2 GB: 203 us a call, 220 without; of up to 16384 119, 129.
 // PACKED: rows lie in LDS as they do in memory, where the 16 rows of a group are 8 d bytes in one
 // piece, for a d that is no multiple of 32 (a row alone does not begin on 16 bytes) or half of D
 // (32 sequences of 8192, heads of 32: 33 us, 39 with rows of D; but of 96, 64 of up to 8192: 72, 67).

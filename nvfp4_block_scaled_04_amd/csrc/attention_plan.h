@@ -59,10 +59,12 @@ inline DecodePlan decode_plan(int64_t b, int64_t t, int64_t q_heads, int64_t hea
     p.row_tiles = (rows + tile - 1) / tile;
     p.once = p.row_tiles == 1;
     p.packed = d % 32 != 0 || 2 * d <= p.width;
-    // Long parts (by the table's size, the lengths being on the device) are better off with three
-    // workgroups a CU and cut finer, so that the last ones end together; short ones with four,
-    // whose beginnings overlap.  64 sequences to 16384: 122 us against 131; 4 to 131072: 109
-    // against 121; 64 of 16384 each: 203 against 193; 256 to 2048: 93 against 79 (not taken).
+    // Long parts (by the table's size, the lengths being on the device) of unequal sequences are
+    // better off with three workgroups a CU and cut finer, so that the last ones end together; short
+    // ones with four, whose beginnings overlap.  64 sequences to 16384: 119 us against 128; 4 to 131072: 113
+    // against 123; 256 to 2048: 89 against 74 (not taken).  Equal long sequences, which the host cannot
+    // tell, lose by it: 64 of 16384 each 203 against 196, 4 of 131072 122 against 106, 32 of 8192
+    // (32 / 8 heads) 66 against 57.
     // Heads of 64 have half the bytes a wave, so five workgroups a CU and more parts: 32 of 8192:
     // 43 us with 1024 parts, 49 with 512, 47 with 2048.
     const int64_t hrs = heads * p.row_tiles;

@@ -13,7 +13,7 @@
 //   needs one exchange between lanes, and only where the maximum moves;
 //   O^T[column, row] = V^T P^T: V^T comes from transposing LDS reads, in the order of
 //   keys in which a lane holds its column of S^T, so P stays where it is.
-// What bounds it: a prompt of 8192, 40 heads of 128, 620 us, 1.11 PFLOP/s: the card's power (on zeros
+// What bounds it: a prompt of 8192, 40 heads of 128, 600 us, 1.14 PFLOP/s: the card's power (on zeros
 // 480 us; the library's product of 8192^3 runs at 1.24-1.32 on such data, 1.76 on zeros); heads of 64
 // the softmax's arithmetic; short prompts the chain of a tile's keys.  Where few rows meet many
 // keys, workgroups share the keys (prefill_parts).
@@ -127,7 +127,8 @@ __device__ __forceinline__ u32x4 raw_buffer(const void* base, uint32_t bytes) {
 // PACK: the rows of all heads of a group lie in one tile, one after the other (row n is head n % G of
 // its token n / G), and share the keys that it reads.
 // KEYS: of a tile.  With 32, two workgroups of heads of 256 share a CU (512 registers and 160 KB),
-// with 64, one has them alone.
+// with 64, one has them alone.  (With 32, 33 registers spill, 55 with PACK: before and behind the
+// loop over the keys and in the second pass, none in the loop.)
 template <int D, int KEYS, int NW, int SPLIT, bool PARTS, bool PACK>
 __global__ __launch_bounds__(64 * NW, D * KEYS <= 128 * 64 ? 2 : 1) void k_attn_prefill(PParams p) {
 #if defined(__HIP_DEVICE_COMPILE__)
