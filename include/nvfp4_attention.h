@@ -101,7 +101,8 @@ int nvfp4_kv_read(const uint8_t* kv, const uint8_t* kv_sf, const float* kv_gs, i
  * holds them already: with L = lengths[i] (clamped to [0, table_pages * page]), token j of
  * sequence i sees the positions below L - (t - 1 - j), and for each of its heads h
  *   out = sum_p softmax_p(scale * q . K_p) V_p,   KV head h / (q_heads / heads).
- * A token that sees nothing gets zeros (and lse = -inf).  Pages outside [0, pages) are
+ * A token that sees nothing gets zeros (and lse = -inf).  Scores times log2(e) have to lie within
+ * fp32's range (this holds for attention_prefill too).  Pages outside [0, pages) are
  * passed over as if their positions were not seen.  The keys and values are
  * exact; q enters the products as fp16 scaled by a power of two per head (exact, but off by up to
  * 2^-39 of the head's largest where it is below 2^-28 of it), the probabilities as fp16 (off by
